@@ -343,6 +343,8 @@ kda_status kda_check(void* stream) {
     kda_status st = tc_take_error(static_cast<cudaStream_t>(stream));
     if (st != KDA_OK) return st;
     if ((st = simt_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
+    if ((st = paged_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
+    if ((st = pages_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -361,6 +363,7 @@ const char* kda_status_str(kda_status s) {
         case KDA_ERR_WORKSPACE: return "workspace missing or too small";
         case KDA_ERR_CUDA: return "CUDA error";
         case KDA_ERR_TIMEOUT: return "device wait timed out";
+        case KDA_ERR_PAGES: return "too few free pages";
     }
     return "unknown status";
 }

@@ -112,4 +112,47 @@ kda_status tc_take_error(cudaStream_t s);
 // limit (cycles); it records KDA_ERR_TIMEOUT for the next kda_check.
 kda_status tc_selftest_timeout(long long limit_cycles, cudaStream_t s);
 
+// ---- paged key-value cache (validated arguments only) ----
+// What the paged kernels take: sizes, pools and tables of one call.
+struct PagedArgs {
+    int S, HQ, HKV, G;                    // G = HQ / HKV
+    int num_pages, page_shift, max_pages; // page_size = 1 << page_shift
+    int cap;                              // max_pages * page_size, at most 2^31 - 1
+    long long page_stride, token_stride, head_stride;
+    float scale;
+    int window, sinks;
+    const void *kp, *vp;
+    const float *ks, *vs;                 // scale per key head (e4m3), may be null
+    const int *table, *lens, *cu;
+    int T;
+    const __nv_bfloat16* q;
+    long long q_stride;
+    __nv_bfloat16* o;
+    float* lse;
+};
+kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void* k,
+                               long long k_stride, const void* v, long long v_stride,
+                               cudaStream_t s);
+size_t paged_decode_ws_bytes(const PagedArgs& a, int D, bool e4m3);
+kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s);
+size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool e4m3);
+kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s);
+// Reads and clears the device error words of the paged kernels.
+kda_status paged_take_error(cudaStream_t s);
+
+// ---- page bookkeeping ----
+size_t pages_ws_bytes(const kda_pages_dims& d);
+kda_status pages_fork_launch(const kda_pages_dims& d, const kda_page_pool* pools, int num_pools,
+                             const int* parents, const int* children, int n, int* table,
+                             int* lens, int* refs, void* ws, cudaStream_t s);
+kda_status pages_extend_launch(const kda_pages_dims& d, const int* add, int add_all, int* table,
+                               int* lens, int* refs, void* ws, cudaStream_t s);
+kda_status pages_free_launch(const kda_pages_dims& d, const int* slots, int n, int* table,
+                             int* lens, int* refs, cudaStream_t s);
+kda_status pages_compact_launch(const kda_pages_dims& d, const kda_page_pool* pools,
+                                int num_pools, int* table, int* refs, void* ws, cudaStream_t s);
+kda_status pages_copy_launch(const kda_page_pool* pools, int num_pools, int num_pages,
+                             const int* src, const int* dst, int n, cudaStream_t s);
+kda_status pages_take_error(cudaStream_t s);
+
 }  // namespace kda

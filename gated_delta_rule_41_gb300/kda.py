@@ -19,7 +19,8 @@ _LIB_PATH = os.path.join(_PKG, "_build", "libkda.so")
 KDA_F32, KDA_BF16 = 0, 1
 IMPLS = {"auto": 0, "simt": 1, "tcgen05": 2}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "invalid shape", 3: "unsupported",
-           4: "alignment", 5: "workspace", 6: "cuda error", 7: "timeout"}
+           4: "alignment", 5: "workspace", 6: "cuda error", 7: "timeout",
+           8: "too few free pages"}
 
 
 class KdaError(RuntimeError):

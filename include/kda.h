@@ -1,6 +1,7 @@
 /*
  * kda.h -- C ABI of libkda.so: Kimi Delta Attention (KDA) chunk scan and
- * single-token decode step, hand-written CUDA for sm_103a (GB300).
+ * single-token decode step, and the paged key-value cache of the softmax
+ * attention layers beside them, hand-written CUDA for sm_103a (GB300).
  *
  * The operation (per batch b and value head hv, state S of K x V floats):
  *
@@ -74,10 +75,12 @@ typedef enum {
     KDA_ERR_ALIGNMENT = 4,    /* a pointer is misaligned (see Alignment above) */
     KDA_ERR_WORKSPACE = 5,    /* workspace missing or smaller than required */
     KDA_ERR_CUDA = 6,         /* a CUDA launch or runtime call failed */
-    KDA_ERR_TIMEOUT = 7       /* a bounded device wait expired */
+    KDA_ERR_TIMEOUT = 7,      /* a bounded device wait expired */
+    KDA_ERR_PAGES = 8         /* the page pool has too few free pages (kda_check) */
 } kda_status;
 
-typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
+/* KDA_E4M3 is a type of the paged key-value cache alone. */
+typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_E4M3 = 2 } kda_dtype;
 
 /* Which kernel family runs the chunk scan.
  *   KDA_IMPL_AUTO     tensor-core path when it supports the sizes, else SIMT.
@@ -263,10 +266,166 @@ kda_status kda_chunk_fwd_noalloc(const kda_dims* dims, const void* q, const void
                                  const void* v, const void* g, const void* beta, const float* h0,
                                  void* o, int output_final_state, float* ht, void* stream);
 
+/* ---- Paged key-value cache ------------------------------------------------
+ *
+ * The softmax-attention layers of a KDA:GQA hybrid keep keys and values per
+ * token, in pages of page_size tokens that a block table maps to sequences.
+ * These entry points write tokens into such a cache, attend over it, and keep
+ * its pages.  They serve inference: no gradients.
+ *
+ * Cache     K and V are two pools of num_pages pages.  Row r of page p, key
+ *           head h, starts at element p * page_stride + r * token_stride +
+ *           h * head_stride of its pool; its D elements are contiguous.  K and V
+ *           share the strides, so both common orders ([pages][rows][heads][D]
+ *           and [pages][heads][rows][D]) and pools that hold K and V side by
+ *           side fit.  Elements are bf16, or e4m3 codes (KDA_E4M3) that stand
+ *           for code * scale[h], with one float scale per key head and pool.
+ * Tables    block_table int32 [S][max_pages] (device): token j of sequence s
+ *           lies in row j % page_size of page block_table[s][j / page_size].
+ *           kv_lens int32 [S] (device): tokens of each sequence in the cache,
+ *           the ones a call writes or asks about included.  Entries past the
+ *           last page of a sequence are not read.  Row slots past a sequence's
+ *           last token may hold anything, NaN included.
+ * Attention Query head h reads key head h / (HQ / HKV).  A query at position p
+ *           sees token j iff  j <= p and (window == 0 or j > p - window or
+ *           j < sinks):  a sliding window of `window` tokens, its own included,
+ *           and the first `sinks` tokens.
+ *               o = sum_j softmax_j(scale q . k_j) v_j,
+ *               lse = log sum_j exp(scale q . k_j)      over the visible j;
+ *           a query that sees no token gets o = 0 and lse = -inf.  Products
+ *           accumulate in fp32 and the softmax statistics are fp32; the
+ *           weights enter the product with V in bf16 (with an e4m3 cache in
+ *           fp16, with q scaled per head by a power of two to fit it).
+ * Types     q, o and new keys and values are bf16, lse float32.
+ * Sizes     D 64 or 128; page_size 16, 32, 64, 128 or 256; HQ a multiple of
+ *           HKV with at most 64 query heads per key head; at most 65535
+ *           sequences, 65535 key heads, 2^30 pages, and 2^30 tokens in a row
+ *           of the table and 2^30 query rows (T * HQ); else
+ *           KDA_ERR_UNSUPPORTED.  Offsets into the pools are 64-bit.
+ * Alignment Pools, q, k, v and o 16 bytes, and so must their strides be; the
+ *           workspace 256 bytes; the rest its element size.
+ * Errors    As above.  What only the device can see is reported by kda_check
+ *           as KDA_ERR_SHAPE, never accessed out of bounds, and has these
+ *           results: kv_lens outside [0, max_pages * page_size] count as 0; a
+ *           page id outside [0, num_pages) of a token that is read makes the
+ *           token's key and value zero, of one that is written drops the
+ *           write; cu_seqlens that do not rise from 0 to T leave the call
+ *           without effect. */
+typedef struct {
+    int S;                      /* sequences: rows of block_table */
+    int HQ, HKV, D;             /* query heads, key/value heads, head width */
+    int num_pages, page_size;   /* pages in a pool, tokens in a page */
+    int max_pages;              /* columns of block_table */
+    kda_dtype cache_dtype;      /* KDA_BF16 or KDA_E4M3 */
+    long long page_stride, token_stride, head_stride;   /* in elements */
+    float scale;                /* multiplies q . k; 1/sqrt(D) is the standard one */
+    int window, sinks;          /* 0, 0: every earlier token is visible */
+} kda_paged_dims;
+
+/* Write new tokens into the cache.  k, v [T][HKV][D] bf16, tokens k_stride and
+ * v_stride elements apart.  cu_seqlens int32 [S + 1] (device): sequence s owns
+ * tokens [cu_seqlens[s], cu_seqlens[s + 1]) and they become the last ones of
+ * its kv_lens[s]; NULL: one token for each sequence (T == S).  A token whose
+ * position would be negative (an idle slot with kv_lens[s] == 0) is dropped.
+ * k_scale, v_scale float [HKV] (device) for KDA_E4M3, NULL for all ones; the
+ * stored code is x * (1 / scale) rounded to nearest even and saturated at
+ * +-448 (NaN stays NaN).  HQ, scale, window and sinks are ignored.  The pages
+ * written must belong to one sequence each. */
+kda_status kda_paged_append(const kda_paged_dims* dims, const int* cu_seqlens, int T,
+                            const void* k, long long k_stride, const void* v, long long v_stride,
+                            const float* k_scale, const float* v_scale, const int* block_table,
+                            const int* kv_lens, void* k_pages, void* v_pages, void* stream);
+
+/* Attention of one new token per sequence: q, o [S][HQ][D] (q rows q_stride
+ * elements apart, o dense), lse float [S][HQ] or NULL; the query stands at
+ * position kv_lens[s] - 1 (its own key and value already appended). */
+size_t kda_paged_decode_workspace_bytes(const kda_paged_dims* dims);
+kda_status kda_paged_decode(const kda_paged_dims* dims, const void* q, long long q_stride,
+                            const void* k_pages, const void* v_pages, const float* k_scale,
+                            const float* v_scale, const int* block_table, const int* kv_lens,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Attention of prompt tokens packed along T: q, o [T][HQ][D], lse float
+ * [T][HQ] or NULL.  Sequence s owns query tokens [cu_seqlens[s],
+ * cu_seqlens[s + 1]), the last ones of its kv_lens[s]: token i of n stands at
+ * position kv_lens[s] - n + i, so a prompt may come in chunks.  Queries at
+ * negative positions (fewer tokens in the cache than queries) see nothing. */
+size_t kda_paged_prefill_workspace_bytes(const kda_paged_dims* dims, int T);
+kda_status kda_paged_prefill(const kda_paged_dims* dims, const int* cu_seqlens, int T,
+                             const void* q, long long q_stride, const void* k_pages,
+                             const void* v_pages, const float* k_scale, const float* v_scale,
+                             const int* block_table, const int* kv_lens, void* o, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Page bookkeeping.  The tables live on the device and every call updates them
+ * there, in stream order, without the host learning a length:
+ *   block_table int32 [S][max_pages]  page ids, -1 past a row's last page
+ *   kv_lens     int32 [S]             tokens of each sequence (0: an idle row)
+ *   refs        int32 [num_pages]     how many rows hold the page; 0: free
+ * A sequence holds ceil(kv_lens[s] / page_size) pages.  A page may be held by
+ * several rows only if it is full in all of them.  Where pages are taken they
+ * are the lowest free ones, in the order of the requests.  A request that the
+ * free pages do not cover, and every later one that needs a page, is refused
+ * (its row stays as it was; a fork's child stays idle) and kda_check reports
+ * KDA_ERR_PAGES.  Row indices out of range, lengths that the table cannot hold
+ * and page ids out of range are skipped and reported as KDA_ERR_SHAPE.
+ *
+ * A pool is memory whose pages are moved with the table: K and V of each
+ * layer.  Page p is the page_bytes contiguous bytes at base + p *
+ * page_stride_bytes; all three are multiples of 16.  At most KDA_MAX_POOLS. */
+#define KDA_MAX_POOLS 64
+typedef struct {
+    void* base;
+    long long page_stride_bytes, page_bytes;
+} kda_page_pool;
+typedef struct {
+    int S, max_pages, num_pages, page_size;
+} kda_pages_dims;
+
+size_t kda_pages_workspace_bytes(const kda_pages_dims* dims);
+
+/* Row children[i] becomes a copy of row parents[i], for i < n (n <= S): full
+ * pages are shared, the partial last one is copied to a page of the child's
+ * own, in every pool.  Children must be distinct idle rows. */
+kda_status kda_pages_fork(const kda_pages_dims* dims, const kda_page_pool* pools, int num_pools,
+                          const int* parents, const int* children, int n, int* block_table,
+                          int* kv_lens, int* refs, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Make room: kv_lens[s] grows by add[s] (int32 [S] on the device, >= 0), or
+ * with add == NULL by add_all for each row with kv_lens[s] > 0, and pages are
+ * taken for the tokens that the last page does not hold. */
+kda_status kda_pages_extend(const kda_pages_dims* dims, const int* add, int add_all,
+                            int* block_table, int* kv_lens, int* refs, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Release the rows slots[0..n) (distinct): their pages' counts drop by one,
+ * the rows become idle. */
+kda_status kda_pages_free(const kda_pages_dims* dims, const int* slots, int n, int* block_table,
+                          int* kv_lens, int* refs, void* stream);
+
+/* Move the held pages with ids at or above their number L, in rising order,
+ * to the free ids below L, in rising order, in every pool, and rename them in
+ * block_table and refs.  Afterwards pages [0, L) are held and the rest free.
+ * Every row that holds pages of the pools must be in block_table. */
+kda_status kda_pages_compact(const kda_pages_dims* dims, const kda_page_pool* pools,
+                             int num_pools, int* block_table, int* refs, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Copy page src[i] to page dst[i], i < n, in every pool of num_pages pages;
+ * pairs with an id out of range are skipped, negative ones silently.  No page
+ * may be the destination of two pairs, or the source of one and the
+ * destination of another.  (With one "page" per sequence this also copies
+ * recurrent states.) */
+kda_status kda_pages_copy(const kda_page_pool* pools, int num_pools, int num_pages,
+                          const int* src, const int* dst, int n, void* stream);
+
 /* Synchronise `stream`, then report (and clear) any error a kernel recorded on
  * the device since the last check: KDA_ERR_TIMEOUT for an expired bounded
  * wait, KDA_ERR_SHAPE for cu_seqlens that break the rules of the varlen
- * entry points, KDA_ERR_CUDA for a runtime error. */
+ * entry points or tables that break those of the paged cache, KDA_ERR_PAGES
+ * for a page request that was refused, KDA_ERR_CUDA for a runtime error. */
 kda_status kda_check(void* stream);
 
 /* Diagnostics: per-kernel device timing.  kda_timing_enable(1) clears the

@@ -185,10 +185,6 @@ kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void*
     return launch_status();
 }
 
-size_t paged_decode_ws_bytes(const PagedArgs&, int, bool) { return 0; }
-kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void*, cudaStream_t s) {
-    return attend_any(a, D, e4m3, "paged_decode", s);
-}
 size_t paged_prefill_ws_bytes(const PagedArgs&, int, bool) { return 0; }
 kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void*, cudaStream_t s) {
     return attend_any(a, D, e4m3, "paged_prefill", s);

@@ -172,9 +172,9 @@ def _attention_workspace(need, workspace, device, stream):
         return None
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         return workspace
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _fresh(stream, ws)
-    return ws
+    # zeroed on the launch's stream: the joining CTAs count from zero
+    with torch.cuda.stream(stream):
+        return torch.zeros(need, dtype=torch.uint8, device=device)
 
 
 def _outputs(q, out, lse, return_lse, stream):
@@ -196,9 +196,10 @@ def _outputs(q, out, lse, return_lse, stream):
 
 def paged_decode_workspace(pages: KVPages, S, HQ, max_pages=1) -> Optional[torch.Tensor]:
     """A workspace for ``paged_decode`` calls of S sequences and HQ heads (any
-    lengths); calls that overlap on the GPU need one each."""
+    lengths), zeroed as it must be before its first use.  Calls that overlap on
+    the GPU need one each."""
     need = int(_lib().kda_paged_decode_workspace_bytes(pages.dims(S, HQ, max_pages)))
-    return torch.empty(need, dtype=torch.uint8, device=pages.k.device) if need else None
+    return torch.zeros(need, dtype=torch.uint8, device=pages.k.device) if need else None
 
 
 def paged_decode(q, pages: KVPages, block_table, kv_lens, scale=None, window=0, sinks=0, out=None,
@@ -228,7 +229,7 @@ def paged_decode(q, pages: KVPages, block_table, kv_lens, scale=None, window=0, 
 def paged_prefill_workspace(pages: KVPages, S, T, HQ, max_pages=1) -> Optional[torch.Tensor]:
     """A workspace for ``paged_prefill`` calls of T query tokens in S sequences."""
     need = int(_lib().kda_paged_prefill_workspace_bytes(pages.dims(S, HQ, max_pages), T))
-    return torch.empty(need, dtype=torch.uint8, device=pages.k.device) if need else None
+    return torch.zeros(need, dtype=torch.uint8, device=pages.k.device) if need else None
 
 
 def paged_prefill(q, pages: KVPages, block_table, kv_lens, cu_seqlens, scale=None, window=0,

@@ -345,6 +345,7 @@ kda_status kda_check(void* stream) {
     if ((st = simt_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
     if ((st = paged_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
     if ((st = paged_decode_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
+    if ((st = paged_prefill_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
     if ((st = pages_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -185,9 +185,11 @@ kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void*
     return launch_status();
 }
 
-size_t paged_prefill_ws_bytes(const PagedArgs&, int, bool) { return 0; }
-kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void*, cudaStream_t s) {
-    return attend_any(a, D, e4m3, "paged_prefill", s);
+size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool e4m3) {
+    return e4m3 ? 0 : paged_prefill_tc_ws_bytes(a, D);
+}
+kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s) {
+    return e4m3 ? attend_any(a, D, true, "paged_prefill", s) : paged_prefill_tc_launch(a, D, ws, s);
 }
 
 kda_status paged_take_error(cudaStream_t s) {

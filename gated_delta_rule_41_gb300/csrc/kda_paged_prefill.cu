@@ -1,0 +1,693 @@
+// Attention of prompt tokens over a paged key-value cache: causal, with a
+// sliding window and sinks, on the tensor cores (tcgen05 + TMEM + TMA).
+//
+// A CTA takes 256 query rows of one (sequence, key head) as two tiles A, B of
+// 128.  A row is a (token, query head) pair, the G heads that share the key
+// head side by side, so shared heads fill the MMA's M axis and every K and V tile is
+// read once for all of them.  Per tile of 128 cached tokens:
+//     S = Q K^T                  tcgen05, fp32 in TMEM, one thread per row reads it
+//     P = exp2(f S - m)          f = scale log2(e); back to TMEM over S
+//     O += P V                   tcgen05, P from TMEM, V as it lies (MN-major)
+// While the softmax of one tile runs, the tensor core works for the other.  For
+// every 128 x 256 block the four products take 2048 cycles at the dense bf16
+// rate and the 32768 exponentials 1024 of the special function units, so
+// the tensor core bounds it if neither chain waits.
+//
+// Softmax.  The running maximum m of a row is raised, and its O and sum
+// rescaled, only when a logit exceeds m by more than 8 (a weight of 256);
+// sums are fp32.  P goes into the product with V as bf16, rounded by up to 2^-8 of
+// each weight.  Over many comparable weights that averages out; where single
+// weights carry the row it would be as large as the output's own rounding, so
+// a tile in which some row has a weight above 1/32 of its sum so far also
+// multiplies what the rounding lost (a second bf16 term, 2^-16 together).
+//
+// K and V tiles arrive by TMA, one box per page, into one ring of slots.  Pages past the
+// sequence's end, and pages out of range, are asked for at a coordinate
+// outside the pool, which TMA fills with zeros; the row slots of the last page
+// past the end are cleared before V is multiplied (they may hold NaN).
+//
+// Roles: warps 0-3 softmax and output of tile A, 4-7 of B, warp 8 TMA, warp 9
+// MMA.  Every wait is bounded; on expiry the error is recorded and the CTA
+// unwinds.  With few query rows the cached tokens are split over several CTAs, whose
+// parts a second kernel joins.
+#include <algorithm>
+#include <mutex>
+
+#include "kda_paged.cuh"
+#include "kda_timing.cuh"
+
+namespace kda {
+
+__device__ int g_paged_prefill_error = 0;   // a kda_status
+
+namespace {
+
+using namespace ptx;
+using namespace paged;
+
+constexpr int kTile = 128;                  // query rows and cached tokens of a tile
+constexpr int kThreads = 320;
+constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
+constexpr float kRaise = 8.f;               // log2 of the weight that raises the maximum
+constexpr float kSplitWeight = 1.f / 32.f;  // weights above this share take two terms
+
+__device__ __forceinline__ void record(kda_status code) {
+    atomicCAS(&g_paged_prefill_error, 0, (int)code);
+}
+
+// Bounded mbarrier wait: gives up after the limit, or when another wait has.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    uint32_t it = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        if ((++it & 255u) == 0) {
+            if (*reinterpret_cast<volatile int*>(&g_paged_prefill_error) == KDA_ERR_TIMEOUT)
+                return false;
+            if (clock64() - t0 > kTimeoutCycles) {
+                atomicExch(&g_paged_prefill_error, (int)KDA_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
+}
+// Time-bounded only: for copies and MMAs that must end before the CTA does.
+__device__ __forceinline__ void wait_bar_drain(uint64_t* bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > kTimeoutCycles) return;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+// D (+)= A B^T with A in tensor memory (bf16 pairs, 8 columns per 16 of K).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16_nw(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+// Whether `p` holds for any of the 128 threads that meet at named barrier id.
+__device__ __forceinline__ bool any128(int id, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)p), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+template <int D>
+struct Plan {
+    static constexpr uint32_t SLOT = kTile * D * 2;           // a K or V tile
+    static constexpr uint32_t HALF = kTile * 128;             // its 64-column half
+    static constexpr int SLOTS = D == 128 ? 5 : 8;
+    static constexpr uint32_t OFF_Q = 0;                      // two tiles
+    static constexpr uint32_t OFF_KV = 2 * SLOT;
+    static constexpr uint32_t OFF_BAR = OFF_KV + SLOTS * SLOT;
+    static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;    // + alignment slack
+    static_assert(SMEM <= 232448, "over the shared memory of a CTA");
+};
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;       // S_A, S_B, O_A, O_B: 128 each
+
+struct Split {                 // parts of a row, one per CTA that works on it
+    float* o;                  // [splits][T * HQ][D], unscaled sums
+    float2* ml;                // [splits][T * HQ] maximum (log2), sum
+};
+
+// The tiles of cached tokens that an item's rows see: those of the sinks, then
+// those from the window's start to the last row's position.
+struct Span {
+    int nsink, first, n;
+    __device__ __forceinline__ int tile(int i) const { return i < nsink ? i : i - nsink + first; }
+};
+__device__ __forceinline__ Span make_span(const PagedArgs& a, int p_min, int p_max) {
+    Span s = {0, 0, 0};
+    if (p_max < 0) return s;
+    const int low = a.window ? max(0, p_min - a.window + 1) : 0;
+    s.first = low / kTile;
+    s.nsink = min((min(a.sinks, low) + kTile - 1) / kTile, s.first);
+    s.n = s.nsink + p_max / kTile + 1 - s.first;
+    return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, int TB, int heads_first,
+               Split part) {
+    using P = Plan<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::OFF_BAR);
+    uint64_t* kv_full = bars;                     // [SLOTS]
+    uint64_t* kv_empty = kv_full + P::SLOTS;      // [SLOTS]
+    uint64_t* q_full = kv_empty + P::SLOTS;       // [2]
+    uint64_t* s_full = q_full + 2;                // [2] S is in TMEM, and O up to the tile before
+    uint64_t* p_full = s_full + 2;                // [2] P is in TMEM
+    uint64_t* o_full = p_full + 2;                // [2] O is complete
+    uint64_t* done = o_full + 2;                  // every MMA has ended (unwinding)
+    int* two_terms = reinterpret_cast<int*>(done + 1);   // [2]
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(two_terms + 2);
+    __shared__ int s_scan[kThreads / 32], s_seq, s_block;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- which item: sequence, block of 2 TB tokens (the last ones, with the
+    // most to read, start first), key head ----
+    const int h = blockIdx.x % a.HKV;
+    {
+        const int each = (a.S + kThreads - 1) / kThreads;
+        const int lo = min(a.S, tid * each), hi = min(a.S, lo + each);
+        bool bad = tid == 0 && (a.cu[0] != 0 || a.cu[a.S] != a.T);
+        int mine = 0;
+        for (int s = lo; s < hi; ++s) {
+            const int n = a.cu[s + 1] - a.cu[s];
+            bad |= n < 0 || a.cu[s] < 0 || a.cu[s + 1] > a.T;
+            if (!bad) mine += (n + 2 * TB - 1) / (2 * TB);
+        }
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) s_scan[warp] = sum;
+        if (tid == 0) s_seq = -1;
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) record(KDA_ERR_SHAPE);
+            return;
+        }
+        int before = sum - mine, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_scan[w];
+            total += s_scan[w];
+        }
+        const int item = total - 1 - (int)(blockIdx.x / a.HKV);
+        if (item >= before && item < before + mine) {
+            int s = lo, at = before;
+            for (;; ++s) {
+                const int n = (a.cu[s + 1] - a.cu[s] + 2 * TB - 1) / (2 * TB);
+                if (item < at + n) break;
+                at += n;
+            }
+            s_seq = s;
+            s_block = item - at;
+        }
+        __syncthreads();
+        if (s_seq < 0) return;
+    }
+    const int s = s_seq, cu0 = a.cu[s], nq = a.cu[s + 1] - cu0;
+    int len = a.lens[s];
+    if (len < 0 || len > a.cap) {
+        if (tid == 0) record(KDA_ERR_SHAPE);
+        len = 0;
+    }
+    const int i0 = s_block * 2 * TB;                         // first token of tile A in the prompt
+    const int p0 = len - nq + i0;                            // its position
+    const int p_last = min(p0 + 2 * TB, len) - 1;
+    const Span sp = make_span(a, p0, p_last);
+    const int n_lo = (int)((long long)sp.n * blockIdx.y / gridDim.y);
+    const int n_hi = (int)((long long)sp.n * (blockIdx.y + 1) / gridDim.y);
+    const int N = n_hi - n_lo;                               // tiles of this CTA
+
+    if (tid == 0) {
+        for (int i = 0; i < P::SLOTS; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&q_full[x], 1);
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], kTile);
+            mbar_init(&o_full[x], 1);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 9 && N > 0) {
+        tmem_alloc(tmem_holder, TM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = N > 0 ? *tmem_holder : 0;
+
+    if (warp == 8 && N > 0) {
+        // ---------------- TMA ----------------
+        if (lane == 0) {
+            for (int x = 0; x < 2; ++x) {
+                mbar_arrive_expect_tx(&q_full[x], (uint32_t)(TB * a.G * D * 2));
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(smem + P::OFF_Q + x * P::SLOT + c * P::HALF, &tm_q, &q_full[x],
+                                64 * c, h * a.G, cu0 + i0 + x * TB);
+            }
+        }
+        const int rows = min(1 << a.page_shift, kTile);      // rows of a box
+        const int boxes = kTile / rows;
+        const int* table = a.table + (size_t)s * a.max_pages;
+        int issued = 0;
+        for (int n = 0; n < N; ++n) {
+            const int j0 = sp.tile(n_lo + n) * kTile;
+            int page = a.num_pages;                          // outside the pool: zeros
+            const int j = j0 + lane * rows;
+            if (lane < boxes && j < len) {
+                page = __ldg(table + (j >> a.page_shift));
+                if ((unsigned)page >= (unsigned)a.num_pages) {
+                    record(KDA_ERR_SHAPE);
+                    page = a.num_pages;
+                }
+            }
+            const int r0 = j & ((1 << a.page_shift) - 1);
+            bool ok = true;
+            for (int kv = 0; kv < 2; ++kv) {
+                const int q = 2 * n + kv, slot = q % P::SLOTS;
+                ok = wait_bar_warp(&kv_empty[slot], ((q / P::SLOTS) & 1) ^ 1);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], P::SLOT);
+                __syncwarp();
+                if (lane < boxes) {
+                    uint8_t* dst = smem + P::OFF_KV + slot * P::SLOT + lane * rows * 128;
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(dst + c * P::HALF, kv ? &tm_v : &tm_k, &kv_full[slot], 64 * c,
+                                    heads_first ? r0 : h, heads_first ? h : r0, page);
+                }
+                issued = q + 1;
+            }
+            if (!ok) break;
+        }
+        if (issued < 2 * N) {                                // unwinding: let the copies land
+            for (int q = max(0, issued - P::SLOTS); q < issued; ++q)
+                wait_bar_drain(&kv_full[q % P::SLOTS], (q / P::SLOTS) & 1);
+            for (int x = 0; x < 2; ++x) wait_bar_drain(&q_full[x], 0);
+        }
+        __syncwarp();
+    } else if (warp == 9 && N > 0) {
+        // ---------------- MMA ----------------
+        constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile);
+        constexpr uint32_t ID_O = idesc_bf16_f32(kTile, D) | kBMajorMN;
+        const uint32_t kv = smem_u32(smem + P::OFF_KV), qs = smem_u32(smem + P::OFF_Q);
+        auto s_mma = [&](int x, int slot) {
+            const uint32_t kt = kv + slot * P::SLOT, qt = qs + x * P::SLOT;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t o = (k >> 2) * P::HALF + (k & 3) * 32;
+                mma_bf16(tmem + TM_S + x * kTile, sdesc_sw128(qt + o), sdesc_sw128(kt + o), ID_S,
+                         k > 0);
+            }
+            mma_commit(&s_full[x]);
+        };
+        bool ok = true;
+        for (int x = 0; x < 2 && ok; ++x) {
+            ok = wait_bar_warp(&q_full[x], 0) && (x > 0 || wait_bar_warp(&kv_full[0], 0));
+            if (ok && lane == 0) {
+                tc_fence_after();
+                s_mma(x, 0);
+                if (x == 1) mma_commit(&kv_empty[0]);
+            }
+        }
+        for (int n = 0; n < N && ok; ++n) {
+            const int qv = 2 * n + 1, vslot = qv % P::SLOTS;
+            const int qk = 2 * n + 2, kslot = qk % P::SLOTS;
+            for (int x = 0; x < 2 && ok; ++x) {
+                if (x == 0) {
+                    ok = wait_bar_warp(&kv_full[vslot], (qv / P::SLOTS) & 1);
+                    // row slots past the sequence's end may hold anything
+                    const int valid = len - sp.tile(n_lo + n) * kTile;
+                    if (ok && valid < kTile) {
+                        uint8_t* vt = smem + P::OFF_KV + vslot * P::SLOT;
+                        for (int i = max(0, valid) * (D / 8) + lane; i < kTile * (D / 8); i += 32) {
+                            const int r = i / (D / 8), c = i % (D / 8);
+                            *reinterpret_cast<uint4*>(vt + (c >> 3) * P::HALF + r * 128 +
+                                                      (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                }
+                ok = ok && wait_bar_warp(&p_full[x], n & 1);
+                if (ok && lane == 0) {
+                    tc_fence_after();
+                    const uint32_t vt = kv + vslot * P::SLOT, pt = tmem + TM_S + x * kTile;
+                    const int terms = two_terms[x] ? 2 : 1;
+                    for (int e = 0; e < terms; ++e)
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(tmem + TM_O + x * kTile, pt + 64 * e + 8 * k,
+                                   sdesc_mn_sw128(vt + k * 2048, P::HALF), ID_O,
+                                   n > 0 || k > 0 || e > 0);
+                    if (x == 1) mma_commit(&kv_empty[vslot]);
+                    if (n + 1 == N) mma_commit(&o_full[x]);
+                }
+                __syncwarp();
+                if (n + 1 < N && ok) {
+                    if (x == 0) ok = wait_bar_warp(&kv_full[kslot], (qk / P::SLOTS) & 1);
+                    if (ok && lane == 0) {
+                        tc_fence_after();
+                        s_mma(x, kslot);
+                        if (x == 1) mma_commit(&kv_empty[kslot]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (!ok) {                                           // unwinding: let the MMAs end
+            if (lane == 0) {
+                mma_commit(done);
+                wait_bar_drain(done, 0);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ---------------- softmax and output: one thread per query row ----------------
+        const int x = warp >> 2, r = tid & 127;
+        const int i = i0 + x * TB + r / a.G;
+        const bool live = r < TB * a.G && i < nq;
+        const int p = live ? len - nq + i : -1;              // a dead row sees nothing
+        const bool flat = a.scale == 0.f;                    // every visible token weighs the same
+        const float f = flat ? 1.f : a.scale * kLog2e;
+        const int px = p0 + x * TB;                          // positions of the tile's rows
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + TM_S + x * kTile + lanes, to = tmem + TM_O + x * kTile + lanes;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int n = 0; n < N; ++n) {
+            const int j0 = sp.tile(n_lo + n) * kTile;
+            ok = wait_bar_warp(&s_full[x], n & 1);
+            // a failed wait: leave in step with the other warps of the tile
+            if (any128(1 + x, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_nw(ts + 32 * c, v[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_ld_dep(v[c]);
+            if (flat)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[c][e] = 0.f;
+            // every row of the tile sees all of it?
+            const bool all = j0 + kTile - 1 <= px && (a.window == 0 || j0 > px + TB - 1 - a.window);
+            if (!all || !live) {
+                const int hi = p - j0, lo = a.window ? p - a.window + 1 - j0 : 0;
+                const int sk = a.sinks - j0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int k = 32 * c + e;
+                        if (k > hi || (k < lo && k >= sk)) v[c][e] = f < 0.f ? INFINITY : -INFINITY;
+                    }
+            }
+            // the largest f S (a negative scale takes the smallest S)
+            float top;
+            if (f >= 0.f) {
+                top = v[0][0];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, v[c][e]);
+            } else {
+                top = v[0][0];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fminf(top, v[c][e]);
+            }
+            top = fabsf(top) == INFINITY ? -INFINITY : top * f;
+            const bool rise = top > m + kRaise;
+            if (__any_sync(0xffffffffu, rise)) {
+                const float up = rise ? top : m;
+                const float keep = up == m ? 1.f : ex2(m - up);
+                m = up;
+                l *= keep;
+                if (n > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(to + 32 * c, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= keep;
+                        tmem_st32_nw(to + 32 * c, o);
+                    }
+                }
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            const bool two = any128(3 + x, ex2(top - mm) > kSplitWeight * l);
+            if (r == 0) two_terms[x] = two;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t hi[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float w0 = ex2(fmaf(v[c][2 * e], f, -mm));
+                    const float w1 = ex2(fmaf(v[c][2 * e + 1], f, -mm));
+                    sum0 += w0;
+                    sum1 += w1;
+                    hi[e] = pack_bf16(w0, w1);
+                    if (two) {
+                        v[c][2 * e] = w0 - __uint_as_float(hi[e] << 16);
+                        v[c][2 * e + 1] = w1 - __uint_as_float(hi[e] & 0xffff0000u);
+                    }
+                }
+                tmem_st16_nw(ts + 16 * c, hi);
+                if (two) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) hi[e] = pack_bf16(v[c][2 * e], v[c][2 * e + 1]);
+                    tmem_st16_nw(ts + 64 + 16 * c, hi);
+                }
+            }
+            l += sum0 + sum1;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[x]);
+        }
+        // ---- output ----
+        if (N > 0) {
+            ok = ok && wait_bar_warp(&o_full[x], 0);
+            tc_fence_after();
+        }
+        const long long row = ((long long)cu0 + i) * a.HQ + h * a.G + r % a.G;
+        if (gridDim.y > 1) {
+            const long long at = (long long)blockIdx.y * a.T * a.HQ + row;
+            if (live) part.ml[at] = make_float2(m, l);
+            if (N > 0 && ok) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(to + 32 * c, o);
+                    if (live && m != -INFINITY)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(part.o + at * D + 32 * c + 4 * e) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+        } else {
+            const bool any = m != -INFINITY;
+            const float inv = any ? 1.f / l : 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                if (N > 0 && ok) tmem_ld32(to + 32 * c, o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (any)
+                        w = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                       pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                       pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    if (live) *reinterpret_cast<uint4*>(a.o + row * D + 32 * c + 8 * e) = w;
+                }
+            }
+            if (live && a.lse) a.lse[row] = any ? (m + lg2(l)) * kLn2 : -INFINITY;
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9 && N > 0) tmem_dealloc(tmem, TM_COLS);
+}
+
+// Joins the parts of a row: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, Split part, int splits) {
+    constexpr int E = D / 32;
+    const long long rows = (long long)a.T * a.HQ;
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    float top = -INFINITY;
+    for (int k = 0; k < splits; ++k) top = fmaxf(top, part.ml[k * rows + row].x);
+    float l = 0.f, o[E] = {};
+    for (int k = 0; k < splits; ++k) {
+        const float2 ml = part.ml[k * rows + row];
+        if (ml.x == -INFINITY) continue;
+        const float w = ex2(ml.x - top);
+        l += w * ml.y;
+        const float* src = part.o + (k * rows + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += w * src[e];
+    }
+    const float inv = top == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(a.o + row * D + lane * E + e) =
+            pack_bf16(o[e] * inv, o[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = top == -INFINITY ? -INFINITY : (top + lg2(l)) * kLn2;
+}
+
+// ---- host ----
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn get_encoder() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return get_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims,
+                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query tokens of a 128-row tile, and upper bounds of the items of a call.
+int tile_tokens(const PagedArgs& a) { return kTile / a.G; }
+long long most_items(const PagedArgs& a) {
+    return ((long long)a.T / (2 * tile_tokens(a)) + std::min(a.S, a.T)) * a.HKV;
+}
+// CTAs per item: enough for the SMs when the items are few.
+int most_splits(const PagedArgs& a) {
+    return (int)std::max(1LL, std::min(32LL, sm_count() / most_items(a)));
+}
+size_t part_bytes(const PagedArgs& a, int D, int splits) {
+    return align256((size_t)splits * a.T * a.HQ * D * sizeof(float));
+}
+
+template <int D>
+kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
+    static bool set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
+    if (!get_encoder()) return KDA_ERR_CUDA;
+    if (!set[dev]) {
+        if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Plan<D>::SMEM) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        set[dev] = true;
+    }
+    const int TB = tile_tokens(a), page = 1 << a.page_shift;
+    CUtensorMap mq, mk, mv;
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.HQ, (cuuint64_t)a.T};
+        const cuuint64_t strides[2] = {
+            (cuuint64_t)D * 2, (cuuint64_t)(a.T > 1 ? a.q_stride : (long long)a.HQ * D) * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)TB};
+        if (!encode(&mq, a.q, 3, dims, strides, box)) return KDA_ERR_CUDA;
+    }
+    // heads and rows of a page in the order of their strides
+    const bool hf = a.HKV > 1 && a.head_stride > a.token_stride;
+    {
+        const cuuint64_t row = (cuuint64_t)a.token_stride * 2;
+        const cuuint64_t head = a.HKV > 1 ? (cuuint64_t)a.head_stride * 2 : (cuuint64_t)D * 2;
+        const cuuint64_t pg = a.num_pages > 1 ? (cuuint64_t)a.page_stride * 2 : row * page;
+        const cuuint32_t rows = (cuuint32_t)std::min(page, kTile);
+        const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(hf ? page : a.HKV),
+                                    (cuuint64_t)(hf ? a.HKV : page), (cuuint64_t)a.num_pages};
+        const cuuint64_t strides[3] = {hf ? row : head, hf ? head : row, pg};
+        const cuuint32_t box[4] = {64, hf ? rows : 1, hf ? 1 : rows, 1};
+        if (!encode(&mk, a.kp, 4, dims, strides, box) || !encode(&mv, a.vp, 4, dims, strides, box))
+            return KDA_ERR_CUDA;
+    }
+    // a split takes four tiles or more of the longest row
+    const int splits = (int)std::max<long long>(
+        1, std::min<long long>(most_splits(a), a.cap / (4 * kTile)));
+    const Split part = {static_cast<float*>(ws),
+                        reinterpret_cast<float2*>(static_cast<char*>(ws) + part_bytes(a, D, splits))};
+    {
+        TimedLaunch tl("paged_prefill", s);
+        prefill_kernel<D><<<dim3((unsigned)most_items(a), splits), kThreads, Plan<D>::SMEM, s>>>(
+            mq, mk, mv, a, TB, hf ? 1 : 0, part);
+        const kda_status st = launch_status();
+        if (st != KDA_OK || splits == 1) return st;
+    }
+    TimedLaunch tl("paged_prefill_join", s);
+    join_kernel<D><<<(unsigned)(((long long)a.T * a.HQ + 7) / 8), 256, 0, s>>>(a, part, splits);
+    return launch_status();
+}
+
+}  // namespace
+
+size_t paged_prefill_tc_ws_bytes(const PagedArgs& a, int D) {
+    const int splits = most_splits(a);
+    if (splits == 1) return 0;
+    return part_bytes(a, D, splits) + align256((size_t)splits * a.T * a.HQ * sizeof(float2));
+}
+
+kda_status paged_prefill_tc_launch(const PagedArgs& a, int D, void* ws, cudaStream_t s) {
+    return D == 128 ? launch<128>(a, ws, s) : launch<64>(a, ws, s);
+}
+
+kda_status paged_prefill_take_error(cudaStream_t s) {
+    int err = 0;
+    if (cudaMemcpyFromSymbolAsync(&err, g_paged_prefill_error, sizeof(int), 0,
+                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (err == 0) return KDA_OK;
+    const int zero = 0;
+    if (cudaMemcpyToSymbolAsync(g_paged_prefill_error, &zero, sizeof(int), 0,
+                                cudaMemcpyHostToDevice, s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    cudaStreamSynchronize(s);
+    return static_cast<kda_status>(err);
+}
+
+}  // namespace kda

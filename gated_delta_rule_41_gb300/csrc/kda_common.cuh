@@ -141,8 +141,6 @@ kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, 
 kda_status paged_take_error(cudaStream_t s);
 kda_status paged_decode_take_error(cudaStream_t s);
 kda_status paged_prefill_take_error(cudaStream_t s);
-size_t paged_prefill_tc_ws_bytes(const PagedArgs& a, int D);
-kda_status paged_prefill_tc_launch(const PagedArgs& a, int D, void* ws, cudaStream_t s);
 
 // ---- page bookkeeping ----
 size_t pages_ws_bytes(const kda_pages_dims& d);

@@ -1,4 +1,4 @@
-// Paged key-value cache: appending tokens, and attention over the pages.
+// Paged key-value cache: appending tokens.
 #include <cuda_fp8.h>
 
 #include "kda_common.cuh"
@@ -90,81 +90,6 @@ append_kernel(const PagedArgs a, const __nv_bfloat16* __restrict__ k, long long 
     }
 }
 
-template <bool E4M3>
-__device__ __forceinline__ float load_elem(const void* p, long long i) {
-    if (E4M3) {
-        __nv_fp8_e4m3 c;
-        c.__x = static_cast<const unsigned char*>(p)[i];
-        return static_cast<float>(c);
-    }
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-// One warp per query row (token, head): the visible tokens in turn, with the
-// running maximum and sum of the softmax; a lane holds D / 32 channels.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(256) attend_kernel(const PagedArgs a) {
-    constexpr int E = D / 32;
-    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int t = w / a.HQ, hq = w % a.HQ, h = hq / a.G;
-    if (t >= a.T) return;
-    const int s = a.cu ? find_seq(a.cu, a.S, a.T, t) : t;
-    if (s < 0) return;
-    const int p = seq_len(a, s) - (a.cu ? a.cu[s + 1] - t : 1);
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = a.scale * __bfloat162float(a.q[t * a.q_stride + (long long)hq * D + lane * E + e]);
-        o[e] = 0.f;
-    }
-    if (E4M3 && a.ks)
-        for (int e = 0; e < E; ++e) q[e] *= a.ks[h];
-    const int low = a.window ? max(0, p - a.window + 1) : 0;
-    int j = low > 0 && a.sinks > 0 ? 0 : low;
-    for (; j <= p; ++j) {
-        if (j == a.sinks && j < low) j = low;
-        const int page = a.table[(size_t)s * a.max_pages + (j >> a.page_shift)];
-        float x = 0.f, v[E] = {};
-        if ((unsigned)page < (unsigned)a.num_pages) {
-            const long long off = page * a.page_stride +
-                                  (j & ((1 << a.page_shift) - 1)) * a.token_stride +
-                                  h * a.head_stride + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                x += q[e] * load_elem<E4M3>(a.kp, off + e);
-                v[e] = load_elem<E4M3>(a.vp, off + e);
-            }
-        } else {
-            record();
-        }
-#pragma unroll
-        for (int r = 16; r > 0; r >>= 1) x += __shfl_xor_sync(0xffffffffu, x, r);
-        const float top = fmaxf(m, x), keep = expf(m - top), wgt = expf(x - top);
-        l = l * keep + wgt;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + wgt * v[e];
-        m = top;
-    }
-    const float inv = (l > 0.f ? 1.f / l : 0.f) * (E4M3 && a.vs ? a.vs[h] : 1.f);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        a.o[((long long)t * a.HQ + hq) * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[(long long)t * a.HQ + hq] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
-template <int D, bool E4M3>
-kda_status attend(const PagedArgs& a, const char* name, cudaStream_t s) {
-    TimedLaunch tl(name, s);
-    const long long rows = (long long)a.T * a.HQ;
-    attend_kernel<D, E4M3><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
-    return launch_status();
-}
-
-kda_status attend_any(const PagedArgs& a, int D, bool e4m3, const char* name, cudaStream_t s) {
-    if (D == 128) return e4m3 ? attend<128, true>(a, name, s) : attend<128, false>(a, name, s);
-    return e4m3 ? attend<64, true>(a, name, s) : attend<64, false>(a, name, s);
-}
-
 }  // namespace
 
 kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void* k,
@@ -183,13 +108,6 @@ kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void*
     else
         append_kernel<64, false><<<grid, 256, 0, s>>>(a, kk, k_stride, vv, v_stride);
     return launch_status();
-}
-
-size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool e4m3) {
-    return e4m3 ? 0 : paged_prefill_tc_ws_bytes(a, D);
-}
-kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s) {
-    return e4m3 ? attend_any(a, D, true, "paged_prefill", s) : paged_prefill_tc_launch(a, D, ws, s);
 }
 
 kda_status paged_take_error(cudaStream_t s) {

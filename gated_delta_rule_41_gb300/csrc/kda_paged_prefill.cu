@@ -15,21 +15,27 @@
 //
 // Softmax.  The running maximum m of a row is raised, and its O and sum
 // rescaled, only when a logit exceeds m by more than 8 (a weight of 256);
-// sums are fp32.  P goes into the product with V as bf16, rounded by up to 2^-8 of
-// each weight.  Over many comparable weights that averages out; where single
-// weights carry the row it would be as large as the output's own rounding, so
-// a tile in which some row has a weight above 1/32 of its sum so far also
-// multiplies what the rounding lost (a second bf16 term, 2^-16 together).
+// sums are fp32.  P enters the product with V in fp16, which rounds a weight by
+// up to 2^-11, a small part of the output's own rounding (2^-8), at the rate of a bf16 one
+// (which alone would round weights by as much as the output).
 //
-// K and V tiles arrive by TMA, one box per page, into one ring of slots.  Pages past the
-// sequence's end, and pages out of range, are asked for at a coordinate
-// outside the pool, which TMA fills with zeros; the row slots of the last page
-// past the end are cleared before V is multiplied (they may hold NaN).
+// K and V tiles arrive by TMA, one box per page, into one ring of slots, and a
+// warpgroup turns what is not ready for the products into it, in place:
+// * V in bf16 to fp16, scaled by a power of two 2^-E so that large values
+//   fit.  E is 0 while the first tile's largest value lies in [1, 2^15], else
+//   the tile's exponent less 8; a later tile that does not fit raises it, and
+//   the rows' O are rescaled as for a raised maximum.  bf16 values are exact
+//   in fp16 down to 2^-17 of that scale.
+// * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row scaled
+//   by a power of two that its logits' factor gives back.
+// * V rows past the sequence's end (they may hold NaN) to zeros.  Pages past
+//   it, and pages out of range, are asked for at a coordinate outside the
+//   pool, which TMA fills with zeros.
 //
 // Roles: warps 0-3 softmax and output of tile A, 4-7 of B, warp 8 TMA, warp 9
-// MMA.  Every wait is bounded; on expiry the error is recorded and the CTA
-// unwinds.  With few query rows the cached tokens are split over several CTAs, whose
-// parts a second kernel joins.
+// MMA, warps 12-15 the conversions.  Every wait is bounded; on expiry the error
+// is recorded and the CTA unwinds.  With few query rows the cached tokens are split over several
+// CTAs, whose parts a second kernel joins.
 #include <algorithm>
 #include <mutex>
 
@@ -46,10 +52,11 @@ using namespace ptx;
 using namespace paged;
 
 constexpr int kTile = 128;                  // query rows and cached tokens of a tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 512;                // four warpgroups of 128 registers a thread, dealt
+constexpr int kRegsSoftmax = 184, kRegsIssue = 48, kRegsConvert = 96;   // out again as
+static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
 constexpr float kRaise = 8.f;               // log2 of the weight that raises the maximum
-constexpr float kSplitWeight = 1.f / 32.f;  // weights above this share take two terms
 
 __device__ __forceinline__ void record(kda_status code) {
     atomicCAS(&g_paged_prefill_error, 0, (int)code);
@@ -109,25 +116,50 @@ __device__ __forceinline__ void tmem_st16_nw(uint32_t taddr, const uint32_t (&r)
         "r"(r[15])
         : "memory");
 }
-// Whether `p` holds for any of the 128 threads that meet at named barrier id.
-__device__ __forceinline__ bool any128(int id, bool p) {
+// Whether `p` holds for any of the 128 converting threads (named barrier 1).
+__device__ __forceinline__ bool any_convert(bool p) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\t"
+        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((int)p), "r"(id)
+        : "r"((int)p)
         : "memory");
     return r != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// a, b <- f * a + c, f * b + c
+__device__ __forceinline__ void fma2(float& a, float& b, float f, float c) {
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+// 2^e for any e (0 or infinity out of range).
+__device__ __forceinline__ float pow2any(int e) {
+    const int h = max(-126, min(126, e / 2)), k = max(-126, min(126, e - e / 2));
+    return pow2i(h) * pow2i(k);
 }
 
 template <int D>
 struct Plan {
     static constexpr uint32_t SLOT = kTile * D * 2;           // a K or V tile
     static constexpr uint32_t HALF = kTile * 128;             // its 64-column half
-    static constexpr int SLOTS = D == 128 ? 5 : 8;
+    static constexpr int SLOTS = D == 128 ? 4 : 8;            // even: V tiles in odd slots
     static constexpr uint32_t OFF_Q = 0;                      // two tiles
     static constexpr uint32_t OFF_KV = 2 * SLOT;
     static constexpr uint32_t OFF_BAR = OFF_KV + SLOTS * SLOT;
@@ -157,7 +189,7 @@ __device__ __forceinline__ Span make_span(const PagedArgs& a, int p_min, int p_m
     return s;
 }
 
-template <int D>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, int TB, int heads_first,
@@ -167,15 +199,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::OFF_BAR);
-    uint64_t* kv_full = bars;                     // [SLOTS]
-    uint64_t* kv_empty = kv_full + P::SLOTS;      // [SLOTS]
+    uint64_t* kv_full = bars;                     // [SLOTS] loaded
+    uint64_t* kv_ready = kv_full + P::SLOTS;      // [SLOTS] converted
+    uint64_t* kv_empty = kv_ready + P::SLOTS;     // [SLOTS]
     uint64_t* q_full = kv_empty + P::SLOTS;       // [2]
-    uint64_t* s_full = q_full + 2;                // [2] S is in TMEM, and O up to the tile before
+    uint64_t* q_ready = q_full + 2;               // [2] converted (e4m3)
+    uint64_t* s_full = q_ready + 2;               // [2] S is in TMEM, and O up to the tile before
     uint64_t* p_full = s_full + 2;                // [2] P is in TMEM
     uint64_t* o_full = p_full + 2;                // [2] O is complete
     uint64_t* done = o_full + 2;                  // every MMA has ended (unwinding)
-    int* two_terms = reinterpret_cast<int*>(done + 1);   // [2]
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(two_terms + 2);
+    int* v_exp = reinterpret_cast<int*>(done + 1);   // [SLOTS] E of the V tile in the slot
+    int* v_top = v_exp + P::SLOTS;                // bits of a tile's largest |v|
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(v_top + 1);
     __shared__ int s_scan[kThreads / 32], s_seq, s_block;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,15 +276,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (tid == 0) {
         for (int i = 0; i < P::SLOTS; ++i) {
             mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_ready[i], kTile);
             mbar_init(&kv_empty[i], 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&q_full[x], 1);
+            mbar_init(&q_ready[x], kTile);
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], kTile);
             mbar_init(&o_full[x], 1);
         }
         mbar_init(done, 1);
+        *v_top = 0;
         fence_mbar_init();
     }
     if (warp == 9 && N > 0) {
@@ -261,152 +299,301 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = N > 0 ? *tmem_holder : 0;
 
-    if (warp == 8 && N > 0) {
-        // ---------------- TMA ----------------
-        if (lane == 0) {
-            for (int x = 0; x < 2; ++x) {
-                mbar_arrive_expect_tx(&q_full[x], (uint32_t)(TB * a.G * D * 2));
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(smem + P::OFF_Q + x * P::SLOT + c * P::HALF, &tm_q, &q_full[x],
-                                64 * c, h * a.G, cu0 + i0 + x * TB);
-            }
-        }
-        const int rows = min(1 << a.page_shift, kTile);      // rows of a box
-        const int boxes = kTile / rows;
-        const int* table = a.table + (size_t)s * a.max_pages;
-        int issued = 0;
-        for (int n = 0; n < N; ++n) {
-            const int j0 = sp.tile(n_lo + n) * kTile;
-            int page = a.num_pages;                          // outside the pool: zeros
-            const int j = j0 + lane * rows;
-            if (lane < boxes && j < len) {
-                page = __ldg(table + (j >> a.page_shift));
-                if ((unsigned)page >= (unsigned)a.num_pages) {
-                    record(KDA_ERR_SHAPE);
-                    page = a.num_pages;
-                }
-            }
-            const int r0 = j & ((1 << a.page_shift) - 1);
-            bool ok = true;
-            for (int kv = 0; kv < 2; ++kv) {
-                const int q = 2 * n + kv, slot = q % P::SLOTS;
-                ok = wait_bar_warp(&kv_empty[slot], ((q / P::SLOTS) & 1) ^ 1);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], P::SLOT);
-                __syncwarp();
-                if (lane < boxes) {
-                    uint8_t* dst = smem + P::OFF_KV + slot * P::SLOT + lane * rows * 128;
+    if (warp >= 8 && warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 8 && N > 0) {
+            // ---------------- TMA ----------------
+            if (lane == 0) {
+                for (int x = 0; x < 2; ++x) {
+                    mbar_arrive_expect_tx(&q_full[x], (uint32_t)(TB * a.G * D * 2));
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(dst + c * P::HALF, kv ? &tm_v : &tm_k, &kv_full[slot], 64 * c,
-                                    heads_first ? r0 : h, heads_first ? h : r0, page);
+                        tma_load_3d(smem + P::OFF_Q + x * P::SLOT + c * P::HALF, &tm_q, &q_full[x],
+                                    64 * c, h * a.G, cu0 + i0 + x * TB);
                 }
-                issued = q + 1;
             }
-            if (!ok) break;
-        }
-        if (issued < 2 * N) {                                // unwinding: let the copies land
-            for (int q = max(0, issued - P::SLOTS); q < issued; ++q)
-                wait_bar_drain(&kv_full[q % P::SLOTS], (q / P::SLOTS) & 1);
-            for (int x = 0; x < 2; ++x) wait_bar_drain(&q_full[x], 0);
-        }
-        __syncwarp();
-    } else if (warp == 9 && N > 0) {
-        // ---------------- MMA ----------------
-        constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile);
-        constexpr uint32_t ID_O = idesc_bf16_f32(kTile, D) | kBMajorMN;
-        const uint32_t kv = smem_u32(smem + P::OFF_KV), qs = smem_u32(smem + P::OFF_Q);
-        auto s_mma = [&](int x, int slot) {
-            const uint32_t kt = kv + slot * P::SLOT, qt = qs + x * P::SLOT;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t o = (k >> 2) * P::HALF + (k & 3) * 32;
-                mma_bf16(tmem + TM_S + x * kTile, sdesc_sw128(qt + o), sdesc_sw128(kt + o), ID_S,
-                         k > 0);
-            }
-            mma_commit(&s_full[x]);
-        };
-        bool ok = true;
-        for (int x = 0; x < 2 && ok; ++x) {
-            ok = wait_bar_warp(&q_full[x], 0) && (x > 0 || wait_bar_warp(&kv_full[0], 0));
-            if (ok && lane == 0) {
-                tc_fence_after();
-                s_mma(x, 0);
-                if (x == 1) mma_commit(&kv_empty[0]);
-            }
-        }
-        for (int n = 0; n < N && ok; ++n) {
-            const int qv = 2 * n + 1, vslot = qv % P::SLOTS;
-            const int qk = 2 * n + 2, kslot = qk % P::SLOTS;
-            for (int x = 0; x < 2 && ok; ++x) {
-                if (x == 0) {
-                    ok = wait_bar_warp(&kv_full[vslot], (qv / P::SLOTS) & 1);
-                    // row slots past the sequence's end may hold anything
-                    const int valid = len - sp.tile(n_lo + n) * kTile;
-                    if (ok && valid < kTile) {
-                        uint8_t* vt = smem + P::OFF_KV + vslot * P::SLOT;
-                        for (int i = max(0, valid) * (D / 8) + lane; i < kTile * (D / 8); i += 32) {
-                            const int r = i / (D / 8), c = i % (D / 8);
-                            *reinterpret_cast<uint4*>(vt + (c >> 3) * P::HALF + r * 128 +
-                                                      (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            const int rows = min(1 << a.page_shift, kTile);  // rows of a box
+            const int boxes = kTile / rows;
+            const int* table = a.table + (size_t)s * a.max_pages;
+            int issued = 0;
+            for (int n = 0; n < N; ++n) {
+                const int j0 = sp.tile(n_lo + n) * kTile;
+                int page = a.num_pages;                      // outside the pool: zeros
+                const int j = j0 + lane * rows;
+                if (lane < boxes && j < len) {
+                    page = __ldg(table + (j >> a.page_shift));
+                    if ((unsigned)page >= (unsigned)a.num_pages) {
+                        record(KDA_ERR_SHAPE);
+                        page = a.num_pages;
+                    }
+                }
+                const int r0 = j & ((1 << a.page_shift) - 1);
+                const int y = heads_first ? r0 : h, z = heads_first ? h : r0;
+                bool ok = true;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int q = 2 * n + kv, slot = q % P::SLOTS;
+                    ok = wait_bar_warp(&kv_empty[slot], ((q / P::SLOTS) & 1) ^ 1);
+                    if (!ok) break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&kv_full[slot], E4M3 ? P::SLOT / 2 : P::SLOT);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const CUtensorMap* map = kv ? &tm_v : &tm_k;
+                        uint8_t* dst = smem + P::OFF_KV + slot * P::SLOT;
+                        if (E4M3) {
+                            tma_load_4d(dst + lane * rows * D, map, &kv_full[slot], 0, y, z, page);
+                        } else {
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_4d(dst + lane * rows * 128 + c * P::HALF, map,
+                                            &kv_full[slot], 64 * c, y, z, page);
                         }
-                        fence_async_smem();
+                    }
+                    issued = q + 1;
+                }
+                if (!ok) break;
+            }
+            if (issued < 2 * N) {                            // unwinding: let the copies land
+                for (int q = max(0, issued - P::SLOTS); q < issued; ++q)
+                    wait_bar_drain(&kv_full[q % P::SLOTS], (q / P::SLOTS) & 1);
+                for (int x = 0; x < 2; ++x) wait_bar_drain(&q_full[x], 0);
+            }
+            __syncwarp();
+        } else if (warp == 9 && N > 0) {
+            // ---------------- MMA ----------------
+            constexpr uint32_t kF16 = ~((1u << 7) | (1u << 10));   // both operands fp16
+            constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile) & (E4M3 ? kF16 : ~0u);
+            constexpr uint32_t ID_O = (idesc_bf16_f32(kTile, D) & kF16) | kBMajorMN;
+            const uint32_t kv = smem_u32(smem + P::OFF_KV), qs = smem_u32(smem + P::OFF_Q);
+            uint64_t* k_bar = E4M3 ? kv_ready : kv_full;
+            uint64_t* q_bar = E4M3 ? q_ready : q_full;
+            auto s_mma = [&](int x, int slot) {
+                const uint32_t kt = kv + slot * P::SLOT, qt = qs + x * P::SLOT;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = (k >> 2) * P::HALF + (k & 3) * 32;
+                    mma_bf16(tmem + TM_S + x * kTile, sdesc_sw128(qt + o), sdesc_sw128(kt + o),
+                             ID_S, k > 0);
+                }
+                mma_commit(&s_full[x]);
+            };
+            bool ok = true;
+            for (int x = 0; x < 2 && ok; ++x) {
+                ok = wait_bar_warp(&q_bar[x], 0) && (x > 0 || wait_bar_warp(&k_bar[0], 0));
+                if (ok && lane == 0) {
+                    tc_fence_after();
+                    s_mma(x, 0);
+                    if (x == 1) mma_commit(&kv_empty[0]);
+                }
+                __syncwarp();
+            }
+            for (int n = 0; n < N && ok; ++n) {
+                const int qv = 2 * n + 1, vslot = qv % P::SLOTS;
+                const int qk = 2 * n + 2, kslot = qk % P::SLOTS;
+                for (int x = 0; x < 2 && ok; ++x) {
+                    ok = (x > 0 || wait_bar_warp(&kv_ready[vslot], (qv / P::SLOTS) & 1)) &&
+                         wait_bar_warp(&p_full[x], n & 1);
+                    if (ok && lane == 0) {
+                        tc_fence_after();
+                        const uint32_t vt = kv + vslot * P::SLOT, pt = tmem + TM_S + x * kTile;
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(tmem + TM_O + x * kTile, pt + 8 * k,
+                                   sdesc_mn_sw128(vt + k * 2048, P::HALF), ID_O, n > 0 || k > 0);
+                        if (x == 1) mma_commit(&kv_empty[vslot]);
+                        if (n + 1 == N) mma_commit(&o_full[x]);
+                    }
+                    __syncwarp();
+                    if (n + 1 < N && ok) {
+                        if (x == 0) ok = wait_bar_warp(&k_bar[kslot], (qk / P::SLOTS) & 1);
+                        if (ok && lane == 0) {
+                            tc_fence_after();
+                            s_mma(x, kslot);
+                            if (x == 1) mma_commit(&kv_empty[kslot]);
+                        }
                         __syncwarp();
                     }
                 }
-                ok = ok && wait_bar_warp(&p_full[x], n & 1);
-                if (ok && lane == 0) {
-                    tc_fence_after();
-                    const uint32_t vt = kv + vslot * P::SLOT, pt = tmem + TM_S + x * kTile;
-                    const int terms = two_terms[x] ? 2 : 1;
-                    for (int e = 0; e < terms; ++e)
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + TM_O + x * kTile, pt + 64 * e + 8 * k,
-                                   sdesc_mn_sw128(vt + k * 2048, P::HALF), ID_O,
-                                   n > 0 || k > 0 || e > 0);
-                    if (x == 1) mma_commit(&kv_empty[vslot]);
-                    if (n + 1 == N) mma_commit(&o_full[x]);
+            }
+            if (!ok) {                                       // unwinding: let the MMAs end
+                if (lane == 0) {
+                    mma_commit(done);
+                    wait_bar_drain(done, 0);
                 }
                 __syncwarp();
-                if (n + 1 < N && ok) {
-                    if (x == 0) ok = wait_bar_warp(&kv_full[kslot], (qk / P::SLOTS) & 1);
-                    if (ok && lane == 0) {
-                        tc_fence_after();
-                        s_mma(x, kslot);
-                        if (x == 1) mma_commit(&kv_empty[kslot]);
+            }
+        }
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+        // ---------------- conversions ----------------
+        const int t = tid & 127;
+        bool ok = true;
+        int E = 0;
+        for (int n = 0; n < N; ++n) {
+            const int valid = len - sp.tile(n_lo + n) * kTile;   // rows of the sequence
+            if (E4M3) {
+                // A tile's codes fill the first half of its slot.  Lane groups of
+                // D / 16 read a row; every 16 codes become two 16-byte chunks.
+                constexpr int C = D / 16, R = 128 / C, L = kTile / R;
+                const int c = t % C, r0 = t / C;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int q = 2 * n + kv, slot = q % P::SLOTS;
+                    uint8_t* tile = smem + P::OFF_KV + slot * P::SLOT;
+                    ok = ok && wait_bar_warp(&kv_full[slot], (q / P::SLOTS) & 1);
+                    uint4 x[L];
+#pragma unroll
+                    for (int i = 0; i < L; ++i) {
+                        const int r = r0 + i * R;
+                        x[i] = *reinterpret_cast<const uint4*>(tile + r * D + c * 16);
+                        if (r >= valid) x[i] = make_uint4(0, 0, 0, 0);
                     }
-                    __syncwarp();
+                    any_convert(false);                      // all codes are read
+                    if (!ok) continue;
+#pragma unroll
+                    for (int i = 0; i < L; ++i) {
+                        const int r = r0 + i * R;
+                        uint8_t* half = tile + (c >> 2) * P::HALF + r * 128;
+                        const uint4 lo = make_uint4(e4m3x2_f16x2((uint16_t)x[i].x),
+                                                    e4m3x2_f16x2((uint16_t)(x[i].x >> 16)),
+                                                    e4m3x2_f16x2((uint16_t)x[i].y),
+                                                    e4m3x2_f16x2((uint16_t)(x[i].y >> 16)));
+                        const uint4 hi = make_uint4(e4m3x2_f16x2((uint16_t)x[i].z),
+                                                    e4m3x2_f16x2((uint16_t)(x[i].z >> 16)),
+                                                    e4m3x2_f16x2((uint16_t)x[i].w),
+                                                    e4m3x2_f16x2((uint16_t)(x[i].w >> 16)));
+                        // the upper lanes store their second chunk first: eight
+                        // lanes then write eight different banks
+                        const int k = 2 * (c & 3), first = c >> 2;
+                        *reinterpret_cast<uint4*>(half + (((k + first) ^ (r & 7)) << 4)) =
+                            first ? hi : lo;
+                        *reinterpret_cast<uint4*>(half + (((k + 1 - first) ^ (r & 7)) << 4)) =
+                            first ? lo : hi;
+                    }
+                    fence_async_smem();
+                    mbar_arrive(&kv_ready[slot]);
+                }
+            } else {
+                constexpr int L = D / 8;                     // 16-byte chunks of a thread
+                const int q = 2 * n + 1, slot = q % P::SLOTS;
+                uint8_t* tile = smem + P::OFF_KV + slot * P::SLOT;
+                ok = ok && wait_bar_warp(&kv_full[slot], (q / P::SLOTS) & 1);
+                uint4 x[L];
+                uint32_t top = 0;                            // largest |fp16| so far, in pairs
+                auto convert = [&]() {
+                    const float down = pow2any(-E);
+                    top = 0;
+#pragma unroll
+                    for (int i = 0; i < L; ++i) {
+                        const int at = t * 16 + i * 2048;    // byte of the tile
+                        x[i] = *reinterpret_cast<const uint4*>(tile + at);
+                        if ((at % P::HALF) / 128 >= valid) x[i] = make_uint4(0, 0, 0, 0);
+                        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v0 = __uint_as_float(w[e] << 16);
+                            float v1 = __uint_as_float(w[e] & 0xffff0000u);
+                            if (E != 0) {
+                                v0 *= down;
+                                v1 *= down;
+                            }
+                            w[e] = pack_f16(v0, v1);
+                            const __half2 hv = __habs2(*reinterpret_cast<const __half2*>(&w[e]));
+                            const __half2 tv =
+                                __hmax2(hv, *reinterpret_cast<const __half2*>(&top));
+                            top = *reinterpret_cast<const uint32_t*>(&tv);
+                        }
+                    }
+                };
+                convert();
+                // does the tile fit?  The first one also sets the scale.
+                const uint32_t h_top = max(top & 0xffffu, top >> 16);
+                const bool off = n == 0 ? h_top >= 0x7800u : h_top >= 0x7c00u;
+                bool redo = any_convert(off);
+                if (n == 0) redo = !any_convert(h_top >= 0x3c00u) || redo;
+                if (redo) {
+                    float big = 0.f;                         // largest |v| of the tile
+#pragma unroll 1
+                    for (int i = 0; i < L; ++i) {
+                        const int at = t * 16 + i * 2048;
+                        if ((at % P::HALF) / 128 >= valid) continue;
+                        const uint4 y = *reinterpret_cast<const uint4*>(tile + at);
+                        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            big = max3(big, fabsf(__uint_as_float(w[e] << 16)),
+                                       fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+                    }
+                    atomicMax(v_top, __float_as_int(big));   // not negative: ordered as ints
+                    any_convert(false);
+                    const int bits = *reinterpret_cast<volatile int*>(v_top);
+                    const int want = bits == 0 ? -100 : (bits >> 23) - 127 - 8;
+                    any_convert(false);                      // all have read it
+                    if (t == 0) *v_top = 0;
+                    any_convert(false);
+                    E = n == 0 ? want : max(E, want);
+                    convert();
+                }
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < L; ++i)
+                        *reinterpret_cast<uint4*>(tile + t * 16 + i * 2048) = x[i];
+                    if (t == 0) v_exp[slot] = E;
+                    fence_async_smem();
+                    mbar_arrive(&kv_ready[slot]);
                 }
             }
         }
-        if (!ok) {                                           // unwinding: let the MMAs end
-            if (lane == 0) {
-                mma_commit(done);
-                wait_bar_drain(done, 0);
-            }
-            __syncwarp();
-        }
-    } else if (warp < 8) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax and output: one thread per query row ----------------
         const int x = warp >> 2, r = tid & 127;
         const int i = i0 + x * TB + r / a.G;
         const bool live = r < TB * a.G && i < nq;
         const int p = live ? len - nq + i : -1;              // a dead row sees nothing
-        const bool flat = a.scale == 0.f;                    // every visible token weighs the same
-        const float f = flat ? 1.f : a.scale * kLog2e;
+        float f = a.scale * kLog2e;
         const int px = p0 + x * TB;                          // positions of the tile's rows
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + TM_S + x * kTile + lanes, to = tmem + TM_O + x * kTile + lanes;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int n = 0; n < N; ++n) {
+        int E = 0;
+        if (E4M3 && N > 0) {
+            ok = wait_bar_warp(&q_full[x], 0);
+            uint8_t* q = smem + P::OFF_Q + x * P::SLOT + r * 128;
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 y = *reinterpret_cast<const uint4*>(q + (c >> 3) * P::HALF +
+                                                                ((c & 7) ^ (r & 7)) * 16);
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    big = max3(big, fabsf(__uint_as_float(w[e] << 16)),
+                               fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+            }
+            // exponent of the largest, as far as 2^-e is a normal number
+            const int e2 = max(-126, min(126, (__float_as_int(big) >> 23) - 127));
+            const float down = pow2i(-e2);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4* y = reinterpret_cast<uint4*>(q + (c >> 3) * P::HALF +
+                                                    ((c & 7) ^ (r & 7)) * 16);
+                uint4 z = *y;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&z);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_f16(__uint_as_float(w[e] << 16) * down,
+                                    __uint_as_float(w[e] & 0xffff0000u) * down);
+                *y = z;
+            }
+            f *= pow2i(e2) * (a.ks ? a.ks[h] : 1.f);
+            fence_async_smem();
+            mbar_arrive(&q_ready[x]);
+        }
+        const bool flat = f == 0.f;                          // every visible token weighs the same
+        if (flat) f = 1.f;
+        for (int n = 0; n < N && ok; ++n) {
             const int j0 = sp.tile(n_lo + n) * kTile;
             ok = wait_bar_warp(&s_full[x], n & 1);
-            // a failed wait: leave in step with the other warps of the tile
-            if (any128(1 + x, !ok)) {
-                ok = false;
-                break;
-            }
+            if (!ok) break;
             tc_fence_after();
             float v[4][32];
 #pragma unroll
@@ -423,22 +610,26 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (!all || !live) {
                 const int hi = p - j0, lo = a.window ? p - a.window + 1 - j0 : 0;
                 const int sk = a.sinks - j0;
+                const float none = f < 0.f ? INFINITY : -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int k = 32 * c + e;
-                        if (k > hi || (k < lo && k >= sk)) v[c][e] = f < 0.f ? INFINITY : -INFINITY;
+                        if (k > hi || (k < lo && k >= sk)) v[c][e] = none;
                     }
             }
-            // the largest f S (a negative scale takes the smallest S)
+            // the largest f S (a negative factor takes the smallest S)
             float top;
             if (f >= 0.f) {
-                top = v[0][0];
+                float t4[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    t4[c] = fmaxf(v[c][0], v[c][1]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, v[c][e]);
+                    for (int e = 2; e < 32; e += 2) t4[c] = max3(t4[c], v[c][e], v[c][e + 1]);
+                }
+                top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             } else {
                 top = v[0][0];
 #pragma unroll
@@ -447,50 +638,51 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int e = 0; e < 32; ++e) top = fminf(top, v[c][e]);
             }
             top = fabsf(top) == INFINITY ? -INFINITY : top * f;
-            const bool rise = top > m + kRaise;
-            if (__any_sync(0xffffffffu, rise)) {
-                const float up = rise ? top : m;
-                const float keep = up == m ? 1.f : ex2(m - up);
-                m = up;
+            bool change = false;
+            float keep = 1.f;
+            if (top > m + kRaise) {
+                keep = ex2(m - top);
+                m = top;
                 l *= keep;
-                if (n > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(to + 32 * c, o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= keep;
-                        tmem_st32_nw(to + 32 * c, o);
-                    }
+                change = true;
+            }
+            if (!E4M3) {
+                // the scale of this tile's V (ready long before, as a rule)
+                const int q = 2 * n + 1, slot = q % P::SLOTS;
+                ok = wait_bar_warp(&kv_ready[slot], (q / P::SLOTS) & 1);
+                if (!ok) break;
+                const int Ev = v_exp[slot];
+                if (Ev != E) {
+                    keep *= pow2any(E - Ev);
+                    E = Ev;
+                    change = true;
                 }
             }
-            const float mm = m == -INFINITY ? 0.f : m;
-            const bool two = any128(3 + x, ex2(top - mm) > kSplitWeight * l);
-            if (r == 0) two_terms[x] = two;
-            float sum0 = 0.f, sum1 = 0.f;
+            if (n > 0 && __any_sync(0xffffffffu, change)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(to + 32 * c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= keep;
+                    tmem_st32_nw(to + 32 * c, o);
+                }
+            }
+            const float mm = m == -INFINITY ? 0.f : -m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t hi[16];
+                uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float w0 = ex2(fmaf(v[c][2 * e], f, -mm));
-                    const float w1 = ex2(fmaf(v[c][2 * e + 1], f, -mm));
-                    sum0 += w0;
-                    sum1 += w1;
-                    hi[e] = pack_bf16(w0, w1);
-                    if (two) {
-                        v[c][2 * e] = w0 - __uint_as_float(hi[e] << 16);
-                        v[c][2 * e + 1] = w1 - __uint_as_float(hi[e] & 0xffff0000u);
-                    }
+                    fma2(v[c][2 * e], v[c][2 * e + 1], f, mm);
+                    const float w0 = ex2(v[c][2 * e]), w1 = ex2(v[c][2 * e + 1]);
+                    add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], w0, w1);
+                    w[e] = pack_f16(w0, w1);
                 }
-                tmem_st16_nw(ts + 16 * c, hi);
-                if (two) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) hi[e] = pack_bf16(v[c][2 * e], v[c][2 * e + 1]);
-                    tmem_st16_nw(ts + 64 + 16 * c, hi);
-                }
+                tmem_st16_nw(ts + 16 * c, w);
             }
-            l += sum0 + sum1;
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[x]);
@@ -501,41 +693,43 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc_fence_after();
         }
         const long long row = ((long long)cu0 + i) * a.HQ + h * a.G + r % a.G;
-        if (gridDim.y > 1) {
-            const long long at = (long long)blockIdx.y * a.T * a.HQ + row;
-            if (live) part.ml[at] = make_float2(m, l);
+        const bool any = m != -INFINITY;
+        const bool split = gridDim.y > 1;
+        const long long at = (long long)blockIdx.y * a.T * a.HQ + row;
+        // O is in units of 2^E and of the head's scale
+        const float unit = E4M3 ? (a.vs ? a.vs[h] : 1.f) : pow2any(E);
+        const float by = any ? (split ? unit : unit / l) : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            float o[32];
             if (N > 0 && ok) {
+                tmem_ld32(to + 32 * c, o);
+            } else {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    tmem_ld32(to + 32 * c, o);
-                    if (live && m != -INFINITY)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4*>(part.o + at * D + 32 * c + 4 * e) =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                }
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
             }
-        } else {
-            const bool any = m != -INFINITY;
-            const float inv = any ? 1.f / l : 0.f;
+            if (!live) continue;
+            if (split) {
+                if (any)
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                if (N > 0 && ok) tmem_ld32(to + 32 * c, o);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(part.o + at * D + 32 * c + 4 * e) = make_float4(
+                            by * o[4 * e], by * o[4 * e + 1], by * o[4 * e + 2], by * o[4 * e + 3]);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (any)
-                        w = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                       pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                       pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                       pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                    if (live) *reinterpret_cast<uint4*>(a.o + row * D + 32 * c + 8 * e) = w;
+                        w = make_uint4(pack_bf16(o[8 * e] * by, o[8 * e + 1] * by),
+                                       pack_bf16(o[8 * e + 2] * by, o[8 * e + 3] * by),
+                                       pack_bf16(o[8 * e + 4] * by, o[8 * e + 5] * by),
+                                       pack_bf16(o[8 * e + 6] * by, o[8 * e + 7] * by));
+                    *reinterpret_cast<uint4*>(a.o + row * D + 32 * c + 8 * e) = w;
                 }
             }
-            if (live && a.lse) a.lse[row] = any ? (m + lg2(l)) * kLn2 : -INFINITY;
         }
+        if (live && split) part.ml[at] = make_float2(m, l);
+        if (live && !split && a.lse) a.lse[row] = any ? (m + lg2(l)) * kLn2 : -INFINITY;
         tc_fence_before();
     }
     __syncthreads();
@@ -589,12 +783,16 @@ EncodeFn get_encoder() {
     });
     return fn;
 }
-bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+// bf16 tiles in the 128-byte swizzle, or codes as they lie.
+bool encode(CUtensorMap* m, bool codes, const void* ptr, int rank, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box) {
     const cuuint32_t one[4] = {1, 1, 1, 1};
-    return get_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims,
-                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return get_encoder()(m,
+                         codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         rank, const_cast<void*>(ptr), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -611,14 +809,14 @@ size_t part_bytes(const PagedArgs& a, int D, int splits) {
     return align256((size_t)splits * a.T * a.HQ * D * sizeof(float));
 }
 
-template <int D>
+template <int D, bool E4M3>
 kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
     static bool set[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
     if (!get_encoder()) return KDA_ERR_CUDA;
     if (!set[dev]) {
-        if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Plan<D>::SMEM) != cudaSuccess)
             return KDA_ERR_CUDA;
         set[dev] = true;
@@ -630,20 +828,21 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
         const cuuint64_t strides[2] = {
             (cuuint64_t)D * 2, (cuuint64_t)(a.T > 1 ? a.q_stride : (long long)a.HQ * D) * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)TB};
-        if (!encode(&mq, a.q, 3, dims, strides, box)) return KDA_ERR_CUDA;
+        if (!encode(&mq, false, a.q, 3, dims, strides, box)) return KDA_ERR_CUDA;
     }
     // heads and rows of a page in the order of their strides
     const bool hf = a.HKV > 1 && a.head_stride > a.token_stride;
     {
-        const cuuint64_t row = (cuuint64_t)a.token_stride * 2;
-        const cuuint64_t head = a.HKV > 1 ? (cuuint64_t)a.head_stride * 2 : (cuuint64_t)D * 2;
-        const cuuint64_t pg = a.num_pages > 1 ? (cuuint64_t)a.page_stride * 2 : row * page;
+        const cuuint64_t size = E4M3 ? 1 : 2, row = (cuuint64_t)a.token_stride * size;
+        const cuuint64_t head = (cuuint64_t)(a.HKV > 1 ? a.head_stride : D) * size;
+        const cuuint64_t pg = a.num_pages > 1 ? (cuuint64_t)a.page_stride * size : row * page;
         const cuuint32_t rows = (cuuint32_t)std::min(page, kTile);
         const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(hf ? page : a.HKV),
                                     (cuuint64_t)(hf ? a.HKV : page), (cuuint64_t)a.num_pages};
         const cuuint64_t strides[3] = {hf ? row : head, hf ? head : row, pg};
-        const cuuint32_t box[4] = {64, hf ? rows : 1, hf ? 1 : rows, 1};
-        if (!encode(&mk, a.kp, 4, dims, strides, box) || !encode(&mv, a.vp, 4, dims, strides, box))
+        const cuuint32_t box[4] = {E4M3 ? (cuuint32_t)D : 64, hf ? rows : 1, hf ? 1 : rows, 1};
+        if (!encode(&mk, E4M3, a.kp, 4, dims, strides, box) ||
+            !encode(&mv, E4M3, a.vp, 4, dims, strides, box))
             return KDA_ERR_CUDA;
     }
     // a split takes four tiles or more of the longest row
@@ -653,7 +852,7 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
                         reinterpret_cast<float2*>(static_cast<char*>(ws) + part_bytes(a, D, splits))};
     {
         TimedLaunch tl("paged_prefill", s);
-        prefill_kernel<D><<<dim3((unsigned)most_items(a), splits), kThreads, Plan<D>::SMEM, s>>>(
+        prefill_kernel<D, E4M3><<<dim3((unsigned)most_items(a), splits), kThreads, Plan<D>::SMEM, s>>>(
             mq, mk, mv, a, TB, hf ? 1 : 0, part);
         const kda_status st = launch_status();
         if (st != KDA_OK || splits == 1) return st;
@@ -665,14 +864,15 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_prefill_tc_ws_bytes(const PagedArgs& a, int D) {
+size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool) {
     const int splits = most_splits(a);
     if (splits == 1) return 0;
     return part_bytes(a, D, splits) + align256((size_t)splits * a.T * a.HQ * sizeof(float2));
 }
 
-kda_status paged_prefill_tc_launch(const PagedArgs& a, int D, void* ws, cudaStream_t s) {
-    return D == 128 ? launch<128>(a, ws, s) : launch<64>(a, ws, s);
+kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s) {
+    if (D == 128) return e4m3 ? launch<128, true>(a, ws, s) : launch<128, false>(a, ws, s);
+    return e4m3 ? launch<64, true>(a, ws, s) : launch<64, false>(a, ws, s);
 }
 
 kda_status paged_prefill_take_error(cudaStream_t s) {

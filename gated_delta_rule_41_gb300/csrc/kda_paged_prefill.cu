@@ -38,6 +38,7 @@
 // CTAs, whose parts a second kernel joins.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "kda_paged.cuh"
 #include "kda_timing.cuh"
@@ -97,14 +98,42 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
-// D (+)= A B^T with A in tensor memory (bf16 pairs, 8 columns per 16 of K).
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
+// One lane of the warp, the same every time.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+// MMAs and commits that only the elected lane issues.  The whole warp runs the
+// code around them, so that descriptors are computed once per warp.
+// D (+)= A B^T, both operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t adesc,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// The same with A in tensor memory (16-bit pairs, 8 columns per 16 of K).
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(leader)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16_nw(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -359,68 +388,67 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             __syncwarp();
         } else if (warp == 9 && N > 0) {
             // ---------------- MMA ----------------
+            const uint32_t leader = elect_one();
             constexpr uint32_t kF16 = ~((1u << 7) | (1u << 10));   // both operands fp16
             constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile) & (E4M3 ? kF16 : ~0u);
             constexpr uint32_t ID_O = (idesc_bf16_f32(kTile, D) & kF16) | kBMajorMN;
-            const uint32_t kv = smem_u32(smem + P::OFF_KV), qs = smem_u32(smem + P::OFF_Q);
             uint64_t* k_bar = E4M3 ? kv_ready : kv_full;
             uint64_t* q_bar = E4M3 ? q_ready : q_full;
+            // descriptors: the address field counts 16 bytes
+            const uint64_t qd = sdesc_sw128(smem_u32(smem + P::OFF_Q));
+            const uint64_t kd = sdesc_sw128(smem_u32(smem + P::OFF_KV));
+            const uint64_t vd = sdesc_mn_sw128(smem_u32(smem + P::OFF_KV), P::HALF);
             auto s_mma = [&](int x, int slot) {
-                const uint32_t kt = kv + slot * P::SLOT, qt = qs + x * P::SLOT;
+                const uint64_t qx = qd + x * (P::SLOT / 16), kx = kd + slot * (P::SLOT / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t o = (k >> 2) * P::HALF + (k & 3) * 32;
-                    mma_bf16(tmem + TM_S + x * kTile, sdesc_sw128(qt + o), sdesc_sw128(kt + o),
-                             ID_S, k > 0);
+                    const uint32_t o = ((k >> 2) * P::HALF + (k & 3) * 32) / 16;
+                    mma_ss(leader, tmem + TM_S + x * kTile, qx + o, kx + o, ID_S, k > 0);
                 }
-                mma_commit(&s_full[x]);
+                commit(leader, &s_full[x]);
             };
-            bool ok = true;
-            for (int x = 0; x < 2 && ok; ++x) {
-                ok = wait_bar_warp(&q_bar[x], 0) && (x > 0 || wait_bar_warp(&k_bar[0], 0));
-                if (ok && lane == 0) {
-                    tc_fence_after();
-                    s_mma(x, 0);
-                    if (x == 1) mma_commit(&kv_empty[0]);
-                }
-                __syncwarp();
+            bool ok = wait_bar_warp(&q_bar[0], 0) && wait_bar_warp(&k_bar[0], 0);
+            if (ok) {
+                tc_fence_after();
+                s_mma(0, 0);
+                ok = wait_bar_warp(&q_bar[1], 0);
+            }
+            if (ok) {
+                tc_fence_after();
+                s_mma(1, 0);
+                commit(leader, &kv_empty[0]);
             }
             for (int n = 0; n < N && ok; ++n) {
                 const int qv = 2 * n + 1, vslot = qv % P::SLOTS;
                 const int qk = 2 * n + 2, kslot = qk % P::SLOTS;
-                for (int x = 0; x < 2 && ok; ++x) {
-                    ok = (x > 0 || wait_bar_warp(&kv_ready[vslot], (qv / P::SLOTS) & 1)) &&
-                         wait_bar_warp(&p_full[x], n & 1);
-                    if (ok && lane == 0) {
-                        tc_fence_after();
-                        const uint32_t vt = kv + vslot * P::SLOT, pt = tmem + TM_S + x * kTile;
+                const uint64_t vx = vd + vslot * (P::SLOT / 16);
+                ok = wait_bar_warp(&kv_ready[vslot], (qv / P::SLOTS) & 1);
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + TM_O + x * kTile, pt + 8 * k,
-                                   sdesc_mn_sw128(vt + k * 2048, P::HALF), ID_O, n > 0 || k > 0);
-                        if (x == 1) mma_commit(&kv_empty[vslot]);
-                        if (n + 1 == N) mma_commit(&o_full[x]);
-                    }
-                    __syncwarp();
-                    if (n + 1 < N && ok) {
+                for (int x = 0; x < 2; ++x) {
+                    ok = ok && wait_bar_warp(&p_full[x], n & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(leader, tmem + TM_O + x * kTile, tmem + TM_S + x * kTile + 8 * k,
+                               vx + k * (2048 / 16), ID_O, n > 0 || k > 0);
+                    if (x == 1) commit(leader, &kv_empty[vslot]);
+                    if (n + 1 == N) {
+                        commit(leader, &o_full[x]);
+                    } else {
                         if (x == 0) ok = wait_bar_warp(&k_bar[kslot], (qk / P::SLOTS) & 1);
-                        if (ok && lane == 0) {
-                            tc_fence_after();
-                            s_mma(x, kslot);
-                            if (x == 1) mma_commit(&kv_empty[kslot]);
-                        }
-                        __syncwarp();
+                        if (!ok) break;
+                        s_mma(x, kslot);
+                        if (x == 1) commit(leader, &kv_empty[kslot]);
                     }
                 }
             }
             if (!ok) {                                       // unwinding: let the MMAs end
-                if (lane == 0) {
-                    mma_commit(done);
-                    wait_bar_drain(done, 0);
-                }
-                __syncwarp();
+                commit(leader, done);
+                wait_bar_drain(done, 0);
             }
         }
+        __syncwarp();
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         // ---------------- conversions ----------------
@@ -477,7 +505,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 ok = ok && wait_bar_warp(&kv_full[slot], (q / P::SLOTS) & 1);
                 uint4 x[L];
                 uint32_t top = 0;                            // largest |fp16| so far, in pairs
-                auto convert = [&]() {
+                auto convert = [&](auto scaled) {
                     const float down = pow2any(-E);
                     top = 0;
 #pragma unroll
@@ -490,7 +518,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         for (int e = 0; e < 4; ++e) {
                             float v0 = __uint_as_float(w[e] << 16);
                             float v1 = __uint_as_float(w[e] & 0xffff0000u);
-                            if (E != 0) {
+                            if (decltype(scaled)::value) {
                                 v0 *= down;
                                 v1 *= down;
                             }
@@ -502,7 +530,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         }
                     }
                 };
-                convert();
+                if (E == 0) convert(std::false_type{});
+                else convert(std::true_type{});
                 // does the tile fit?  The first one also sets the scale.
                 const uint32_t h_top = max(top & 0xffffu, top >> 16);
                 const bool off = n == 0 ? h_top >= 0x7800u : h_top >= 0x7c00u;
@@ -529,7 +558,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (t == 0) *v_top = 0;
                     any_convert(false);
                     E = n == 0 ? want : max(E, want);
-                    convert();
+                    convert(std::true_type{});
                 }
                 if (ok) {
 #pragma unroll
@@ -592,7 +621,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (flat) f = 1.f;
         for (int n = 0; n < N && ok; ++n) {
             const int j0 = sp.tile(n_lo + n) * kTile;
-            ok = wait_bar_warp(&s_full[x], n & 1);
+            int Ev = 0;
+            if (!E4M3) {                                     // the scale of this tile's V
+                const int q = 2 * n + 1, slot = q % P::SLOTS;
+                ok = wait_bar_warp(&kv_ready[slot], (q / P::SLOTS) & 1);
+                Ev = v_exp[slot];
+            }
+            ok = ok && wait_bar_warp(&s_full[x], n & 1);
             if (!ok) break;
             tc_fence_after();
             float v[4][32];
@@ -646,17 +681,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 l *= keep;
                 change = true;
             }
-            if (!E4M3) {
-                // the scale of this tile's V (ready long before, as a rule)
-                const int q = 2 * n + 1, slot = q % P::SLOTS;
-                ok = wait_bar_warp(&kv_ready[slot], (q / P::SLOTS) & 1);
-                if (!ok) break;
-                const int Ev = v_exp[slot];
-                if (Ev != E) {
-                    keep *= pow2any(E - Ev);
-                    E = Ev;
-                    change = true;
-                }
+            if (Ev != E) {
+                keep *= pow2any(E - Ev);
+                E = Ev;
+                change = true;
             }
             if (n > 0 && __any_sync(0xffffffffu, change)) {
 #pragma unroll 1

@@ -13,9 +13,11 @@
 // rate and the 32768 exponentials 1024 of the special function units, so
 // the tensor core bounds it if neither chain waits.
 //
-// Softmax.  The running maximum m of a row is raised, and its O and sum
-// rescaled, only when a logit exceeds m by more than 8 (a weight of 256);
-// sums are fp32.  P enters the product with V in fp16, which rounds a weight by
+// Softmax.  The weights of a tile are taken against a reference m of the row,
+// the largest logit of its first half tile; only when the weights of a half
+// tile add up to more than 4096 is m moved to its largest logit, O and the sum
+// rescaled and the half weighed again.  So as a rule no maximum is taken at
+// all, and weights stay far inside the range of fp16.  Sums are fp32.  P enters the product with V in fp16, which rounds a weight by
 // up to 2^-11, a small part of the output's own rounding (2^-8), at the rate of a bf16 one
 // (which alone would round weights by as much as the output).
 //
@@ -24,7 +26,7 @@
 // * V in bf16 to fp16, scaled by a power of two 2^-E so that large values
 //   fit.  E is 0 while the first tile's largest value lies in [1, 2^15], else
 //   the tile's exponent less 8; a later tile that does not fit raises it, and
-//   the rows' O are rescaled as for a raised maximum.  bf16 values are exact
+//   the rows' O are rescaled as for a moved reference.  bf16 values are exact
 //   in fp16 down to 2^-17 of that scale.
 // * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row scaled
 //   by a power of two that its logits' factor gives back.
@@ -54,10 +56,10 @@ using namespace paged;
 
 constexpr int kTile = 128;                  // query rows and cached tokens of a tile
 constexpr int kThreads = 512;                // four warpgroups of 128 registers a thread, dealt
-constexpr int kRegsSoftmax = 184, kRegsIssue = 48, kRegsConvert = 96;   // out again as
+constexpr int kRegsSoftmax = 152, kRegsIssue = 88, kRegsConvert = 120;   // out again as
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
-constexpr float kRaise = 8.f;               // log2 of the weight that raises the maximum
+constexpr float kMost = 4096.f;             // sum of a tile's weights that moves the reference
 
 __device__ __forceinline__ void record(kda_status code) {
     atomicCAS(&g_paged_prefill_error, 0, (int)code);
@@ -108,24 +110,27 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 // MMAs and commits that only the elected lane issues.  The whole warp runs the
 // code around them, so that descriptors are computed once per warp.
+// Descriptors are given by their low words; the high one is the same for all.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 // D (+)= A B^T, both operands in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t adesc,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint32_t adesc,
+                                       uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader), "n"(kDescHigh)
         : "memory");
 }
 // The same with A in tensor memory (16-bit pairs, 8 columns per 16 of K).
 __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+                                       uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader), "n"(kDescHigh)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
@@ -163,6 +168,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // a, b <- f * a + c, f * b + c
 __device__ __forceinline__ void fma2(float& a, float& b, float f, float c) {
     asm("{\n\t.reg .b64 x, y, z;\n\t"
@@ -177,6 +187,17 @@ __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
         "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a), "+f"(b)
         : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void mul2(float& a, float& b, float f) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f));
+}
+// The n lowest bits.
+__device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
 }
 // 2^e for any e (0 or infinity out of range).
 __device__ __forceinline__ float pow2any(int e) {
@@ -234,8 +255,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint64_t* q_full = kv_empty + P::SLOTS;       // [2]
     uint64_t* q_ready = q_full + 2;               // [2] converted (e4m3)
     uint64_t* s_full = q_ready + 2;               // [2] S is in TMEM, and O up to the tile before
-    uint64_t* p_full = s_full + 2;                // [2] P is in TMEM
-    uint64_t* o_full = p_full + 2;                // [2] O is complete
+    uint64_t* p_full = s_full + 2;                // [2][2] half of P is in TMEM
+    uint64_t* o_half = p_full + 4;                // [2] O holds the first half of the tile
+    uint64_t* o_full = o_half + 2;                // [2] O is complete
     uint64_t* done = o_full + 2;                  // every MMA has ended (unwinding)
     int* v_exp = reinterpret_cast<int*>(done + 1);   // [SLOTS] E of the V tile in the slot
     int* v_top = v_exp + P::SLOTS;                // bits of a tile's largest |v|
@@ -312,7 +334,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&q_full[x], 1);
             mbar_init(&q_ready[x], kTile);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], kTile);
+            mbar_init(&p_full[2 * x], kTile);
+            mbar_init(&p_full[2 * x + 1], kTile);
+            mbar_init(&o_half[x], 1);
             mbar_init(&o_full[x], 1);
         }
         mbar_init(done, 1);
@@ -395,11 +419,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             uint64_t* k_bar = E4M3 ? kv_ready : kv_full;
             uint64_t* q_bar = E4M3 ? q_ready : q_full;
             // descriptors: the address field counts 16 bytes
-            const uint64_t qd = sdesc_sw128(smem_u32(smem + P::OFF_Q));
-            const uint64_t kd = sdesc_sw128(smem_u32(smem + P::OFF_KV));
-            const uint64_t vd = sdesc_mn_sw128(smem_u32(smem + P::OFF_KV), P::HALF);
+            const uint32_t qd = (uint32_t)sdesc_sw128(smem_u32(smem + P::OFF_Q));
+            const uint32_t kd = (uint32_t)sdesc_sw128(smem_u32(smem + P::OFF_KV));
+            const uint32_t vd = (uint32_t)sdesc_mn_sw128(smem_u32(smem + P::OFF_KV), P::HALF);
             auto s_mma = [&](int x, int slot) {
-                const uint64_t qx = qd + x * (P::SLOT / 16), kx = kd + slot * (P::SLOT / 16);
+                const uint32_t qx = qd + x * (P::SLOT / 16), kx = kd + slot * (P::SLOT / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t o = ((k >> 2) * P::HALF + (k & 3) * 32) / 16;
@@ -421,17 +445,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int n = 0; n < N && ok; ++n) {
                 const int qv = 2 * n + 1, vslot = qv % P::SLOTS;
                 const int qk = 2 * n + 2, kslot = qk % P::SLOTS;
-                const uint64_t vx = vd + vslot * (P::SLOT / 16);
+                const uint32_t vx = vd + vslot * (P::SLOT / 16);
                 ok = wait_bar_warp(&kv_ready[vslot], (qv / P::SLOTS) & 1);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    ok = ok && wait_bar_warp(&p_full[x], n & 1);
-                    if (!ok) break;
-                    tc_fence_after();
+                    for (int e = 0; e < 2; ++e) {
+                        ok = ok && wait_bar_warp(&p_full[2 * x + e], n & 1);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(leader, tmem + TM_O + x * kTile, tmem + TM_S + x * kTile + 8 * k,
-                               vx + k * (2048 / 16), ID_O, n > 0 || k > 0);
+                        for (int k = 0; k < kTile / 32; ++k)
+                            mma_ts(leader, tmem + TM_O + x * kTile,
+                                   tmem + TM_S + x * kTile + 32 * e + 8 * k,
+                                   vx + (4 * e + k) * (2048 / 16), ID_O, n > 0 || e > 0 || k > 0);
+                        if (e == 0) commit(leader, &o_half[x]);
+                    }
+                    if (!ok) break;
                     if (x == 1) commit(leader, &kv_empty[vslot]);
                     if (n + 1 == N) {
                         commit(leader, &o_full[x]);
@@ -453,7 +482,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         // ---------------- conversions ----------------
         const int t = tid & 127;
-        bool ok = true;
+        bool ok = true, scaled = false;
         int E = 0;
         for (int n = 0; n < N; ++n) {
             const int valid = len - sp.tile(n_lo + n) * kTile;   // rows of the sequence
@@ -504,62 +533,60 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 uint8_t* tile = smem + P::OFF_KV + slot * P::SLOT;
                 ok = ok && wait_bar_warp(&kv_full[slot], (q / P::SLOTS) & 1);
                 uint4 x[L];
-                uint32_t top = 0;                            // largest |fp16| so far, in pairs
-                auto convert = [&](auto scaled) {
+                bool again;
+                do {
                     const float down = pow2any(-E);
-                    top = 0;
+                    uint32_t top = 0;                        // largest |fp16| so far, in pairs
 #pragma unroll
                     for (int i = 0; i < L; ++i) {
                         const int at = t * 16 + i * 2048;    // byte of the tile
                         x[i] = *reinterpret_cast<const uint4*>(tile + at);
-                        if ((at % P::HALF) / 128 >= valid) x[i] = make_uint4(0, 0, 0, 0);
                         uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float v0 = __uint_as_float(w[e] << 16);
                             float v1 = __uint_as_float(w[e] & 0xffff0000u);
-                            if (decltype(scaled)::value) {
-                                v0 *= down;
-                                v1 *= down;
-                            }
+                            mul2(v0, v1, down);
                             w[e] = pack_f16(v0, v1);
                             const __half2 hv = __habs2(*reinterpret_cast<const __half2*>(&w[e]));
                             const __half2 tv =
                                 __hmax2(hv, *reinterpret_cast<const __half2*>(&top));
                             top = *reinterpret_cast<const uint32_t*>(&tv);
                         }
+                        if (valid < kTile && (at % P::HALF) / 128 >= valid)
+                            x[i] = make_uint4(0, 0, 0, 0);
                     }
-                };
-                if (E == 0) convert(std::false_type{});
-                else convert(std::true_type{});
-                // does the tile fit?  The first one also sets the scale.
-                const uint32_t h_top = max(top & 0xffffu, top >> 16);
-                const bool off = n == 0 ? h_top >= 0x7800u : h_top >= 0x7c00u;
-                bool redo = any_convert(off);
-                if (n == 0) redo = !any_convert(h_top >= 0x3c00u) || redo;
-                if (redo) {
-                    float big = 0.f;                         // largest |v| of the tile
+                    // Does the tile fit?  The first one also sets the scale.  (What
+                    // lies past the sequence's end may ask for a scale too.)
+                    const uint32_t h_top = max(top & 0xffffu, top >> 16);
+                    again = any_convert(h_top >= (n == 0 ? 0x7800u : 0x7c00u));
+                    if (n == 0) again = !any_convert(h_top >= 0x3c00u) || again;
+                    again = again && !scaled;
+                    scaled = again;
+                    if (again) {
+                        float big = 0.f;                     // largest |v| of the tile
 #pragma unroll 1
-                    for (int i = 0; i < L; ++i) {
-                        const int at = t * 16 + i * 2048;
-                        if ((at % P::HALF) / 128 >= valid) continue;
-                        const uint4 y = *reinterpret_cast<const uint4*>(tile + at);
-                        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                        for (int i = 0; i < L; ++i) {
+                            const int at = t * 16 + i * 2048;
+                            if ((at % P::HALF) / 128 >= valid) continue;
+                            const uint4 y = *reinterpret_cast<const uint4*>(tile + at);
+                            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            big = max3(big, fabsf(__uint_as_float(w[e] << 16)),
-                                       fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+                            for (int e = 0; e < 4; ++e)
+                                big = max3(big, fabsf(__uint_as_float(w[e] << 16)),
+                                           fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+                        }
+                        atomicMax(v_top, __float_as_int(big));   // not negative: ordered as ints
+                        any_convert(false);
+                        const int bits = *reinterpret_cast<volatile int*>(v_top);
+                        const int want = bits == 0 ? -100 : (bits >> 23) - 127 - 8;
+                        any_convert(false);                  // all have read it
+                        if (t == 0) *v_top = 0;
+                        any_convert(false);
+                        E = n == 0 ? (bits >= 0x3f800000 && bits < 0x47000000 ? 0 : want)
+                                   : max(E, want);
                     }
-                    atomicMax(v_top, __float_as_int(big));   // not negative: ordered as ints
-                    any_convert(false);
-                    const int bits = *reinterpret_cast<volatile int*>(v_top);
-                    const int want = bits == 0 ? -100 : (bits >> 23) - 127 - 8;
-                    any_convert(false);                      // all have read it
-                    if (t == 0) *v_top = 0;
-                    any_convert(false);
-                    E = n == 0 ? want : max(E, want);
-                    convert(std::true_type{});
-                }
+                } while (again);
                 if (ok) {
 #pragma unroll
                     for (int i = 0; i < L; ++i)
@@ -581,7 +608,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int px = p0 + x * TB;                          // positions of the tile's rows
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + TM_S + x * kTile + lanes, to = tmem + TM_O + x * kTile + lanes;
-        float m = -INFINITY, l = 0.f;
+        float m = live ? -INFINITY : 0.f, l = 0.f;           // a dead row asks for nothing
         bool ok = true;
         int E = 0;
         if (E4M3 && N > 0) {
@@ -617,8 +644,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             fence_async_smem();
             mbar_arrive(&q_ready[x]);
         }
-        const bool flat = f == 0.f;                          // every visible token weighs the same
-        if (flat) f = 1.f;
+        // every visible token weighs the same: 2^0 for any logit, and -infinity stays
+        if (f == 0.f) f = 1e-37f;
         for (int n = 0; n < N && ok; ++n) {
             const int j0 = sp.tile(n_lo + n) * kTile;
             int Ev = 0;
@@ -630,90 +657,96 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             ok = ok && wait_bar_warp(&s_full[x], n & 1);
             if (!ok) break;
             tc_fence_after();
-            float v[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_nw(ts + 32 * c, v[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld_dep(v[c]);
-            if (flat)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[c][e] = 0.f;
             // every row of the tile sees all of it?
             const bool all = j0 + kTile - 1 <= px && (a.window == 0 || j0 > px + TB - 1 - a.window);
-            if (!all || !live) {
-                const int hi = p - j0, lo = a.window ? p - a.window + 1 - j0 : 0;
-                const int sk = a.sinks - j0;
-                const float none = f < 0.f ? INFINITY : -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int k = 32 * c + e;
-                        if (k > hi || (k < lo && k >= sk)) v[c][e] = none;
-                    }
-            }
-            // the largest f S (a negative factor takes the smallest S)
-            float top;
-            if (f >= 0.f) {
-                float t4[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    t4[c] = fmaxf(v[c][0], v[c][1]);
-#pragma unroll
-                    for (int e = 2; e < 32; e += 2) t4[c] = max3(t4[c], v[c][e], v[c][e + 1]);
-                }
-                top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            } else {
-                top = v[0][0];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fminf(top, v[c][e]);
-            }
-            top = fabsf(top) == INFINITY ? -INFINITY : top * f;
-            bool change = false;
-            float keep = 1.f;
-            if (top > m + kRaise) {
-                keep = ex2(m - top);
-                m = top;
-                l *= keep;
-                change = true;
-            }
-            if (Ev != E) {
-                keep *= pow2any(E - Ev);
-                E = Ev;
-                change = true;
-            }
-            if (n > 0 && __any_sync(0xffffffffu, change)) {
+            const bool edge = __any_sync(0xffffffffu, !all || !live);
+            // Half a tile at a time: weights exp2(f S - m) against the reference m
+            // as it stands.  A row that has none yet, or whose weights add up to
+            // more than kMost, takes its largest logit for it, and the half is weighed
+            // (again).  S stays in TMEM until the weights hold.
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    tmem_ld32(to + 32 * c, o);
+            for (int e2 = 0; e2 < 2; ++e2) {
+                float sum, keep = 1.f;
+                uint32_t w[2][16];
+                bool want = m == -INFINITY;
+                bool look = __any_sync(0xffffffffu, want);
+                do {
+                    float v[2][32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= keep;
-                    tmem_st32_nw(to + 32 * c, o);
+                    for (int c = 0; c < 2; ++c) tmem_ld32_nw(ts + 64 * e2 + 32 * c, v[c]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tmem_wait_ld_dep(v[c]);
+                    if (edge) {
+                        const int hi = p + 1 - j0 - 64 * e2;
+                        const int lo = a.window ? p - a.window + 1 - j0 - 64 * e2 : 0;
+                        const int sk = a.sinks - j0 - 64 * e2;
+                        const float none = f < 0.f ? INFINITY : -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t seen = below(hi - 32 * c) &
+                                                  (~below(lo - 32 * c) | below(sk - 32 * c));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) v[c][e] = none;
+                        }
+                    }
+                    if (look) {
+                        float hi = v[0][0], lo = v[0][0];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                hi = max3(hi, v[c][e], v[c][e + 1]);
+                                lo = min3(lo, v[c][e], v[c][e + 1]);
+                            }
+                        const float top = (f < 0.f ? lo : hi) * f;
+                        if (want && top > -INFINITY) {
+                            keep = m == -INFINITY ? 0.f : keep * ex2(m - top);
+                            m = top;
+                        }
+                    }
+                    const float add = m == -INFINITY ? 0.f : -m;
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            fma2(v[c][2 * e], v[c][2 * e + 1], f, add);
+                            const float w0 = ex2(v[c][2 * e]), w1 = ex2(v[c][2 * e + 1]);
+                            add2(part[2 * (e & 1)], part[2 * (e & 1) + 1], w0, w1);
+                            w[c][e] = pack_f16(w0, w1);
+                        }
+                    sum = (part[0] + part[1]) + (part[2] + part[3]);
+                    want = sum > kMost;
+                    look = __any_sync(0xffffffffu, want);
+                } while (look);
+                l = l * keep + sum;
+                if (Ev != E) {
+                    keep *= pow2any(E - Ev);
+                    E = Ev;
                 }
-            }
-            const float mm = m == -INFINITY ? 0.f : -m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                if ((n > 0 || e2 > 0) && __any_sync(0xffffffffu, keep != 1.f)) {
+                    // O must hold the half before
+                    if (e2 > 0) {
+                        ok = wait_bar_warp(&o_half[x], n & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(to + 32 * c, o);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    fma2(v[c][2 * e], v[c][2 * e + 1], f, mm);
-                    const float w0 = ex2(v[c][2 * e]), w1 = ex2(v[c][2 * e + 1]);
-                    add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], w0, w1);
-                    w[e] = pack_f16(w0, w1);
+                        for (int e = 0; e < 32; ++e) o[e] *= keep;
+                        tmem_st32_nw(to + 32 * c, o);
+                    }
                 }
-                tmem_st16_nw(ts + 16 * c, w);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) tmem_st16_nw(ts + 32 * e2 + 16 * c, w[c]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[2 * x + e2]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_full[x]);
         }
         // ---- output ----
         if (N > 0) {

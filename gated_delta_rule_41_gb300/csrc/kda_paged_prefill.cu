@@ -24,8 +24,8 @@
 // K and V tiles arrive by TMA, one box per page, into one ring of slots, and a
 // warpgroup turns what is not ready for the products into it, in place:
 // * V in bf16 to fp16, scaled by a power of two 2^-E so that large values
-//   fit.  E is 0 while the first tile's largest value lies in [1, 2^15], else
-//   the tile's exponent less 8; a later tile that does not fit raises it, and
+//   fit.  E is 0 if the first tile's largest value lies in [1, 2^15), else the
+//   exponent of that value less 8; a later tile that does not fit raises it, and
 //   the rows' O are rescaled as for a moved reference.  bf16 values are exact
 //   in fp16 down to 2^-17 of that scale.
 // * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row scaled
@@ -209,7 +209,8 @@ template <int D>
 struct Plan {
     static constexpr uint32_t SLOT = kTile * D * 2;           // a K or V tile
     static constexpr uint32_t HALF = kTile * 128;             // its 64-column half
-    static constexpr int SLOTS = D == 128 ? 4 : 8;            // even: V tiles in odd slots
+    // V waits for its conversion, so its ring is the longer one
+    static constexpr int KS = D == 128 ? 2 : 4, VS = D == 128 ? 3 : 4, SLOTS = KS + VS;
     static constexpr uint32_t OFF_Q = 0;                      // two tiles
     static constexpr uint32_t OFF_KV = 2 * SLOT;
     static constexpr uint32_t OFF_BAR = OFF_KV + SLOTS * SLOT;
@@ -249,9 +250,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::OFF_BAR);
+    // slots of K, then of V
     uint64_t* kv_full = bars;                     // [SLOTS] loaded
     uint64_t* kv_ready = kv_full + P::SLOTS;      // [SLOTS] converted
     uint64_t* kv_empty = kv_ready + P::SLOTS;     // [SLOTS]
+    // slot of tile n, and the parity of its barriers
+    auto k_slot = [](int n) { return n % P::KS; };
+    auto v_slot = [](int n) { return P::KS + n % P::VS; };
+    auto k_par = [](int n) { return (uint32_t)(n / P::KS) & 1; };
+    auto v_par = [](int n) { return (uint32_t)(n / P::VS) & 1; };
     uint64_t* q_full = kv_empty + P::SLOTS;       // [2]
     uint64_t* q_ready = q_full + 2;               // [2] converted (e4m3)
     uint64_t* s_full = q_ready + 2;               // [2] S is in TMEM, and O up to the tile before
@@ -383,8 +390,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int y = heads_first ? r0 : h, z = heads_first ? h : r0;
                 bool ok = true;
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int q = 2 * n + kv, slot = q % P::SLOTS;
-                    ok = wait_bar_warp(&kv_empty[slot], ((q / P::SLOTS) & 1) ^ 1);
+                    const int slot = kv ? v_slot(n) : k_slot(n);
+                    ok = wait_bar_warp(&kv_empty[slot], (kv ? v_par(n) : k_par(n)) ^ 1);
                     if (!ok) break;
                     if (lane == 0)
                         mbar_arrive_expect_tx(&kv_full[slot], E4M3 ? P::SLOT / 2 : P::SLOT);
@@ -400,13 +407,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                             &kv_full[slot], 64 * c, y, z, page);
                         }
                     }
-                    issued = q + 1;
+                    issued = 2 * n + kv + 1;
                 }
                 if (!ok) break;
             }
             if (issued < 2 * N) {                            // unwinding: let the copies land
-                for (int q = max(0, issued - P::SLOTS); q < issued; ++q)
-                    wait_bar_drain(&kv_full[q % P::SLOTS], (q / P::SLOTS) & 1);
+                for (int q = max(0, issued - 2 * P::SLOTS); q < issued; ++q) {
+                    const int n = q >> 1, kv = q & 1;
+                    // (of a slot's copies the last one)
+                    if (2 * (n + (kv ? P::VS : P::KS)) + kv < issued) continue;
+                    wait_bar_drain(&kv_full[kv ? v_slot(n) : k_slot(n)], kv ? v_par(n) : k_par(n));
+                }
                 for (int x = 0; x < 2; ++x) wait_bar_drain(&q_full[x], 0);
             }
             __syncwarp();
@@ -443,10 +454,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 commit(leader, &kv_empty[0]);
             }
             for (int n = 0; n < N && ok; ++n) {
-                const int qv = 2 * n + 1, vslot = qv % P::SLOTS;
-                const int qk = 2 * n + 2, kslot = qk % P::SLOTS;
+                const int vslot = v_slot(n), kslot = k_slot(n + 1);
                 const uint32_t vx = vd + vslot * (P::SLOT / 16);
-                ok = wait_bar_warp(&kv_ready[vslot], (qv / P::SLOTS) & 1);
+                ok = wait_bar_warp(&kv_ready[vslot], v_par(n));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     for (int e = 0; e < 2; ++e) {
@@ -465,7 +475,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (n + 1 == N) {
                         commit(leader, &o_full[x]);
                     } else {
-                        if (x == 0) ok = wait_bar_warp(&k_bar[kslot], (qk / P::SLOTS) & 1);
+                        if (x == 0) ok = wait_bar_warp(&k_bar[kslot], k_par(n + 1));
                         if (!ok) break;
                         s_mma(x, kslot);
                         if (x == 1) commit(leader, &kv_empty[kslot]);
@@ -482,7 +492,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         // ---------------- conversions ----------------
         const int t = tid & 127;
-        bool ok = true, scaled = false;
+        bool ok = true;
         int E = 0;
         for (int n = 0; n < N; ++n) {
             const int valid = len - sp.tile(n_lo + n) * kTile;   // rows of the sequence
@@ -492,9 +502,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 constexpr int C = D / 16, R = 128 / C, L = kTile / R;
                 const int c = t % C, r0 = t / C;
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int q = 2 * n + kv, slot = q % P::SLOTS;
+                    const int slot = kv ? v_slot(n) : k_slot(n);
                     uint8_t* tile = smem + P::OFF_KV + slot * P::SLOT;
-                    ok = ok && wait_bar_warp(&kv_full[slot], (q / P::SLOTS) & 1);
+                    ok = ok && wait_bar_warp(&kv_full[slot], kv ? v_par(n) : k_par(n));
                     uint4 x[L];
 #pragma unroll
                     for (int i = 0; i < L; ++i) {
@@ -529,72 +539,57 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             } else {
                 constexpr int L = D / 8;                     // 16-byte chunks of a thread
-                const int q = 2 * n + 1, slot = q % P::SLOTS;
+                const int slot = v_slot(n);
                 uint8_t* tile = smem + P::OFF_KV + slot * P::SLOT;
-                ok = ok && wait_bar_warp(&kv_full[slot], (q / P::SLOTS) & 1);
-                uint4 x[L];
-                bool again;
-                do {
-                    const float down = pow2any(-E);
-                    uint32_t top = 0;                        // largest |fp16| so far, in pairs
-#pragma unroll
-                    for (int i = 0; i < L; ++i) {
-                        const int at = t * 16 + i * 2048;    // byte of the tile
-                        x[i] = *reinterpret_cast<const uint4*>(tile + at);
-                        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v0 = __uint_as_float(w[e] << 16);
-                            float v1 = __uint_as_float(w[e] & 0xffff0000u);
-                            mul2(v0, v1, down);
-                            w[e] = pack_f16(v0, v1);
-                            const __half2 hv = __habs2(*reinterpret_cast<const __half2*>(&w[e]));
-                            const __half2 tv =
-                                __hmax2(hv, *reinterpret_cast<const __half2*>(&top));
-                            top = *reinterpret_cast<const uint32_t*>(&tv);
-                        }
-                        if (valid < kTile && (at % P::HALF) / 128 >= valid)
-                            x[i] = make_uint4(0, 0, 0, 0);
+                ok = ok && wait_bar_warp(&kv_full[slot], v_par(n));
+                uint8_t* mine = tile + t * 16;               // chunk i lies 2048 i further
+                const int rows = valid - t / 8;              // 16 (i mod 8) < rows: in the sequence
+                // the tile's largest |v|, by the bits of pairs
+                uint32_t top = 0;
+#pragma unroll 4
+                for (int i = 0; i < L; ++i) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(mine + i * 2048);
+                    if (16 * (i & 7) < rows) {
+                        top = __vmaxu2(top, y.x & 0x7fff7fffu);
+                        top = __vmaxu2(top, y.y & 0x7fff7fffu);
+                        top = __vmaxu2(top, y.z & 0x7fff7fffu);
+                        top = __vmaxu2(top, y.w & 0x7fff7fffu);
                     }
-                    // Does the tile fit?  The first one also sets the scale.  (What
-                    // lies past the sequence's end may ask for a scale too.)
-                    const uint32_t h_top = max(top & 0xffffu, top >> 16);
-                    again = any_convert(h_top >= (n == 0 ? 0x7800u : 0x7c00u));
-                    if (n == 0) again = !any_convert(h_top >= 0x3c00u) || again;
-                    again = again && !scaled;
-                    scaled = again;
-                    if (again) {
-                        float big = 0.f;                     // largest |v| of the tile
-#pragma unroll 1
-                        for (int i = 0; i < L; ++i) {
-                            const int at = t * 16 + i * 2048;
-                            if ((at % P::HALF) / 128 >= valid) continue;
-                            const uint4 y = *reinterpret_cast<const uint4*>(tile + at);
-                            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                big = max3(big, fabsf(__uint_as_float(w[e] << 16)),
-                                           fabsf(__uint_as_float(w[e] & 0xffff0000u)));
-                        }
-                        atomicMax(v_top, __float_as_int(big));   // not negative: ordered as ints
-                        any_convert(false);
-                        const int bits = *reinterpret_cast<volatile int*>(v_top);
-                        const int want = bits == 0 ? -100 : (bits >> 23) - 127 - 8;
-                        any_convert(false);                  // all have read it
-                        if (t == 0) *v_top = 0;
-                        any_convert(false);
-                        E = n == 0 ? (bits >= 0x3f800000 && bits < 0x47000000 ? 0 : want)
-                                   : max(E, want);
-                    }
-                } while (again);
-                if (ok) {
-#pragma unroll
-                    for (int i = 0; i < L; ++i)
-                        *reinterpret_cast<uint4*>(tile + t * 16 + i * 2048) = x[i];
-                    if (t == 0) v_exp[slot] = E;
-                    fence_async_smem();
-                    mbar_arrive(&kv_ready[slot]);
                 }
+                top = max(top & 0xffffu, top >> 16);         // a bf16 without its sign
+                // Does it fit at the scale as it stands?  The first tile sets the
+                // scale: 0 if the largest lies in [1, 2^15).
+                const uint32_t most = (uint32_t)max(0, min(0xff, 127 + 15 + E)) << 7;
+                bool again = any_convert(top >= most);
+                if (n == 0) again = !any_convert(top >= 0x3f80u) || again;
+                if (__builtin_expect(again, 0)) {
+                    atomicMax(v_top, (int)top);
+                    any_convert(false);
+                    const int bits = *reinterpret_cast<volatile int*>(v_top);
+                    const int want = bits == 0 ? -100 : (bits >> 7) - 127 - 8;
+                    any_convert(false);                      // all have read it
+                    if (t == 0) *v_top = 0;
+                    any_convert(false);
+                    E = n == 0 ? want : max(E, want);
+                }
+                const float down = pow2any(-E);
+                if (!ok) continue;
+#pragma unroll 4
+                for (int i = 0; i < L; ++i) {
+                    uint4 y = *reinterpret_cast<const uint4*>(mine + i * 2048);
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v0 = __uint_as_float(w[e] << 16);
+                        float v1 = __uint_as_float(w[e] & 0xffff0000u);
+                        mul2(v0, v1, down);
+                        w[e] = 16 * (i & 7) < rows ? pack_f16(v0, v1) : 0;
+                    }
+                    *reinterpret_cast<uint4*>(mine + i * 2048) = y;
+                }
+                if (t == 0) v_exp[slot] = E;
+                fence_async_smem();
+                mbar_arrive(&kv_ready[slot]);
             }
         }
     } else {
@@ -650,9 +645,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int j0 = sp.tile(n_lo + n) * kTile;
             int Ev = 0;
             if (!E4M3) {                                     // the scale of this tile's V
-                const int q = 2 * n + 1, slot = q % P::SLOTS;
-                ok = wait_bar_warp(&kv_ready[slot], (q / P::SLOTS) & 1);
-                Ev = v_exp[slot];
+                ok = wait_bar_warp(&kv_ready[v_slot(n)], v_par(n));
+                Ev = v_exp[v_slot(n)];
             }
             ok = ok && wait_bar_warp(&s_full[x], n & 1);
             if (!ok) break;
@@ -676,7 +670,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int c = 0; c < 2; ++c) tmem_ld32_nw(ts + 64 * e2 + 32 * c, v[c]);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_wait_ld_dep(v[c]);
-                    if (edge) {
+                    if (__builtin_expect(edge, 0)) {
                         const int hi = p + 1 - j0 - 64 * e2;
                         const int lo = a.window ? p - a.window + 1 - j0 - 64 * e2 : 0;
                         const int sk = a.sinks - j0 - 64 * e2;
@@ -690,7 +684,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 if (!(seen >> e & 1)) v[c][e] = none;
                         }
                     }
-                    if (look) {
+                    if (__builtin_expect(look, 0)) {
                         float hi = v[0][0], lo = v[0][0];
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
@@ -719,13 +713,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     sum = (part[0] + part[1]) + (part[2] + part[3]);
                     want = sum > kMost;
                     look = __any_sync(0xffffffffu, want);
-                } while (look);
+                } while (__builtin_expect(look, 0));
                 l = l * keep + sum;
-                if (Ev != E) {
+                if (__builtin_expect(Ev != E, 0)) {
                     keep *= pow2any(E - Ev);
                     E = Ev;
                 }
-                if ((n > 0 || e2 > 0) && __any_sync(0xffffffffu, keep != 1.f)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, keep != 1.f), 0) && (n > 0 || e2 > 0)) {
                     // O must hold the half before
                     if (e2 > 0) {
                         ok = wait_bar_warp(&o_half[x], n & 1);

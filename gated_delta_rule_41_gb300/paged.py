@@ -74,8 +74,18 @@ def _lib():
     return _bound
 
 
+# The current stream's handle, without the Stream object that torch.cuda's
+# own call makes for it (a few microseconds of a small call).
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _get_device is None or _get_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _get_stream(_get_device())
 
 
 def _fresh(stream, *tensors):
@@ -102,10 +112,11 @@ def _tokens(name, t, heads, D):
         raise KdaError(3, f"{name}: {t.dtype} (bf16 only)")
     if not t.is_cuda or t.dim() != 3 or t.shape[2] != D or (heads and t.shape[1] != heads):
         raise KdaError(1, f"{name} must be a CUDA tensor [tokens, {heads or 'heads'}, {D}]")
-    st = t.stride()
-    if st[2] != 1 or (t.shape[1] > 1 and st[1] != D):
+    n, h, _ = t.shape
+    a, b, c = t.stride()
+    if c != 1 or (h > 1 and b != D):
         raise KdaError(1, f"{name}: the heads of a token must be contiguous")
-    return st[0] if t.shape[0] > 1 else t.shape[1] * D
+    return a if n > 1 else h * D
 
 
 class KVPages:
@@ -138,6 +149,7 @@ class KVPages:
         self._code = codes[k.dtype]
         st = k.stride()   # of a dimension of one, torch may report any stride
         self._strides = tuple(0 if n == 1 else x for n, x in zip(k.shape, st))
+        self._calls = {}   # dims (and workspace bytes) of the calls seen
         self._ptrs = (k.data_ptr(), v.data_ptr(),
                       None if k_scale is None else k_scale.data_ptr(),
                       None if v_scale is None else v_scale.data_ptr())
@@ -147,6 +159,24 @@ class KVPages:
         return KdaPagedDims(S, HQ, self.HKV, self.D, self.num_pages, self.page_size, max_pages,
                             self._code, st[0], st[1], st[2],
                             self.D ** -0.5 if scale is None else scale, window, sinks)
+
+
+    def _call(self, S, HQ, max_pages, scale, window, sinks, T=None):
+        """Dims pointer and workspace bytes of a call, built once per set of
+        sizes.  T None: decode; 0: append; else prompt attention of T tokens."""
+        key = (S, HQ, max_pages, scale, window, sinks, T)
+        got = self._calls.get(key)
+        if got is None:
+            if len(self._calls) >= 256:
+                self._calls.clear()
+            d = ctypes.pointer(self.dims(S, HQ, max_pages, scale, window, sinks))
+            need = 0
+            if T is None:
+                need = int(_lib().kda_paged_decode_workspace_bytes(d))
+            elif T > 0:
+                need = int(_lib().kda_paged_prefill_workspace_bytes(d, T))
+            got = self._calls[key] = (d, need)
+        return got
 
 
 def paged_append(pages: KVPages, k, v, block_table, kv_lens, cu_seqlens=None, stream=None):
@@ -161,7 +191,7 @@ def paged_append(pages: KVPages, k, v, block_table, kv_lens, cu_seqlens=None, st
         raise KdaError(2, "paged_append: k and v differ in tokens")
     table, lens = _ints("block_table", block_table, 2), _ints("kv_lens", kv_lens, 1, S)
     cu = None if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, 1, S + 1)
-    d = pages.dims(S, pages.HKV, width)
+    d, _ = pages._call(S, pages.HKV, width, None, 0, 0, 0)
     kp, vp, sk, sv = pages._ptrs
     _raise(lib.kda_paged_append(d, cu, T, k.data_ptr(), ks, v.data_ptr(), vs, sk, sv, table, lens,
                                 kp, vp, _raw_stream(stream)), "kda_paged_append")
@@ -179,7 +209,8 @@ def _attention_workspace(need, workspace, device, stream):
 
 def _outputs(q, out, lse, return_lse, stream):
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = (torch.empty_like(q) if q.is_contiguous() else
+               torch.empty(q.shape, dtype=q.dtype, device=q.device))
         _fresh(stream, out)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda \
             or not out.is_contiguous():
@@ -214,9 +245,8 @@ def paged_decode(q, pages: KVPages, block_table, kv_lens, scale=None, window=0, 
     if block_table.shape[0] != S:
         raise KdaError(2, "paged_decode: block_table has other rows than q")
     table, lens = _ints("block_table", block_table, 2), _ints("kv_lens", kv_lens, 1, S)
-    d = pages.dims(S, HQ, block_table.shape[1], scale, window, sinks)
+    d, need = pages._call(S, HQ, block_table.shape[1], scale, window, sinks)
     out, lse = _outputs(q, out, lse, return_lse, stream)
-    need = int(lib.kda_paged_decode_workspace_bytes(d))
     ws = _attention_workspace(need, workspace, q.device, stream)
     kp, vp, sk, sv = pages._ptrs
     _raise(lib.kda_paged_decode(d, q.data_ptr(), qs, kp, vp, sk, sv, table, lens, out.data_ptr(),
@@ -244,9 +274,8 @@ def paged_prefill(q, pages: KVPages, block_table, kv_lens, cu_seqlens, scale=Non
     S, width = block_table.shape
     table, lens = _ints("block_table", block_table, 2), _ints("kv_lens", kv_lens, 1, S)
     cu = _ints("cu_seqlens", cu_seqlens, 1, S + 1)
-    d = pages.dims(S, HQ, width, scale, window, sinks)
+    d, need = pages._call(S, HQ, width, scale, window, sinks, T)
     out, lse = _outputs(q, out, lse, return_lse, stream)
-    need = int(lib.kda_paged_prefill_workspace_bytes(d, T))
     ws = _attention_workspace(need, workspace, q.device, stream)
     kp, vp, sk, sv = pages._ptrs
     _raise(lib.kda_paged_prefill(d, cu, T, q.data_ptr(), qs, kp, vp, sk, sv, table, lens,
@@ -301,15 +330,20 @@ class PageBook:
         if len(self.pools) > MAX_POOLS:
             raise KdaError(3, f"{len(self.pools)} pools (at most {MAX_POOLS})")
         self._arr = _pool_array(self.pools, num_pages)
-        self._ws, self._need = None, 0
+        self._ws, self._need, self._dims = None, 0, {}
 
     def _args(self, block_table, kv_lens, refs, stream):
         table = _ints("block_table", block_table, 2)
         S, width = block_table.shape
         lens = _ints("kv_lens", kv_lens, 1, S)
         counts = _ints("refs", refs, 1, self.num_pages)
-        d = KdaPagesDims(S, width, self.num_pages, self.page_size)
-        need = int(_lib().kda_pages_workspace_bytes(d))
+        got = self._dims.get((S, width))
+        if got is None:
+            if len(self._dims) >= 256:
+                self._dims.clear()
+            d = ctypes.pointer(KdaPagesDims(S, width, self.num_pages, self.page_size))
+            got = self._dims[S, width] = (d, int(_lib().kda_pages_workspace_bytes(d)))
+        d, need = got
         if need > self._need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=refs.device)
             self._need = need
@@ -332,7 +366,7 @@ class PageBook:
         tokens), and rows get the pages they then need."""
         d, table, lens, counts, ws, n_ws = self._args(block_table, kv_lens, refs, stream)
         each = isinstance(add, torch.Tensor)
-        more = _ints("add", add, 1, d.S) if each else None
+        more = _ints("add", add, 1, kv_lens.shape[0]) if each else None
         _raise(_lib().kda_pages_extend(d, more, 0 if each else int(add), table, lens, counts, ws,
                                        n_ws, _raw_stream(stream)), "kda_pages_extend")
 

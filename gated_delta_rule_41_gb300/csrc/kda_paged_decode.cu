@@ -9,15 +9,18 @@
 //   query heads).  The tiles of all of them form one line, of which each
 //   resident CTA takes an equal stretch (a prefix sum over the lengths, taken
 //   by every CTA for itself), so a few long rows spread over the SMs like many
-//   unequal ones.  A row that ends up in one CTA is written at once; of the
-//   others each CTA leaves its part (sums, weights' maximum and total), and the
-//   CTA that arrives last joins the parts in their order along the row, so the
-//   result does not depend on which one that is.
+//   unequal ones.
 // * A warp owns 16 tokens of a tile at a time.  They lie in one page (pages are
-//   multiples of 16), so one table entry, read an iteration ahead, gives their
-//   addresses.  K and V rows come by 16-byte asynchronous copies into the warp's own ring of stages;
-//   no barrier is needed within a row.  Rows that the query does not see are
-//   filled with zeros instead of being read.
+//   multiples of 16), so one table entry, read a step ahead, gives their
+//   addresses.  K and V come by 16-byte asynchronous copies into the warp's own
+//   ring of stages, which runs on over the ends of rows: while a row is
+//   finished, the copies of the next one are on their way.  Rows that the
+//   query does not see are filled with zeros instead of being read.
+// * At the end of a row warps 1-3 leave their sums in shared memory, in the
+//   order of the MMA fragments, and go on; warp 0 adds them to its own.  A row
+//   that lies in one stretch is written at once; of the others each CTA leaves its
+//   part, and the CTA that arrives last joins the parts in their order along
+//   the row, so the result does not depend on which one that is.
 // * S^T = K Q^T has the tokens on the M axis of mma.m16n8k16 and 8 query heads
 //   on N, O^T = V^T P the channels on M, so up to 8 heads cost 16 MMAs for 16
 //   tokens.  The transposed weights come from movmatrix.
@@ -41,7 +44,6 @@ using namespace paged;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGroup = 16;                 // tokens of a warp's step
-constexpr int kPartHeads = 16;             // query heads of a CTA, at most
 
 __device__ __forceinline__ void record() { atomicCAS(&g_paged_decode_error, 0, (int)KDA_ERR_SHAPE); }
 
@@ -75,33 +77,163 @@ struct Shape {
     static constexpr int RB = D * (E4M3 ? 1 : 2);        // bytes of a row
     static constexpr int RC = RB / 16;                   // 16-byte chunks of a row
     static constexpr int TILE = kGroup * RB;             // K (or V) of a step
-    // ring of stages: 24 KB (bf16, D = 128) per warp, two CTAs on an SM
-    static constexpr int STAGES = RB == 256 ? 3 : RB == 128 ? 6 : 8;
+    // CTAs of an SM, and the stages of a warp's ring (as many as fit)
+    static constexpr int OCC = NH == 2 || D == 128 ? 2 : 3;
+    static constexpr int STAGES = RB == 256   ? (NH == 1 ? 3 : 2)
+                                  : RB == 128 ? (OCC == 3 ? 4 : D == 64 || NH == 1 ? 6 : 5)
+                                              : 8;
     static constexpr int RING = STAGES * 2 * TILE;       // bytes per warp
-    static constexpr int OS = D + 4;                     // row of the join buffer, floats
-    static constexpr size_t SMEM = kWarps * RING;
-    static_assert(NH * 8 * OS * 4 <= RING, "join buffer does not fit the ring");
+    static constexpr int KS = D / 16;                    // k steps of S, m tiles of O
+    // what a warp knows of a row, per lane: O fragments, maxima, sums
+    static constexpr int FRAG = KS * NH + NH;            // float4
+    static constexpr size_t SMEM = kWarps * RING + (kWarps - 1) * FRAG * 512;
+    static_assert(OCC * (SMEM + 2048) <= 228 * 1024, "over the shared memory of an SM");
+};
+constexpr int kMostCtas = 3;                             // of an SM, over all shapes
+
+// Shuffled layout of a row's state: [FRAG][32 lanes] float4.  Fragment k NH + n
+// holds channels of m tile k for heads 8n + 2t and 8n + 2t + 1 (the accumulator of
+// an MMA), fragment KS NH + n the two maxima and this lane's two sums.
+template <int D, bool E4M3, int NH>
+struct State {
+    static constexpr int KS = D / 16;
+    float o[NH][KS][4], m[NH][2], l[NH][2];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][k][i] = 0.f;
+        }
+    }
+    // fragment i of this lane
+    __device__ __forceinline__ float4 frag(int i) const {
+        const int n = i % NH, k = i / NH;
+        return k < KS ? make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3])
+                      : make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+    }
+    __device__ __forceinline__ void store(float4* to) const {   // to: this lane's
+#pragma unroll
+        for (int i = 0; i < (KS + 1) * NH; ++i) to[i * 32] = frag(i);
+    }
+    // Adds another state of the row; from(i): its fragment i of this lane.  (The
+    // roundings are spelled out: all copies of this code give the same bits.)
+    template <typename F>
+    __device__ __forceinline__ void add(F from) {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const float4 z = from(KS * NH + n);
+            const float zm[2] = {z.x, z.y}, zl[2] = {z.z, z.w};
+            float mine[2], theirs[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float top = fmaxf(m[n][c], zm[c]);
+                mine[c] = m[n][c] == top ? 1.f : ex2(m[n][c] - top);
+                theirs[c] = zm[c] == -INFINITY ? 0.f : ex2(zm[c] - top);
+                m[n][c] = top;
+                l[n][c] = fmaf(theirs[c], zl[c], __fmul_rn(mine[c], l[n][c]));
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const float4 y = from(k * NH + n);
+                o[n][k][0] = fmaf(theirs[0], y.x, __fmul_rn(mine[0], o[n][k][0]));
+                o[n][k][1] = fmaf(theirs[1], y.y, __fmul_rn(mine[1], o[n][k][1]));
+                o[n][k][2] = fmaf(theirs[0], y.z, __fmul_rn(mine[0], o[n][k][2]));
+                o[n][k][3] = fmaf(theirs[1], y.w, __fmul_rn(mine[1], o[n][k][3]));
+            }
+        }
+    }
 };
 
-// A part of a row: per head the maximum, the sum and D sums of a CTA.
-template <int D>
-struct Part {
-    float m[kPartHeads], l[kPartHeads];
-    float o[kPartHeads][D];
+// Where a row's result goes, and the units of its O.
+struct RowOut {
+    long long at;      // row of q, o, lse: s HQ + first head
+    int heads;         // of the block
+    float unit;        // what a unit of V is worth (e4m3)
 };
+
+// Writes one fragment (m tile k, heads 8n + 2t + {0, 1}) of a finished row.
+template <int D, bool E4M3>
+__device__ __forceinline__ void write_frag(const PagedArgs& a, const RowOut& r, int n, int k,
+                                           int g, int t, const float (&o)[4],
+                                           const float (&by)[2]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int head = 8 * n + 2 * t + c;
+        if (head >= r.heads) continue;
+        __nv_bfloat16* to = a.o + (r.at + head) * D + 16 * k;
+        // rows g, g + 8 of the m tile are channels g, g + 8 (bf16) or 2g, 2g + 1
+        if (E4M3) {
+            *reinterpret_cast<uint32_t*>(to + 2 * g) = ptx::pack_bf16(o[c] * by[c], o[c + 2] * by[c]);
+        } else {
+            to[g] = __float2bfloat16_rn(o[c] * by[c]);
+            to[g + 8] = __float2bfloat16_rn(o[c + 2] * by[c]);
+        }
+    }
+}
+// The factors of a finished row's O (heads 8n + 2t + c), and its lse.
+__device__ __forceinline__ void finish_heads(const PagedArgs& a, const RowOut& r, int n, int g,
+                                             int t, const float (&m)[2], float (&l)[2], bool lse,
+                                             float (&by)[2]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+        const bool any = m[c] != -INFINITY;
+        const int head = 8 * n + 2 * t + c;
+        by[c] = any ? r.unit / l[c] : 0.f;
+        if (lse && a.lse && g == 0 && head < r.heads)
+            a.lse[r.at + head] = any ? (m[c] + lg2(l[c])) * kLn2 : -INFINITY;
+    }
+}
+
+// Adds parts w, w + kWarps, ... of a row's `count` to st: part 0 lies at
+// `first`, the others from `rest` on, `step` float4 apart.  B parts are on their
+// way at once.
+template <int B, int D, bool E4M3, int NH>
+__device__ __forceinline__ void add_parts(State<D, E4M3, NH>& st, const float4* first,
+                                          const float4* rest, int count, int step, int w, int lane) {
+    constexpr int F = Shape<D, E4M3, NH>::FRAG;
+#pragma unroll 1
+    for (int i = w; i < count; i += B * kWarps) {
+        float4 y[B][F];
+#pragma unroll
+        for (int e = 0; e < B; ++e) {
+            const int j = i + e * kWarps;
+            const float4* p = (j == 0 ? first : rest + (long long)(j - 1) * step) + lane;
+#pragma unroll
+            for (int k = 0; k < F; ++k)
+                y[e][k] = j < count ? __ldcg(p + k * 32)
+                                    : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < B; ++e)
+            if (i + e * kWarps < count) st.add([&](int k) { return y[e][k]; });
+    }
+}
+
+__device__ __forceinline__ void bar_sync(int id) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id) {
+    asm volatile("barrier.cta.arrive %0, 128;" ::"r"(id) : "memory");
+}
 
 template <int D, bool E4M3, int NH>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shape<D, E4M3, NH>::OCC)
 decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
-              Part<D>* __restrict__ parts) {
+              float4* __restrict__ parts) {
     using Sh = Shape<D, E4M3, NH>;
-    constexpr int KS = D / 16;                           // k steps of S, m tiles of O
+    constexpr int KS = Sh::KS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_scan[kWarps];
     __shared__ int s_seq;
     __shared__ long long s_at;
-    __shared__ float s_m[kWarps][kPartHeads], s_l[kWarps][kPartHeads];
-    __shared__ unsigned s_ticket;
+    __shared__ int s_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rows = a.HKV * HB;                         // rows of a sequence
@@ -118,6 +250,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         if (lane >= o) sum += y;
     }
     if (lane == 31) s_scan[warp] = sum;
+    if (tid == 0) s_last = 0;
     __syncthreads();
     long long before = sum - mine, total = 0;
 #pragma unroll
@@ -142,22 +275,94 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         s_at = at;
     }
     __syncthreads();
-    int s = s_seq;
-    long long seq_at = s_at;                             // line index of sequence s's first tile
     const uint32_t ring = ptx::smem_u32(smem) + warp * Sh::RING;
-    float* join = reinterpret_cast<float*>(smem + warp * Sh::RING);
+    float4* mail = reinterpret_cast<float4*>(smem + kWarps * Sh::RING) + lane;   // of warps 1-3
+    const int gshift = a.page_shift - 4;                 // groups per page, log2
 
-    for (long long at = begin; at < end;) {
-        Span sp = make_span(a, seq_len(a, s));
-        while (at >= seq_at + (long long)sp.tiles() * rows) {
-            seq_at += (long long)sp.tiles() * rows;
-            sp = make_span(a, seq_len(a, ++s));
+    // A stretch's piece of one row, as the warp sees it.
+    struct Piece {
+        int s, row, tile0, tile1, tiles;
+        long long seq_at, at;                            // line index of its sequence, of itself
+        Span sp;
+        int g0, steps;                                   // the warp's first group, groups
+    };
+    auto enter = [&](Piece& p) {                         // p.s, p.seq_at, p.at are set
+        p.sp = make_span(a, seq_len(a, p.s));
+        while (p.at >= p.seq_at + (long long)p.sp.tiles() * rows) {
+            p.seq_at += (long long)p.sp.tiles() * rows;
+            p.sp = make_span(a, seq_len(a, ++p.s));
         }
-        const int tiles = sp.tiles();
-        const int row = (int)((at - seq_at) / tiles), tile0 = (int)((at - seq_at) % tiles);
-        const int tile1 = (int)min((long long)tiles, tile0 + (end - at));
-        const int h = row / HB, hq0 = h * a.G + row % HB * (8 * NH);
-        const int heads = min(8 * NH, (h + 1) * a.G - hq0);
+        p.tiles = p.sp.tiles();
+        p.row = (int)((p.at - p.seq_at) / p.tiles);
+        p.tile0 = (int)((p.at - p.seq_at) % p.tiles);
+        p.tile1 = (int)min((long long)p.tiles, p.tile0 + (end - p.at));
+        p.g0 = p.tile0 * kWarps + warp;
+        const int g1 = min(p.sp.n, p.tile1 * kWarps);
+        p.steps = p.g0 < g1 ? (g1 - p.g0 + kWarps - 1) / kWarps : 0;
+    };
+    Piece in;                                            // being loaded
+    in.s = s_seq;
+    in.seq_at = s_at;
+    in.at = begin;
+    enter(in);
+    Piece cur = in;                                      // being worked on
+
+    // ---- loads: one step of the warp, or nothing, is one group of copies ----
+    int in_step = 0, in_stage = 0;
+    auto page_of = [&]() {
+        return in_step < in.steps
+                   ? __ldg(a.table + (size_t)in.s * a.max_pages +
+                           (in.sp.group(in.g0 + in_step * kWarps) >> gshift))
+                   : 0;
+    };
+    int page = page_of();
+    auto issue = [&]() {
+        while (in_step >= in.steps && in.at + (in.tile1 - in.tile0) < end) {
+            in.at += in.tile1 - in.tile0;
+            enter(in);
+            in_step = 0;
+            page = page_of();
+        }
+        if (in_step < in.steps) {
+            const int grp = in.sp.group(in.g0 + in_step * kWarps), j0 = grp * kGroup;
+            const bool good = (unsigned)page < (unsigned)a.num_pages;
+            if (!good) record();
+            const long long off = (good ? page : 0) * a.page_stride +
+                                  (grp & ((1 << gshift) - 1)) * kGroup * a.token_stride +
+                                  (in.row / HB) * a.head_stride;
+            const char* kp = static_cast<const char*>(a.kp) + off * (E4M3 ? 1 : 2);
+            const char* vp = static_cast<const char*>(a.vp) + off * (E4M3 ? 1 : 2);
+            const long long ts = a.token_stride * (E4M3 ? 1 : 2);
+            const uint32_t st = ring + in_stage * (2 * Sh::TILE);
+#pragma unroll
+            for (int r = 0; r < Sh::TILE / 512; ++r) {
+                const int x = r * 32 + lane, row_ = x / Sh::RC, c = x % Sh::RC;
+                const int j = j0 + row_;
+                const bool on = good && j < in.sp.len && (j >= in.sp.low || j < in.sp.sinks);
+                // chunks are permuted within 128 bytes so that eight rows of
+                // one chunk lie in different banks
+                const int sw = Sh::RC >= 8 ? (row_ & 7) : ((row_ >> 1) & 3);
+                const uint32_t d = st + row_ * Sh::RB + ((c ^ sw) << 4);
+                const long long o = row_ * ts + c * 16;
+                cp_async16_zfill(d, kp + o, on);
+                cp_async16_zfill(d + Sh::TILE, vp + o, on);
+            }
+            ++in_step;
+            in_stage = in_stage + 1 == Sh::STAGES ? 0 : in_stage + 1;
+            page = page_of();
+        }
+        ptx::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < Sh::STAGES - 1; ++i) issue();
+
+    int stage = 0;
+    for (bool first = true;; first = false) {
+        const int h = cur.row / HB, hq0 = h * a.G + cur.row % HB * (8 * NH);
+        RowOut out;
+        out.at = (long long)cur.s * a.HQ + hq0;
+        out.heads = min(8 * NH, (h + 1) * a.G - hq0);
+        out.unit = E4M3 && a.vs ? a.vs[h] : 1.f;
 
         // ---- Q as the B operand: head g (+ 8 n), channels of this lane ----
         // e4m3: q in fp16, scaled by a power of two to at most 2 (put back into
@@ -167,8 +372,8 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         float f[NH][2];                                  // logit factors of heads 2t, 2t + 1
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            const bool on = 8 * n + g < heads;
-            const __nv_bfloat16* q = a.q + s * a.q_stride + (long long)(hq0 + 8 * n + g) * D;
+            const bool on = 8 * n + g < out.heads;
+            const __nv_bfloat16* q = a.q + cur.s * a.q_stride + (long long)(hq0 + 8 * n + g) * D;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 if (E4M3) {
@@ -211,73 +416,21 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
             }
         }
 
-        // ---- the warp's groups of this stretch: gi0, gi0 + 4, ... ----
-        const int gi0 = tile0 * kWarps + warp, gi1 = min(sp.n, tile1 * kWarps);
-        const int steps = gi0 < gi1 ? (gi1 - gi0 + kWarps - 1) / kWarps : 0;
-        const int* table = a.table + (size_t)s * a.max_pages;
-        const int gshift = a.page_shift - 4;             // groups per page, log2
-        auto page_of = [&](int i) {
-            return i < steps ? __ldg(table + (sp.group(gi0 + i * kWarps) >> gshift)) : 0;
-        };
-        auto issue = [&](int i, int page) {
-            if (i < steps) {
-                const int grp = sp.group(gi0 + i * kWarps), j0 = grp * kGroup;
-                const bool good = (unsigned)page < (unsigned)a.num_pages;
-                if (!good) record();
-                const long long off = (good ? page : 0) * a.page_stride +
-                                      (grp & ((1 << gshift) - 1)) * kGroup * a.token_stride +
-                                      h * a.head_stride;
-                const char* kp = static_cast<const char*>(a.kp) + off * (E4M3 ? 1 : 2);
-                const char* vp = static_cast<const char*>(a.vp) + off * (E4M3 ? 1 : 2);
-                const long long ts = a.token_stride * (E4M3 ? 1 : 2);
-                const uint32_t st = ring + (i % Sh::STAGES) * (2 * Sh::TILE);
-#pragma unroll
-                for (int r = 0; r < Sh::TILE / 512; ++r) {
-                    const int x = r * 32 + lane, row_ = x / Sh::RC, c = x % Sh::RC;
-                    const int j = j0 + row_;
-                    const bool on = good && j < sp.len && (j >= sp.low || j < sp.sinks);
-                    // chunks are permuted within 128 bytes so that eight rows of
-                    // one chunk lie in different banks
-                    const int sw = Sh::RC >= 8 ? (row_ & 7) : ((row_ >> 1) & 3);
-                    const uint32_t d = st + row_ * Sh::RB + ((c ^ sw) << 4);
-                    const long long o = row_ * ts + c * 16;
-                    cp_async16_zfill(d, kp + o, on);
-                    cp_async16_zfill(d + Sh::TILE, vp + o, on);
-                }
-            }
-            ptx::cp_async_commit();
-        };
-        int page = page_of(0);
-#pragma unroll
-        for (int i = 0; i < Sh::STAGES - 1; ++i) {
-            const int next = page_of(i + 1);
-            issue(i, page);
-            page = next;
-        }
-
-        float o[NH][KS][4], m[NH][2], l[NH][2];
-#pragma unroll
-        for (int n = 0; n < NH; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][k][i] = 0.f;
-        }
-
-        for (int i = 0; i < steps; ++i) {
-            const int next = page_of(i + Sh::STAGES);
+        State<D, E4M3, NH> st;
+        st.clear();
+        for (int i = 0; i < cur.steps; ++i) {
             cp_async_wait<Sh::STAGES - 2>();
-            __syncwarp();                                // every lane's copies, and step i - 1 read
-            issue(i + Sh::STAGES - 1, page);
-            page = next;
-            const uint32_t kt = ring + (i % Sh::STAGES) * (2 * Sh::TILE), vt = kt + Sh::TILE;
+            __syncwarp();                                // every lane's copies, and the step before read
+            issue();
+            const uint32_t kt = ring + stage * (2 * Sh::TILE), vt = kt + Sh::TILE;
+            stage = stage + 1 == Sh::STAGES ? 0 : stage + 1;
 
-            // ---- S^T = K Q^T ----
-            float x[NH][4];
+            // ---- S^T = K Q^T, in two chains of sums ----
+            float x[NH][4], y[NH][4];
 #pragma unroll
-            for (int n = 0; n < NH; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] = y[n][e] = 0.f;
             {
                 const int r = lane & 15, up = lane >> 4;
                 const int sw = Sh::RC >= 8 ? (r & 7) : ((r >> 1) & 3);
@@ -288,7 +441,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                         ldsm4(af, kt + r * Sh::RB + (((2 * k + up) ^ sw) << 4));
 #pragma unroll
                         for (int n = 0; n < NH; ++n)
-                            mma16816<false>(x[n], af, qf[n][k][0], qf[n][k][1]);
+                            mma16816<false>(k & 1 ? y[n] : x[n], af, qf[n][k][0], qf[n][k][1]);
                     }
                 } else {
 #pragma unroll
@@ -304,43 +457,45 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                                                     e4m3x2_f16x2((uint16_t)(hi >> 16))};
 #pragma unroll
                             for (int n = 0; n < NH; ++n)
-                                mma16816<true>(x[n], af, qf[n][k + e][0], qf[n][k + e][1]);
+                                mma16816<true>(e ? y[n] : x[n], af, qf[n][k + e][0],
+                                               qf[n][k + e][1]);
                         }
                     }
                 }
             }
 
             // ---- weights ----
-            const int j0 = sp.group(gi0 + i * kWarps) * kGroup;
-            const bool edge = j0 + kGroup > sp.len || (j0 < sp.low);
+            const int j0 = cur.sp.group(cur.g0 + i * kWarps) * kGroup;
+            const bool edge = j0 + kGroup > cur.sp.len || j0 < cur.sp.low;
             bool rise = false;
 #pragma unroll
             for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[n][e] *= f[n][e & 1];
+                    x[n][e] = (x[n][e] + y[n][e]) * f[n][e & 1];
                     if (edge) {
                         const int j = j0 + g + 8 * (e >> 1);
-                        if (!(j < sp.len && (j >= sp.low || j < sp.sinks))) x[n][e] = -INFINITY;
+                        if (!(j < cur.sp.len && (j >= cur.sp.low || j < cur.sp.sinks)))
+                            x[n][e] = -INFINITY;
                     }
-                    rise |= x[n][e] > m[n][e & 1] + 8.f;
+                    rise |= x[n][e] > st.m[n][e & 1] + 8.f;
                 }
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float top = fmaxf(m[n][c], fmaxf(x[n][c], x[n][c + 2]));
+                        float top = fmaxf(st.m[n][c], fmaxf(x[n][c], x[n][c + 2]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const float keep = m[n][c] == top ? 1.f : ex2(m[n][c] - top);
-                        m[n][c] = top;
-                        l[n][c] *= keep;
+                        const float keep = st.m[n][c] == top ? 1.f : ex2(st.m[n][c] - top);
+                        st.m[n][c] = top;
+                        st.l[n][c] *= keep;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
-                            o[n][k][c] *= keep;
-                            o[n][k][c + 2] *= keep;
+                            st.o[n][k][c] *= keep;
+                            st.o[n][k][c + 2] *= keep;
                         }
                     }
             }
@@ -350,11 +505,11 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float top = m[n][e & 1];
+                    const float top = st.m[n][e & 1];
                     w[e] = ex2(x[n][e] - (top == -INFINITY ? 0.f : top));
                 }
-                l[n][0] += w[0] + w[2];
-                l[n][1] += w[1] + w[3];
+                st.l[n][0] += w[0] + w[2];
+                st.l[n][1] += w[1] + w[3];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float w0 = w[2 * e], w1 = w[2 * e + 1];
@@ -379,8 +534,8 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                     ldsm4_t(af, vt + r * Sh::RB + (((2 * k + up) ^ sw) << 4));
 #pragma unroll
                     for (int n = 0; n < NH; ++n) {
-                        mma16816<false>(o[n][k], af, pf[n][0], pf[n][1]);
-                        mma16816<false>(o[n][k], af, pl[n][0], pl[n][1]);
+                        mma16816<false>(st.o[n][k], af, pf[n][0], pf[n][1]);
+                        mma16816<false>(st.o[n][k], af, pl[n][0], pl[n][1]);
                     }
                 }
             } else {
@@ -402,116 +557,103 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                                                 e4m3x2_f16x2((uint16_t)(hi >> 16))};
 #pragma unroll
                         for (int n = 0; n < NH; ++n)
-                            mma16816<true>(o[n][k + e], af, pf[n][0], pf[n][1]);
+                            mma16816<true>(st.o[n][k + e], af, pf[n][0], pf[n][1]);
                     }
                 }
             }
         }
-        cp_async_wait<0>();
-        __syncwarp();
 
-        // ---- join the warps ----
+        // ---- the end of the piece: warp 0 collects ----
+        const long long next = cur.at + (cur.tile1 - cur.tile0);
+        const bool last = next >= end, whole = cur.tile0 == 0 && cur.tile1 == cur.tiles;
+        const long long row_at = cur.seq_at + (long long)cur.row * cur.tiles;
+        const int c0 = (int)(row_at / per), c1 = (int)((row_at + cur.tiles - 1) / per);
+        // the parts of the row: CTA c0 leaves its own in its second slot, the others in their
+        // first
+        float4* slots = parts + (2LL * c0 + 1) * (Sh::FRAG * 32);
+        auto send = [&]() { st.store(mail + (warp - 1) * (Sh::FRAG * 32)); };
+        auto collect = [&]() {
+#pragma unroll 1
+            for (int w = 0; w < kWarps - 1; ++w)
+                st.add([&](int i) { return mail[(w * Sh::FRAG + i) * 32]; });
+        };
+        auto write = [&]() {
 #pragma unroll
-        for (int n = 0; n < NH; ++n)
+            for (int n = 0; n < NH; ++n) {
+                float by[2];
+                finish_heads(a, out, n, g, t, st.m[n], st.l[n], true, by);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
-                const int head = 8 * n + 2 * t + c;
-                if (g == 0) {
-                    s_m[warp][head] = m[n][c];
-                    s_l[warp][head] = l[n][c];
-                }
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    // rows g, g + 8 of the m tile are channels g, g + 8 (bf16) or
-                    // 2g, 2g + 1 (e4m3)
-                    const int d0 = 16 * k + (E4M3 ? 2 * g : g);
-                    join[head * Sh::OS + d0] = o[n][k][c];
-                    join[head * Sh::OS + d0 + (E4M3 ? 1 : 8)] = o[n][k][c + 2];
-                }
+                for (int k = 0; k < KS; ++k)
+                    write_frag<D, E4M3>(a, out, n, k, g, t, st.o[n][k], by);
             }
-        __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == tiles;
-        const float vs = E4M3 && a.vs ? a.vs[h] : 1.f;
-        const long long row_at = seq_at + (long long)row * tiles;   // line index of the row
-        Part<D>* part = parts + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
-        for (int i = tid; i < heads * (D / 4); i += kThreads) {
-            const int head = i / (D / 4), d = i % (D / 4) * 4;
-            float top = -INFINITY, sum_l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][head]);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float k = s_m[w][head] == -INFINITY ? 0.f : ex2(s_m[w][head] - top);
-                const float4 y = *reinterpret_cast<const float4*>(
-                    smem + w * Sh::RING + (head * Sh::OS + d) * 4);
-                sum_l += k * s_l[w][head];
-                v.x += k * y.x;
-                v.y += k * y.y;
-                v.z += k * y.z;
-                v.w += k * y.w;
-            }
+        };
+        constexpr int kStep = 2 * Sh::FRAG * 32;
+        if (warp > 0) {
+            if (!first) bar_sync(2);                     // warp 0 has read the last one
+            send();
+            bar_arrive(1);
+        } else {
+            bar_sync(1);
+            collect();
+            if (!last) bar_arrive(2);
             if (whole) {
-                const float inv = top == -INFINITY ? 0.f : vs / sum_l;
-                const long long out = (long long)s * a.HQ + hq0 + head;
-                *reinterpret_cast<uint2*>(a.o + out * D + d) = make_uint2(
-                    ptx::pack_bf16(v.x * inv, v.y * inv), ptx::pack_bf16(v.z * inv, v.w * inv));
-                if (a.lse && d == 0)
-                    a.lse[out] = top == -INFINITY ? -INFINITY : (top + lg2(sum_l)) * kLn2;
+                write();
             } else {
-                *reinterpret_cast<float4*>(&part->o[head][d]) = v;
-                if (d == 0) {
-                    part->m[head] = top;
-                    part->l[head] = sum_l;
-                }
-            }
-        }
-        if (!whole) {
-            // ---- the row's parts: CTA c0 holds its first tile, c1 its last ----
-            const int c0 = (int)(row_at / per), c1 = (int)((row_at + tiles - 1) / per);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_ticket = atomicAdd(tickets + c0, 1u);
-            __syncthreads();
-            if (s_ticket == (unsigned)(c1 - c0)) {
+                float4* slot = (int)blockIdx.x == c0
+                                   ? slots
+                                   : slots + Sh::FRAG * 32 +
+                                         (long long)((int)blockIdx.x - c0 - 1) * kStep;
+                st.store(slot + lane);
                 __threadfence();
-                if (tid == 0) tickets[c0] = 0;           // as the next call expects it
-                for (int i = tid; i < heads * (D / 4); i += kThreads) {
-                    const int head = i / (D / 4), d = i % (D / 4) * 4;
-                    float top = -INFINITY, sum_l = 0.f;
-                    for (int c = c0; c <= c1; ++c)
-                        top = fmaxf(top, __ldcg(&parts[2 * c + (c == c0)].m[head]));
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const Part<D>* p = parts + 2 * c + (c == c0);
-                        const float pm = __ldcg(&p->m[head]);
-                        const float k = pm == -INFINITY ? 0.f : ex2(pm - top);
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(&p->o[head][d]));
-                        sum_l += k * __ldcg(&p->l[head]);
-                        v.x += k * y.x;
-                        v.y += k * y.y;
-                        v.z += k * y.z;
-                        v.w += k * y.w;
+                __syncwarp();
+                unsigned ticket = 0;
+                if (lane == 0) ticket = atomicAdd(tickets + c0, 1u);
+                ticket = __shfl_sync(0xffffffffu, ticket, 0);
+                if (ticket == (unsigned)(c1 - c0)) {
+                    __threadfence();
+                    if (lane == 0) tickets[c0] = 0;      // as the next call expects it
+                    if (last) {
+                        if (lane == 0) s_last = 1;       // all warps join it below
+                    } else {
+                        // alone, with the sums that the four warps would take
+                        st.clear();
+                        add_parts<1>(st, slots, slots + Sh::FRAG * 32, c1 - c0 + 1, kStep, 0, lane);
+#pragma unroll 1
+                        for (int w = 1; w < kWarps; ++w) {
+                            State<D, E4M3, NH> more;
+                            more.clear();
+                            add_parts<1>(more, slots, slots + Sh::FRAG * 32, c1 - c0 + 1, kStep, w,
+                                         lane);
+                            st.add([&](int i) { return more.frag(i); });
+                        }
+                        write();
                     }
-                    const float inv = top == -INFINITY ? 0.f : vs / sum_l;
-                    const long long out = (long long)s * a.HQ + hq0 + head;
-                    *reinterpret_cast<uint2*>(a.o + out * D + d) = make_uint2(
-                        ptx::pack_bf16(v.x * inv, v.y * inv), ptx::pack_bf16(v.z * inv, v.w * inv));
-                    if (a.lse && d == 0)
-                        a.lse[out] = top == -INFINITY ? -INFINITY : (top + lg2(sum_l)) * kLn2;
                 }
             }
         }
-        __syncthreads();                                 // the join buffers are read
-        at += tile1 - tile0;
+        if (last) {
+            __syncthreads();
+            if (s_last) {
+                st.clear();
+                add_parts<NH == 1 ? 3 : 1>(st, slots, slots + Sh::FRAG * 32, c1 - c0 + 1, kStep,
+                                           warp, lane);
+                if (warp > 0) send();
+                __syncthreads();
+                if (warp == 0) {
+                    collect();
+                    write();
+                }
+            }
+            break;
+        }
+        cur.at = next;
+        enter(cur);
     }
+    cp_async_wait<0>();
 }
 
-// CTAs of a call: two on each SM.  The workspace does not depend on lengths.
-int decode_grid() { return 2 * sm_count(); }
+// The workspace: a counter for each CTA, then two parts for each.
+size_t tickets_bytes() { return align256((size_t)kMostCtas * sm_count() * sizeof(unsigned)); }
 
 template <int D, bool E4M3, int NH>
 kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
@@ -526,21 +668,26 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
             return KDA_ERR_CUDA;
         set[dev] = true;
     }
-    const int HB = (a.G + 8 * NH - 1) / (8 * NH), W = decode_grid();
+    const int HB = (a.G + 8 * NH - 1) / (8 * NH), W = Sh::OCC * sm_count();
     const long long most = (long long)a.S * a.HKV * HB * ((a.cap + 63LL) / 64 + 1);
     TimedLaunch tl("paged_decode", s);
     fn<<<(unsigned)(most < W ? most : W), kThreads, Sh::SMEM, s>>>(
         a, HB, static_cast<unsigned*>(ws),
-        reinterpret_cast<Part<D>*>(static_cast<char*>(ws) + align256(W * sizeof(unsigned))));
+        reinterpret_cast<float4*>(static_cast<char*>(ws) + tickets_bytes()));
     return launch_status();
 }
 
 }  // namespace
 
-size_t paged_decode_ws_bytes(const PagedArgs&, int D, bool) {
-    const size_t W = decode_grid();
-    return align256(W * sizeof(unsigned)) +
-           align256(2 * W * (D == 128 ? sizeof(Part<128>) : sizeof(Part<64>)));
+template <int D, int NH>
+size_t parts_bytes() {
+    const size_t of_cta = 2 * Shape<D, false, NH>::FRAG * 512;   // the same for both cache types
+    return align256(of_cta * (NH == 1 ? kMostCtas : 2) * sm_count());
+}
+
+size_t paged_decode_ws_bytes(const PagedArgs& a, int D, bool) {
+    if (D == 128) return tickets_bytes() + (a.G <= 8 ? parts_bytes<128, 1>() : parts_bytes<128, 2>());
+    return tickets_bytes() + (a.G <= 8 ? parts_bytes<64, 1>() : parts_bytes<64, 2>());
 }
 
 kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s) {

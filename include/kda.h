@@ -339,9 +339,8 @@ kda_status kda_paged_append(const kda_paged_dims* dims, const int* cu_seqlens, i
 /* Attention of one new token per sequence: q, o [S][HQ][D] (q rows q_stride
  * elements apart, o dense), lse float [S][HQ] or NULL; the query stands at
  * position kv_lens[s] - 1 (its own key and value already appended).  The
- * workspace's size does not depend on S, lengths or the table.  It must be
- * all zeros before its first use; every call leaves it fit for the next one,
- * of any sizes.  Calls that may overlap need one each. */
+ * workspace's size depends on D and HQ / HKV alone.  It must be all zeros
+ * before its first use; every call leaves it fit for the next one.  Calls that may overlap need one each. */
 size_t kda_paged_decode_workspace_bytes(const kda_paged_dims* dims);
 kda_status kda_paged_decode(const kda_paged_dims* dims, const void* q, long long q_stride,
                             const void* k_pages, const void* v_pages, const float* k_scale,

@@ -44,6 +44,7 @@ using namespace paged;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGroup = 16;                 // tokens of a warp's step
+constexpr int kRowEnd = 3;                 // tiles that the end of a row counts for
 
 __device__ __forceinline__ void record() { atomicCAS(&g_paged_decode_error, 0, (int)KDA_ERR_SHAPE); }
 
@@ -54,6 +55,8 @@ struct Span {
     int nsink, first, n;     // groups of sinks; first group of the window; groups in all
     __device__ __forceinline__ int group(int i) const { return i < nsink ? i : i - nsink + first; }
     __device__ __forceinline__ int tiles() const { return max(1, (n + kWarps - 1) / kWarps); }
+    // a row's length in the line of tiles: its end costs time too
+    __device__ __forceinline__ int slots() const { return tiles() + kRowEnd; }
 };
 __device__ __forceinline__ Span make_span(const PagedArgs& a, int len) {
     Span s;
@@ -242,7 +245,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     const int per_thread = (a.S + kThreads - 1) / kThreads;
     const int s_lo = min(a.S, tid * per_thread), s_hi = min(a.S, s_lo + per_thread);
     long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) mine += make_span(a, seq_len(a, s)).tiles();
+    for (int s = s_lo; s < s_hi; ++s) mine += make_span(a, seq_len(a, s)).slots();
     long long sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -267,7 +270,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         long long at = before;                           // the sequence that holds `begin`
         int s = s_lo;
         for (;; ++s) {
-            const long long n = (long long)make_span(a, seq_len(a, s)).tiles() * rows;
+            const long long n = (long long)make_span(a, seq_len(a, s)).slots() * rows;
             if (begin < at + n) break;
             at += n;
         }
@@ -282,33 +285,47 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     // A stretch's piece of one row, as the warp sees it.
     struct Piece {
         int s, row, tile0, tile1, tiles;
-        long long seq_at, at;                            // line index of its sequence, of itself
+        long long seq_at, at, next;                      // line index of its sequence, of itself,
+                                                         // of what follows
         Span sp;
         int g0, steps;                                   // the warp's first group, groups
     };
-    auto enter = [&](Piece& p) {                         // p.s, p.seq_at, p.at are set
-        p.sp = make_span(a, seq_len(a, p.s));
-        while (p.at >= p.seq_at + (long long)p.sp.tiles() * rows) {
-            p.seq_at += (long long)p.sp.tiles() * rows;
-            p.sp = make_span(a, seq_len(a, ++p.s));
+    // p.s, p.seq_at, p.at are set; whether a piece begins there (or after the
+    // end of a row that reaches into the stretch)
+    auto enter = [&](Piece& p) {
+        int len;
+        for (;;) {
+            if (p.at >= end) return false;
+            p.sp = make_span(a, seq_len(a, p.s));
+            len = p.sp.slots();
+            while (p.at >= p.seq_at + (long long)len * rows) {
+                p.seq_at += (long long)len * rows;
+                p.sp = make_span(a, seq_len(a, ++p.s));
+                len = p.sp.slots();
+            }
+            p.tiles = p.sp.tiles();
+            p.row = (int)((p.at - p.seq_at) / len);
+            p.tile0 = (int)((p.at - p.seq_at) % len);
+            if (p.tile0 < p.tiles) break;
+            p.at += len - p.tile0;                       // the row's last tiles were before
         }
-        p.tiles = p.sp.tiles();
-        p.row = (int)((p.at - p.seq_at) / p.tiles);
-        p.tile0 = (int)((p.at - p.seq_at) % p.tiles);
         p.tile1 = (int)min((long long)p.tiles, p.tile0 + (end - p.at));
+        p.next = p.at + (p.tile1 == p.tiles ? len - p.tile0 : p.tile1 - p.tile0);
         p.g0 = p.tile0 * kWarps + warp;
         const int g1 = min(p.sp.n, p.tile1 * kWarps);
         p.steps = p.g0 < g1 ? (g1 - p.g0 + kWarps - 1) / kWarps : 0;
+        return true;
     };
     Piece in;                                            // being loaded
     in.s = s_seq;
     in.seq_at = s_at;
     in.at = begin;
-    enter(in);
+    if (!enter(in)) return;
     Piece cur = in;                                      // being worked on
 
     // ---- loads: one step of the warp, or nothing, is one group of copies ----
     int in_step = 0, in_stage = 0;
+    bool more = true;
     auto page_of = [&]() {
         return in_step < in.steps
                    ? __ldg(a.table + (size_t)in.s * a.max_pages +
@@ -317,13 +334,14 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     };
     int page = page_of();
     auto issue = [&]() {
-        while (in_step >= in.steps && in.at + (in.tile1 - in.tile0) < end) {
-            in.at += in.tile1 - in.tile0;
-            enter(in);
+        while (in_step >= in.steps && more) {
+            in.at = in.next;
+            more = enter(in);
+            if (!more) break;
             in_step = 0;
             page = page_of();
         }
-        if (in_step < in.steps) {
+        if (more && in_step < in.steps) {
             const int grp = in.sp.group(in.g0 + in_step * kWarps), j0 = grp * kGroup;
             const bool good = (unsigned)page < (unsigned)a.num_pages;
             if (!good) record();
@@ -564,12 +582,14 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         }
 
         // ---- the end of the piece: warp 0 collects ----
-        const long long next = cur.at + (cur.tile1 - cur.tile0);
-        const bool last = next >= end, whole = cur.tile0 == 0 && cur.tile1 == cur.tiles;
-        const long long row_at = cur.seq_at + (long long)cur.row * cur.tiles;
+        const bool whole = cur.tile0 == 0 && cur.tile1 == cur.tiles;
+        const long long row_at = cur.seq_at + (long long)cur.row * cur.sp.slots();
         const int c0 = (int)(row_at / per), c1 = (int)((row_at + cur.tiles - 1) / per);
         // the parts of the row: CTA c0 leaves its own in its second slot, the others in their
         // first
+        Piece then = cur;
+        then.at = cur.next;
+        const bool last = !enter(then);
         float4* slots = parts + (2LL * c0 + 1) * (Sh::FRAG * 32);
         auto send = [&]() { st.store(mail + (warp - 1) * (Sh::FRAG * 32)); };
         auto collect = [&]() {
@@ -646,8 +666,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
             }
             break;
         }
-        cur.at = next;
-        enter(cur);
+        cur = then;
     }
     cp_async_wait<0>();
 }

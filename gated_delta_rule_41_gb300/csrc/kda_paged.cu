@@ -1,7 +1,9 @@
 // Paged key-value cache: appending tokens.
 #include <cuda_fp8.h>
 
-#include "kda_common.cuh"
+#include <algorithm>
+
+#include "kda_paged.cuh"
 #include "kda_timing.cuh"
 
 namespace kda {
@@ -11,27 +13,6 @@ __device__ int g_paged_error = 0;   // a kda_status
 namespace {
 
 __device__ __forceinline__ void record() { atomicCAS(&g_paged_error, 0, (int)KDA_ERR_SHAPE); }
-
-// The sequence that owns packed token t, or -1 if cu does not rise from 0 to T
-// or t lies outside.  All lanes of a warp call it with the same t.
-__device__ __forceinline__ int find_seq(const int* __restrict__ cu, int S, int T, int t) {
-    const int lane = threadIdx.x & 31;
-    bool bad = lane == 0 && (cu[0] != 0 || cu[S] != T);
-    int at = -1;
-    for (int i = lane; i < S; i += 32) {
-        const int a = cu[i], b = cu[i + 1];
-        bad |= a > b || a < 0;
-        if (a <= t && t < b) at = i;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) at = max(at, __shfl_xor_sync(0xffffffffu, at, o));
-    if (bad) {
-        if (lane == 0) record();
-        return -1;
-    }
-    return at;
-}
 
 __device__ __forceinline__ int seq_len(const PagedArgs& a, int s) {
     const int len = a.lens[s];
@@ -57,37 +38,105 @@ __device__ __forceinline__ uint2 quant8(const uint4 v, float inv) {
     return r;
 }
 
-// One warp per (token, key head) row pair; D / 8 lanes hold eight elements each
-// of K, then of V.
+// A pass of copies bounded by HBM: T (HKV D) (2 + code) bytes each of K and V.
+// A CTA takes TB tokens, whole rows of K and V, as items of eight elements.
+// Its first items are on their way before the tokens' places are looked up
+// (sequence, length, table entry: three dependent reads), so that the copies do
+// not wait for them.
+constexpr int kAppendThreads = 256, kAppendItems = 8;   // of a thread at a time
+constexpr int kAppendTokens = 64;                       // of a CTA, at most
+
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(256)
-append_kernel(const PagedArgs a, const __nv_bfloat16* __restrict__ k, long long k_stride,
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, long long k_stride,
               const __nv_bfloat16* __restrict__ v, long long v_stride) {
-    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int t = w / a.HKV, h = w % a.HKV;
-    if (t >= a.T) return;
-    const int s = a.cu ? find_seq(a.cu, a.S, a.T, t) : t;
-    if (s < 0) return;
-    const int pos = seq_len(a, s) - (a.cu ? a.cu[s + 1] - t : 1);
-    if (pos < 0) return;
-    const int page = a.table[(size_t)s * a.max_pages + (pos >> a.page_shift)];
-    if ((unsigned)page >= (unsigned)a.num_pages) {
-        record();
-        return;
+    __shared__ int s_seq[kAppendTokens];
+    __shared__ long long s_off[kAppendTokens];          // element of the token's row, or -1
+    const int tid = threadIdx.x, t0 = blockIdx.x * TB, n = min(TB, a.T - t0);
+    const int row = a.HKV * (D / 8), per = 2 * row;     // items of a row of K, of a token
+    const int items = n * per;
+
+    uint4 x[kAppendItems];
+    int tok[kAppendItems], at[kAppendItems];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < kAppendItems; ++i) {
+            const int it = base + tid + i * kAppendThreads;
+            tok[i] = -1;
+            if (it >= items) continue;
+            tok[i] = it / per;
+            at[i] = it - tok[i] * per;
+            const long long t = t0 + tok[i];
+            x[i] = __ldcs(reinterpret_cast<const uint4*>(
+                at[i] < row ? k + t * k_stride + 8LL * at[i]
+                            : v + t * v_stride + 8LL * (at[i] - row)));
+        }
+    };
+    load(0);
+
+    if (a.cu) {
+        // who owns the tokens; cu must rise from 0 to T
+        bool bad = tid == 0 && (a.cu[0] != 0 || a.cu[a.S] != a.T);
+        for (int i = tid; i < a.S; i += kAppendThreads) {
+            const int lo = a.cu[i], hi = a.cu[i + 1];
+            bad |= lo < 0 || lo > hi || hi > a.T;
+            if (bad) break;
+            for (int t = max(lo, t0); t < min(hi, t0 + n); ++t) s_seq[t - t0] = i;
+        }
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) record();
+            return;
+        }
     }
-    const long long off = page * a.page_stride +
-                          (pos & ((1 << a.page_shift) - 1)) * a.token_stride + h * a.head_stride;
-    const int which = lane / (D / 8), c = lane % (D / 8) * 8;
-    if (which > 1) return;
-    const __nv_bfloat16* src = (which ? v + t * v_stride : k + t * k_stride) + (long long)h * D + c;
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
-    char* pool = static_cast<char*>(const_cast<void*>(which ? a.vp : a.kp));
-    if (E4M3) {
-        const float* sc = which ? a.vs : a.ks;
-        *reinterpret_cast<uint2*>(pool + off + c) = quant8(x, sc ? 1.0f / sc[h] : 1.0f);
-    } else {
-        *reinterpret_cast<uint4*>(pool + 2 * (off + c)) = x;
+    if (tid < n) {
+        const int t = t0 + tid, s = a.cu ? s_seq[tid] : t;
+        const int pos = seq_len(a, s) - (a.cu ? a.cu[s + 1] - t : 1);
+        long long off = -1;                             // before the sequence's start: dropped
+        if (pos >= 0) {
+            const int page = a.table[(size_t)s * a.max_pages + (pos >> a.page_shift)];
+            if ((unsigned)page < (unsigned)a.num_pages)
+                off = page * a.page_stride + (pos & ((1 << a.page_shift) - 1)) * a.token_stride;
+            else
+                record();
+        }
+        s_off[tid] = off;
     }
+    __syncthreads();
+
+    for (int base = 0;;) {
+#pragma unroll
+        for (int i = 0; i < kAppendItems; ++i) {
+            if (tok[i] < 0 || s_off[tok[i]] < 0) continue;
+            const bool of_v = at[i] >= row;
+            const int c = of_v ? at[i] - row : at[i], h = c / (D / 8);
+            const long long e = s_off[tok[i]] + h * a.head_stride + c % (D / 8) * 8;
+            char* pool = static_cast<char*>(const_cast<void*>(of_v ? a.vp : a.kp));
+            if (E4M3) {
+                const float* sc = of_v ? a.vs : a.ks;
+                *reinterpret_cast<uint2*>(pool + e) = quant8(x[i], sc ? 1.0f / sc[h] : 1.0f);
+            } else {
+                *reinterpret_cast<uint4*>(pool + 2 * e) = x[i];
+            }
+        }
+        base += kAppendThreads * kAppendItems;
+        if (base >= items) break;
+        load(base);
+    }
+}
+
+template <int D, bool E4M3>
+kda_status append(const PagedArgs& a, const void* k, long long k_stride, const void* v,
+                  long long v_stride, cudaStream_t s) {
+    // tokens of a CTA: its threads' items, but fewer while CTAs are few
+    const int per = 2 * a.HKV * (D / 8);
+    const int full = std::min(kAppendTokens,
+                              std::max(1, kAppendThreads * kAppendItems / per));
+    const int TB = std::max(1, std::min(full, a.T / (2 * paged::sm_count())));
+    TimedLaunch tl("paged_append", s);
+    append_kernel<D, E4M3><<<(unsigned)((a.T + TB - 1) / TB), kAppendThreads, 0, s>>>(
+        a, TB, static_cast<const __nv_bfloat16*>(k), k_stride,
+        static_cast<const __nv_bfloat16*>(v), v_stride);
+    return launch_status();
 }
 
 }  // namespace
@@ -95,19 +144,11 @@ append_kernel(const PagedArgs a, const __nv_bfloat16* __restrict__ k, long long 
 kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void* k,
                                long long k_stride, const void* v, long long v_stride,
                                cudaStream_t s) {
-    TimedLaunch tl("paged_append", s);
-    const unsigned grid = (unsigned)(((long long)a.T * a.HKV + 7) / 8);
-    auto* kk = static_cast<const __nv_bfloat16*>(k);
-    auto* vv = static_cast<const __nv_bfloat16*>(v);
-    if (D == 128 && e4m3)
-        append_kernel<128, true><<<grid, 256, 0, s>>>(a, kk, k_stride, vv, v_stride);
-    else if (D == 128)
-        append_kernel<128, false><<<grid, 256, 0, s>>>(a, kk, k_stride, vv, v_stride);
-    else if (e4m3)
-        append_kernel<64, true><<<grid, 256, 0, s>>>(a, kk, k_stride, vv, v_stride);
-    else
-        append_kernel<64, false><<<grid, 256, 0, s>>>(a, kk, k_stride, vv, v_stride);
-    return launch_status();
+    if (D == 128)
+        return e4m3 ? append<128, true>(a, k, k_stride, v, v_stride, s)
+                    : append<128, false>(a, k, k_stride, v, v_stride, s);
+    return e4m3 ? append<64, true>(a, k, k_stride, v, v_stride, s)
+                : append<64, false>(a, k, k_stride, v, v_stride, s);
 }
 
 kda_status paged_take_error(cudaStream_t s) {

@@ -45,6 +45,7 @@ __device__ __forceinline__ uint2 quant8(const uint4 v, float inv) {
 // not wait for them.
 constexpr int kAppendThreads = 256, kAppendItems = 8;   // of a thread at a time
 constexpr int kAppendTokens = 64;                       // of a CTA, at most
+constexpr int kAppendHeads = 128;                       // whose inverse scales are kept
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads)
@@ -52,28 +53,41 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
               const __nv_bfloat16* __restrict__ v, long long v_stride) {
     __shared__ int s_seq[kAppendTokens];
     __shared__ long long s_off[kAppendTokens];          // element of the token's row, or -1
+    __shared__ float s_inv[2 * kAppendHeads];           // 1 / scale of K, V per head
     const int tid = threadIdx.x, t0 = blockIdx.x * TB, n = min(TB, a.T - t0);
     const int row = a.HKV * (D / 8), per = 2 * row;     // items of a row of K, of a token
-    const int items = n * per;
 
-    uint4 x[kAppendItems];
-    int tok[kAppendItems], at[kAppendItems];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int i = 0; i < kAppendItems; ++i) {
-            const int it = base + tid + i * kAppendThreads;
-            tok[i] = -1;
-            if (it >= items) continue;
-            tok[i] = it / per;
-            at[i] = it - tok[i] * per;
-            const long long t = t0 + tok[i];
-            x[i] = __ldcs(reinterpret_cast<const uint4*>(
-                at[i] < row ? k + t * k_stride + 8LL * at[i]
-                            : v + t * v_stride + 8LL * (at[i] - row)));
+    // A thread's items lie kAppendThreads apart: (token, item of it), stepped
+    // without a division.
+    const int step_tok = kAppendThreads / per, step_at = kAppendThreads % per;
+    auto step = [&](int& tok, int& at) {
+        tok += step_tok;
+        at += step_at;
+        if (at >= per) {
+            at -= per;
+            ++tok;
         }
     };
-    load(0);
+    uint4 x[kAppendItems];
+    int tok0 = tid / per, at0 = tid % per;              // of the thread's first item of a round
+    auto load = [&]() {
+        int tok = tok0, at = at0;
+#pragma unroll
+        for (int i = 0; i < kAppendItems; ++i, step(tok, at)) {
+            if (tok >= n) continue;
+            const long long t = t0 + tok;
+            x[i] = __ldcs(reinterpret_cast<const uint4*>(
+                at < row ? k + t * k_stride + 8LL * at : v + t * v_stride + 8LL * (at - row)));
+        }
+    };
+    load();
 
+    if (E4M3) {
+        for (int i = tid; i < 2 * min(a.HKV, kAppendHeads); i += kAppendThreads) {
+            const float* sc = i & 1 ? a.vs : a.ks;
+            s_inv[i] = sc ? 1.0f / sc[i >> 1] : 1.0f;
+        }
+    }
     if (a.cu) {
         // who owns the tokens; cu must rise from 0 to T
         bool bad = tid == 0 && (a.cu[0] != 0 || a.cu[a.S] != a.T);
@@ -103,24 +117,32 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
     }
     __syncthreads();
 
-    for (int base = 0;;) {
+    for (;;) {
+        int tok = tok0, at = at0;
 #pragma unroll
-        for (int i = 0; i < kAppendItems; ++i) {
-            if (tok[i] < 0 || s_off[tok[i]] < 0) continue;
-            const bool of_v = at[i] >= row;
-            const int c = of_v ? at[i] - row : at[i], h = c / (D / 8);
-            const long long e = s_off[tok[i]] + h * a.head_stride + c % (D / 8) * 8;
+        for (int i = 0; i < kAppendItems; ++i, step(tok, at)) {
+            if (tok >= n || s_off[tok] < 0) continue;
+            const bool of_v = at >= row;
+            const int c = of_v ? at - row : at, h = c / (D / 8);
+            const long long e = s_off[tok] + h * a.head_stride + c % (D / 8) * 8;
             char* pool = static_cast<char*>(const_cast<void*>(of_v ? a.vp : a.kp));
             if (E4M3) {
-                const float* sc = of_v ? a.vs : a.ks;
-                *reinterpret_cast<uint2*>(pool + e) = quant8(x[i], sc ? 1.0f / sc[h] : 1.0f);
+                float inv;
+                if (h < kAppendHeads) {
+                    inv = s_inv[2 * h + of_v];
+                } else {
+                    const float* sc = of_v ? a.vs : a.ks;
+                    inv = sc ? 1.0f / sc[h] : 1.0f;
+                }
+                *reinterpret_cast<uint2*>(pool + e) = quant8(x[i], inv);
             } else {
                 *reinterpret_cast<uint4*>(pool + 2 * e) = x[i];
             }
         }
-        base += kAppendThreads * kAppendItems;
-        if (base >= items) break;
-        load(base);
+        tok0 = tok;
+        at0 = at;
+        if (!__syncthreads_or(tok0 < n)) break;
+        load();
     }
 }
 

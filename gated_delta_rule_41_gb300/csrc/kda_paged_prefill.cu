@@ -56,7 +56,7 @@ using namespace paged;
 
 constexpr int kTile = 128;                  // query rows and cached tokens of a tile
 constexpr int kThreads = 512;                // four warpgroups of 128 registers a thread, dealt
-constexpr int kRegsSoftmax = 152, kRegsIssue = 88, kRegsConvert = 120;   // out again as
+constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;   // out again as
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
 constexpr float kMost = 4096.f;             // sum of a tile's weights that moves the reference
@@ -598,7 +598,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int x = warp >> 2, r = tid & 127;
         const int i = i0 + x * TB + r / a.G;
         const bool live = r < TB * a.G && i < nq;
-        const int p = live ? len - nq + i : -1;              // a dead row sees nothing
+        const int p = min(len - nq + i, len - 1);            // (a dead row goes along)
         float f = a.scale * kLog2e;
         const int px = p0 + x * TB;                          // positions of the tile's rows
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -652,14 +652,53 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (!ok) break;
             tc_fence_after();
             // every row of the tile sees all of it?
-            const bool all = j0 + kTile - 1 <= px && (a.window == 0 || j0 > px + TB - 1 - a.window);
-            const bool edge = __any_sync(0xffffffffu, !all || !live);
+            const bool edge = !(j0 + kTile - 1 <= px &&
+                                (a.window == 0 || j0 > px + TB - 1 - a.window));
             // Half a tile at a time: weights exp2(f S - m) against the reference m
-            // as it stands.  A row that has none yet, or whose weights add up to
-            // more than kMost, takes its largest logit for it, and the half is weighed
-            // (again).  S stays in TMEM until the weights hold.
+            // as it stands, if that is all there is to do.
+            auto weigh = [&](float (&v)[2][32], uint32_t (&w)[2][16]) {
+                const float add = m == -INFINITY ? 0.f : -m;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        fma2(v[c][2 * e], v[c][2 * e + 1], f, add);
+                        const float w0 = ex2(v[c][2 * e]), w1 = ex2(v[c][2 * e + 1]);
+                        add2(part[2 * (e & 1)], part[2 * (e & 1) + 1], w0, w1);
+                        w[c][e] = pack_f16(w0, w1);
+                    }
+                return (part[0] + part[1]) + (part[2] + part[3]);
+            };
+            auto hand_over = [&](int e2, const uint32_t (&w)[2][16]) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) tmem_st16_nw(ts + 32 * e2 + 16 * c, w[c]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[2 * x + e2]);
+            };
+            int e2 = 0;
+            if (!edge && Ev == E && !__any_sync(0xffffffffu, m == -INFINITY)) {
+                float v[2][2][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32_nw(ts + 32 * c, v[c >> 1][c & 1]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_wait_ld_dep(v[c >> 1][c & 1]);
+#pragma unroll
+                for (int i2 = 0; i2 < 2; ++i2) {
+                    uint32_t w[2][16];
+                    const float sum = weigh(v[i2], w);
+                    if (__any_sync(0xffffffffu, sum > kMost)) break;
+                    l += sum;
+                    hand_over(i2, w);
+                    ++e2;
+                }
+            }
+            // Else a row that has no reference yet, or whose weights add up to
+            // more than kMost, takes its largest logit for it, and the half is
+            // weighed (again).  S stays in TMEM until the weights hold.
 #pragma unroll 1
-            for (int e2 = 0; e2 < 2; ++e2) {
+            for (; e2 < 2; ++e2) {
                 float sum, keep = 1.f;
                 uint32_t w[2][16];
                 bool want = m == -INFINITY;
@@ -699,18 +738,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             m = top;
                         }
                     }
-                    const float add = m == -INFINITY ? 0.f : -m;
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            fma2(v[c][2 * e], v[c][2 * e + 1], f, add);
-                            const float w0 = ex2(v[c][2 * e]), w1 = ex2(v[c][2 * e + 1]);
-                            add2(part[2 * (e & 1)], part[2 * (e & 1) + 1], w0, w1);
-                            w[c][e] = pack_f16(w0, w1);
-                        }
-                    sum = (part[0] + part[1]) + (part[2] + part[3]);
+                    sum = weigh(v, w);
                     want = sum > kMost;
                     look = __any_sync(0xffffffffu, want);
                 } while (__builtin_expect(look, 0));
@@ -735,11 +763,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         tmem_st32_nw(to + 32 * c, o);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) tmem_st16_nw(ts + 32 * e2 + 16 * c, w[c]);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&p_full[2 * x + e2]);
+                hand_over(e2, w);
             }
         }
         // ---- output ----

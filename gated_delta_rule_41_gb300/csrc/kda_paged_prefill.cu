@@ -546,14 +546,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int rows = valid - t / 8;              // 16 (i mod 8) < rows: in the sequence
                 // the tile's largest |v|, by the bits of pairs
                 uint32_t top = 0;
-#pragma unroll 4
+                auto larger = [&](uint32_t w) {
+                    const __nv_bfloat162 z = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+                    top = *reinterpret_cast<const uint32_t*>(&z);
+                };
+#pragma unroll 8
                 for (int i = 0; i < L; ++i) {
                     const uint4 y = *reinterpret_cast<const uint4*>(mine + i * 2048);
                     if (16 * (i & 7) < rows) {
-                        top = __vmaxu2(top, y.x & 0x7fff7fffu);
-                        top = __vmaxu2(top, y.y & 0x7fff7fffu);
-                        top = __vmaxu2(top, y.z & 0x7fff7fffu);
-                        top = __vmaxu2(top, y.w & 0x7fff7fffu);
+                        larger(y.x);
+                        larger(y.y);
+                        larger(y.z);
+                        larger(y.w);
                     }
                 }
                 top = max(top & 0xffffu, top >> 16);         // a bf16 without its sign
@@ -574,7 +579,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 const float down = pow2any(-E);
                 if (!ok) continue;
-#pragma unroll 4
+#pragma unroll 8
                 for (int i = 0; i < L; ++i) {
                     uint4 y = *reinterpret_cast<const uint4*>(mine + i * 2048);
                     uint32_t* w = reinterpret_cast<uint32_t*>(&y);

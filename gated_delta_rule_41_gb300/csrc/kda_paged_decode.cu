@@ -269,7 +269,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     if (mine > 0 && before <= begin && begin < before + mine * rows) {
         long long at = before;                           // the sequence that holds `begin`
         int s = s_lo;
-        for (;; ++s) {
+        for (; s + 1 < s_hi; ++s) {
             const long long n = (long long)make_span(a, seq_len(a, s)).slots() * rows;
             if (begin < at + n) break;
             at += n;
@@ -298,7 +298,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
             if (p.at >= end) return false;
             p.sp = make_span(a, seq_len(a, p.s));
             len = p.sp.slots();
-            while (p.at >= p.seq_at + (long long)len * rows) {
+            while (p.at >= p.seq_at + (long long)len * rows && p.s + 1 < a.S) {
                 p.seq_at += (long long)len * rows;
                 p.sp = make_span(a, seq_len(a, ++p.s));
                 len = p.sp.slots();

@@ -15,8 +15,8 @@
 //
 // Softmax.  The weights of a tile are taken against a reference m of the row,
 // the largest logit of its first half tile; only when the weights of a half
-// tile add up to more than 4096 is m moved to its largest logit, O and the sum
-// rescaled and the half weighed again.  So as a rule no maximum is taken at
+// tile add up to more than 4096 is a larger logit looked for, m moved to it, O
+// and the sum rescaled and the half weighed again.  So as a rule no maximum is taken at
 // all, and weights stay far inside the range of fp16.  Sums are fp32.  P enters the product with V in fp16, which rounds a weight by
 // up to 2^-11, a small part of the output's own rounding (2^-8), at the rate of a bf16 one
 // (which alone would round weights by as much as the output).
@@ -59,7 +59,8 @@ constexpr int kThreads = 512;                // four warpgroups of 128 registers
 constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;   // out again as
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
-constexpr float kMost = 4096.f;             // sum of a tile's weights that moves the reference
+constexpr float kMost = 4096.f;             // sum of half a tile's weights that calls for a look
+constexpr float kRaise = 8.f;               // log2 of the weight that then moves the reference
 
 __device__ __forceinline__ void record(kda_status code) {
     atomicCAS(&g_paged_prefill_error, 0, (int)code);
@@ -306,7 +307,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int item = total - 1 - (int)(blockIdx.x / a.HKV);
         if (item >= before && item < before + mine) {
             int s = lo, at = before;
-            for (;; ++s) {
+            for (; s + 1 < hi; ++s) {
                 const int n = (a.cu[s + 1] - a.cu[s] + 2 * TB - 1) / (2 * TB);
                 if (item < at + n) break;
                 at += n;
@@ -568,7 +569,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 bool again = any_convert(top >= most);
                 if (n == 0) again = !any_convert(top >= 0x3f80u) || again;
                 if (__builtin_expect(again, 0)) {
-                    atomicMax(v_top, (int)top);
+                    // of the finite ones (infinities stay what they are)
+                    uint32_t big = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 4 * L; ++i) {
+                        if (16 * ((i >> 2) & 7) >= rows) continue;
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                            mine + (i >> 2) * 2048 + (i & 3) * 4);
+                        const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
+                        if (lo < 0x7f80u) big = max(big, lo);
+                        if (hi < 0x7f80u) big = max(big, hi);
+                    }
+                    atomicMax(v_top, (int)big);
                     any_convert(false);
                     const int bits = *reinterpret_cast<volatile int*>(v_top);
                     const int want = bits == 0 ? -100 : (bits >> 7) - 127 - 8;
@@ -661,8 +673,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 (a.window == 0 || j0 > px + TB - 1 - a.window));
             // Half a tile at a time: weights exp2(f S - m) against the reference m
             // as it stands, if that is all there is to do.
-            auto weigh = [&](float (&v)[2][32], uint32_t (&w)[2][16]) {
-                const float add = m == -INFINITY ? 0.f : -m;
+            auto weigh = [&](float (&v)[2][32], uint32_t (&w)[2][16], float add) {
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -692,29 +703,30 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int i2 = 0; i2 < 2; ++i2) {
                     uint32_t w[2][16];
-                    const float sum = weigh(v[i2], w);
+                    const float sum = weigh(v[i2], w, -m);
                     if (__any_sync(0xffffffffu, sum > kMost)) break;
                     l += sum;
                     hand_over(i2, w);
                     ++e2;
                 }
             }
-            // Else a row that has no reference yet, or whose weights add up to
-            // more than kMost, takes its largest logit for it, and the half is
-            // weighed (again).  S stays in TMEM until the weights hold.
+            // Else, at the second round at the latest, every row looks at its
+            // largest logit, and takes it for reference if it has none or
+            // lies more than kRaise below it; S stays in TMEM until then.  (Against
+            // a reference taken here the exponents are differences of logits, so that the
+            // largest weight is 1 for logits of any size.)
 #pragma unroll 1
             for (; e2 < 2; ++e2) {
                 float sum, keep = 1.f;
                 uint32_t w[2][16];
-                bool want = m == -INFINITY;
-                bool look = __any_sync(0xffffffffu, want);
-                do {
+                bool look = __any_sync(0xffffffffu, m == -INFINITY);
+                for (;;) {
                     float v[2][32];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_ld32_nw(ts + 64 * e2 + 32 * c, v[c]);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_wait_ld_dep(v[c]);
-                    if (__builtin_expect(edge, 0)) {
+                    if (edge) {
                         const int hi = p + 1 - j0 - 64 * e2;
                         const int lo = a.window ? p - a.window + 1 - j0 - 64 * e2 : 0;
                         const int sk = a.sinks - j0 - 64 * e2;
@@ -728,7 +740,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 if (!(seen >> e & 1)) v[c][e] = none;
                         }
                     }
-                    if (__builtin_expect(look, 0)) {
+                    float add = m == -INFINITY ? 0.f : -m;
+                    if (look) {
                         float hi = v[0][0], lo = v[0][0];
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
@@ -737,16 +750,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 hi = max3(hi, v[c][e], v[c][e + 1]);
                                 lo = min3(lo, v[c][e], v[c][e + 1]);
                             }
-                        const float top = (f < 0.f ? lo : hi) * f;
-                        if (want && top > -INFINITY) {
-                            keep = m == -INFINITY ? 0.f : keep * ex2(m - top);
+                        const float s_top = f < 0.f ? lo : hi, top = s_top * f;
+                        float sub = 0.f;
+                        if (m == -INFINITY ? top > -INFINITY : top - m > kRaise) {
+                            keep = m == -INFINITY ? 0.f : ex2(m - top);
                             m = top;
+                            sub = -s_top;
+                            add = 0.f;
                         }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                add2(v[c][e], v[c][e + 1], sub, sub);
                     }
-                    sum = weigh(v, w);
-                    want = sum > kMost;
-                    look = __any_sync(0xffffffffu, want);
-                } while (__builtin_expect(look, 0));
+                    sum = weigh(v, w, add);
+                    if (look) break;
+                    look = __any_sync(0xffffffffu, sum > kMost);
+                    if (!look) break;
+                }
                 l = l * keep + sum;
                 if (__builtin_expect(Ev != E, 0)) {
                     keep *= pow2any(E - Ev);

@@ -294,8 +294,13 @@ kda_status kda_chunk_fwd_noalloc(const kda_dims* dims, const void* q, const void
  *               lse = log sum_j exp(scale q . k_j)      over the visible j;
  *           a query that sees no token gets o = 0 and lse = -inf.  Products
  *           accumulate in fp32 and the softmax statistics are fp32; the
- *           weights enter the product with V in bf16 (with an e4m3 cache in
- *           fp16, with q scaled per head by a power of two to fit it).
+ *           weights enter the product with V in two bf16 terms (decode) or in
+ *           fp16 (prompts, and both with an e4m3 cache, where q is scaled by a
+ *           power of two to fit fp16 too).  For prompts V goes to fp16 with a
+ *           power of two shared by the tokens that a block of query rows
+ *           reads: values below 2^-33 of the largest finite |v| among them lose
+ *           bits.  V of a token should be finite: an infinity or NaN also reaches,
+ *           in its channel, prompt queries up to 127 tokens before it.
  * Types     q, o and new keys and values are bf16, lse float32.
  * Sizes     D 64 or 128; page_size 16, 32, 64, 128 or 256; HQ a multiple of
  *           HKV with at most 64 query heads per key head; at most 65535

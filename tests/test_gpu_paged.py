@@ -392,3 +392,86 @@ def test_refusals():
     assert status(lambda: kda.paged_append(pages, q[:1, :2], q[:1, :2], t, n)) == 2
     assert kda.paged_prefill(q[:0], pages, t, n, cu).shape == (0, 4, 64)
     kda.check()
+
+
+# ---- values of any size, repeats ----
+
+@pytest.mark.parametrize("case", ["tiny", "huge", "zeros_first", "outliers", "infinite"])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_values_of_any_size(prefill, case):
+    """V scaled as a whole, a first tile of zeros, a few tokens a million times
+    larger than the others, and infinities that only later queries see."""
+    lens, qn = [700], [300]
+    c = make_cache(lens, 32, 2, 128, BF16, 40)
+    page = lambda j: c["table"][0, j // 32].item()
+    if case == "tiny":
+        c["v"].mul_(2.0 ** -60)
+    elif case == "huge":
+        c["v"].mul_(2.0 ** 60)
+    elif case == "zeros_first":
+        for j in range(0, 160, 32):
+            c["v"][page(j)] = 0
+    elif case == "outliers":
+        for j in (130, 450, 690):
+            c["v"][page(j), j % 32] *= 2.0 ** 20
+    else:
+        c["v"][page(650), 650 % 32, :, 3] = math.inf
+    if prefill:
+        q = rand_q(300, 4, 128, 41)
+        cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+        o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], cu, return_lse=True)
+        ref = ref_prefill(q, c, qn, 128 ** -0.5)
+    else:
+        q = rand_q(1, 4, 128, 41)
+        o, lse = kda.paged_decode(q, kv(c), c["table"], c["lens"], return_lse=True)
+        ref = ref_decode(q, c, 128 ** -0.5)
+    kda.check()
+    if case == "infinite":
+        # queries behind the infinity, and the other channels, are as ever
+        other = [d for d in range(128) if d != 3]
+        sees = torch.tensor([j >= 650 for j in range(400, 700)] if prefill else [True])
+        assert not torch.isfinite(o[sees.cuda()][..., 3]).any()
+        keep = ~sees
+        ref = [x[..., other] if x.dim() == 3 else x for x in ref]
+        check_attention(o[..., other][keep.cuda()], lse[keep.cuda()], [x[keep] for x in ref])
+    else:
+        check_attention(o, lse, ref)
+
+
+@pytest.mark.parametrize("amp", [1e8, 1e16, 1e25, 1e37])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_logits_beyond_single_precision(amp, dtype):
+    """Logits so large that their rounding errors exceed any weight: the calls
+    end, and every output is a mean of values."""
+    c = make_cache([400, 200], 32, 1, 128, dtype, 47)
+    q = rand_q(300, 5, 128, 48, amp)
+    cu = torch.tensor([0, 200, 300], dtype=torch.int32, device="cuda")
+    o, _ = kda.paged_prefill(q, kv(c), c["table"], c["lens"], cu, scale=1.0, return_lse=True)
+    d, _ = kda.paged_decode(q[:2], kv(c), c["table"], c["lens"], scale=1.0, return_lse=True)
+    kda.check()
+    for x in (o, d) if amp < 1e36 else ():
+        assert torch.isfinite(x).all() and x.abs().max() < 20
+
+
+@pytest.mark.parametrize("lens,qn", [([9000], [5]), ([3000, 500, 40], [3000, 77, 40])])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_prefill_repeats_bit_for_bit(lens, qn, dtype):
+    q, c, cu, o, lse = run_prefill(lens, qn, 6, 2, 128, 64, dtype, seed=42)
+    for _ in range(4):
+        b = kda.paged_prefill(q, kv(c), c["table"], c["lens"], cu, return_lse=True)
+        assert torch.equal(o, b[0]) and torch.equal(lse, b[1])
+
+
+def test_decode_workspace_serves_calls_of_any_sizes():
+    """One workspace through calls of other batches and lengths, in turn."""
+    a = make_cache([5000, 1, 800], 64, 2, 128, BF16, 43)
+    b = make_cache([60] * 33 + [20000], 64, 2, 128, BF16, 44)
+    qa, qb = rand_q(3, 8, 128, 45), rand_q(34, 8, 128, 46)
+    pa, pb = kv(a), kv(b)
+    ws = kda.paged_decode_workspace(pa, 3, 8)
+    want = (kda.paged_decode(qa, pa, a["table"], a["lens"]),
+            kda.paged_decode(qb, pb, b["table"], b["lens"]))
+    for _ in range(3):
+        got = (kda.paged_decode(qa, pa, a["table"], a["lens"], workspace=ws),
+               kda.paged_decode(qb, pb, b["table"], b["lens"], workspace=ws))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

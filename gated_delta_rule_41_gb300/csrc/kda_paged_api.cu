@@ -31,13 +31,13 @@ kda_status check_dims(const kda_paged_dims* d, bool attend) {
     if ((d->D != 64 && d->D != 128) || page_shift(d->page_size) < 0) return KDA_ERR_UNSUPPORTED;
     if (d->S > 65535 || d->HKV > 65535 || d->num_pages > kMaxPages) return KDA_ERR_UNSUPPORTED;
     if ((long long)d->max_pages * d->page_size > INT_MAX / 2) return KDA_ERR_UNSUPPORTED;
+    const long long per16 = d->cache_dtype == KDA_E4M3 ? 16 : 8;
+    if (d->page_stride % per16 || d->token_stride % per16 || d->head_stride % per16)
+        return KDA_ERR_ALIGNMENT;
     // rows do not overlap; the stride of a dimension of one is not used
     if (d->token_stride < d->D || (d->HKV > 1 && d->head_stride < d->D) ||
         (d->num_pages > 1 && d->page_stride < d->D) || d->page_stride < 0 || d->head_stride < 0)
         return KDA_ERR_SHAPE;
-    const long long per16 = d->cache_dtype == KDA_E4M3 ? 16 : 8;
-    if (d->page_stride % per16 || d->token_stride % per16 || d->head_stride % per16)
-        return KDA_ERR_ALIGNMENT;
     if (!attend) return KDA_OK;
     if (d->HQ <= 0 || d->HQ % d->HKV != 0) return KDA_ERR_SHAPE;
     if (d->HQ / d->HKV > 64) return KDA_ERR_UNSUPPORTED;

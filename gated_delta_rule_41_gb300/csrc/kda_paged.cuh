@@ -80,6 +80,33 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Programmatic dependent launch.  A kernel launched by launch_overlapped may
+// get its CTAs onto SMs that the kernel before it in the stream leaves idle; it
+// calls wait_for_previous() before it touches memory, which returns when that kernel is
+// done and its writes are visible.  let_next_start(): the CTAs of the next
+// such kernel may come as soon as every CTA has called it.
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+kda_status launch_overlapped(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                             A... args) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, fn, P(args)...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 // SMs of the current device (cached per device).
 inline int sm_count() {
     static int cache[64] = {};

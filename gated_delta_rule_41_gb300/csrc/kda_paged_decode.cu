@@ -240,6 +240,8 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rows = a.HKV * HB;                         // rows of a sequence
+    wait_for_previous();
+    let_next_start();
 
     // ---- this CTA's stretch of the line of tiles ----
     const int per_thread = (a.S + kThreads - 1) / kThreads;
@@ -690,10 +692,9 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
     const int HB = (a.G + 8 * NH - 1) / (8 * NH), W = Sh::OCC * sm_count();
     const long long most = (long long)a.S * a.HKV * HB * ((a.cap + 63LL) / 64 + 1);
     TimedLaunch tl("paged_decode", s);
-    fn<<<(unsigned)(most < W ? most : W), kThreads, Sh::SMEM, s>>>(
-        a, HB, static_cast<unsigned*>(ws),
-        reinterpret_cast<float4*>(static_cast<char*>(ws) + tickets_bytes()));
-    return launch_status();
+    return launch_overlapped(fn, (unsigned)(most < W ? most : W), kThreads, Sh::SMEM, s, a, HB,
+                             static_cast<unsigned*>(ws),
+                             reinterpret_cast<float4*>(static_cast<char*>(ws) + tickets_bytes()));
 }
 
 }  // namespace

@@ -15,9 +15,11 @@
 //
 // Softmax.  The weights of a tile are taken against a reference m of the row,
 // the largest logit of its first half tile; only when the weights of a half
-// tile add up to more than 4096 is a larger logit looked for, m moved to it, O
-// and the sum rescaled and the half weighed again.  So as a rule no maximum is taken at
-// all, and weights stay far inside the range of fp16.  Sums are fp32.  P enters the product with V in fp16, which rounds a weight by
+// tile add up to more than 2^15 is a larger logit looked for, m moved to it, O
+// and the sum rescaled and the half weighed again.  So as a rule no maximum is
+// taken at all, and weights stay inside the range of fp16, which a low
+// reference only uses better.  (At 2^12 a window's rows, whose first tile holds a few
+// sinks, looked again ten times in 34 tiles.)  Sums are fp32.  P enters the product with V in fp16, which rounds a weight by
 // up to 2^-11, a small part of the output's own rounding (2^-8), at the rate of a bf16 one
 // (which alone would round weights by as much as the output).
 //
@@ -59,7 +61,7 @@ constexpr int kThreads = 512;                // four warpgroups of 128 registers
 constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;   // out again as
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
-constexpr float kMost = 4096.f;             // sum of half a tile's weights that calls for a look
+constexpr float kMost = 32768.f;            // sum of half a tile's weights that calls for a look
 constexpr float kRaise = 8.f;               // log2 of the weight that then moves the reference
 
 __device__ __forceinline__ void record(kda_status code) {

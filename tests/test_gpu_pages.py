@@ -248,3 +248,52 @@ def test_serving_loop():
     prompts([0, 50, 0, 0, 0, 7])
     step()
     attend(None)
+
+
+def test_pools_of_many_pages():
+    """More pages than one round of the plans' scans, held ones far apart."""
+    S, width, pages, page = 500, 40, 50021, 16
+    host, dev, dpools, book = start(S, width, pages, page, n_pools=1, row=4)
+    rng = random.Random(9)
+    add = [rng.randint(0, width * page) for _ in range(S)]
+    for step in range(4):
+        book.extend(ints(add), *dev)
+        host.extend(add)
+        check(host)
+        same(host, dev, dpools)
+        gone = rng.sample(range(S), 300) if step < 3 else list(range(0, S, 2))
+        gone = [s for s in gone if host.lens[s]]
+        book.free(ints(gone), *dev)
+        host.free(gone)
+        idle = [s for s in range(S) if host.lens[s] == 0]
+        live = [s for s in range(S) if host.lens[s] > 0]
+        par, ch = [rng.choice(live) for _ in range(50)], rng.sample(idle, 50)
+        book.fork(ints(par), ints(ch), *dev)
+        host.fork(par, ch)
+        check(host)
+        same(host, dev, dpools)
+        add = [rng.randint(0, width * page) if host.lens[s] == 0 else 0 for s in range(S)]
+    book.compact(*dev)
+    host.compact()
+    check(host)
+    same(host, dev, dpools)
+
+
+def test_plans_read_counts_at_any_alignment():
+    for shift in range(4):
+        host, _, dpools, book = start(6, 5, 70, 16)
+        buf = torch.zeros(80, dtype=torch.int32, device="cuda")
+        dev = [torch.full((6, 5), -1, dtype=torch.int32, device="cuda"),
+               torch.zeros(6, dtype=torch.int32, device="cuda"), buf[shift:shift + 70]]
+        add = [40, 0, 70, 16, 1, 0]
+        book.extend(ints(add), *dev)
+        host.extend(add)
+        book.free(ints([2]), *dev)
+        host.free([2])
+        book.fork(ints([0]), ints([5]), *dev)
+        host.fork([0], [5])
+        book.compact(*dev)
+        host.compact()
+        kda.check()
+        same(host, dev, dpools)
+        assert (buf[70 + shift:] == 0).all() and (buf[:shift] == 0).all()

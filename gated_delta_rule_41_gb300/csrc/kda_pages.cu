@@ -10,7 +10,7 @@
 // TB/s; 515 moves of 262 KB (4 pools) 45 us.
 #include <algorithm>
 
-#include "kda_common.cuh"
+#include "kda_paged.cuh"
 #include "kda_timing.cuh"
 
 namespace kda {
@@ -212,6 +212,7 @@ fork_plan_kernel(kda_pages_dims d, const int* __restrict__ parents,
                  const int* __restrict__ lens, int* refs, Plan pl) {
     __shared__ long long s_wide[32];
     __shared__ int s[32];
+    paged::let_next_start();
     long long run = 0;
     for (int at = 0; at < n; at += kPlanThreads) {
         const int i = at + threadIdx.x;
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 fork_kernel(const __grid_constant__ Pools pools, kda_pages_dims d,
             const int* __restrict__ parents, const int* __restrict__ children, int n, int* table,
             int* lens, int* refs, Plan pl) {
+    paged::wait_for_previous();
     if ((int)blockIdx.y < pools.n) {
         copy_pages(pools, d.num_pages, pl.src, pl.dst, n);
         return;
@@ -371,6 +373,7 @@ free_kernel(kda_pages_dims d, const int* __restrict__ slots, int* table, int* le
 __global__ void __launch_bounds__(kPlanThreads)
 compact_plan_kernel(int num_pages, int* refs, Plan pl) {
     __shared__ long long s[32];
+    paged::let_next_start();
     long long total, L = 0;
     for (int p0 = threadIdx.x * kPlanPages; p0 < num_pages; p0 += kPlanThreads * kPlanPages) {
         int count[kPlanPages];
@@ -421,6 +424,7 @@ compact_plan_kernel(int num_pages, int* refs, Plan pl) {
 // blockIdx.y == number of pools: the table; else the page copies.
 __global__ void __launch_bounds__(kCopyThreads)
 compact_kernel(const __grid_constant__ Pools pools, kda_pages_dims d, int* table, Plan pl) {
+    paged::wait_for_previous();
     const int moves = pl.count[0], L = pl.count[1];
     if ((int)blockIdx.y < pools.n) {
         copy_pages(pools, d.num_pages, pl.src, pl.dst, moves);
@@ -482,9 +486,9 @@ kda_status pages_fork_launch(const kda_pages_dims& d, const kda_page_pool* pools
     }
     TimedLaunch tl("pages_fork", s);
     const dim3 grid(std::max(copy_grid(pools, num_pools, n), std::min(n, 152)), num_pools + 1);
-    fork_kernel<<<grid, kCopyThreads, 0, s>>>(make_pools(pools, num_pools), d, parents, children,
-                                              n, table, lens, refs, pl);
-    return launch_status();
+    return paged::launch_overlapped(fork_kernel, grid, kCopyThreads, 0, s,
+                                    make_pools(pools, num_pools), d, parents, children, n, table,
+                                    lens, refs, pl);
 }
 
 kda_status pages_free_launch(const kda_pages_dims& d, const int* slots, int n, int* table,
@@ -505,8 +509,8 @@ kda_status pages_compact_launch(const kda_pages_dims& d, const kda_page_pool* po
     }
     TimedLaunch tl("pages_compact", s);
     const dim3 grid(copy_grid(pools, num_pools, d.num_pages), num_pools + 1);
-    compact_kernel<<<grid, kCopyThreads, 0, s>>>(make_pools(pools, num_pools), d, table, pl);
-    return launch_status();
+    return paged::launch_overlapped(compact_kernel, grid, kCopyThreads, 0, s,
+                                    make_pools(pools, num_pools), d, table, pl);
 }
 
 kda_status pages_copy_launch(const kda_page_pool* pools, int num_pools, int num_pages,

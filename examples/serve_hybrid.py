@@ -165,7 +165,8 @@ def main(argv=None):
     torch.cuda.synchronize()
     kda.check()
     held = int((m.refs > 0).sum())
-    print(f"{args.steps} steps of {args.layers} layers, {(time.perf_counter() - t) / args.steps * 1e3:.2f} ms each; "
+    ms = (time.perf_counter() - t) / args.steps * 1e3
+    print(f"{args.steps} steps of {args.layers} layers, {ms:.2f} ms each; "
           f"lengths {m.lens.tolist()}, {held} pages held")
 
 

@@ -3,46 +3,52 @@
 //
 // A CTA takes 256 query rows of one (sequence, key head) as two tiles A, B of
 // 128.  A row is a (token, query head) pair, the G heads that share the key
-// head side by side, so shared heads fill the MMA's M axis and every K and V tile is
-// read once for all of them.  Per tile of 128 cached tokens:
+// head side by side, so shared heads fill the MMA's M axis and every K and V
+// tile is read once for all of them.  Per tile of 128 cached tokens:
 //     S = Q K^T                  tcgen05, fp32 in TMEM, one thread per row reads it
-//     P = exp2(f S - m)          f = scale log2(e); back to TMEM over S
+//     P = exp2(f S - m)          f = scale log2(e); back to TMEM over S, in halves
 //     O += P V                   tcgen05, P from TMEM, V as it lies (MN-major)
-// While the softmax of one tile runs, the tensor core works for the other.  For
-// every 128 x 256 block the four products take 2048 cycles at the dense bf16
-// rate and the 32768 exponentials 1024 of the special function units, so
-// the tensor core bounds it if neither chain waits.
+// While the softmax of one tile runs, the tensor core works for the other.
+//
+// What bounds it: for every 128 x 256 block the four products take 2240 cycles
+// of the tensor core as measured alone (70 for each 128 x 128 x 16), the 32768
+// exponentials 1024 of the special function units.  A pair of tiles takes 2900
+// cycles: a chain of S -> weights (1500) -> P V and the next S (1100) -> on to
+// the softmax again (300) is longer than the tensor core's work.  A prompt of
+// 8192 tokens, 16 heads over 4, D = 128: 202 us, 1360 TFLOP/s, 0.73 of the
+// bf16 rate of cuBLAS; the first and the last tile of an item, which are
+// slower, and the items' unequal lengths are the rest.
 //
 // Softmax.  The weights of a tile are taken against a reference m of the row,
 // the largest logit of its first half tile; only when the weights of a half
 // tile add up to more than 2^15 is a larger logit looked for, m moved to it, O
 // and the sum rescaled and the half weighed again.  So as a rule no maximum is
 // taken at all, and weights stay inside the range of fp16, which a low
-// reference only uses better.  (At 2^12 a window's rows, whose first tile holds a few
-// sinks, looked again ten times in 34 tiles.)  Sums are fp32.  P enters the product with V in fp16, which rounds a weight by
-// up to 2^-11, a small part of the output's own rounding (2^-8), at the rate of a bf16 one
-// (which alone would round weights by as much as the output).
+// reference only uses better.  (At 2^12 a window's rows, whose first tile holds
+// a few sinks, looked again ten times in 34 tiles: 150 us against 131.)  Sums are
+// fp32.  P enters the product with V in fp16, which rounds a weight by up to
+// 2^-11, a small part of the output's own rounding (2^-8), at the rate of a
+// bf16 one (which alone would round weights by as much as the output).
 //
-// K and V tiles arrive by TMA, one box per page, into one ring of slots, and a
+// K and V tiles arrive by TMA, one box per page, into rings of slots, and a
 // warpgroup turns what is not ready for the products into it, in place:
 // * V in bf16 to fp16, scaled by a power of two 2^-E so that large values
 //   fit.  E is 0 if the first tile's largest value lies in [1, 2^15), else the
 //   exponent of that value less 8; a later tile that does not fit raises it, and
 //   the rows' O are rescaled as for a moved reference.  bf16 values are exact
 //   in fp16 down to 2^-17 of that scale.
-// * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row scaled
-//   by a power of two that its logits' factor gives back.
+// * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row
+//   scaled by a power of two that its logits' factor gives back.
 // * V rows past the sequence's end (they may hold NaN) to zeros.  Pages past
 //   it, and pages out of range, are asked for at a coordinate outside the
 //   pool, which TMA fills with zeros.
 //
 // Roles: warps 0-3 softmax and output of tile A, 4-7 of B, warp 8 TMA, warp 9
 // MMA, warps 12-15 the conversions.  Every wait is bounded; on expiry the error
-// is recorded and the CTA unwinds.  With few query rows the cached tokens are split over several
-// CTAs, whose parts a second kernel joins.
+// is recorded and the CTA unwinds.  With few query rows the cached tokens are
+// split over several CTAs, whose parts a second kernel joins.
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "kda_paged.cuh"
 #include "kda_timing.cuh"
@@ -57,8 +63,9 @@ using namespace ptx;
 using namespace paged;
 
 constexpr int kTile = 128;                  // query rows and cached tokens of a tile
-constexpr int kThreads = 512;                // four warpgroups of 128 registers a thread, dealt
-constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;   // out again as
+// four warpgroups of 128 registers a thread at launch, dealt out again by role
+constexpr int kThreads = 512;
+constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
 constexpr float kMost = 32768.f;            // sum of half a tile's weights that calls for a look
@@ -279,6 +286,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // ---- which item: sequence, block of 2 TB tokens (the last ones, with the
     // most to read, start first), key head ----
     const int h = blockIdx.x % a.HKV;
+    if (tid == 8 * 32) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
     {
         const int each = (a.S + kThreads - 1) / kThreads;
         const int lo = min(a.S, tid * each), hi = min(a.S, lo + each);
@@ -550,8 +562,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 // the tile's largest |v|, by the bits of pairs
                 uint32_t top = 0;
                 auto larger = [&](uint32_t w) {
-                    const __nv_bfloat162 z = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top),
-                                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+                    const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&w);
+                    const __nv_bfloat162 z =
+                        __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top), __habs2(y));
                     top = *reinterpret_cast<const uint32_t*>(&z);
                 };
 #pragma unroll 8
@@ -776,7 +789,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     keep *= pow2any(E - Ev);
                     E = Ev;
                 }
-                if (__builtin_expect(__any_sync(0xffffffffu, keep != 1.f), 0) && (n > 0 || e2 > 0)) {
+                const bool change = __any_sync(0xffffffffu, keep != 1.f);
+                if (change && (n > 0 || e2 > 0)) {
                     // O must hold the half before
                     if (e2 > 0) {
                         ok = wait_bar_warp(&o_half[x], n & 1);
@@ -924,7 +938,8 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
     if (!get_encoder()) return KDA_ERR_CUDA;
     if (!set[dev]) {
-        if (cudaFuncSetAttribute(prefill_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(prefill_kernel<D, E4M3>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Plan<D>::SMEM) != cudaSuccess)
             return KDA_ERR_CUDA;
         set[dev] = true;
@@ -956,12 +971,14 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
     // a split takes four tiles or more of the longest row
     const int splits = (int)std::max<long long>(
         1, std::min<long long>(most_splits(a), a.cap / (4 * kTile)));
+    char* w = static_cast<char*>(ws);
     const Split part = {static_cast<float*>(ws),
-                        reinterpret_cast<float2*>(static_cast<char*>(ws) + part_bytes(a, D, splits))};
+                        reinterpret_cast<float2*>(w + part_bytes(a, D, splits))};
     {
         TimedLaunch tl("paged_prefill", s);
-        prefill_kernel<D, E4M3><<<dim3((unsigned)most_items(a), splits), kThreads, Plan<D>::SMEM, s>>>(
-            mq, mk, mv, a, TB, hf ? 1 : 0, part);
+        const dim3 grid((unsigned)most_items(a), splits);
+        prefill_kernel<D, E4M3><<<grid, kThreads, Plan<D>::SMEM, s>>>(mq, mk, mv, a, TB,
+                                                                      hf ? 1 : 0, part);
         const kda_status st = launch_status();
         if (st != KDA_OK || splits == 1) return st;
     }

@@ -345,7 +345,8 @@ kda_status kda_paged_append(const kda_paged_dims* dims, const int* cu_seqlens, i
  * elements apart, o dense), lse float [S][HQ] or NULL; the query stands at
  * position kv_lens[s] - 1 (its own key and value already appended).  The
  * workspace's size depends on D and HQ / HKV alone.  It must be all zeros
- * before its first use; every call leaves it fit for the next one.  Calls that may overlap need one each. */
+ * before its first use; every call leaves it fit for the next one.  Calls that
+ * may overlap need one each. */
 size_t kda_paged_decode_workspace_bytes(const kda_paged_dims* dims);
 kda_status kda_paged_decode(const kda_paged_dims* dims, const void* q, long long q_stride,
                             const void* k_pages, const void* v_pages, const float* k_scale,

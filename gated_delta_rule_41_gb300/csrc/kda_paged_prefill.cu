@@ -15,7 +15,7 @@
 // exponentials 1024 of the special function units.  A pair of tiles takes 2900
 // cycles: a chain of S -> weights (1500) -> P V and the next S (1100) -> on to
 // the softmax again (300) is longer than the tensor core's work.  A prompt of
-// 8192 tokens, 16 heads over 4, D = 128: 202 us, 1360 TFLOP/s, 0.73 of the
+// 8192 tokens, 16 heads over 4, D = 128: 204 us, 1350 TFLOP/s, 0.72 of the
 // bf16 rate of cuBLAS; the first and the last tile of an item, which are
 // slower, and the items' unequal lengths are the rest.
 //
@@ -253,8 +253,8 @@ __device__ __forceinline__ Span make_span(const PagedArgs& a, int p_min, int p_m
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, int TB, int heads_first,
-               Split part) {
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+               const PagedArgs a, int TB, int heads_first, Split part) {
     using P = Plan<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -279,7 +279,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     int* v_exp = reinterpret_cast<int*>(done + 1);   // [SLOTS] E of the V tile in the slot
     int* v_top = v_exp + P::SLOTS;                // bits of a tile's largest |v|
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(v_top + 1);
-    __shared__ int s_scan[kThreads / 32], s_seq, s_block;
+    __shared__ int s_scan[kThreads / 32], s_seq, s_block, s_cu[2], s_len;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -296,6 +296,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int lo = min(a.S, tid * each), hi = min(a.S, lo + each);
         bool bad = tid == 0 && (a.cu[0] != 0 || a.cu[a.S] != a.T);
         int mine = 0;
+        const int len_lo = lo < hi ? a.lens[lo] : 0;         // on its way with the others
         for (int s = lo; s < hi; ++s) {
             const int n = a.cu[s + 1] - a.cu[s];
             bad |= n < 0 || a.cu[s] < 0 || a.cu[s + 1] > a.T;
@@ -308,7 +309,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (lane >= o) sum += y;
         }
         if (lane == 31) s_scan[warp] = sum;
-        if (tid == 0) s_seq = -1;
         if (__syncthreads_or(bad)) {
             if (tid == 0) record(KDA_ERR_SHAPE);
             return;
@@ -319,6 +319,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             total += s_scan[w];
         }
         const int item = total - 1 - (int)(blockIdx.x / a.HKV);
+        if (item < 0) return;
         if (item >= before && item < before + mine) {
             int s = lo, at = before;
             for (; s + 1 < hi; ++s) {
@@ -328,25 +329,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             s_seq = s;
             s_block = item - at;
+            s_cu[0] = a.cu[s];
+            s_cu[1] = a.cu[s + 1];
+            s_len = s == lo ? len_lo : a.lens[s];
         }
-        __syncthreads();
-        if (s_seq < 0) return;
     }
-    const int s = s_seq, cu0 = a.cu[s], nq = a.cu[s + 1] - cu0;
-    int len = a.lens[s];
-    if (len < 0 || len > a.cap) {
-        if (tid == 0) record(KDA_ERR_SHAPE);
-        len = 0;
-    }
-    const int i0 = s_block * 2 * TB;                         // first token of tile A in the prompt
-    const int p0 = len - nq + i0;                            // its position
-    const int p_last = min(p0 + 2 * TB, len) - 1;
-    const Span sp = make_span(a, p0, p_last);
-    const int n_lo = (int)((long long)sp.n * blockIdx.y / gridDim.y);
-    const int n_hi = (int)((long long)sp.n * (blockIdx.y + 1) / gridDim.y);
-    const int N = n_hi - n_lo;                               // tiles of this CTA
-
-    if (tid == 0) {
+    if (tid == 10 * 32) {
         for (int i = 0; i < P::SLOTS; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_ready[i], kTile);
@@ -365,14 +353,27 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         *v_top = 0;
         fence_mbar_init();
     }
-    if (warp == 9 && N > 0) {
+    if (warp == 9) {
         tmem_alloc(tmem_holder, TM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = N > 0 ? *tmem_holder : 0;
+    const uint32_t tmem = *tmem_holder;
+    const int s = s_seq, cu0 = s_cu[0], nq = s_cu[1] - cu0;
+    int len = s_len;
+    if (len < 0 || len > a.cap) {
+        if (tid == 0) record(KDA_ERR_SHAPE);
+        len = 0;
+    }
+    const int i0 = s_block * 2 * TB;                         // first token of tile A in the prompt
+    const int p0 = len - nq + i0;                            // its position
+    const int p_last = min(p0 + 2 * TB, len) - 1;
+    const Span sp = make_span(a, p0, p_last);
+    const int n_lo = (int)((long long)sp.n * blockIdx.y / gridDim.y);
+    const int n_hi = (int)((long long)sp.n * (blockIdx.y + 1) / gridDim.y);
+    const int N = n_hi - n_lo;                               // tiles of this CTA
 
     if (warp >= 8 && warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -675,8 +676,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (f == 0.f) f = 1e-37f;
         for (int n = 0; n < N && ok; ++n) {
             const int j0 = sp.tile(n_lo + n) * kTile;
-            int Ev = 0;
-            if (!E4M3) {                                     // the scale of this tile's V
+            int Ev = E;
+            if (!E4M3 && n > 0) {                            // the scale of this tile's V
                 ok = wait_bar_warp(&kv_ready[v_slot(n)], v_par(n));
                 Ev = v_exp[v_slot(n)];
             }
@@ -806,6 +807,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         tmem_st32_nw(to + 32 * c, o);
                     }
                 }
+                // the first tile's scale, before its slot can be filled again (a warp
+                // that does not come here has no row to write)
+                if (!E4M3 && n == 0 && e2 == 1) {
+                    ok = wait_bar_warp(&kv_ready[v_slot(0)], v_par(0));
+                    E = v_exp[v_slot(0)];
+                }
                 hand_over(e2, w);
             }
         }
@@ -821,6 +828,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // O is in units of 2^E and of the head's scale
         const float unit = E4M3 ? (a.vs ? a.vs[h] : 1.f) : pow2any(E);
         const float by = any ? (split ? unit : unit / l) : 0.f;
+        // A whole tile leaves through shared memory (Q's, which is read) by one TMA
+        // store: rows of 256 bytes, where a thread alone would write 16 at a time.
+        const bool whole = !split && i0 + (x + 1) * TB <= nq;
+        uint8_t* stage = smem + P::OFF_Q + x * P::SLOT + r * 128;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             float o[32];
@@ -830,14 +841,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
             }
-            if (!live) continue;
-            if (split) {
+            if (live && split) {
                 if (any)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         *reinterpret_cast<float4*>(part.o + at * D + 32 * c + 4 * e) = make_float4(
                             by * o[4 * e], by * o[4 * e + 1], by * o[4 * e + 2], by * o[4 * e + 3]);
-            } else {
+            } else if (live) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint4 w = make_uint4(0, 0, 0, 0);
@@ -846,8 +856,24 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                        pack_bf16(o[8 * e + 2] * by, o[8 * e + 3] * by),
                                        pack_bf16(o[8 * e + 4] * by, o[8 * e + 5] * by),
                                        pack_bf16(o[8 * e + 6] * by, o[8 * e + 7] * by));
-                    *reinterpret_cast<uint4*>(a.o + row * D + 32 * c + 8 * e) = w;
+                    const int k = 4 * c + e;                 // 16-byte chunk of the row
+                    if (whole)
+                        *reinterpret_cast<uint4*>(stage + (k >> 3) * P::HALF +
+                                                  (((k & 7) ^ (r & 7)) << 4)) = w;
+                    else
+                        *reinterpret_cast<uint4*>(a.o + row * D + 8 * k) = w;
                 }
+            }
+            __syncwarp();                                    // together into the next load
+        }
+        if (whole) {
+            fence_async_smem();
+            asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + x) : "memory");
+            if (r == 0) {
+                for (int c = 0; c < D / 64; ++c)
+                    tma_store_3d(&tm_o, stage + c * P::HALF, 64 * c, h * a.G, cu0 + i0 + x * TB);
+                bulk_commit_group();
+                bulk_wait_read_all();
             }
         }
         if (live && split) part.ml[at] = make_float2(m, l);
@@ -856,7 +882,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 9 && N > 0) tmem_dealloc(tmem, TM_COLS);
+    if (warp == 9) tmem_dealloc(tmem, TM_COLS);
 }
 
 // Joins the parts of a row: one warp per row.
@@ -945,13 +971,16 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
         set[dev] = true;
     }
     const int TB = tile_tokens(a), page = 1 << a.page_shift;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.HQ, (cuuint64_t)a.T};
         const cuuint64_t strides[2] = {
             (cuuint64_t)D * 2, (cuuint64_t)(a.T > 1 ? a.q_stride : (long long)a.HQ * D) * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)TB};
-        if (!encode(&mq, false, a.q, 3, dims, strides, box)) return KDA_ERR_CUDA;
+        const cuuint64_t dense[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.HQ * D * 2};
+        if (!encode(&mq, false, a.q, 3, dims, strides, box) ||
+            !encode(&mo, false, a.o, 3, dims, dense, box))
+            return KDA_ERR_CUDA;
     }
     // heads and rows of a page in the order of their strides
     const bool hf = a.HKV > 1 && a.head_stride > a.token_stride;
@@ -977,7 +1006,7 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
     {
         TimedLaunch tl("paged_prefill", s);
         const dim3 grid((unsigned)most_items(a), splits);
-        prefill_kernel<D, E4M3><<<grid, kThreads, Plan<D>::SMEM, s>>>(mq, mk, mv, a, TB,
+        prefill_kernel<D, E4M3><<<grid, kThreads, Plan<D>::SMEM, s>>>(mq, mk, mv, mo, a, TB,
                                                                       hf ? 1 : 0, part);
         const kda_status st = launch_status();
         if (st != KDA_OK || splits == 1) return st;

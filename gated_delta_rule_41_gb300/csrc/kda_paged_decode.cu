@@ -66,9 +66,15 @@ struct Span {
     int len, low, sinks;     // token j is seen iff j < len and (j >= low or j < sinks)
     int nsink, first, n;     // groups of sinks; first group of the window; groups in all
     __device__ __forceinline__ int group(int i) const { return i < nsink ? i : i - nsink + first; }
-    __device__ __forceinline__ int tiles() const { return max(1, (n + kWarps - 1) / kWarps); }
-    // a row's length in the line of tiles: its end costs time too
-    __device__ __forceinline__ int slots() const { return tiles() + kRowEnd; }
+    // tiles of TW warps; a row's length in the line of tiles: its end costs time too
+    template <int TW>
+    __device__ __forceinline__ int tiles() const {
+        return max(1, (n + TW - 1) / TW);
+    }
+    template <int TW>
+    __device__ __forceinline__ int slots() const {
+        return tiles<TW>() + kRowEnd;
+    }
 };
 __device__ __forceinline__ Span make_span(const PagedArgs& a, int len) {
     Span s;
@@ -104,7 +110,7 @@ struct Shape {
     static constexpr size_t SMEM = kWarps * RING + (kWarps - 1) * FRAG * 512;
     static_assert(OCC * (SMEM + 2048) <= 228 * 1024, "over the shared memory of an SM");
 };
-constexpr int kMostCtas = 3;                             // of an SM, over all shapes
+constexpr int kMostCtas = 3, kMostRows = 2;              // of an SM, of a CTA, over all shapes
 
 // Shuffled layout of a row's state: [FRAG][32 lanes] float4.  Fragment k NH + n
 // holds channels of m tile k for heads 8n + 2t and 8n + 2t + 1 (the accumulator of
@@ -207,20 +213,20 @@ __device__ __forceinline__ void finish_heads(const PagedArgs& a, const RowOut& r
     }
 }
 
-// Adds parts w, w + kWarps, ... of a row's `count` to st: part 0 lies at
+// Adds parts w, w + TW, ... of a row's `count` to st: part 0 lies at
 // `first`, the others from `rest` on, `step` float4 apart.  B parts are on their
 // way at once.
-template <int B, int D, bool E4M3, int NH>
+template <int B, int TW, int D, bool E4M3, int NH>
 __device__ __forceinline__ void add_parts(State<D, E4M3, NH>& st, const float4* first,
                                           const float4* rest, int count, int step, int w,
                                           int lane) {
     constexpr int F = Shape<D, E4M3, NH>::FRAG;
 #pragma unroll 1
-    for (int i = w; i < count; i += B * kWarps) {
+    for (int i = w; i < count; i += B * TW) {
         float4 y[B][F];
 #pragma unroll
         for (int e = 0; e < B; ++e) {
-            const int j = i + e * kWarps;
+            const int j = i + e * TW;
             const float4* p = (j == 0 ? first : rest + (long long)(j - 1) * step) + lane;
 #pragma unroll
             for (int k = 0; k < F; ++k)
@@ -229,31 +235,33 @@ __device__ __forceinline__ void add_parts(State<D, E4M3, NH>& st, const float4* 
         }
 #pragma unroll
         for (int e = 0; e < B; ++e)
-            if (i + e * kWarps < count) st.add([&](int k) { return y[e][k]; });
+            if (i + e * TW < count) st.add([&](int k) { return y[e][k]; });
     }
 }
 
-__device__ __forceinline__ void bar_sync(int id) {
-    asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(int id) {
-    asm volatile("barrier.cta.arrive %0, 128;" ::"r"(id) : "memory");
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-template <int D, bool E4M3, int NH>
+// WH rows (blocks of query heads) side by side, of TW warps each.
+template <int D, bool E4M3, int NH, int WH>
 __global__ void __launch_bounds__(kThreads, Shape<D, E4M3, NH>::OCC)
 decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
               float4* __restrict__ parts) {
     using Sh = Shape<D, E4M3, NH>;
-    constexpr int KS = Sh::KS;
+    constexpr int KS = Sh::KS, TW = kWarps / WH;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_scan[kWarps];
     __shared__ int s_seq;
     __shared__ long long s_at;
-    __shared__ int s_last;
+    __shared__ int s_last[WH];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rows = a.HKV * HB;                         // rows of a sequence
+    const int hs = warp / TW, tw = warp % TW;            // the warp's row, its place in it
+    const int rows = a.HKV * HB / WH;                    // (groups of WH) rows of a sequence
     wait_for_previous();
     let_next_start();
 
@@ -261,7 +269,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     const int per_thread = (a.S + kThreads - 1) / kThreads;
     const int s_lo = min(a.S, tid * per_thread), s_hi = min(a.S, s_lo + per_thread);
     long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) mine += make_span(a, seq_len(a, s)).slots();
+    for (int s = s_lo; s < s_hi; ++s) mine += make_span(a, seq_len(a, s)).slots<TW>();
     long long sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -269,7 +277,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         if (lane >= o) sum += y;
     }
     if (lane == 31) s_scan[warp] = sum;
-    if (tid == 0) s_last = 0;
+    if (tid < WH) s_last[tid] = 0;
     __syncthreads();
     long long before = sum - mine, total = 0;
 #pragma unroll
@@ -286,7 +294,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         long long at = before;                           // the sequence that holds `begin`
         int s = s_lo;
         for (; s + 1 < s_hi; ++s) {
-            const long long n = (long long)make_span(a, seq_len(a, s)).slots() * rows;
+            const long long n = (long long)make_span(a, seq_len(a, s)).slots<TW>() * rows;
             if (begin < at + n) break;
             at += n;
         }
@@ -295,7 +303,9 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     }
     __syncthreads();
     const uint32_t ring = ptx::smem_u32(smem) + warp * Sh::RING;
-    float4* mail = reinterpret_cast<float4*>(smem + kWarps * Sh::RING) + lane;   // of warps 1-3
+    // of the row's warps but the first
+    float4* mail = reinterpret_cast<float4*>(smem + kWarps * Sh::RING) + lane +
+                   hs * (TW - 1) * (Sh::FRAG * 32);
     const int gshift = a.page_shift - 4;                 // groups per page, log2
 
     // A stretch's piece of one row, as the warp sees it.
@@ -313,13 +323,13 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         for (;;) {
             if (p.at >= end) return false;
             p.sp = make_span(a, seq_len(a, p.s));
-            len = p.sp.slots();
+            len = p.sp.slots<TW>();
             while (p.at >= p.seq_at + (long long)len * rows && p.s + 1 < a.S) {
                 p.seq_at += (long long)len * rows;
                 p.sp = make_span(a, seq_len(a, ++p.s));
-                len = p.sp.slots();
+                len = p.sp.slots<TW>();
             }
-            p.tiles = p.sp.tiles();
+            p.tiles = p.sp.tiles<TW>();
             p.row = (int)((p.at - p.seq_at) / len);
             p.tile0 = (int)((p.at - p.seq_at) % len);
             if (p.tile0 < p.tiles) break;
@@ -327,9 +337,9 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         }
         p.tile1 = (int)min((long long)p.tiles, p.tile0 + (end - p.at));
         p.next = p.at + (p.tile1 == p.tiles ? len - p.tile0 : p.tile1 - p.tile0);
-        p.g0 = p.tile0 * kWarps + warp;
-        const int g1 = min(p.sp.n, p.tile1 * kWarps);
-        p.steps = p.g0 < g1 ? (g1 - p.g0 + kWarps - 1) / kWarps : 0;
+        p.g0 = p.tile0 * TW + tw;
+        const int g1 = min(p.sp.n, p.tile1 * TW);
+        p.steps = p.g0 < g1 ? (g1 - p.g0 + TW - 1) / TW : 0;
         return true;
     };
     Piece in;                                            // being loaded
@@ -345,7 +355,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     auto page_of = [&]() {
         return in_step < in.steps
                    ? __ldg(a.table + (size_t)in.s * a.max_pages +
-                           (in.sp.group(in.g0 + in_step * kWarps) >> gshift))
+                           (in.sp.group(in.g0 + in_step * TW) >> gshift))
                    : 0;
     };
     int page = page_of();
@@ -358,12 +368,12 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
             page = page_of();
         }
         if (more && in_step < in.steps) {
-            const int grp = in.sp.group(in.g0 + in_step * kWarps), j0 = grp * kGroup;
+            const int grp = in.sp.group(in.g0 + in_step * TW), j0 = grp * kGroup;
             const bool good = (unsigned)page < (unsigned)a.num_pages;
             if (!good) record();
             const long long off = (good ? page : 0) * a.page_stride +
                                   (grp & ((1 << gshift) - 1)) * kGroup * a.token_stride +
-                                  (in.row / HB) * a.head_stride;
+                                  ((in.row * WH + hs) / HB) * a.head_stride;
             const char* kp = static_cast<const char*>(a.kp) + off * (E4M3 ? 1 : 2);
             const char* vp = static_cast<const char*>(a.vp) + off * (E4M3 ? 1 : 2);
             const long long ts = a.token_stride * (E4M3 ? 1 : 2);
@@ -392,7 +402,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
 
     int stage = 0;
     for (bool first = true;; first = false) {
-        const int h = cur.row / HB, hq0 = h * a.G + cur.row % HB * (8 * NH);
+        const int u = cur.row * WH + hs, h = u / HB, hq0 = h * a.G + u % HB * (8 * NH);
         RowOut out;
         out.at = (long long)cur.s * a.HQ + hq0;
         out.heads = min(8 * NH, (h + 1) * a.G - hq0);
@@ -500,7 +510,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
             }
 
             // ---- weights ----
-            const int j0 = cur.sp.group(cur.g0 + i * kWarps) * kGroup;
+            const int j0 = cur.sp.group(cur.g0 + i * TW) * kGroup;
             const bool edge = j0 + kGroup > cur.sp.len || j0 < cur.sp.low;
             bool rise = false;
 #pragma unroll
@@ -598,20 +608,21 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
             }
         }
 
-        // ---- the end of the piece: warp 0 collects ----
+        // ---- the end of the piece: the row's first warp collects ----
         const bool whole = cur.tile0 == 0 && cur.tile1 == cur.tiles;
-        const long long row_at = cur.seq_at + (long long)cur.row * cur.sp.slots();
+        const long long row_at = cur.seq_at + (long long)cur.row * cur.sp.slots<TW>();
         const int c0 = (int)(row_at / per), c1 = (int)((row_at + cur.tiles - 1) / per);
         // the parts of the row: CTA c0 leaves its own in its second slot, the others in their
         // first
         Piece then = cur;
         then.at = cur.next;
         const bool last = !enter(then);
-        float4* slots = parts + (2LL * c0 + 1) * (Sh::FRAG * 32);
-        auto send = [&]() { st.store(mail + (warp - 1) * (Sh::FRAG * 32)); };
+        constexpr int kPart = WH * Sh::FRAG * 32, kStep = 2 * kPart;   // float4 between slots, CTAs
+        float4* slots = parts + (2LL * c0 + 1) * kPart + hs * (Sh::FRAG * 32);
+        auto send = [&]() { st.store(mail + (tw - 1) * (Sh::FRAG * 32)); };
         auto collect = [&]() {
 #pragma unroll 1
-            for (int w = 0; w < kWarps - 1; ++w)
+            for (int w = 0; w < TW - 1; ++w)
                 st.add([&](int i) { return mail[(w * Sh::FRAG + i) * 32]; });
         };
         auto write = [&]() {
@@ -624,43 +635,42 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                     write_frag<D, E4M3>(a, out, n, k, g, t, st.o[n][k], by);
             }
         };
-        constexpr int kStep = 2 * Sh::FRAG * 32;
-        if (warp > 0) {
-            if (!first) bar_sync(2);                     // warp 0 has read the last one
+        if (tw > 0) {
+            if (!first) bar_sync(2 + 2 * hs, 32 * TW);   // the first warp has read the last one
             send();
-            bar_arrive(1);
+            bar_arrive(1 + 2 * hs, 32 * TW);
         } else {
-            bar_sync(1);
+            bar_sync(1 + 2 * hs, 32 * TW);
             collect();
-            if (!last) bar_arrive(2);
+            if (!last) bar_arrive(2 + 2 * hs, 32 * TW);
             if (whole) {
                 write();
             } else {
                 float4* slot = (int)blockIdx.x == c0
                                    ? slots
-                                   : slots + Sh::FRAG * 32 +
+                                   : slots + kPart +
                                          (long long)((int)blockIdx.x - c0 - 1) * kStep;
                 st.store(slot + lane);
                 __threadfence();
                 __syncwarp();
                 unsigned ticket = 0;
-                if (lane == 0) ticket = atomicAdd(tickets + c0, 1u);
+                if (lane == 0) ticket = atomicAdd(tickets + c0 * WH + hs, 1u);
                 ticket = __shfl_sync(0xffffffffu, ticket, 0);
                 if (ticket == (unsigned)(c1 - c0)) {
                     __threadfence();
-                    if (lane == 0) tickets[c0] = 0;      // as the next call expects it
+                    if (lane == 0) tickets[c0 * WH + hs] = 0;   // as the next call expects it
                     if (last) {
-                        if (lane == 0) s_last = 1;       // all warps join it below
+                        if (lane == 0) s_last[hs] = 1;   // the row's warps join it below
                     } else {
-                        // alone, with the sums that the four warps would take
+                        // alone, with the sums that the row's warps would take
                         st.clear();
-                        add_parts<1>(st, slots, slots + Sh::FRAG * 32, c1 - c0 + 1, kStep, 0, lane);
+                        add_parts<1, TW>(st, slots, slots + kPart, c1 - c0 + 1, kStep, 0, lane);
 #pragma unroll 1
-                        for (int w = 1; w < kWarps; ++w) {
+                        for (int w = 1; w < TW; ++w) {
                             State<D, E4M3, NH> more;
                             more.clear();
-                            add_parts<1>(more, slots, slots + Sh::FRAG * 32, c1 - c0 + 1, kStep, w,
-                                         lane);
+                            add_parts<1, TW>(more, slots, slots + kPart, c1 - c0 + 1, kStep, w,
+                                             lane);
                             st.add([&](int i) { return more.frag(i); });
                         }
                         write();
@@ -670,13 +680,19 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         }
         if (last) {
             __syncthreads();
-            if (s_last) {
-                st.clear();
-                add_parts<NH == 1 ? 3 : 1>(st, slots, slots + Sh::FRAG * 32, c1 - c0 + 1, kStep,
-                                           warp, lane);
-                if (warp > 0) send();
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < WH; ++i) any |= s_last[i] != 0;
+            if (any) {
+                const bool mine_too = s_last[hs] != 0;
+                if (mine_too) {
+                    st.clear();
+                    add_parts<NH == 1 ? 3 : 1, TW>(st, slots, slots + kPart, c1 - c0 + 1, kStep,
+                                                   tw, lane);
+                    if (tw > 0) send();
+                }
                 __syncthreads();
-                if (warp == 0) {
+                if (mine_too && tw == 0) {
                     collect();
                     write();
                 }
@@ -688,16 +704,18 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
     cp_async_wait<0>();
 }
 
-// The workspace: a counter for each CTA, then two parts for each.
-size_t tickets_bytes() { return align256((size_t)kMostCtas * sm_count() * sizeof(unsigned)); }
+// The workspace: a counter for each CTA and row, then two parts for each.
+size_t tickets_bytes() {
+    return align256((size_t)kMostRows * kMostCtas * sm_count() * sizeof(unsigned));
+}
 
-template <int D, bool E4M3, int NH>
-kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
+template <int D, bool E4M3, int NH, int WH>
+kda_status launch_rows(const PagedArgs& a, void* ws, cudaStream_t s) {
     using Sh = Shape<D, E4M3, NH>;
     static bool set[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
-    auto* fn = decode_kernel<D, E4M3, NH>;
+    auto* fn = decode_kernel<D, E4M3, NH, WH>;
     if (!set[dev]) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Sh::SMEM) != cudaSuccess)
@@ -705,24 +723,44 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
         set[dev] = true;
     }
     const int HB = (a.G + 8 * NH - 1) / (8 * NH), W = Sh::OCC * sm_count();
-    const long long most = (long long)a.S * a.HKV * HB * ((a.cap + 63LL) / 64 + 1);
+    const long long most = (long long)a.S * a.HKV * HB * ((a.cap + 63LL) / 64 + 1 + kRowEnd);
     TimedLaunch tl("paged_decode", s);
     return launch_overlapped(fn, (unsigned)(most < W ? most : W), kThreads, Sh::SMEM, s, a, HB,
                              static_cast<unsigned*>(ws),
                              reinterpret_cast<float4*>(static_cast<char*>(ws) + tickets_bytes()));
 }
 
-}  // namespace
-
-template <int D, int NH>
-size_t parts_bytes() {
-    const size_t of_cta = 2 * Shape<D, false, NH>::FRAG * 512;   // the same for both cache types
-    return align256(of_cta * (NH == 1 ? kMostCtas : 2) * sm_count());
+// One row per CTA, or two: K and V rows of 128 bytes or less come from HBM at
+// 0.87 of the rate of longer pieces, so where the next head's rows lie beside
+// them, both are taken at once.
+template <int D, bool E4M3, int NH>
+kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
+    if constexpr (Shape<D, E4M3, NH>::RB <= 128) {
+        const int HB = (a.G + 8 * NH - 1) / (8 * NH);
+        if (a.head_stride == D && a.HKV * HB % 2 == 0) return launch_rows<D, E4M3, NH, 2>(a, ws, s);
+    }
+    return launch_rows<D, E4M3, NH, 1>(a, ws, s);
 }
 
-size_t paged_decode_ws_bytes(const PagedArgs& a, int D, bool) {
-    const size_t parts = D == 128 ? (a.G <= 8 ? parts_bytes<128, 1>() : parts_bytes<128, 2>())
-                                  : (a.G <= 8 ? parts_bytes<64, 1>() : parts_bytes<64, 2>());
+template <int D, bool E4M3, int NH>
+size_t parts_bytes() {
+    using Sh = Shape<D, E4M3, NH>;
+    const size_t rows = Sh::RB <= 128 ? kMostRows : 1;
+    return align256(rows * 2 * Sh::FRAG * 512 * Sh::OCC * sm_count());
+}
+
+}  // namespace
+
+size_t paged_decode_ws_bytes(const PagedArgs& a, int D, bool e4m3) {
+    size_t parts;
+    if (D == 128 && a.G <= 8)
+        parts = e4m3 ? parts_bytes<128, true, 1>() : parts_bytes<128, false, 1>();
+    else if (D == 128)
+        parts = e4m3 ? parts_bytes<128, true, 2>() : parts_bytes<128, false, 2>();
+    else if (a.G <= 8)
+        parts = e4m3 ? parts_bytes<64, true, 1>() : parts_bytes<64, false, 1>();
+    else
+        parts = e4m3 ? parts_bytes<64, true, 2>() : parts_bytes<64, false, 2>();
     return tickets_bytes() + parts;
 }
 

@@ -344,7 +344,7 @@ kda_status kda_paged_append(const kda_paged_dims* dims, const int* cu_seqlens, i
 /* Attention of one new token per sequence: q, o [S][HQ][D] (q rows q_stride
  * elements apart, o dense), lse float [S][HQ] or NULL; the query stands at
  * position kv_lens[s] - 1 (its own key and value already appended).  The
- * workspace's size depends on D and HQ / HKV alone.  It must be all zeros
+ * workspace's size depends on D, HQ / HKV and the cache type.  It must be all zeros
  * before its first use; every call leaves it fit for the next one.  Calls that
  * may overlap need one each. */
 size_t kda_paged_decode_workspace_bytes(const kda_paged_dims* dims);

@@ -5,8 +5,8 @@
 // bf16: 8 flop a byte) as long as the products run on the tensor cores.  The
 // plan is therefore about keeping loads in flight and all SMs equally busy:
 //
-// * Work is cut into tiles of 64 tokens of one (sequence, key head, block of
-//   query heads).  The tiles of all of them form one line, of which each
+// * Work is cut into tiles (16 tokens for each warp) of one (sequence, key head,
+//   block of query heads).  The tiles of all of them form one line, of which each
 //   resident CTA takes an equal stretch (a prefix sum over the lengths, taken
 //   by every CTA for itself), so a few long rows spread over the SMs like many
 //   unequal ones.  The end of a row counts for three tiles: it costs the CTA
@@ -17,8 +17,8 @@
 //   ring of stages, which runs on over the ends of rows: while a row is
 //   finished, the copies of the next one are on their way.  Rows that the
 //   query does not see are filled with zeros instead of being read.
-// * At the end of a row warps 1-3 leave their sums in shared memory, in the
-//   order of the MMA fragments, and go on; warp 0 adds them to its own.  A row
+// * At the end of a row its other warps leave their sums in shared memory, in the
+//   order of the MMA fragments, and go on; the first adds them to its own.  A row
 //   that lies in one stretch is written at once; of the others each CTA leaves
 //   its part, and the CTA that arrives last joins the parts, always in the same
 //   order, so the result does not depend on which one that is.
@@ -33,14 +33,18 @@
 //   alone (2^-8) would cost as much as the output's own rounding and the
 //   second product is free here.
 //
-// Measured: a call costs about 10 us beside its bytes (5 to start and find its
-// work, 4 to join rows that several CTAs share), which then pass at the copy
-// rate (64 rows of 2048 tokens 49 us, of 4096 89 us: 6.8 TB/s between them) in
-// pieces of 256 bytes, 0.87 of it in pieces of 128 (D = 64, or e4m3).  64 rows of 200
-// to 8192 tokens, 16 heads over 4, D = 128, bf16: 51 us, 5.5 TB/s, and DRAM
-// reads 283.2 MB, what the rows hold.  Two CTAs on an SM with D = 128, three with
-// D = 64 (a 128-row window batch: 46 us against 40); more make no difference,
-// and neither do smaller shares handed out as CTAs get done.
+// * K and V rows of 128 bytes or less (D = 64, or e4m3) of two neighbouring heads
+//   are taken by one CTA side by side, two warps each: HBM gives pieces of 128
+//   bytes at 0.87 of the rate of longer ones (128 window rows of 64 channels: 39 us
+//   with one head per CTA, 36 with two, 38 with four, whose parts take longer to join).
+//
+// Measured: a call costs about 9 us beside its bytes (5 to start and find its
+// work, 3 to join rows that several CTAs share), which then pass at the copy
+// rate (64 rows of 2048 tokens 49 us, of 4096 89 us: 6.8 TB/s between them).
+// 64 rows of 200 to 8192 tokens, 16 heads over 4, D = 128, bf16: 50 us, 5.6 TB/s,
+// and DRAM reads 283.2 MB, what the rows hold.  Two CTAs on an SM with D = 128,
+// three with D = 64 (the window rows: 46 us against 40 then); more make no
+// difference, and neither do smaller shares handed out as CTAs get done.
 #include "kda_paged.cuh"
 #include "kda_timing.cuh"
 

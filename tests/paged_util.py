@@ -80,9 +80,10 @@ def attend(q, k, v, p, scale, window, sinks):
 
 
 def check_attention(o, lse, ref):
-    """Element bounds.  Output: half an ulp of bf16 (2^-9 relative).  Weights:
-    2^-9 relative each from their rounding to bf16 (less in fp16), and the
-    error of their logits.  Logits: D <= 128 products summed in fp32, in any
+    """Element bounds.  Output: bf16 rounds by up to 2^-8 |o|, which is at most
+    2^-9 |o| + 2^-9 A, since |o| <= A = sum w |v|.  Weights: what that leaves of
+    2^-9 A (the kernels keep a weight to 2^-11 or better), and the error of
+    their logits.  Logits: D <= 128 products summed in fp32, in any
     order and with truncation, are off by at most 128 * 2^-23 of the sum of
     magnitudes X, 2^-16 X; exp2 adds 2^-21.  All of it times A = sum w |v|, twice
     where the sum of the weights carries it too."""

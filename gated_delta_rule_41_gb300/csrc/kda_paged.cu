@@ -57,7 +57,8 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
     __shared__ long long s_off[kAppendTokens];          // element of the token's row, or -1
     __shared__ float s_inv[2 * kAppendHeads];           // 1 / scale of K, V per head
     const int tid = threadIdx.x, t0 = blockIdx.x * TB, n = min(TB, a.T - t0);
-    const int row = a.HKV * (D / 8), per = 2 * row;     // items of a row of K, of a token
+    constexpr int V = E4M3 ? 2 : 1, EL = 8 * V;         // 16-byte loads, elements of an item
+    const int row = a.HKV * (D / EL), per = 2 * row;    // items of a row of K, of a token
 
     // A thread's items lie kAppendThreads apart: (token, item of it), stepped
     // without a division.
@@ -70,16 +71,20 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
             ++tok;
         }
     };
-    uint4 x[kAppendItems];
+    constexpr int kItems = kAppendItems / V;
+    uint4 x[kItems][V];
     int tok0 = tid / per, at0 = tid % per;              // of the thread's first item of a round
     auto load = [&]() {
         int tok = tok0, at = at0;
 #pragma unroll
-        for (int i = 0; i < kAppendItems; ++i, step(tok, at)) {
+        for (int i = 0; i < kItems; ++i, step(tok, at)) {
             if (tok >= n) continue;
             const long long t = t0 + tok;
-            x[i] = __ldcs(reinterpret_cast<const uint4*>(
-                at < row ? k + t * k_stride + 8LL * at : v + t * v_stride + 8LL * (at - row)));
+            const uint4* src = reinterpret_cast<const uint4*>(
+                at < row ? k + t * k_stride + (long long)EL * at
+                         : v + t * v_stride + (long long)EL * (at - row));
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[i][e] = __ldcs(src + e);
         }
     };
     load();
@@ -122,11 +127,11 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
     for (;;) {
         int tok = tok0, at = at0;
 #pragma unroll
-        for (int i = 0; i < kAppendItems; ++i, step(tok, at)) {
+        for (int i = 0; i < kItems; ++i, step(tok, at)) {
             if (tok >= n || s_off[tok] < 0) continue;
             const bool of_v = at >= row;
-            const int c = of_v ? at - row : at, h = c / (D / 8);
-            const long long e = s_off[tok] + h * a.head_stride + c % (D / 8) * 8;
+            const int c = of_v ? at - row : at, h = c / (D / EL);
+            const long long e = s_off[tok] + h * a.head_stride + c % (D / EL) * EL;
             char* pool = static_cast<char*>(const_cast<void*>(of_v ? a.vp : a.kp));
             if (E4M3) {
                 float inv;
@@ -136,9 +141,10 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
                     const float* sc = of_v ? a.vs : a.ks;
                     inv = sc ? 1.0f / sc[h] : 1.0f;
                 }
-                *reinterpret_cast<uint2*>(pool + e) = quant8(x[i], inv);
+                const uint2 lo = quant8(x[i][0], inv), hi = quant8(x[i][V - 1], inv);
+                *reinterpret_cast<uint4*>(pool + e) = make_uint4(lo.x, lo.y, hi.x, hi.y);
             } else {
-                *reinterpret_cast<uint4*>(pool + 2 * e) = x[i];
+                *reinterpret_cast<uint4*>(pool + 2 * e) = x[i][0];
             }
         }
         tok0 = tok;
@@ -152,7 +158,7 @@ template <int D, bool E4M3>
 kda_status append(const PagedArgs& a, const void* k, long long k_stride, const void* v,
                   long long v_stride, cudaStream_t s) {
     // tokens of a CTA: its threads' items, but fewer while CTAs are few
-    const int per = 2 * a.HKV * (D / 8);
+    const int per = 2 * a.HKV * (D / 8);                 // 16-byte loads of a token
     const int full = std::min(kAppendTokens,
                               std::max(1, kAppendThreads * kAppendItems / per));
     const int TB = std::max(1, std::min(full, a.T / (2 * paged::sm_count())));

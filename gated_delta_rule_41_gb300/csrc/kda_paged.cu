@@ -39,11 +39,12 @@ __device__ __forceinline__ uint2 quant8(const uint4 v, float inv) {
 }
 
 // A pass of copies bounded by HBM: T (HKV D) (2 + code) bytes each of K and V.
-// A CTA takes TB tokens, whole rows of K and V, as items of eight elements.
-// Its first items are on their way before the tokens' places are looked up
+// A CTA takes TB tokens, whole rows of K and V, as items that end in one 16-byte
+// store: eight elements, or sixteen from two loads for e4m3 (41 us below with
+// eight).  Its first items are on their way before the tokens' places are looked up
 // (sequence, length, table entry: three dependent reads), so that the copies do
-// not wait for them.  32k tokens of 8 heads of 128 into e4m3 pages, 194 MB: 41 us,
-// 4.8 TB/s (one warp per row and head, each with its own look-up: 66 us); 256
+// not wait for them.  32k tokens of 8 heads of 128 into e4m3 pages, 194 MB: 35 us,
+// 5.5 TB/s (one warp per row and head, each with its own look-up: 66 us); 256
 // single tokens 2.4 us.
 constexpr int kAppendThreads = 256, kAppendItems = 8;   // of a thread at a time
 constexpr int kAppendTokens = 64;                       // of a CTA, at most

@@ -232,6 +232,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;       // S_A, S_B, O_A, 
 struct Split {                 // parts of a row, one per CTA that works on it
     float* o;                  // [splits][T * HQ][D], unscaled sums
     float2* ml;                // [splits][T * HQ] maximum (log2), sum
+    int* valid;                // whether cu_seqlens held, for the kernel that joins the parts
 };
 
 // The tiles of cached tokens that an item's rows see: those of the sinks, then
@@ -309,7 +310,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (lane >= o) sum += y;
         }
         if (lane == 31) s_scan[warp] = sum;
-        if (__syncthreads_or(bad)) {
+        const bool refused = __syncthreads_or(bad);
+        if (gridDim.y > 1 && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) *part.valid = !refused;
+        if (refused) {
             if (tid == 0) record(KDA_ERR_SHAPE);
             return;
         }
@@ -892,7 +895,7 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, Split part
     const long long rows = (long long)a.T * a.HQ;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
+    if (row >= rows || *part.valid == 0) return;
     float top = -INFINITY;
     for (int k = 0; k < splits; ++k) top = fmaxf(top, part.ml[k * rows + row].x);
     float l = 0.f, o[E] = {};
@@ -956,6 +959,9 @@ int most_splits(const PagedArgs& a) {
 size_t part_bytes(const PagedArgs& a, int D, int splits) {
     return align256((size_t)splits * a.T * a.HQ * D * sizeof(float));
 }
+size_t ml_bytes(const PagedArgs& a, int splits) {
+    return align256((size_t)splits * a.T * a.HQ * sizeof(float2));
+}
 
 template <int D, bool E4M3>
 kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
@@ -1002,7 +1008,8 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
         1, std::min<long long>(most_splits(a), a.cap / (4 * kTile)));
     char* w = static_cast<char*>(ws);
     const Split part = {static_cast<float*>(ws),
-                        reinterpret_cast<float2*>(w + part_bytes(a, D, splits))};
+                        reinterpret_cast<float2*>(w + part_bytes(a, D, splits)),
+                        reinterpret_cast<int*>(w + part_bytes(a, D, splits) + ml_bytes(a, splits))};
     {
         TimedLaunch tl("paged_prefill", s);
         const dim3 grid((unsigned)most_items(a), splits);
@@ -1021,7 +1028,7 @@ kda_status launch(const PagedArgs& a, void* ws, cudaStream_t s) {
 size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool) {
     const int splits = most_splits(a);
     if (splits == 1) return 0;
-    return part_bytes(a, D, splits) + align256((size_t)splits * a.T * a.HQ * sizeof(float2));
+    return part_bytes(a, D, splits) + ml_bytes(a, splits) + align256(sizeof(int));
 }
 
 kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s) {

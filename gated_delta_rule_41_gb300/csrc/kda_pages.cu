@@ -368,8 +368,10 @@ free_kernel(kda_pages_dims d, const int* __restrict__ slots, int* table, int* le
 
 // ---- compact ----
 // One CTA: L = the number of held pages; the held pages at or above L (src,
-// with their rank) and the free ones below L (dst), each in rising order; the
-// two lists are equally long.  Then the counts move along.
+// with their rank) and the others below L (dst), each in rising order; the
+// two lists are equally long, since every page is one or the other: a negative
+// count, which no book keeps, is reported and not held.  Then the counts move
+// along.
 __global__ void __launch_bounds__(kPlanThreads)
 compact_plan_kernel(int num_pages, int* refs, Plan pl) {
     __shared__ long long s[32];
@@ -379,7 +381,10 @@ compact_plan_kernel(int num_pages, int* refs, Plan pl) {
         int count[kPlanPages];
         load_counts(refs, num_pages, p0, count);
 #pragma unroll
-        for (int i = 0; i < kPlanPages; ++i) L += count[i] > 0;
+        for (int i = 0; i < kPlanPages; ++i) {
+            L += count[i] > 0;
+            if (count[i] < 0 && p0 + i < num_pages) record(KDA_ERR_SHAPE);
+        }
     }
     block_scan<long long>(L, s, &total);
     L = total;
@@ -392,7 +397,7 @@ compact_plan_kernel(int num_pages, int* refs, Plan pl) {
         long long mine = 0;
 #pragma unroll
         for (int i = 0; i < kPlanPages; ++i) {
-            if (count[i] == 0 && p0 + i < L) ++mine;
+            if (count[i] <= 0 && p0 + i < L) ++mine;
             if (count[i] > 0 && p0 + i >= L) mine += 1LL << 32;
         }
         const long long before = run + block_scan<long long>(mine, s, &total);
@@ -401,7 +406,7 @@ compact_plan_kernel(int num_pages, int* refs, Plan pl) {
         if (mine != 0) {
 #pragma unroll
             for (int i = 0; i < kPlanPages; ++i) {
-                if (count[i] == 0 && p0 + i < L) pl.dst[h++] = p0 + i;
+                if (count[i] <= 0 && p0 + i < L) pl.dst[h++] = p0 + i;
                 if (count[i] > 0 && p0 + i >= L) {
                     pl.src[m] = p0 + i;
                     pl.rank[p0 + i] = m++;

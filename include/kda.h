@@ -416,6 +416,7 @@ kda_status kda_pages_free(const kda_pages_dims* dims, const int* slots, int n, i
 /* Move the held pages with ids at or above their number L, in rising order,
  * to the free ids below L, in rising order, in every pool, and rename them in
  * block_table and refs.  Afterwards pages [0, L) are held and the rest free.
+ * (A negative count is reported as KDA_ERR_SHAPE, and its page is not held.)
  * Every row that holds pages of the pools must be in block_table. */
 kda_status kda_pages_compact(const kda_pages_dims* dims, const kda_page_pool* pools,
                              int num_pools, int* block_table, int* refs, void* workspace,

@@ -66,3 +66,33 @@ def test_refused_prompts_write_nothing_when_tokens_are_split(cu, dtype):
     o, l = kda.paged_prefill(q, kv(c), c["table"], c["lens"], good, return_lse=True)
     kda.check()
     check_attention(o, l, ref_prefill(q, c, [20, 20, 10], 64 ** -0.5))
+
+
+# ---- page counts that no book keeps ----
+
+def test_compact_reports_negative_counts_and_stays_in_range():
+    """A negative count is neither a holder nor a hole left over: the page counts as
+    free, the held ones close up, and nothing else changes."""
+    pages, g = 40, torch.Generator().manual_seed(50)
+    pool = torch.randint(0, 1 << 15, (pages, 4, 4), generator=g, dtype=torch.int32).cuda()
+    refs = torch.zeros(pages, dtype=torch.int32)
+    held = [0, 2, 7, 8, 21, 30, 39]
+    refs[held] = 1
+    refs[[1, 3, 5, 25, 38]] = torch.tensor([-1, -3, -2 ** 31, -1, -7], dtype=torch.int32)
+    table = torch.full((2, 5), -1, dtype=torch.int32)
+    table[0, :3], table[1, :4] = torch.tensor(held[:3]), torch.tensor(held[3:])
+    want_table, want_pool, want_refs = table.clone(), pool.clone(), refs.clone()
+    n = len(held)
+    to = dict(zip([p for p in held if p >= n], [p for p in range(n) if refs[p] <= 0]))
+    for a, b in to.items():
+        want_table[table == a] = b
+        want_pool[b] = pool[a]
+        want_refs[b], want_refs[a] = refs[a], 0
+    dev = [table.cuda(), ints([12, 16]), refs.cuda()]
+    book = kda.PageBook(pages, 4, [pool])
+    book.compact(*dev)
+    with pytest.raises(kda.KdaError) as e:
+        kda.check()
+    assert e.value.status == 2
+    assert torch.equal(dev[0].cpu(), want_table) and torch.equal(dev[2].cpu(), want_refs)
+    assert torch.equal(pool, want_pool)

@@ -209,7 +209,8 @@ __device__ __forceinline__ void finish_heads(const PagedArgs& a, const RowOut& r
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-        const bool any = m[c] != -INFINITY;
+        // (a sum of zero: nothing was seen.  The maximum would not tell it from NaN.)
+        const bool any = l[c] != 0.f;
         const int head = 8 * n + 2 * t + c;
         by[c] = any ? r.unit / l[c] : 0.f;
         if (lse && a.lse && g == 0 && head < r.heads)

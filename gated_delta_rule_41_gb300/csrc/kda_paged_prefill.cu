@@ -825,7 +825,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc_fence_after();
         }
         const long long row = ((long long)cu0 + i) * a.HQ + h * a.G + r % a.G;
-        const bool any = m != -INFINITY;
+        const bool any = l != 0.f;                           // 0: nothing was seen (NaN is not 0)
         const bool split = gridDim.y > 1;
         const long long at = (long long)blockIdx.y * a.T * a.HQ + row;
         // O is in units of 2^E and of the head's scale
@@ -901,19 +901,19 @@ __global__ void __launch_bounds__(256) join_kernel(const PagedArgs a, Split part
     float l = 0.f, o[E] = {};
     for (int k = 0; k < splits; ++k) {
         const float2 ml = part.ml[k * rows + row];
-        if (ml.x == -INFINITY) continue;
+        if (ml.y == 0.f) continue;                           // nothing seen (but NaN is not 0)
         const float w = ex2(ml.x - top);
         l += w * ml.y;
         const float* src = part.o + (k * rows + row) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += w * src[e];
     }
-    const float inv = top == -INFINITY ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t*>(a.o + row * D + lane * E + e) =
             pack_bf16(o[e] * inv, o[e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = top == -INFINITY ? -INFINITY : (top + lg2(l)) * kLn2;
+    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + lg2(l)) * kLn2;
 }
 
 // ---- host ----

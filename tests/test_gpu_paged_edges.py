@@ -96,3 +96,55 @@ def test_compact_reports_negative_counts_and_stays_in_range():
     assert e.value.status == 2
     assert torch.equal(dev[0].cpu(), want_table) and torch.equal(dev[2].cpu(), want_refs)
     assert torch.equal(pool, want_pool)
+
+
+# ---- NaN in queries and keys ----
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_decode_nan_query_or_keys_give_nan(dtype, D):
+    """A NaN in a query, or in the key of an only token, is not an empty row."""
+    c = make_cache([700, 40, 1, 0, 3000], 32, 2, D, dtype, 51)
+    q = rand_q(5, 8, D, 52)
+    q[0, 3, 5] = math.nan
+    q[3, 0, 0] = math.nan                     # of a row that sees nothing
+    k = c["k"].view(torch.uint8) if dtype == E4M3 else c["k"]
+    k[c["table"][2, 0].item(), 0, 1] = 0x7F if dtype == E4M3 else math.nan
+    o, lse = kda.paged_decode(q, kv(c), c["table"], c["lens"], return_lse=True)
+    kda.check()
+    assert o[0, 3].isnan().all() and lse[0, 3].isnan()
+    assert o[2, 4:].isnan().all() and lse[2, 4:].isnan().all()
+    assert (o[3] == 0).all() and (lse[3] == -math.inf).all()
+    ref = ref_decode(torch.nan_to_num(q), c, D ** -0.5)
+    heads = [0, 1, 2, 4, 5, 6, 7]
+    check_attention(o[:1, heads], lse[:1, heads], [x[:1, heads] for x in ref])
+    check_attention(o[2:3, :4], lse[2:3, :4], [x[2:3, :4] for x in ref])
+    check_attention(*rows_of(o, lse, ref, [1, 4]))
+
+
+@pytest.mark.parametrize("D,wide", [(64, 0), (128, 0), (128, 8192)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_prompt_nan_query_or_keys_give_nan(dtype, D, wide):
+    lens, qn = [600, 1, 5], [300, 1, 9]       # the last one: four queries that see nothing
+    c = make_cache(lens, 32, 2, D, dtype, 53)
+    if wide:
+        lens, qn = [6000, 1, 5], [3, 1, 9]
+        c = widened(make_cache(lens, 32, 2, D, dtype, 53), wide)
+    q = rand_q(sum(qn), 4, D, 54)
+    bad = 1
+    q[bad, 2, 7] = math.nan
+    q[sum(qn[:2]), :, 0] = math.nan           # sees nothing
+    k = c["k"].view(torch.uint8) if dtype == E4M3 else c["k"]
+    k[c["table"][1, 0].item(), 0, 0] = 0x7F if dtype == E4M3 else math.nan
+    cu = ints([0] + qn).cumsum(0).to(torch.int32)
+    o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], cu, return_lse=True)
+    kda.check()
+    assert o[bad, 2].isnan().all() and lse[bad, 2].isnan()
+    one = qn[0]                               # the only token's key of head 0 is NaN
+    assert o[one, :2].isnan().all() and lse[one, :2].isnan().all()
+    assert (o[one + 1] == 0).all() and (lse[one + 1] == -math.inf).all()
+    ref = ref_prefill(torch.nan_to_num(q), c, qn, D ** -0.5)
+    check_attention(o[one:one + 1, 2:], lse[one:one + 1, 2:], [x[one:one + 1, 2:] for x in ref])
+    check_attention(*rows_of(o, lse, ref, [i for i in range(sum(qn)) if i not in (bad, one)]))
+    check_attention(o[bad:bad + 1, [0, 1, 3]], lse[bad:bad + 1, [0, 1, 3]],
+                    [x[bad:bad + 1, [0, 1, 3]] for x in ref])

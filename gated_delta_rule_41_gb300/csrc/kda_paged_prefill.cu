@@ -22,7 +22,10 @@
 // Softmax.  The weights of a tile are taken against a reference m of the row,
 // the largest logit of its first half tile; only when the weights of a half
 // tile add up to more than 2^15 is a larger logit looked for, m moved to it, O
-// and the sum rescaled and the half weighed again.  So as a rule no maximum is
+// and the sum rescaled and the half weighed again.  (f S - m in one rounding: m is
+// off by its own, which the weights of such tiles share.  Above 2^10 that would show
+// beside those of other tiles; there the exponent is f (S - S of the reference), so
+// equal keys weigh the same for logits of any size.)  So as a rule no maximum is
 // taken at all, and weights stay inside the range of fp16, which a low
 // reference only uses better.  (At 2^12 a window's rows, whose first tile holds
 // a few sinks, looked again ten times in 34 tiles: 150 us against 131.)  Sums are
@@ -69,7 +72,7 @@ constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
 constexpr float kMost = 32768.f;            // sum of half a tile's weights that calls for a look
-constexpr float kRaise = 8.f;               // log2 of the weight that then moves the reference
+constexpr float kFar = 1024.f;              // references up to here serve the usual path
 
 __device__ __forceinline__ void record(kda_status code) {
     atomicCAS(&g_paged_prefill_error, 0, (int)code);
@@ -639,7 +642,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int px = p0 + x * TB;                          // positions of the tile's rows
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + TM_S + x * kTile + lanes, to = tmem + TM_O + x * kTile + lanes;
-        float m = live ? -INFINITY : 0.f, l = 0.f;           // a dead row asks for nothing
+        // the reference as a logit and as it stands in S (a dead row asks for nothing)
+        float m = live ? -INFINITY : 0.f, s_ref = 0.f, l = 0.f;
         bool ok = true;
         int E = 0;
         if (E4M3 && N > 0) {
@@ -677,6 +681,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         // every visible token weighs the same: 2^0 for any logit, and -infinity stays
         if (f == 0.f) f = 1e-37f;
+        if (!live) f = 0.f;                                  // whatever its row of Q holds
         for (int n = 0; n < N && ok; ++n) {
             const int j0 = sp.tile(n_lo + n) * kTile;
             int Ev = E;
@@ -713,7 +718,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 mbar_arrive(&p_full[2 * x + e2]);
             };
             int e2 = 0;
-            if (!edge && Ev == E && !__any_sync(0xffffffffu, m == -INFINITY)) {
+            if (!edge && Ev == E && !__any_sync(0xffffffffu, !(fabsf(m) < kFar))) {
                 float v[2][2][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_nw(ts + 32 * c, v[c >> 1][c & 1]);
@@ -730,10 +735,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             }
             // Else, at the second round at the latest, every row looks at its
-            // largest logit, and takes it for reference if it has none or
-            // lies more than kRaise below it; S stays in TMEM until then.  (Against
-            // a reference taken here the exponents are differences of logits, so that the
-            // largest weight is 1 for logits of any size.)
+            // largest logit, and takes it for reference if it is larger than the one it
+            // has; S stays in TMEM until then.  The exponents are differences of logits,
+            // so that the largest weight is 1 for logits of any size.
 #pragma unroll 1
             for (; e2 < 2; ++e2) {
                 float sum, keep = 1.f;
@@ -759,7 +763,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 if (!(seen >> e & 1)) v[c][e] = none;
                         }
                     }
-                    float add = m == -INFINITY ? 0.f : -m;
                     if (look) {
                         float hi = v[0][0], lo = v[0][0];
 #pragma unroll
@@ -770,20 +773,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 lo = min3(lo, v[c][e], v[c][e + 1]);
                             }
                         const float s_top = f < 0.f ? lo : hi, top = s_top * f;
-                        float sub = 0.f;
-                        if (m == -INFINITY ? top > -INFINITY : top - m > kRaise) {
-                            keep = m == -INFINITY ? 0.f : ex2(m - top);
+                        if (top > m) {
+                            keep = m == -INFINITY ? 0.f : ex2((s_ref - s_top) * f);
                             m = top;
-                            sub = -s_top;
-                            add = 0.f;
+                            s_ref = s_top;
                         }
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                add2(v[c][e], v[c][e + 1], sub, sub);
                     }
-                    sum = weigh(v, w, add);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            add2(v[c][e], v[c][e + 1], -s_ref, -s_ref);
+                    sum = weigh(v, w, 0.f);
                     if (look) break;
                     look = __any_sync(0xffffffffu, sum > kMost);
                     if (!look) break;

@@ -148,3 +148,31 @@ def test_prompt_nan_query_or_keys_give_nan(dtype, D, wide):
     check_attention(*rows_of(o, lse, ref, [i for i in range(sum(qn)) if i not in (bad, one)]))
     check_attention(o[bad:bad + 1, [0, 1, 3]], lse[bad:bad + 1, [0, 1, 3]],
                     [x[bad:bad + 1, [0, 1, 3]] for x in ref])
+
+
+# ---- large logits ----
+
+@pytest.mark.parametrize("amp", [3e3, 1.1e6, 1.7e6, 2.3e7, 1e9, 1e30])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("lens,qn", [([600], [600]), ([6000], [3])])
+def test_equal_keys_weigh_the_same_at_logits_of_any_size(lens, qn, dtype, scale, amp):
+    """All keys equal: o is the mean of the visible values, whatever the logit.
+    Weights are equal but for their rounding, 2^-11 each, and the output is
+    rounded to bf16: |o - mean| <= 2^-8 |mean| + 2^-10 mean |v|."""
+    c = make_cache(lens, 32, 1, 128, dtype, 55, poison=False)
+    c["k"].fill_(1.0)
+    if c["ks"] is not None:
+        c["ks"].fill_(1.0)
+    q = torch.full((sum(qn), 2, 128), amp, dtype=BF16, device="cuda")
+    cu = ints([0] + qn).cumsum(0).to(torch.int32)
+    o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], cu, scale=scale, return_lse=True)
+    d, dl = kda.paged_decode(q[:1], kv(c), c["table"], c["lens"], scale=scale, return_lse=True)
+    kda.check()
+    ref = ref_prefill(q * 0, c, qn, 1.0)       # weights of one, in the reference too
+    dref = ref_decode(q[:1] * 0, c, 1.0)
+    top = scale * 128 * q[0, 0, 0].double().item()
+    for x, l, r in ((o, lse, ref), (d, dl, dref)):
+        bound = 2.0 ** -8 * r[0].abs() + 2.0 ** -10 * r[2]
+        assert ((x.double().cpu() - r[0]).abs() <= bound).all()
+        assert ((l.double().cpu() - (r[1] + top)).abs() <= 2.0 ** -21 * abs(top) + 1e-5).all()

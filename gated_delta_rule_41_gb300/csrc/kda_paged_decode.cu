@@ -27,11 +27,12 @@
 //   tokens.  The transposed weights come from movmatrix.
 // * Softmax: a running maximum m per head and warp, raised (and the sums
 //   rescaled) only when a logit exceeds it by more than 2^8 in weight; the sums
-//   are fp32, and weights up to 256 lose nothing in floating point.  Beside
-//   e4m3 codes, which are exact in fp16, the weights enter the product with V
-//   in fp16 (2^-11); beside bf16 values in two bf16 terms (2^-16), since one
-//   alone (2^-8) would cost as much as the output's own rounding and the
-//   second product is free here.
+//   are fp32.  Beside e4m3 codes, which are exact in fp16, the weights enter the
+//   product with V in fp16 (2^-11), with 2^7 at the maximum, so that only weights
+//   below 2^-21 of it leave the normal range (and are rounded by up to 2^-32 of
+//   it); beside bf16 values in two bf16 terms (2^-16), since one alone (2^-8)
+//   would cost as much as the output's own rounding and the second product is
+//   free here.
 //
 // * K and V rows of 128 bytes or less (D = 64, or e4m3) of two neighbouring heads
 //   are taken by one CTA side by side, two warps each: HBM gives pieces of 128
@@ -59,6 +60,9 @@ using namespace paged;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGroup = 16;                 // tokens of a warp's step
 constexpr int kRowEnd = 3;                 // tiles that the end of a row counts for
+// log2 of the weight at the running maximum (weights reach 2^8 times that)
+template <bool E4M3>
+constexpr float kLow = E4M3 ? 7.f : 0.f;
 
 __device__ __forceinline__ void record() {
     atomicCAS(&g_paged_decode_error, 0, (int)KDA_ERR_SHAPE);
@@ -202,6 +206,7 @@ __device__ __forceinline__ void write_frag(const PagedArgs& a, const RowOut& r, 
     }
 }
 // The factors of a finished row's O (heads 8n + 2t + c), and its lse.
+template <bool E4M3>
 __device__ __forceinline__ void finish_heads(const PagedArgs& a, const RowOut& r, int n, int g,
                                              int t, const float (&m)[2], float (&l)[2], bool lse,
                                              float (&by)[2]) {
@@ -214,7 +219,7 @@ __device__ __forceinline__ void finish_heads(const PagedArgs& a, const RowOut& r
         const int head = 8 * n + 2 * t + c;
         by[c] = any ? r.unit / l[c] : 0.f;
         if (lse && a.lse && g == 0 && head < r.heads)
-            a.lse[r.at + head] = any ? (m[c] + lg2(l[c])) * kLn2 : -INFINITY;
+            a.lse[r.at + head] = any ? (m[c] + (lg2(l[c]) - kLow<E4M3>)) * kLn2 : -INFINITY;
     }
 }
 
@@ -556,7 +561,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float top = st.m[n][e & 1];
-                    w[e] = ex2(x[n][e] - (top == -INFINITY ? 0.f : top));
+                    w[e] = ex2(x[n][e] - (top == -INFINITY ? 0.f : top) + kLow<E4M3>);
                 }
                 st.l[n][0] += w[0] + w[2];
                 st.l[n][1] += w[1] + w[3];
@@ -634,7 +639,7 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
                 float by[2];
-                finish_heads(a, out, n, g, t, st.m[n], st.l[n], true, by);
+                finish_heads<E4M3>(a, out, n, g, t, st.m[n], st.l[n], true, by);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
                     write_frag<D, E4M3>(a, out, n, k, g, t, st.o[n][k], by);

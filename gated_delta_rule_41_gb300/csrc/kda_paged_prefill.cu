@@ -6,7 +6,7 @@
 // head side by side, so shared heads fill the MMA's M axis and every K and V
 // tile is read once for all of them.  Per tile of 128 cached tokens:
 //     S = Q K^T                  tcgen05, fp32 in TMEM, one thread per row reads it
-//     P = exp2(f S - m)          f = scale log2(e); back to TMEM over S, in halves
+//     P = exp2(f S - m + 7)      f = scale log2(e); back to TMEM over S, in halves
 //     O += P V                   tcgen05, P from TMEM, V as it lies (MN-major)
 // While the softmax of one tile runs, the tensor core works for the other.
 //
@@ -21,17 +21,20 @@
 //
 // Softmax.  The weights of a tile are taken against a reference m of the row,
 // the largest logit of its first half tile; only when the weights of a half
-// tile add up to more than 2^15 is a larger logit looked for, m moved to it, O
+// tile add up to more than 65000 is a larger logit looked for, m moved to it, O
 // and the sum rescaled and the half weighed again.  (f S - m in one rounding: m is
 // off by its own, which the weights of such tiles share.  Above 2^10 that would show
 // beside those of other tiles; there the exponent is f (S - S of the reference), so
 // equal keys weigh the same for logits of any size.)  So as a rule no maximum is
-// taken at all, and weights stay inside the range of fp16, which a low
-// reference only uses better.  (At 2^12 a window's rows, whose first tile holds
-// a few sinks, looked again ten times in 34 tiles: 150 us against 131.)  Sums are
-// fp32.  P enters the product with V in fp16, which rounds a weight by up to
-// 2^-11, a small part of the output's own rounding (2^-8), at the rate of a
-// bf16 one (which alone would round weights by as much as the output).
+// taken at all, and weights stay inside the range of fp16.  Sums are fp32.  P enters
+// the product with V in fp16, which rounds a weight by up to 2^-11, a small part of
+// the output's own rounding (2^-8), at the rate of a bf16 one (which alone would
+// round weights by as much as the output).  The reference weighs 2^7, so that only
+// weights below 2^-21 of it leave fp16's normal range (and are rounded by up to 2^-32
+// of it): a long tail behind one strong token would show it if the reference weighed
+// 1.  That leaves 2^9 for larger logits: a prompt of 8192 tokens does not look
+// more often (at 2^9 for the reference it does: 225 us against 209), a window's rows, which
+// start from a few sinks, do (137 us against 132).
 //
 // K and V tiles arrive by TMA, one box per page, into rings of slots, and a
 // warpgroup turns what is not ready for the products into it, in place:
@@ -71,7 +74,8 @@ constexpr int kThreads = 512;
 constexpr int kRegsSoftmax = 176, kRegsIssue = 80, kRegsConvert = 80;
 static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "registers of the launch");
 constexpr long long kTimeoutCycles = 4000000000LL;   // ~2 s
-constexpr float kMost = 32768.f;            // sum of half a tile's weights that calls for a look
+constexpr float kLow = 7.f;                 // log2 of the weight at the reference
+constexpr float kMost = 65000.f;            // sum of half a tile's weights that calls for a look
 constexpr float kFar = 1024.f;              // references up to here serve the usual path
 
 __device__ __forceinline__ void record(kda_status code) {
@@ -718,6 +722,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 mbar_arrive(&p_full[2 * x + e2]);
             };
             int e2 = 0;
+            bool look = false;
             if (!edge && Ev == E && !__any_sync(0xffffffffu, !(fabsf(m) < kFar))) {
                 float v[2][2][32];
 #pragma unroll
@@ -727,8 +732,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int i2 = 0; i2 < 2; ++i2) {
                     uint32_t w[2][16];
-                    const float sum = weigh(v[i2], w, -m);
-                    if (__any_sync(0xffffffffu, sum > kMost)) break;
+                    const float sum = weigh(v[i2], w, kLow - m);
+                    look = __any_sync(0xffffffffu, sum > kMost);
+                    if (look) break;
                     l += sum;
                     hand_over(i2, w);
                     ++e2;
@@ -737,12 +743,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // Else, at the second round at the latest, every row looks at its
             // largest logit, and takes it for reference if it is larger than the one it
             // has; S stays in TMEM until then.  The exponents are differences of logits,
-            // so that the largest weight is 1 for logits of any size.
+            // so that the largest weight is 2^7 for logits of any size.
 #pragma unroll 1
             for (; e2 < 2; ++e2) {
                 float sum, keep = 1.f;
                 uint32_t w[2][16];
-                bool look = __any_sync(0xffffffffu, m == -INFINITY);
+                look = look || __any_sync(0xffffffffu, m == -INFINITY);
                 for (;;) {
                     float v[2][32];
 #pragma unroll
@@ -784,11 +790,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
                             add2(v[c][e], v[c][e + 1], -s_ref, -s_ref);
-                    sum = weigh(v, w, 0.f);
+                    sum = weigh(v, w, kLow);
                     if (look) break;
                     look = __any_sync(0xffffffffu, sum > kMost);
                     if (!look) break;
                 }
+                look = false;
                 l = l * keep + sum;
                 if (__builtin_expect(Ev != E, 0)) {
                     keep *= pow2any(E - Ev);
@@ -827,10 +834,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         const long long row = ((long long)cu0 + i) * a.HQ + h * a.G + r % a.G;
         const bool any = l != 0.f;                           // 0: nothing was seen (NaN is not 0)
+        const float back = pow2i(-(int)kLow);                // to weights of 1 at the reference
+        l *= back;
         const bool split = gridDim.y > 1;
         const long long at = (long long)blockIdx.y * a.T * a.HQ + row;
         // O is in units of 2^E and of the head's scale
-        const float unit = E4M3 ? (a.vs ? a.vs[h] : 1.f) : pow2any(E);
+        const float unit = (E4M3 ? (a.vs ? a.vs[h] : 1.f) : pow2any(E)) * back;
         const float by = any ? (split ? unit : unit / l) : 0.f;
         // A whole tile leaves through shared memory (Q's, which is read) by one TMA
         // store: rows of 256 bytes, where a thread alone would write 16 at a time.

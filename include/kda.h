@@ -296,7 +296,8 @@ kda_status kda_chunk_fwd_noalloc(const kda_dims* dims, const void* q, const void
  *           accumulate in fp32 and the softmax statistics are fp32; the
  *           weights enter the product with V in two bf16 terms (decode) or in
  *           fp16 (prompts, and both with an e4m3 cache, where q is scaled by a
- *           power of two to fit fp16 too).  For prompts V goes to fp16 with a
+ *           power of two to fit fp16 too): fp16 rounds a weight by 2^-11 of
+ *           itself, or by up to 2^-32 of the row's largest.  For prompts V goes to fp16 with a
  *           power of two shared by the tokens that a block of query rows
  *           reads: values below 2^-33 of the largest finite |v| among them lose
  *           bits.  V of a token should be finite: an infinity or NaN also reaches,

@@ -176,3 +176,49 @@ def test_equal_keys_weigh_the_same_at_logits_of_any_size(lens, qn, dtype, scale,
         bound = 2.0 ** -8 * r[0].abs() + 2.0 ** -10 * r[2]
         assert ((x.double().cpu() - r[0]).abs() <= bound).all()
         assert ((l.double().cpu() - (r[1] + top)).abs() <= 2.0 ** -21 * abs(top) + 1e-5).all()
+
+
+# ---- a token that outweighs a long tail ----
+
+@pytest.mark.parametrize("nats", [12.0, 16.6, 17.5])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_small_weights_of_a_long_tail(prefill, dtype, nats):
+    """The first token takes almost all of the weight and its value is zero: what
+    is left is the tail's, all of one sign.  A weight is rounded by up to 2^-11 of itself (that is in
+    the usual bound) or, where it is small, by 2^-32 of the largest: half of fp16's
+    smallest step, 2^-25, with the largest at 2^7 or more.  The rows are many, so that
+    no other CTA takes part of one."""
+    n = 131072
+    c = make_cache([n], 128, 2, 64, dtype, 56, poison=False)
+    if c["ks"] is not None:
+        c["ks"].fill_(1.0)
+    c["k"].zero_()
+    first = c["table"][0, 0].item()
+    c["k"][first, 0, :, 0] = 1.0
+    v = c["v"].view(torch.uint8) if dtype == E4M3 else c["v"].view(torch.int16)
+    v &= 0x7F if dtype == E4M3 else 0x7FFF     # |v|: the tail adds up
+    v[first, 0] = 0
+    T = 8192 if prefill else 160
+    q = torch.zeros(T, 4, 64, dtype=BF16, device="cuda")
+    q[..., 0] = nats
+    nats = q[0, 0, 0].item()
+    if prefill:
+        o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, T]), scale=1.0,
+                                   return_lse=True)
+        o, lse, q = o[-2:], lse[-2:], q[-2:]
+        ref = ref_prefill(q, c, [2], 1.0)
+    else:
+        table = c["table"].expand(T, -1).contiguous()
+        o, lse = kda.paged_decode(q, kv(c), table, ints([n] * T), scale=1.0, return_lse=True)
+        o, lse, q = o[:1], lse[:1], q[:1]
+        ref = ref_decode(q, c, 1.0)
+    kda.check()
+    ro, rl, A, X = ref
+    vmean = A.max() / (1 - math.exp(nats - rl.min().item()))     # mean |v| of the tail
+    logit = 2.0 ** -16 * X + 2.0 ** -20
+    bound = (2.0 ** -9 * ro.abs() + (2.0 ** -9 + 2 * logit[..., None]) * 1.01 * A
+             + n * 2.0 ** -32 * vmean)
+    worst = ((o.double().cpu() - ro).abs() / bound).max()
+    assert worst <= 1, f"off: {worst:.3g} of its bound"
+    assert ((lse.double().cpu() - rl).abs() <= logit + 2.0 ** -22 * rl.abs()).all()

@@ -38,11 +38,12 @@
 //
 // K and V tiles arrive by TMA, one box per page, into rings of slots, and a
 // warpgroup turns what is not ready for the products into it, in place:
-// * V in bf16 to fp16, scaled by a power of two 2^-E so that large values
-//   fit.  E is 0 if the first tile's largest value lies in [1, 2^15), else the
-//   exponent of that value less 8; a later tile that does not fit raises it, and
-//   the rows' O are rescaled as for a moved reference.  bf16 values are exact
-//   in fp16 down to 2^-17 of that scale.
+// * V in bf16 to fp16, scaled by a power of two 2^-E: the first tile's largest
+//   value then lies in [2^12, 2^13); a later tile with values of 2^16 or more
+//   raises E in the same way, and the rows' O are rescaled as for a moved
+//   reference.  So the largest value so far is 2^12 or more, and bf16 values,
+//   exact in fp16 down to 2^-17, are exact down to 2^-29 of it (but for
+//   magnitudes below 2^-117: E is -100 at least).
 // * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row
 //   scaled by a power of two that its logits' factor gives back.
 // * V rows past the sequence's end (they may hold NaN) to zeros.  Pages past
@@ -589,30 +590,30 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
                 top = max(top & 0xffffu, top >> 16);         // a bf16 without its sign
-                // Does it fit at the scale as it stands?  The first tile sets the
-                // scale: 0 if the largest lies in [1, 2^15).
-                const uint32_t most = (uint32_t)max(0, min(0xff, 127 + 15 + E)) << 7;
-                bool again = any_convert(top >= most);
-                if (n == 0) again = !any_convert(top >= 0x3f80u) || again;
-                if (__builtin_expect(again, 0)) {
-                    // of the finite ones (infinities stay what they are)
-                    uint32_t big = 0;
+                // Does it fit at the scale as it stands?  The first tile sets the scale.
+                const uint32_t most = (uint32_t)max(0, min(0xff, 127 + 16 + E)) << 7;
+                if (n == 0 || any_convert(top >= most)) {
+                    // the largest of the finite ones (infinities stay what they are)
+                    uint32_t big = top;
+                    if (__builtin_expect(top >= 0x7f80u, 0)) {
+                        big = 0;
 #pragma unroll 1
-                    for (int i = 0; i < 4 * L; ++i) {
-                        if (16 * ((i >> 2) & 7) >= rows) continue;
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                            mine + (i >> 2) * 2048 + (i & 3) * 4);
-                        const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
-                        if (lo < 0x7f80u) big = max(big, lo);
-                        if (hi < 0x7f80u) big = max(big, hi);
+                        for (int i = 0; i < 4 * L; ++i) {
+                            if (16 * ((i >> 2) & 7) >= rows) continue;
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                                mine + (i >> 2) * 2048 + (i & 3) * 4);
+                            const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
+                            if (lo < 0x7f80u) big = max(big, lo);
+                            if (hi < 0x7f80u) big = max(big, hi);
+                        }
                     }
-                    atomicMax(v_top, (int)big);
+                    big = __reduce_max_sync(0xffffffffu, big);
+                    if (lane == 0) atomicMax(v_top, (int)big);
                     any_convert(false);
                     const int bits = *reinterpret_cast<volatile int*>(v_top);
-                    const int want = bits == 0 ? -100 : (bits >> 7) - 127 - 8;
+                    const int want = max(-100, (bits >> 7) - 127 - 12);
                     any_convert(false);                      // all have read it
-                    if (t == 0) *v_top = 0;
-                    any_convert(false);
+                    if (t == 0) *v_top = 0;                  // seen by the next tile's any_convert
                     E = n == 0 ? want : max(E, want);
                 }
                 const float down = pow2any(-E);

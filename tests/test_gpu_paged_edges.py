@@ -185,8 +185,8 @@ def test_equal_keys_weigh_the_same_at_logits_of_any_size(lens, qn, dtype, scale,
 @pytest.mark.parametrize("prefill", [False, True])
 def test_small_weights_of_a_long_tail(prefill, dtype, nats):
     """The first token takes almost all of the weight and its value is zero: what
-    is left is the tail's, all of one sign.  A weight is rounded by up to 2^-11 of itself (that is in
-    the usual bound) or, where it is small, by 2^-32 of the largest: half of fp16's
+    is left is the tail's, all of one sign.  A weight is rounded by up to 2^-11 of
+    itself (that is in the usual bound) or, where it is small, by 2^-32 of the largest: half of fp16's
     smallest step, 2^-25, with the largest at 2^7 or more.  The rows are many, so that
     no other CTA takes part of one."""
     n = 131072
@@ -222,3 +222,49 @@ def test_small_weights_of_a_long_tail(prefill, dtype, nats):
     worst = ((o.double().cpu() - ro).abs() / bound).max()
     assert worst <= 1, f"off: {worst:.3g} of its bound"
     assert ((lse.double().cpu() - rl).abs() <= logit + 2.0 ** -22 * rl.abs()).all()
+
+
+# ---- values of unequal channels ----
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("big", [1.0, 2.0 ** 20, 2.0 ** -40])
+def test_channels_far_smaller_than_others(prefill, big):
+    """Channels 2^-20 and 2^-30 of the others keep the precision that is stated:
+    a value is rounded by up to 2^-37 of the largest |v|."""
+    lens, qn = [700], [300]
+    c = make_cache(lens, 32, 2, 128, BF16, 57, poison=False)
+    c["v"].mul_(big)
+    c["v"][..., 10:20] *= 2.0 ** -20
+    c["v"][..., 30:40] *= 2.0 ** -30
+    top = c["v"].abs().max().item()
+    q = rand_q(300 if prefill else 1, 4, 128, 58)
+    if prefill:
+        o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, 300]),
+                                   return_lse=True)
+        ref = ref_prefill(q, c, qn, 128 ** -0.5)
+    else:
+        o, lse = kda.paged_decode(q, kv(c), c["table"], c["lens"], return_lse=True)
+        ref = ref_decode(q, c, 128 ** -0.5)
+    kda.check()
+    ro, rl, A, X = ref
+    logit = 2.0 ** -16 * X + 2.0 ** -20
+    bound = (2.0 ** -9 * ro.abs() + (2.0 ** -9 + 2 * logit[..., None]) * 1.01 * A
+             + 2.0 ** -37 * top)
+    for part in (slice(0, 10), slice(10, 20), slice(30, 40), slice(40, 128)):
+        worst = ((o.double().cpu() - ro).abs() / bound)[..., part].max()
+        assert worst <= 1, f"channels {part}: {worst:.3g} of the bound"
+
+
+@pytest.mark.parametrize("big", [2.0 ** -110, 2.0 ** -125, 2.0 ** 110])
+def test_values_at_the_ends_of_the_range(big):
+    """The smallest values (some denormal) and the largest stay finite; what is below 2^-117
+    may be rounded by 2^-125."""
+    c = make_cache([400], 32, 1, 64, BF16, 76, poison=False)
+    c["v"].copy_((c["v"].double() * big).to(BF16))
+    q = rand_q(400, 2, 64, 77)
+    o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, 400]), return_lse=True)
+    kda.check()
+    ro, rl, A, X = ref_prefill(q, c, [400], 0.125)
+    logit = 2.0 ** -16 * X + 2.0 ** -20
+    bound = (2.0 ** -9 * ro.abs() + (2.0 ** -9 + 2 * logit[..., None]) * 1.01 * A + 2.0 ** -124)
+    assert ((o.double().cpu() - ro).abs() <= bound).all()

@@ -46,6 +46,9 @@
 //   magnitudes below 2^-117: E is -100 at least).
 // * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row
 //   scaled by a power of two that its logits' factor gives back.
+// * Infinities and NaN in V to zeros (e4m3: in tiles that not all rows see whole), since a
+//   weight of 0 would not keep them from the rows that do not see their token; the rows
+//   that do get them at the end.
 // * V rows past the sequence's end (they may hold NaN) to zeros.  Pages past
 //   it, and pages out of range, are asked for at a coordinate outside the
 //   pool, which TMA fills with zeros.
@@ -55,6 +58,7 @@
 // is recorded and the CTA unwinds.  With few query rows the cached tokens are
 // split over several CTAs, whose parts a second kernel joins.
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "kda_paged.cuh"
@@ -259,6 +263,46 @@ __device__ __forceinline__ Span make_span(const PagedArgs& a, int p_min, int p_m
     return s;
 }
 
+// The infinities and NaN of V that a query at position p sees in tiles [t0, t1] of
+// its span, in 32 channels: a bit per channel for +inf (x) and -inf (y), both for NaN.
+// v: the head's row 0 of page 0, at the first of the channels.
+template <bool E4M3>
+__device__ __noinline__ uint2 not_finite(const char* v, const int* table, Span sp, int t0, int t1,
+                                         int p, int window, int sinks, int page_shift,
+                                         int num_pages, long long page_bytes,
+                                         long long token_bytes) {
+    uint2 r = make_uint2(0, 0);
+    for (int t = t0; t <= t1; ++t) {
+        const int j0 = sp.tile(t) * kTile;
+        for (int j = j0; j < j0 + kTile && j <= p; ++j) {
+            if (window && j <= p - window && j >= sinks) continue;
+            const int page = table[j >> page_shift];
+            if ((unsigned)page >= (unsigned)num_pages) continue;
+            const uint4* row = reinterpret_cast<const uint4*>(
+                v + page * page_bytes + (j & ((1 << page_shift) - 1)) * token_bytes);
+#pragma unroll 1
+            for (int c = 0; c < (E4M3 ? 2 : 4); ++c) {
+                const uint4 y = row[c];
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < (E4M3 ? 16 : 8); ++e) {
+                    if (E4M3) {
+                        const bool nan = (w[e >> 2] >> 8 * (e & 3) & 0x7fu) == 0x7fu;
+                        r.x |= (uint32_t)nan << (16 * c + e);
+                        r.y |= (uint32_t)nan << (16 * c + e);
+                    } else {
+                        const uint32_t b = w[e >> 1] >> 16 * (e & 1) & 0xffffu;
+                        const bool nan = (b & 0x7fffu) > 0x7f80u;
+                        r.x |= (uint32_t)(nan || b == 0x7f80u) << (8 * c + e);
+                        r.y |= (uint32_t)(nan || b == 0xff80u) << (8 * c + e);
+                    }
+                }
+            }
+        }
+    }
+    return r;
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -287,7 +331,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint64_t* done = o_full + 2;                  // every MMA has ended (unwinding)
     int* v_exp = reinterpret_cast<int*>(done + 1);   // [SLOTS] E of the V tile in the slot
     int* v_top = v_exp + P::SLOTS;                // bits of a tile's largest |v|
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(v_top + 1);
+    int* v_bad = v_top + 1;                       // [2] first, last tile with an infinity or NaN
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(v_bad + 2);
     __shared__ int s_scan[kThreads / 32], s_seq, s_block, s_cu[2], s_len;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -362,6 +407,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         mbar_init(done, 1);
         *v_top = 0;
+        v_bad[0] = INT_MAX;
+        v_bad[1] = -1;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -521,17 +568,40 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int t = tid & 127;
         bool ok = true;
         int E = 0;
+        auto note_bad = [&](int n) {
+            atomicMin(v_bad, n);
+            atomicMax(v_bad + 1, n);
+        };
         for (int n = 0; n < N; ++n) {
-            const int valid = len - sp.tile(n_lo + n) * kTile;   // rows of the sequence
+            const int j0 = sp.tile(n_lo + n) * kTile, valid = len - j0;   // rows of the sequence
             if (E4M3) {
                 // A tile's codes fill the first half of its slot.  Lane groups of
                 // D / 16 read a row; every 16 codes become two 16-byte chunks.
                 constexpr int C = D / 16, R = 128 / C, L = kTile / R;
                 const int c = t % C, r0 = t / C;
+                // Do all rows see all of it?  Then they all get its NaN codes; else
+                // these are looked for (in every tile: 148 us for 141 of the window case).
+                const bool mixed = !(j0 + kTile - 1 <= p0 &&
+                                     (a.window == 0 || j0 > p0 + 2 * TB - 1 - a.window));
                 for (int kv = 0; kv < 2; ++kv) {
                     const int slot = kv ? v_slot(n) : k_slot(n);
                     uint8_t* tile = smem + P::OFF_KV + slot * P::SLOT;
                     ok = ok && wait_bar_warp(&kv_full[slot], kv ? v_par(n) : k_par(n));
+                    if (kv && mixed) {
+#pragma unroll 1
+                        for (int r = r0; r < min(kTile, valid); r += R) {
+                            uint32_t* w = reinterpret_cast<uint32_t*>(tile + r * D + c * 16);
+                            // the low bits of a NaN code are all ones
+                            auto ones = [](uint32_t y) { return (y & 0x7f7f7f7fu) + 0x01010101u; };
+                            const uint4 y = *reinterpret_cast<const uint4*>(w);
+                            if (((ones(y.x) | ones(y.y) | ones(y.z) | ones(y.w)) & 0x80808080u) == 0)
+                                continue;
+#pragma unroll 1
+                            for (int e = 0; e < 4; ++e)
+                                w[e] &= ~((ones(w[e]) >> 7 & 0x01010101u) * 0xffu);
+                            note_bad(n);
+                        }
+                    }
                     uint4 x[L];
 #pragma unroll
                     for (int i = 0; i < L; ++i) {
@@ -576,7 +646,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 auto larger = [&](uint32_t w) {
                     const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&w);
                     const __nv_bfloat162 z =
-                        __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top), __habs2(y));
+                        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top), __habs2(y));
                     top = *reinterpret_cast<const uint32_t*>(&z);
                 };
 #pragma unroll 8
@@ -593,22 +663,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 // Does it fit at the scale as it stands?  The first tile sets the scale.
                 const uint32_t most = (uint32_t)max(0, min(0xff, 127 + 16 + E)) << 7;
                 if (n == 0 || any_convert(top >= most)) {
-                    // the largest of the finite ones (infinities stay what they are)
+                    // the largest of the finite ones; the others become zeros
                     uint32_t big = top;
                     if (__builtin_expect(top >= 0x7f80u, 0)) {
                         big = 0;
 #pragma unroll 1
                         for (int i = 0; i < 4 * L; ++i) {
                             if (16 * ((i >> 2) & 7) >= rows) continue;
-                            const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                                mine + (i >> 2) * 2048 + (i & 3) * 4);
-                            const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
-                            if (lo < 0x7f80u) big = max(big, lo);
-                            if (hi < 0x7f80u) big = max(big, hi);
+                            uint32_t* at =
+                                reinterpret_cast<uint32_t*>(mine + (i >> 2) * 2048 + (i & 3) * 4);
+                            uint32_t w = *at;
+                            if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                            if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+                            *at = w;
+                            big = max(big, max(w & 0x7fffu, w >> 16 & 0x7fffu));
                         }
                     }
                     big = __reduce_max_sync(0xffffffffu, big);
                     if (lane == 0) atomicMax(v_top, (int)big);
+                    if (top >= 0x7f80u) note_bad(n);
                     any_convert(false);
                     const int bits = *reinterpret_cast<volatile int*>(v_top);
                     const int want = max(-100, (bits >> 7) - 127 - 12);
@@ -830,9 +903,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         // ---- output ----
         if (N > 0) {
-            ok = ok && wait_bar_warp(&o_full[x], 0);
+            // (the last V tile's conversion: v_bad is as it stays)
+            ok = ok && wait_bar_warp(&kv_ready[v_slot(N - 1)], v_par(N - 1)) &&
+                 wait_bar_warp(&o_full[x], 0);
             tc_fence_after();
         }
+        const int last_bad = N > 0 && ok && live ? v_bad[1] : -1;
         const long long row = ((long long)cu0 + i) * a.HQ + h * a.G + r % a.G;
         const bool any = l != 0.f;                           // 0: nothing was seen (NaN is not 0)
         const float back = pow2i(-(int)kLow);                // to weights of 1 at the reference
@@ -880,6 +956,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             __syncwarp();                                    // together into the next load
         }
+        // the infinities and NaN that the row sees, in place of what was summed
+        if (__builtin_expect(last_bad >= 0, 0)) {
+            constexpr int B = E4M3 ? 1 : 2;                  // bytes of an element
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                const uint2 y = not_finite<E4M3>(
+                    static_cast<const char*>(a.vp) + (h * a.head_stride + 32 * c) * B,
+                    a.table + (size_t)s * a.max_pages, sp, n_lo + v_bad[0], n_lo + last_bad, p,
+                    a.window, a.sinks, a.page_shift, a.num_pages, a.page_stride * B,
+                    a.token_stride * B);
+                for (uint32_t left = y.x | y.y; left != 0; left &= left - 1) {
+                    const int e = __ffs(left) - 1, d = 32 * c + e;
+                    // (a NaN that the sum has by itself, of a NaN weight, stays)
+                    const float v = !(l == l) || (y.x & y.y) >> e & 1 ? NAN
+                                    : y.x >> e & 1                    ? INFINITY
+                                                                      : -INFINITY;
+                    if (split)
+                        part.o[at * D + d] = v;
+                    else if (whole)
+                        *reinterpret_cast<__nv_bfloat16*>(
+                            stage + (d >> 6) * P::HALF + (((d >> 3 & 7) ^ (r & 7)) << 4) +
+                            (d & 7) * 2) = __float2bfloat16_rn(v);
+                    else
+                        a.o[row * D + d] = __float2bfloat16_rn(v);
+                }
+            }
+        }
+        __syncwarp();                                        // (not every lane was there)
         if (whole) {
             fence_async_smem();
             asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + x) : "memory");

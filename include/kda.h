@@ -297,11 +297,12 @@ kda_status kda_chunk_fwd_noalloc(const kda_dims* dims, const void* q, const void
  *           weights enter the product with V in two bf16 terms (decode) or in
  *           fp16 (prompts, and both with an e4m3 cache, where q is scaled by a
  *           power of two to fit fp16 too): fp16 rounds a weight by 2^-11 of
- *           itself, or by up to 2^-32 of the row's largest.  For prompts V goes to fp16 with a
- *           power of two shared by the tokens that a block of query rows
- *           reads: values below 2^-29 of the largest finite |v| among them (or
- *           below 2^-117) are rounded, by up to 2^-37 of it.  V of a token should be finite: an infinity or NaN also reaches,
- *           in its channel, prompt queries up to 127 tokens before it.
+ *           itself, or by up to 2^-32 of the row's largest.  For prompts V
+ *           goes to fp16 with a power of two shared by the tokens that a block
+ *           of query rows reads: values below 2^-29 of the largest finite |v|
+ *           among them (or below 2^-117) are rounded, by up to 2^-37 of it.
+ *           An infinity or NaN in V reaches, in its channel, the queries that
+ *           see its token, and no others.
  * Types     q, o and new keys and values are bf16, lse float32.
  * Sizes     D 64 or 128; page_size 16, 32, 64, 128 or 256; HQ a multiple of
  *           HKV with at most 64 query heads per key head; at most 65535

@@ -187,8 +187,8 @@ def test_small_weights_of_a_long_tail(prefill, dtype, nats):
     """The first token takes almost all of the weight and its value is zero: what
     is left is the tail's, all of one sign.  A weight is rounded by up to 2^-11 of
     itself (that is in the usual bound) or, where it is small, by 2^-32 of the largest: half of fp16's
-    smallest step, 2^-25, with the largest at 2^7 or more.  The rows are many, so that
-    no other CTA takes part of one."""
+    smallest step, 2^-25, with the largest at 2^7 or more.  The rows are many, so that no
+    other CTA takes part of one."""
     n = 131072
     c = make_cache([n], 128, 2, 64, dtype, 56, poison=False)
     if c["ks"] is not None:
@@ -268,3 +268,73 @@ def test_values_at_the_ends_of_the_range(big):
     logit = 2.0 ** -16 * X + 2.0 ** -20
     bound = (2.0 ** -9 * ro.abs() + (2.0 ** -9 + 2 * logit[..., None]) * 1.01 * A + 2.0 ** -124)
     assert ((o.double().cpu() - ro).abs() <= bound).all()
+
+
+# ---- infinities and NaN among values ----
+
+VALUES = [math.nan, math.inf, -math.inf]
+
+
+def poisoned(c, s, j, value, channel):
+    v = c["v"].view(torch.uint8) if c["v"].dtype == E4M3 else c["v"]
+    page = c["v"].shape[1]
+    v[c["table"][s, j // page].item(), j % page, :, channel] = (
+        0x7F if c["v"].dtype == E4M3 else value)
+
+
+@pytest.mark.parametrize("kind", [(BF16, 0), (BF16, 1), (BF16, 2), (E4M3, 0)])
+@pytest.mark.parametrize("heads", [(2, 2), (8, 2)])
+@pytest.mark.parametrize("window,sinks,at", [(0, 0, (450,)), (0, 0, (3, 600, 699)), (100, 4, (50,)),
+                                             (100, 4, (2, 500)), (300, 0, (0, 399, 400))])
+@pytest.mark.parametrize("tokens", [700, 2100])
+def test_values_reach_only_the_queries_that_see_them(tokens, window, sinks, at, heads, kind):
+    """NaN and infinities in V, in one channel of some tokens: queries that see
+    one get it, the others and the other channels are as ever."""
+    dtype, which = kind
+    n = 400 if tokens == 700 else 9           # 2100: split over the cached tokens
+    at = [j + tokens - 700 if j > 60 else j for j in at]
+    c = make_cache([tokens], 32, heads[1], 128, dtype, 59)
+    if n == 9:
+        c = widened(c, 8192)
+    for j in at:
+        poisoned(c, 0, j, VALUES[which], 3)
+    q = rand_q(n, heads[0], 128, 60)
+    o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, n]), window=window,
+                               sinks=sinks, return_lse=True)
+    kda.check()
+    p = torch.arange(tokens - n, tokens)
+    sees = torch.zeros(n, dtype=torch.bool)
+    for j in at:
+        see = j <= p
+        if window:
+            see &= (j > p - window) | torch.tensor(j < sinks)
+        sees |= see
+    x = o[..., 3].float().cpu()
+    if which == 0:
+        assert x[sees].isnan().all()
+    else:
+        assert (x[sees] == VALUES[which]).all()
+    clean = dict(c, v=torch.nan_to_num(c["v"], 0, 0, 0) if dtype == BF16 else c["v"])
+    if dtype == E4M3:
+        raw = c["v"].view(torch.uint8).clone()
+        raw[raw == 0x7F] = 0
+        clean = dict(c, v=raw.view(E4M3))
+    ref = ref_prefill(q, clean, [n], 128 ** -0.5, window, sinks)
+    other = [d for d in range(128) if d != 3]
+    check_attention(o[..., other], lse, [y[..., other] if y.dim() == 3 and y.shape[-1] == 128
+                                         else y for y in ref])
+    if not sees.all():
+        check_attention(*rows_of(o, lse, ref, ~sees))
+
+
+def test_infinities_of_both_signs_make_nan():
+    c = make_cache([300], 32, 1, 64, BF16, 61)
+    poisoned(c, 0, 100, math.inf, 3)
+    poisoned(c, 0, 250, -math.inf, 3)
+    poisoned(c, 0, 130, -math.inf, 40)
+    q = rand_q(300, 1, 64, 62)
+    o = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, 300])).float()
+    kda.check()
+    assert o[:100].isfinite().all()
+    assert (o[100:250, 0, 3] == math.inf).all() and o[250:, 0, 3].isnan().all()
+    assert o[:130].isfinite()[..., 40].all() and (o[130:, 0, 40] == -math.inf).all()

@@ -67,6 +67,8 @@ class Hybrid:
         self.table = torch.full((rows, max_pages), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
         self.refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+        # tokens that rows gained in this step: none where the pages ran out
+        self.granted = torch.zeros(rows, dtype=torch.int32, device="cuda")
         first = next(l for l in self.layers if l["kind"] == "attn")["kv"]
         self.ws = kda.paged_decode_workspace(first, rows, heads)
 
@@ -93,7 +95,7 @@ class Hybrid:
             cu[s + 1] = cu[s] + add[s]
         ids = torch.tensor([t for i in order for t in tokens[i]], device="cuda")
         cu = ints(cu)
-        self.book.extend(ints(add), self.table, self.lens, self.refs)
+        self.book.extend(ints(add), self.table, self.lens, self.refs, granted=self.granted)
         x = self.emb[ids]
         for l in self.layers:
             y = self._norm(x)
@@ -113,14 +115,14 @@ class Hybrid:
         H, HKV, D = self.H, self.HKV, self.D
         qkv = (y @ l["qkv"]).view(y.shape[0], H + 2 * HKV, D)
         q, k, v = qkv[:, :H], qkv[:, H:H + HKV], qkv[:, H + HKV:]
-        kda.paged_append(l["kv"], k, v, self.table, self.lens, cu)
+        kda.paged_append(l["kv"], k, v, self.table, self.lens, cu, granted=self.granted)
         if cu is not None:
             return kda.paged_prefill(q, l["kv"], self.table, self.lens, cu)
         return kda.paged_decode(q, l["kv"], self.table, self.lens, workspace=self.ws)
 
     def step(self, ids):
         """One token for each row (idle rows go along); logits [rows, vocab]."""
-        self.book.extend(1, self.table, self.lens, self.refs)
+        self.book.extend(1, self.table, self.lens, self.refs, granted=self.granted)
         x = self.emb[ids]
         for l in self.layers:
             y = self._norm(x)

@@ -132,7 +132,7 @@ struct PagedArgs {
 };
 kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void* k,
                                long long k_stride, const void* v, long long v_stride,
-                               cudaStream_t s);
+                               const int* granted, cudaStream_t s);
 size_t paged_decode_ws_bytes(const PagedArgs& a, int D, bool e4m3);
 kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s);
 size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool e4m3);
@@ -148,7 +148,7 @@ kda_status pages_fork_launch(const kda_pages_dims& d, const kda_page_pool* pools
                              const int* parents, const int* children, int n, int* table,
                              int* lens, int* refs, void* ws, cudaStream_t s);
 kda_status pages_extend_launch(const kda_pages_dims& d, const int* add, int add_all, int* table,
-                               int* lens, int* refs, void* ws, cudaStream_t s);
+                               int* lens, int* refs, int* granted, void* ws, cudaStream_t s);
 kda_status pages_free_launch(const kda_pages_dims& d, const int* slots, int n, int* table,
                              int* lens, int* refs, cudaStream_t s);
 kda_status pages_compact_launch(const kda_pages_dims& d, const kda_page_pool* pools,

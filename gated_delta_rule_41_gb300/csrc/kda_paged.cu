@@ -53,7 +53,7 @@ constexpr int kAppendHeads = 128;                       // whose inverse scales 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, long long k_stride,
-              const __nv_bfloat16* __restrict__ v, long long v_stride) {
+              const __nv_bfloat16* __restrict__ v, long long v_stride, const int* granted) {
     __shared__ int s_seq[kAppendTokens];
     __shared__ long long s_off[kAppendTokens];          // element of the token's row, or -1
     __shared__ float s_inv[2 * kAppendHeads];           // 1 / scale of K, V per head
@@ -113,8 +113,9 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
     if (tid < n) {
         const int t = t0 + tid, s = a.cu ? s_seq[tid] : t;
         const int pos = seq_len(a, s) - (a.cu ? a.cu[s + 1] - t : 1);
-        long long off = -1;                             // before the sequence's start: dropped
-        if (pos >= 0) {
+        // before the sequence's start, or meant for a refused row: dropped
+        long long off = -1;
+        if (pos >= 0 && (!granted || granted[s] > 0)) {
             const int page = a.table[(size_t)s * a.max_pages + (pos >> a.page_shift)];
             if ((unsigned)page < (unsigned)a.num_pages)
                 off = page * a.page_stride + (pos & ((1 << a.page_shift) - 1)) * a.token_stride;
@@ -157,7 +158,7 @@ append_kernel(const PagedArgs a, int TB, const __nv_bfloat16* __restrict__ k, lo
 
 template <int D, bool E4M3>
 kda_status append(const PagedArgs& a, const void* k, long long k_stride, const void* v,
-                  long long v_stride, cudaStream_t s) {
+                  long long v_stride, const int* granted, cudaStream_t s) {
     // tokens of a CTA: its threads' items, but fewer while CTAs are few
     const int per = 2 * a.HKV * (D / 8);                 // 16-byte loads of a token
     const int full = std::min(kAppendTokens,
@@ -166,7 +167,7 @@ kda_status append(const PagedArgs& a, const void* k, long long k_stride, const v
     TimedLaunch tl("paged_append", s);
     append_kernel<D, E4M3><<<(unsigned)((a.T + TB - 1) / TB), kAppendThreads, 0, s>>>(
         a, TB, static_cast<const __nv_bfloat16*>(k), k_stride,
-        static_cast<const __nv_bfloat16*>(v), v_stride);
+        static_cast<const __nv_bfloat16*>(v), v_stride, granted);
     return launch_status();
 }
 
@@ -174,12 +175,12 @@ kda_status append(const PagedArgs& a, const void* k, long long k_stride, const v
 
 kda_status paged_append_launch(const PagedArgs& a, int D, bool e4m3, const void* k,
                                long long k_stride, const void* v, long long v_stride,
-                               cudaStream_t s) {
+                               const int* granted, cudaStream_t s) {
     if (D == 128)
-        return e4m3 ? append<128, true>(a, k, k_stride, v, v_stride, s)
-                    : append<128, false>(a, k, k_stride, v, v_stride, s);
-    return e4m3 ? append<64, true>(a, k, k_stride, v, v_stride, s)
-                : append<64, false>(a, k, k_stride, v, v_stride, s);
+        return e4m3 ? append<128, true>(a, k, k_stride, v, v_stride, granted, s)
+                    : append<128, false>(a, k, k_stride, v, v_stride, granted, s);
+    return e4m3 ? append<64, true>(a, k, k_stride, v, v_stride, granted, s)
+                : append<64, false>(a, k, k_stride, v, v_stride, granted, s);
 }
 
 kda_status paged_take_error(cudaStream_t s) {

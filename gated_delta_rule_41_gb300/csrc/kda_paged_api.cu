@@ -163,13 +163,22 @@ kda_status kda_paged_append(const kda_paged_dims* d, const int* cu, int T, const
                             long long k_stride, const void* v, long long v_stride,
                             const float* ks, const float* vs, const int* table, const int* lens,
                             void* kp, void* vp, void* stream) {
+    return kda_paged_append_granted(d, cu, T, k, k_stride, v, v_stride, ks, vs, table, lens,
+                                    nullptr, kp, vp, stream);
+}
+
+kda_status kda_paged_append_granted(const kda_paged_dims* d, const int* cu, int T, const void* k,
+                                    long long k_stride, const void* v, long long v_stride,
+                                    const float* ks, const float* vs, const int* table,
+                                    const int* lens, const int* granted, void* kp, void* vp,
+                                    void* stream) {
     kda_status st = check_dims(d, false);
     if (st != KDA_OK) return st;
     if (T < 0 || (!cu && T != d->S)) return KDA_ERR_SHAPE;
     if ((long long)T * d->HKV > INT_MAX / 32) return KDA_ERR_UNSUPPORTED;
     if (T == 0) return KDA_OK;
     if (d->S == 0) return KDA_ERR_SHAPE;
-    if (!aligned(cu, 4)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(cu, 4) || !aligned(granted, 4)) return KDA_ERR_ALIGNMENT;
     if ((st = check_cache(kp, vp, ks, vs, table, lens)) != KDA_OK) return st;
     const long long row = (long long)d->HKV * d->D;
     if ((st = check_tokens(k, k_stride, T, row)) != KDA_OK) return st;
@@ -177,7 +186,7 @@ kda_status kda_paged_append(const kda_paged_dims* d, const int* cu, int T, const
     PagedArgs a = make_args(*d);
     fill(a, cu, T, nullptr, 0, kp, vp, ks, vs, table, lens, nullptr, nullptr);
     return paged_append_launch(a, d->D, d->cache_dtype == KDA_E4M3, k, k_stride, v, v_stride,
-                               static_cast<cudaStream_t>(stream));
+                               granted, static_cast<cudaStream_t>(stream));
 }
 
 size_t kda_paged_decode_workspace_bytes(const kda_paged_dims* d) {
@@ -240,14 +249,21 @@ kda_status kda_pages_fork(const kda_pages_dims* d, const kda_page_pool* pools, i
 
 kda_status kda_pages_extend(const kda_pages_dims* d, const int* add, int add_all, int* table,
                             int* lens, int* refs, void* ws, size_t ws_bytes, void* stream) {
+    return kda_pages_extend_granted(d, add, add_all, table, lens, refs, nullptr, ws, ws_bytes,
+                                    stream);
+}
+
+kda_status kda_pages_extend_granted(const kda_pages_dims* d, const int* add, int add_all,
+                                    int* table, int* lens, int* refs, int* granted, void* ws,
+                                    size_t ws_bytes, void* stream) {
     kda_status st = check_pages_dims(d);
     if (st != KDA_OK) return st;
     if (!add && add_all < 0) return KDA_ERR_SHAPE;
     if (d->S == 0) return KDA_OK;
-    if (!aligned(add, 4)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(add, 4) || !aligned(granted, 4)) return KDA_ERR_ALIGNMENT;
     if ((st = check_ints({table, lens, refs})) != KDA_OK) return st;
     if ((st = check_ws(pages_ws_bytes(*d), ws, ws_bytes)) != KDA_OK) return st;
-    return pages_extend_launch(*d, add, add_all, table, lens, refs, ws,
+    return pages_extend_launch(*d, add, add_all, table, lens, refs, granted, ws,
                                static_cast<cudaStream_t>(stream));
 }
 

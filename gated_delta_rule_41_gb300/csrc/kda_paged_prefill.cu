@@ -594,8 +594,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             // the low bits of a NaN code are all ones
                             auto ones = [](uint32_t y) { return (y & 0x7f7f7f7fu) + 0x01010101u; };
                             const uint4 y = *reinterpret_cast<const uint4*>(w);
-                            if (((ones(y.x) | ones(y.y) | ones(y.z) | ones(y.w)) & 0x80808080u) == 0)
-                                continue;
+                            const uint32_t any = ones(y.x) | ones(y.y) | ones(y.z) | ones(y.w);
+                            if ((any & 0x80808080u) == 0) continue;
 #pragma unroll 1
                             for (int e = 0; e < 4; ++e)
                                 w[e] &= ~((ones(w[e]) >> 7 & 0x01010101u) * 0xffu);

@@ -156,10 +156,11 @@ __device__ void deal(const int* list, int found, const int* before, int n, F tak
 // ---- extend ----
 // One CTA.  Request i wants the pages that row i's new length needs beyond
 // those it holds; those that the listed free pages do not cover are refused as
-// a whole, and their rows stay as they were.
+// a whole, and their rows stay as they were.  `granted` (may be null): the
+// tokens that each row gained.
 __global__ void __launch_bounds__(kPlanThreads)
 extend_kernel(kda_pages_dims d, const int* __restrict__ add, int add_all, int* table, int* lens,
-              int* refs, Plan pl) {
+              int* refs, int* granted, Plan pl) {
     __shared__ long long s_wide[32];
     __shared__ int s[32];
     const long long cap = (long long)d.max_pages * d.page_size;
@@ -192,6 +193,7 @@ extend_kernel(kda_pages_dims d, const int* __restrict__ add, int add_all, int* t
     });
     for (int i = threadIdx.x; i < d.S; i += kPlanThreads) {
         const int len = lens[i], more = gain(i, len);
+        if (granted) granted[i] = 0;
         if (more <= 0) continue;
         if (pages_of(len + more, d.page_size) > pages_of(len, d.page_size) &&
             pl.before[i + 1] > have) {
@@ -199,6 +201,7 @@ extend_kernel(kda_pages_dims d, const int* __restrict__ add, int add_all, int* t
             continue;
         }
         lens[i] = len + more;
+        if (granted) granted[i] = more;
     }
 }
 
@@ -473,9 +476,10 @@ int copy_grid(const kda_page_pool* pools, int num_pools, long long pairs) {
 size_t pages_ws_bytes(const kda_pages_dims& d) { return align256(plan_ints(d) * sizeof(int)); }
 
 kda_status pages_extend_launch(const kda_pages_dims& d, const int* add, int add_all, int* table,
-                               int* lens, int* refs, void* ws, cudaStream_t s) {
+                               int* lens, int* refs, int* granted, void* ws, cudaStream_t s) {
     TimedLaunch tl("pages_extend", s);
-    extend_kernel<<<1, kPlanThreads, 0, s>>>(d, add, add_all, table, lens, refs, carve(d, ws));
+    extend_kernel<<<1, kPlanThreads, 0, s>>>(d, add, add_all, table, lens, refs, granted,
+                                             carve(d, ws));
     return launch_status();
 }
 

@@ -6,8 +6,8 @@ all on the device:
 
     pages = KVPages(k, v)                   # pools [num_pages, page_size, HKV, D]
     book = PageBook(num_pages, page_size, pools)
-    book.extend(add, table, lens, refs)     # room for the new tokens
-    paged_append(pages, k_new, v_new, table, lens, cu_seqlens)
+    book.extend(add, table, lens, refs, granted=granted)   # room for the new tokens
+    paged_append(pages, k_new, v_new, table, lens, cu_seqlens, granted=granted)
     o = paged_prefill(q, pages, table, lens, cu_seqlens)      # prompts
     o = paged_decode(q, pages, table, lens)                   # one new token each
 
@@ -58,6 +58,7 @@ def _lib():
         D, G, O = (ctypes.POINTER(x) for x in (KdaPagedDims, KdaPagesDims, KdaPagePool))
         for name, res, args in (
                 ("kda_paged_append", I, [D, P, I, P, L, P, L, P, P, P, P, P, P, P]),
+                ("kda_paged_append_granted", I, [D, P, I, P, L, P, L, P, P, P, P, P, P, P, P]),
                 ("kda_paged_decode_workspace_bytes", S, [D]),
                 ("kda_paged_decode", I, [D, P, L] + [P] * 9 + [S, P]),
                 ("kda_paged_prefill_workspace_bytes", S, [D, I]),
@@ -65,6 +66,7 @@ def _lib():
                 ("kda_pages_workspace_bytes", S, [G]),
                 ("kda_pages_fork", I, [G, O, I, P, P, I, P, P, P, P, S, P]),
                 ("kda_pages_extend", I, [G, P, I, P, P, P, P, S, P]),
+                ("kda_pages_extend_granted", I, [G, P, I, P, P, P, P, P, S, P]),
                 ("kda_pages_free", I, [G, P, I, P, P, P, P]),
                 ("kda_pages_compact", I, [G, O, I, P, P, P, S, P]),
                 ("kda_pages_copy", I, [O, I, I, P, P, I, P])):
@@ -179,11 +181,14 @@ class KVPages:
         return got
 
 
-def paged_append(pages: KVPages, k, v, block_table, kv_lens, cu_seqlens=None, stream=None):
+def paged_append(pages: KVPages, k, v, block_table, kv_lens, cu_seqlens=None, stream=None,
+                 granted=None):
     """Write new tokens k, v [T, HKV, D] (bf16; slices of a wider projection
     will do) into the pages.  ``kv_lens`` [S] counts the new tokens already:
     with ``cu_seqlens`` [S + 1] sequence s owns tokens cu_seqlens[s] to
-    cu_seqlens[s + 1] and they become its last ones; without, one each."""
+    cu_seqlens[s + 1] and they become its last ones; without, one each.
+    ``granted`` [S], from ``PageBook.extend``: tokens of a row that gained none
+    are dropped; without it they would replace the last ones of a refused row."""
     lib = _lib()
     ks, vs = _tokens("k", k, pages.HKV, pages.D), _tokens("v", v, pages.HKV, pages.D)
     T, (S, width) = k.shape[0], block_table.shape
@@ -193,8 +198,10 @@ def paged_append(pages: KVPages, k, v, block_table, kv_lens, cu_seqlens=None, st
     cu = None if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, 1, S + 1)
     d, _ = pages._call(S, pages.HKV, width, None, 0, 0, 0)
     kp, vp, sk, sv = pages._ptrs
-    _raise(lib.kda_paged_append(d, cu, T, k.data_ptr(), ks, v.data_ptr(), vs, sk, sv, table, lens,
-                                kp, vp, _raw_stream(stream)), "kda_paged_append")
+    got = None if granted is None else _ints("granted", granted, 1, S)
+    _raise(lib.kda_paged_append_granted(d, cu, T, k.data_ptr(), ks, v.data_ptr(), vs, sk, sv, table,
+                                        lens, got, kp, vp, _raw_stream(stream)),
+           "kda_paged_append")
 
 
 def _attention_workspace(need, workspace, device, stream):
@@ -321,7 +328,9 @@ class PageBook:
     tensors, updated in place in stream order: block_table int32 [S, max_pages]
     (-1: no page), kv_lens int32 [S], refs int32 [num_pages] (0: free).  Pages
     are taken lowest id first.  Refused requests (too few free pages) show in
-    ``check()`` as KdaError with status 8; their rows stay as they were.
+    ``check()`` as KdaError with status 8; their rows stay as they were, and the
+    new tokens meant for them are dropped if ``extend``'s ``granted`` goes on to
+    ``paged_append``.
 
     A PageBook keeps one workspace: its calls belong on one stream at a time."""
 
@@ -361,14 +370,17 @@ class PageBook:
         _raise(_lib().kda_pages_fork(d, self._arr, len(self.pools), p, c, n, table, lens, counts,
                                      ws, n_ws, _raw_stream(stream)), "kda_pages_fork")
 
-    def extend(self, add, block_table, kv_lens, refs, stream=None):
+    def extend(self, add, block_table, kv_lens, refs, stream=None, granted=None):
         """Lengths grow by ``add`` (int32 [S]; or an int, for the rows with
-        tokens), and rows get the pages they then need."""
+        tokens), and rows get the pages they then need.  ``granted`` (int32 [S],
+        written): the tokens that each row gained, for ``paged_append``."""
         d, table, lens, counts, ws, n_ws = self._args(block_table, kv_lens, refs, stream)
         each = isinstance(add, torch.Tensor)
         more = _ints("add", add, 1, kv_lens.shape[0]) if each else None
-        _raise(_lib().kda_pages_extend(d, more, 0 if each else int(add), table, lens, counts, ws,
-                                       n_ws, _raw_stream(stream)), "kda_pages_extend")
+        got = None if granted is None else _ints("granted", granted, 1, kv_lens.shape[0])
+        _raise(_lib().kda_pages_extend_granted(d, more, 0 if each else int(add), table, lens,
+                                               counts, got, ws, n_ws, _raw_stream(stream)),
+               "kda_pages_extend")
 
     def free(self, slots, block_table, kv_lens, refs, stream=None):
         """Release the rows ``slots`` (int32, distinct)."""

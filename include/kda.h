@@ -343,6 +343,18 @@ kda_status kda_paged_append(const kda_paged_dims* dims, const int* cu_seqlens, i
                             const float* k_scale, const float* v_scale, const int* block_table,
                             const int* kv_lens, void* k_pages, void* v_pages, void* stream);
 
+/* The same for a step whose room kda_pages_extend_granted made: granted int32
+ * [S] (device, may be NULL) are the tokens that each row gained, and the new
+ * tokens of a row that gained none are dropped.  (Without it they would become
+ * the last tokens that the refused row already has, in a page that other rows may
+ * share.) */
+kda_status kda_paged_append_granted(const kda_paged_dims* dims, const int* cu_seqlens, int T,
+                                    const void* k, long long k_stride, const void* v,
+                                    long long v_stride, const float* k_scale,
+                                    const float* v_scale, const int* block_table,
+                                    const int* kv_lens, const int* granted, void* k_pages,
+                                    void* v_pages, void* stream);
+
 /* Attention of one new token per sequence: q, o [S][HQ][D] (q rows q_stride
  * elements apart, o dense), lse float [S][HQ] or NULL; the query stands at
  * position kv_lens[s] - 1 (its own key and value already appended).  The
@@ -409,6 +421,14 @@ kda_status kda_pages_fork(const kda_pages_dims* dims, const kda_page_pool* pools
 kda_status kda_pages_extend(const kda_pages_dims* dims, const int* add, int add_all,
                             int* block_table, int* kv_lens, int* refs, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* The same; granted int32 [S] (device, may be NULL) gets the tokens that each
+ * row gained: what was asked for, or 0 where the request was refused.  Pass it
+ * on to kda_paged_append_granted: a refused row keeps its length, and its new token
+ * must not be written over its last one. */
+kda_status kda_pages_extend_granted(const kda_pages_dims* dims, const int* add, int add_all,
+                                    int* block_table, int* kv_lens, int* refs, int* granted,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Release the rows slots[0..n) (distinct): their pages' counts drop by one,
  * the rows become idle. */

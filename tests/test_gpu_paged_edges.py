@@ -338,3 +338,76 @@ def test_infinities_of_both_signs_make_nan():
     assert o[:100].isfinite().all()
     assert (o[100:250, 0, 3] == math.inf).all() and o[250:, 0, 3].isnan().all()
     assert o[:130].isfinite()[..., 40].all() and (o[130:, 0, 40] == -math.inf).all()
+
+
+# ---- refused requests and the tokens that were meant for them ----
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("packed", [False, True])
+def test_tokens_of_a_refused_row_are_dropped(packed, dtype):
+    """Rows 0 and 1 share a full page, the pool has one page left, rows 0, 1 and 2
+    each need one: row 0 gets it, and the tokens of the others change nothing."""
+    page, HKV, D, pages = 16, 1, 64, 5
+    k = torch.zeros(pages, page, HKV, D, device="cuda").to(dtype)
+    v = k.clone()
+    cache, book = kda.KVPages(k, v), kda.PageBook(pages, page, [k, v])
+    table = torch.full((5, 4), -1, dtype=torch.int32, device="cuda")
+    lens, refs = ints([0] * 5), ints([0] * pages)
+    granted = ints([9] * 5)
+    args = table, lens, refs
+
+    def tokens(n, value):
+        return torch.full((n, HKV, D), value, dtype=BF16, device="cuda")
+
+    book.extend(ints([32, 0, 16, 5, 0]), *args, granted=granted)
+    assert granted.tolist() == [32, 0, 16, 5, 0]
+    x = tokens(53, 1.0)
+    kda.paged_append(cache, x, x, table, lens, ints([0, 32, 32, 48, 53, 53]), granted=granted)
+    book.fork(ints([0]), ints([1]), *args)
+    kda.check()
+    assert lens.tolist() == [32, 32, 16, 5, 0] and int((refs == 0).sum()) == 1
+    before = k.clone(), v.clone()
+    if packed:
+        n = [2, 3, 1, 1, 0]
+        book.extend(ints(n), *args, granted=granted)
+        x = torch.cat([tokens(m, 2.0 + i) for i, m in enumerate(n)])
+        cu = ints([0] + n).cumsum(0).to(torch.int32)
+        kda.paged_append(cache, x, x, table, lens, cu, granted=granted)
+    else:
+        n = [1, 1, 1, 1, 0]
+        book.extend(1, *args, granted=granted)
+        x = torch.cat([tokens(1, 2.0 + i) for i in range(5)])
+        kda.paged_append(cache, x, x, table, lens, granted=granted)
+    with pytest.raises(kda.KdaError) as e:
+        kda.check()
+    assert e.value.status == 8
+    assert granted.tolist() == [n[0], 0, 0, n[3], 0]
+    assert lens.tolist() == [32 + n[0], 32, 16, 5 + n[3], 0]
+    for pool, old in zip((k, v), before):
+        want = old.clone().float()
+        want[table[0, 2].item(), :n[0]] = 2.0
+        want[table[3, 0].item(), 5:5 + n[3]] = 5.0
+        assert torch.equal(pool.float(), want)
+
+
+def test_granted_of_requests_that_cannot_be():
+    book = kda.PageBook(9, 16)
+    table = torch.full((4, 2), -1, dtype=torch.int32, device="cuda")
+    args = table, ints([0, 3, 0, 0]), ints([0] * 9)
+    table[1, 0] = 8
+    args[2][8] = 1
+    granted = ints([7] * 4)
+    book.extend(ints([33, -1, 20, 0]), *args, granted=granted)
+    with pytest.raises(kda.KdaError) as e:
+        kda.check()
+    assert e.value.status == 2
+    assert granted.tolist() == [0, 0, 20, 0] and args[1].tolist() == [0, 3, 20, 0]
+    with pytest.raises(kda.KdaError) as e:
+        book.extend(1, *args, granted=granted[:3])
+    assert e.value.status == 1
+    k = torch.zeros(9, 16, 1, 64, dtype=BF16, device="cuda")
+    x = torch.ones(4, 1, 64, dtype=BF16, device="cuda")
+    with pytest.raises(kda.KdaError) as e:
+        kda.paged_append(kda.KVPages(k, k), x, x, table, args[1], granted=granted.long())
+    assert e.value.status == 1
+    kda.check()

@@ -90,13 +90,16 @@ def _raw_stream(stream) -> int:
     return _get_stream(_get_device())
 
 
-def _fresh(stream, *tensors):
-    """Tensors allocated here for a launch on ``stream``: the allocator may
-    not hand their memory to the current stream before that launch is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _fresh(stream, shape, dtype, device):
+    """A tensor that a launch on ``stream`` writes and the caller goes on with: of
+    that stream's memory, since what was given back on the current one may still
+    be in use there; and not given back before the current stream is done too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 def _ints(name, t, dim, n=None):
@@ -216,16 +219,13 @@ def _attention_workspace(need, workspace, device, stream):
 
 def _outputs(q, out, lse, return_lse, stream):
     if out is None:
-        out = (torch.empty_like(q) if q.is_contiguous() else
-               torch.empty(q.shape, dtype=q.dtype, device=q.device))
-        _fresh(stream, out)
+        out = _fresh(stream, q.shape, q.dtype, q.device)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda \
             or not out.is_contiguous():
         raise KdaError(1, "out must be a contiguous CUDA tensor of q's shape and type")
     if lse is None:
         if return_lse:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-            _fresh(stream, lse)
+            lse = _fresh(stream, q.shape[:2], torch.float32, q.device)
     elif lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_cuda \
             or not lse.is_contiguous():
         raise KdaError(1, "lse must be a contiguous float32 CUDA tensor [rows, HQ]")
@@ -339,7 +339,7 @@ class PageBook:
         if len(self.pools) > MAX_POOLS:
             raise KdaError(3, f"{len(self.pools)} pools (at most {MAX_POOLS})")
         self._arr = _pool_array(self.pools, num_pages)
-        self._ws, self._need, self._dims = None, 0, {}
+        self._ws, self._need, self._home, self._dims = None, 0, None, {}
 
     def _args(self, block_table, kv_lens, refs, stream):
         table = _ints("block_table", block_table, 2)
@@ -354,10 +354,11 @@ class PageBook:
             got = self._dims[S, width] = (d, int(_lib().kda_pages_workspace_bytes(d)))
         d, need = got
         if need > self._need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=refs.device)
-            self._need = need
-        if self._ws is not None:
-            _fresh(stream, self._ws)
+            self._ws = _fresh(stream, need, torch.uint8, refs.device)
+            self._need, self._home = need, _raw_stream(stream)
+        elif self._ws is not None and _raw_stream(stream) != self._home:
+            # not given back before that one is done
+            self._ws.record_stream(torch.cuda.current_stream() if stream is None else stream)
         return (d, table, lens, counts, None if self._ws is None else self._ws.data_ptr(),
                 self._need)
 

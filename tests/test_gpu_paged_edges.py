@@ -411,3 +411,53 @@ def test_granted_of_requests_that_cannot_be():
         kda.paged_append(kda.KVPages(k, k), x, x, table, args[1], granted=granted.long())
     assert e.value.status == 1
     kda.check()
+
+
+# ---- streams ----
+
+@pytest.mark.parametrize("call", ["decode", "prefill", "extend"])
+def test_memory_of_a_call_on_another_stream(call):
+    """Memory that was given back on the current stream, where work on it is still
+    queued, is not written early by a call on another stream."""
+    c = make_cache([100] * 64, 32, 2, 128, BF16, 63, poison=False)
+    q, pages = rand_q(64, 32, 128, 64), kv(c)
+    ws = kda.paged_decode_workspace(pages, 64, 32)
+    side = torch.cuda.Stream()
+    cu = torch.arange(65, dtype=torch.int32, device="cuda")
+    lse = torch.empty(64, 32, device="cuda")
+    table = torch.full((2, 30000), -1, dtype=torch.int32, device="cuda")
+    args = table, ints([0, 0]), ints([0] * 40000)
+    add = ints([450000, 10])
+    def run():
+        if call == "decode":
+            kda.paged_decode(q, pages, c["table"], c["lens"], lse=lse, workspace=ws, stream=side)
+        elif call == "prefill":
+            kda.paged_prefill(q, pages, c["table"], c["lens"], cu, lse=lse, stream=side)
+        else:
+            kda.PageBook(40000, 16).extend(add, *args, stream=side)
+
+    run()                                     # (a first launch may wait for the GPU)
+    torch.cuda.synchronize()
+    args[1].zero_()
+    args[2].zero_()
+    need = 1 << 19                            # bytes of q, and about the book's workspace
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # every free piece of that size, all given back with a copy of them still queued
+    ys = torch.zeros(256, need, dtype=torch.uint8, device="cuda")
+    xs = [torch.full((need,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    held = torch.cuda.memory_reserved()
+    while held == torch.cuda.memory_reserved():
+        xs.append(torch.full((need,), 7, dtype=torch.uint8, device="cuda"))
+    xs.pop()
+    torch.cuda.empty_cache()
+    n = len(xs)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    for x, y in zip(xs, ys):
+        y.copy_(x)
+    del x, xs
+    run()
+    torch.cuda.synchronize()
+    kda.check()
+    assert (ys[:n] == 7).all()

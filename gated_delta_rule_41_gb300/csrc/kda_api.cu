@@ -3,11 +3,53 @@
 // nothing and writes nothing.
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "kda_common.cuh"
 
 namespace {
 
 using namespace kda;
+
+// The kernels' error words, read and cleared together: one launch, one copy and one wait
+// for a check, whatever the number of words.
+constexpr int kErrorWords = 6, kCheckSlots = 64;
+struct ErrorWords {
+    int* p[kErrorWords];
+    int code[kErrorWords];   // what a word that is not 0 stands for; 0: itself
+};
+__device__ int g_check[kCheckSlots];
+
+__global__ void take_errors(ErrorWords w, unsigned slot) {
+    int first = 0;
+    for (int i = 0; i < kErrorWords; ++i) {
+        const int e = atomicExch(w.p[i], 0);
+        if (first == 0 && e != 0) first = w.code[i] ? w.code[i] : e;
+    }
+    g_check[slot] = first;
+}
+
+// Their addresses on the current device.
+bool error_words(ErrorWords& w) {
+    static ErrorWords known[64];
+    static std::atomic<bool> have[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!have[dev].load(std::memory_order_acquire)) {
+        w = {{tc_error_word(), simt_error_word(), paged_error_word(), paged_decode_error_word(),
+              paged_prefill_error_word(), pages_error_word()},
+             {KDA_ERR_TIMEOUT, KDA_ERR_SHAPE, 0, 0, 0, 0}};
+        for (int* p : w.p)
+            if (!p) return false;
+        static std::mutex m;
+        std::lock_guard<std::mutex> lock(m);
+        known[dev] = w;
+        have[dev].store(true, std::memory_order_release);
+    }
+    w = known[dev];
+    return true;
+}
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -338,15 +380,19 @@ kda_status kda_recurrent_step(const kda_dims* d, const void* q, const void* k, c
 }
 
 kda_status kda_check(void* stream) {
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ErrorWords w;
+    if (!error_words(w)) return KDA_ERR_CUDA;
+    // a slot for each call, as other threads may ask on other streams
+    static std::atomic<unsigned> calls{0};
+    const unsigned slot = calls.fetch_add(1) % kCheckSlots;
+    take_errors<<<1, 1, 0, s>>>(w, slot);
+    int err = 0;
+    if (cudaMemcpyFromSymbolAsync(&err, g_check, sizeof(int), slot * sizeof(int),
+                                  cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
         return KDA_ERR_CUDA;
-    kda_status st = tc_take_error(static_cast<cudaStream_t>(stream));
-    if (st != KDA_OK) return st;
-    if ((st = simt_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
-    if ((st = paged_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
-    if ((st = paged_decode_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
-    if ((st = paged_prefill_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
-    if ((st = pages_take_error(static_cast<cudaStream_t>(stream))) != KDA_OK) return st;
+    if (err != 0) return static_cast<kda_status>(err);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -72,9 +72,8 @@ kda_status simt_bwd_varlen(const kda_dims& d, const int* cu, int nseq, const voi
                            const float* h0, const void* dout, const float* dht, void* dq,
                            void* dk, void* dv, void* dg, void* dbeta, float* dh0, void* ws,
                            cudaStream_t s);
-// Reads and clears the device error word of the SIMT kernels (invalid
-// cu_seqlens: KDA_ERR_SHAPE).
-kda_status simt_take_error(cudaStream_t s);
+// The device error word of the SIMT kernels (not 0: invalid cu_seqlens).
+int* simt_error_word();
 // The chunk table of a packed batch (both kernel families): ctab [NT][2] =
 // (first token, valid rows) of every chunk slot, sfirst [nseq + 1] = each
 // sequence's first slot; an invalid cu_seqlens is recorded for kda_check and
@@ -106,8 +105,8 @@ kda_status tc_bwd_varlen(const kda_dims& d, const int* cu, int nseq, const void*
                          const void* dout, const float* dht, void* dq, void* dk, void* dv,
                          void* dg, void* dbeta, float* dh0, void* ws, bool from_saved,
                          cudaStream_t s);
-// Reads and clears the device error word of the tensor-core kernels.
-kda_status tc_take_error(cudaStream_t s);
+// The device error word of the tensor-core kernels (not 0: a wait expired).
+int* tc_error_word();
 // Diagnostic: a bounded wait on an mbarrier nothing arrives at, with the given
 // limit (cycles); it records KDA_ERR_TIMEOUT for the next kda_check.
 kda_status tc_selftest_timeout(long long limit_cycles, cudaStream_t s);
@@ -137,10 +136,10 @@ size_t paged_decode_ws_bytes(const PagedArgs& a, int D, bool e4m3);
 kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s);
 size_t paged_prefill_ws_bytes(const PagedArgs& a, int D, bool e4m3);
 kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, cudaStream_t s);
-// Reads and clears the device error words of the paged kernels.
-kda_status paged_take_error(cudaStream_t s);
-kda_status paged_decode_take_error(cudaStream_t s);
-kda_status paged_prefill_take_error(cudaStream_t s);
+// Device error words of the paged kernels (a kda_status).
+int* paged_error_word();
+int* paged_decode_error_word();
+int* paged_prefill_error_word();
 
 // ---- page bookkeeping ----
 size_t pages_ws_bytes(const kda_pages_dims& d);
@@ -155,6 +154,6 @@ kda_status pages_compact_launch(const kda_pages_dims& d, const kda_page_pool* po
                                 int num_pools, int* table, int* refs, void* ws, cudaStream_t s);
 kda_status pages_copy_launch(const kda_page_pool* pools, int num_pools, int num_pages,
                              const int* src, const int* dst, int n, cudaStream_t s);
-kda_status pages_take_error(cudaStream_t s);
+int* pages_error_word();
 
 }  // namespace kda

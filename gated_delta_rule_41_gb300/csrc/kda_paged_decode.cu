@@ -785,19 +785,9 @@ kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void* ws, c
     return e4m3 ? launch<64, true, 2>(a, ws, s) : launch<64, false, 2>(a, ws, s);
 }
 
-kda_status paged_decode_take_error(cudaStream_t s) {
-    int err = 0;
-    if (cudaMemcpyFromSymbolAsync(&err, g_paged_decode_error, sizeof(int), 0,
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    if (err == 0) return KDA_OK;
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_paged_decode_error, &zero, sizeof(int), 0,
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    cudaStreamSynchronize(s);
-    return static_cast<kda_status>(err);
+int* paged_decode_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_paged_decode_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace kda

@@ -1151,19 +1151,9 @@ kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, 
     return e4m3 ? launch<64, true>(a, ws, s) : launch<64, false>(a, ws, s);
 }
 
-kda_status paged_prefill_take_error(cudaStream_t s) {
-    int err = 0;
-    if (cudaMemcpyFromSymbolAsync(&err, g_paged_prefill_error, sizeof(int), 0,
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    if (err == 0) return KDA_OK;
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_paged_prefill_error, &zero, sizeof(int), 0,
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    cudaStreamSynchronize(s);
-    return static_cast<kda_status>(err);
+int* paged_prefill_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_paged_prefill_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace kda

@@ -531,19 +531,9 @@ kda_status pages_copy_launch(const kda_page_pool* pools, int num_pools, int num_
     return launch_status();
 }
 
-kda_status pages_take_error(cudaStream_t s) {
-    int err = 0;
-    if (cudaMemcpyFromSymbolAsync(&err, g_pages_error, sizeof(int), 0, cudaMemcpyDeviceToHost,
-                                  s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    if (err == 0) return KDA_OK;
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_pages_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-        cudaSuccess)
-        return KDA_ERR_CUDA;
-    cudaStreamSynchronize(s);
-    return static_cast<kda_status>(err);
+int* pages_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_pages_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace kda

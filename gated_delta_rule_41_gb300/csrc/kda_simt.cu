@@ -1244,19 +1244,9 @@ kda_status simt_bwd_varlen(const kda_dims& kd, const int* cu, int nseq, const vo
                              s);
 }
 
-kda_status simt_take_error(cudaStream_t s) {
-    int err = 0;
-    if (cudaMemcpyFromSymbolAsync(&err, g_simt_error, sizeof(int), 0, cudaMemcpyDeviceToHost,
-                                  s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    if (err == 0) return KDA_OK;
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_simt_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-        cudaSuccess)
-        return KDA_ERR_CUDA;
-    cudaStreamSynchronize(s);
-    return KDA_ERR_SHAPE;
+int* simt_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_simt_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 kda_status group_sum_launch(const kda_dims& kd, const float* dqh, const float* dkh,

@@ -3861,19 +3861,9 @@ kda_status tc_selftest_timeout(long long limit_cycles, cudaStream_t s) {
     return launch_status();
 }
 
-kda_status tc_take_error(cudaStream_t s) {
-    int err = 0;
-    if (cudaMemcpyFromSymbolAsync(&err, g_tc_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
-        cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    if (err == 0) return KDA_OK;
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_tc_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-        cudaSuccess)
-        return KDA_ERR_CUDA;
-    cudaStreamSynchronize(s);
-    return KDA_ERR_TIMEOUT;
+int* tc_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_tc_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace kda

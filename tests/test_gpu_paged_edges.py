@@ -461,3 +461,20 @@ def test_memory_of_a_call_on_another_stream(call):
     torch.cuda.synchronize()
     kda.check()
     assert (ys[:n] == 7).all()
+
+
+# ---- errors ----
+
+def test_one_check_reports_and_clears_every_error():
+    c = make_cache([40, 20], 16, 1, 64, BF16, 65, poison=False)
+    q = rand_q(2, 2, 64, 66)
+    bad = ints([-1, 20])
+    for _ in range(2):
+        kda.paged_append(kv(c), q[:, :1], q[:, 1:], c["table"] - 5000, c["lens"])
+        kda.paged_decode(q, kv(c), c["table"], bad)
+        kda.paged_prefill(q, kv(c), c["table"], bad, ints([0, 1, 2]))
+        kda.PageBook(4, 16).extend(-1 * ints([1]), ints([[-1]]), ints([0]), ints([0] * 4))
+        with pytest.raises(kda.KdaError) as e:
+            kda.check()
+        assert e.value.status == 2
+        kda.check()

@@ -59,8 +59,10 @@ PagedArgs make_args(const kda_paged_dims& d) {
     a.token_stride = d.token_stride;
     a.head_stride = d.head_stride;
     a.scale = d.scale;
-    a.window = d.window;
-    a.sinks = d.window ? d.sinks : 0;
+    // a window as wide as the table hides nothing (and the kernels' sums of positions and
+    // windows stay in range)
+    a.window = d.window < a.cap ? d.window : 0;
+    a.sinks = a.window ? d.sinks : 0;
     return a;
 }
 

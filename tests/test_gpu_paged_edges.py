@@ -478,3 +478,24 @@ def test_one_check_reports_and_clears_every_error():
             kda.check()
         assert e.value.status == 2
         kda.check()
+
+
+# ---- windows and tables ----
+
+@pytest.mark.parametrize("window", [10, 79, 80, 1 << 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_windows_as_wide_as_can_be(dtype, window):
+    """A window past any length hides nothing, with queries before the first
+    token too."""
+    lens, qn = [10, 0, 70], [30, 4, 75]
+    c = make_cache(lens, 16, 1, 64, dtype, 67)
+    c = dict(c, table=c["table"].contiguous())
+    q = rand_q(sum(qn), 2, 64, 68)
+    cu = ints([0] + qn).cumsum(0).to(torch.int32)
+    o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], cu, window=window, sinks=3,
+                               return_lse=True)
+    d, dl = kda.paged_decode(q[:3], kv(c), c["table"], c["lens"], window=window, sinks=2 ** 31 - 1,
+                             return_lse=True)
+    kda.check()
+    check_attention(o, lse, ref_prefill(q, c, qn, 0.125, window, 3))
+    check_attention(d, dl, ref_decode(q[:3], c, 0.125, window, 2 ** 31 - 1))

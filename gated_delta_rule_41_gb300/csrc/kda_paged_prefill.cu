@@ -49,8 +49,8 @@
 // * Infinities and NaN in V to zeros (e4m3: in tiles that not all rows see whole), since a
 //   weight of 0 would not keep them from the rows that do not see their token; the rows
 //   that do get them at the end.
-// * V rows past the sequence's end (they may hold NaN) to zeros.  Pages past
-//   it, and pages out of range, are asked for at a coordinate outside the
+// * V rows past the sequence's end (they may hold NaN) to zeros.  Pages that none
+//   of the rows sees, and pages out of range, are asked for at a coordinate outside the
 //   pool, which TMA fills with zeros.
 //
 // Roles: warps 0-3 softmax and output of tile A, 4-7 of B, warp 8 TMA, warp 9
@@ -448,12 +448,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int rows = min(1 << a.page_shift, kTile);  // rows of a box
             const int boxes = kTile / rows;
             const int* table = a.table + (size_t)s * a.max_pages;
+            const int low = a.window ? p0 - a.window + 1 : 0;    // first token of the window
             int issued = 0;
             for (int n = 0; n < N; ++n) {
                 const int j0 = sp.tile(n_lo + n) * kTile;
                 int page = a.num_pages;                      // outside the pool: zeros
                 const int j = j0 + lane * rows;
-                if (lane < boxes && j < len) {
+                // (pages that none of the rows sees may have been given back)
+                if (lane < boxes && j <= p_last && (j + rows > low || j < a.sinks)) {
                     page = __ldg(table + (j >> a.page_shift));
                     if ((unsigned)page >= (unsigned)a.num_pages) {
                         record(KDA_ERR_SHAPE);

@@ -284,7 +284,8 @@ kda_status kda_chunk_fwd_noalloc(const kda_dims* dims, const void* q, const void
  *           lies in row j % page_size of page block_table[s][j / page_size].
  *           kv_lens int32 [S] (device): tokens of each sequence in the cache,
  *           the ones a call writes or asks about included.  Entries past the
- *           last page of a sequence are not read.  Row slots past a sequence's
+ *           last page of a sequence, and those of pages that no query of a
+ *           call sees (behind its window), are not read.  Row slots past a sequence's
  *           last token may hold anything, NaN included.
  * Attention Query head h reads key head h / (HQ / HKV).  A query at position p
  *           sees token j iff  j <= p and (window == 0 or j > p - window or

@@ -499,3 +499,28 @@ def test_windows_as_wide_as_can_be(dtype, window):
     kda.check()
     check_attention(o, lse, ref_prefill(q, c, qn, 0.125, window, 3))
     check_attention(d, dl, ref_decode(q[:3], c, 0.125, window, 2 ** 31 - 1))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("sinks", [0, 4])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_pages_behind_the_window_may_be_released(dtype, sinks, page):
+    """A window layer may give pages back that no query sees any more: they are
+    not read, and not reported."""
+    tokens, n, window = 1000, 20, 300
+    c = make_cache([tokens], page, 2, 64, dtype, 69)
+    low = tokens - n - window + 1              # the first token that a query sees
+    gone = [i for i in range(low // page) if i * page >= sinks]
+    keep = c["table"].clone()
+    c["table"][0, gone] = -1
+    q = rand_q(n, 4, 64, 70)
+    for wide in (0, 4096):
+        t = widened(c, wide)["table"] if wide else c["table"]
+        o, lse = kda.paged_prefill(q, kv(c), t, c["lens"], ints([0, n]), window=window,
+                                   sinks=sinks, return_lse=True)
+        kda.check()
+        check_attention(o, lse, ref_prefill(q, dict(c, table=keep), [n], 0.125, window, sinks))
+    d, dl = kda.paged_decode(q[-1:], kv(c), c["table"], c["lens"], window=window, sinks=sinks,
+                             return_lse=True)
+    kda.check()
+    check_attention(d, dl, ref_decode(q[-1:], dict(c, table=keep), 0.125, window, sinks))

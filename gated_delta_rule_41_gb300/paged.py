@@ -136,7 +136,9 @@ class KVPages:
             if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
                 raise KdaError(1, f"{n} pool must be a CUDA tensor [pages, rows, HKV, D] with "
                                   "contiguous D")
-        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        # of a dimension of one, torch may report any stride
+        st, sv = ([0 if n == 1 else x for n, x in zip(t.shape, t.stride())] for t in (k, v))
+        if k.shape != v.shape or k.dtype != v.dtype or st != sv:
             raise KdaError(1, "the K and V pools must share shape, type and strides")
         codes = {torch.bfloat16: KDA_BF16, torch.float8_e4m3fn: KDA_E4M3, torch.float32: KDA_F32}
         if k.dtype not in codes:
@@ -152,8 +154,7 @@ class KVPages:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.HKV, self.D = k.shape
         self._code = codes[k.dtype]
-        st = k.stride()   # of a dimension of one, torch may report any stride
-        self._strides = tuple(0 if n == 1 else x for n, x in zip(k.shape, st))
+        self._strides = tuple(st)
         self._calls = {}   # dims (and workspace bytes) of the calls seen
         self._ptrs = (k.data_ptr(), v.data_ptr(),
                       None if k_scale is None else k_scale.data_ptr(),

@@ -524,3 +524,18 @@ def test_pages_behind_the_window_may_be_released(dtype, sinks, page):
                              return_lse=True)
     kda.check()
     check_attention(d, dl, ref_decode(q[-1:], dict(c, table=keep), 0.125, window, sinks))
+
+
+# ---- pools with a dimension of one ----
+
+def test_strides_of_a_dimension_of_one_do_not_matter():
+    g = torch.Generator().manual_seed(74)
+    k = torch.randn(6, 1, 16, 64, generator=g).to(BF16).cuda().transpose(1, 2)
+    v = torch.randn(6, 16, 1, 64, generator=g).to(BF16).cuda()
+    assert k.shape == v.shape and k.stride() != v.stride()
+    table, lens = ints([[3, 1, 5]]), ints([40])
+    q = rand_q(1, 4, 64, 75)
+    o = kda.paged_decode(q, kda.KVPages(k, v), table, lens)
+    same = kda.paged_decode(q, kda.KVPages(k.contiguous(), v), table, lens)
+    kda.check()
+    assert torch.equal(o, same)

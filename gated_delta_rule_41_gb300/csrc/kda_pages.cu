@@ -467,7 +467,7 @@ int copy_grid(const kda_page_pool* pools, int num_pools, long long pairs) {
     long long most = 1;
     for (int i = 0; i < num_pools; ++i)
         most = std::max(most, (pools[i].page_bytes + kPieceBytes - 1) / kPieceBytes);
-    const long long want = std::max<long long>(1, 152 * 8 / std::max(1, num_pools));
+    const long long want = std::max(1, paged::sm_count() * 8 / std::max(1, num_pools));
     return (int)std::max<long long>(1, std::min(want, most * pairs));
 }
 
@@ -494,7 +494,8 @@ kda_status pages_fork_launch(const kda_pages_dims& d, const kda_page_pool* pools
         if (st != KDA_OK) return st;
     }
     TimedLaunch tl("pages_fork", s);
-    const dim3 grid(std::max(copy_grid(pools, num_pools, n), std::min(n, 152)), num_pools + 1);
+    const dim3 grid(std::max(copy_grid(pools, num_pools, n), std::min(n, paged::sm_count())),
+                    num_pools + 1);
     return paged::launch_overlapped(fork_kernel, grid, kCopyThreads, 0, s,
                                     make_pools(pools, num_pools), d, parents, children, n, table,
                                     lens, refs, pl);

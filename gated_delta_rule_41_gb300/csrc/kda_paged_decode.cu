@@ -419,9 +419,10 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
         out.unit = E4M3 && a.vs ? a.vs[h] : 1.f;
 
         // ---- Q as the B operand: head g (+ 8 n), channels of this lane ----
-        // e4m3: q in fp16, scaled by a power of two to at most 2 (put back into
-        // the logits' factor); channel pairs in the order that a 32-bit piece
-        // of a K row gives them.
+        // e4m3: q in fp16, the largest scaled by a power of two to [2^14, 2^15) (put
+        // back into the logits' factor), so that channels down to 2^-31 of it are
+        // exact; channel pairs in the order that a 32-bit piece of a K row gives
+        // them.
         uint32_t qf[NH][KS][2];
         float f[NH][2];                                  // logit factors of heads 2t, 2t + 1
 #pragma unroll
@@ -454,8 +455,8 @@ decode_kernel(const PagedArgs a, int HB, unsigned* __restrict__ tickets,
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // exponent of the largest, as far as 2^-e is a normal number
-                const int e = max(-126, min(126, (int)(__float_as_uint(top) >> 23) - 127));
+                // as far as 2^-e is a normal number
+                const int e = max(-126, min(126, (int)(__float_as_uint(top) >> 23) - 127 - 14));
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -787,7 +788,8 @@ kda_status paged_decode_launch(const PagedArgs& a, int D, bool e4m3, void* ws, c
 
 int* paged_decode_error_word() {
     void* p = nullptr;
-    return cudaGetSymbolAddress(&p, g_paged_decode_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
+    return cudaGetSymbolAddress(&p, g_paged_decode_error) == cudaSuccess ? static_cast<int*>(p)
+                                                                         : nullptr;
 }
 
 }  // namespace kda

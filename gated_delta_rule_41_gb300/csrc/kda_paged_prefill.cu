@@ -45,7 +45,8 @@
 //   exact in fp16 down to 2^-17, are exact down to 2^-29 of it (but for
 //   magnitudes below 2^-117: E is -100 at least).
 // * e4m3 codes of K and V to fp16, exactly.  Q then goes to fp16 too, every row
-//   scaled by a power of two that its logits' factor gives back.
+//   scaled by a power of two that its logits' factor gives back: its largest value lies in
+//   [2^14, 2^15), and those down to 2^-31 of that are exact.
 // * Infinities and NaN in V to zeros (e4m3: in tiles that not all rows see whole), since a
 //   weight of 0 would not keep them from the rows that do not see their token; the rows
 //   that do get them at the end.
@@ -740,8 +741,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     big = max3(big, fabsf(__uint_as_float(w[e] << 16)),
                                fabsf(__uint_as_float(w[e] & 0xffff0000u)));
             }
-            // exponent of the largest, as far as 2^-e is a normal number
-            const int e2 = max(-126, min(126, (__float_as_int(big) >> 23) - 127));
+            // the largest to [2^14, 2^15), as far as 2^-e is a normal number
+            const int e2 = max(-126, min(126, (__float_as_int(big) >> 23) - 127 - 14));
             const float down = pow2i(-e2);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
@@ -1155,7 +1156,8 @@ kda_status paged_prefill_launch(const PagedArgs& a, int D, bool e4m3, void* ws, 
 
 int* paged_prefill_error_word() {
     void* p = nullptr;
-    return cudaGetSymbolAddress(&p, g_paged_prefill_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
+    return cudaGetSymbolAddress(&p, g_paged_prefill_error) == cudaSuccess ? static_cast<int*>(p)
+                                                                         : nullptr;
 }
 
 }  // namespace kda

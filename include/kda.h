@@ -296,9 +296,10 @@ kda_status kda_chunk_fwd_noalloc(const kda_dims* dims, const void* q, const void
  *           a query that sees no token gets o = 0 and lse = -inf.  Products
  *           accumulate in fp32 and the softmax statistics are fp32; the
  *           weights enter the product with V in two bf16 terms (decode) or in
- *           fp16 (prompts, and both with an e4m3 cache, where q is scaled by a
- *           power of two to fit fp16 too): fp16 rounds a weight by 2^-11 of
- *           itself, or by up to 2^-32 of the row's largest.  For prompts V
+ *           fp16 (prompts, and both with an e4m3 cache): fp16 rounds a weight
+ *           by 2^-11 of itself, or by up to 2^-32 of the row's largest.  With an
+ *           e4m3 cache q goes to fp16 with a power of two per query: values
+ *           below 2^-31 of its largest are rounded, by up to 2^-39 of it.  For prompts V
  *           goes to fp16 with a power of two shared by the tokens that a block
  *           of query rows reads: values below 2^-29 of the largest finite |v|
  *           among them (or below 2^-117) are rounded, by up to 2^-37 of it.

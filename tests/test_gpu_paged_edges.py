@@ -186,8 +186,8 @@ def test_equal_keys_weigh_the_same_at_logits_of_any_size(lens, qn, dtype, scale,
 def test_small_weights_of_a_long_tail(prefill, dtype, nats):
     """The first token takes almost all of the weight and its value is zero: what
     is left is the tail's, all of one sign.  A weight is rounded by up to 2^-11 of
-    itself (that is in the usual bound) or, where it is small, by 2^-32 of the largest: half of fp16's
-    smallest step, 2^-25, with the largest at 2^7 or more.  The rows are many, so that no
+    itself (that is in the usual bound) or, where it is small, by 2^-32 of the
+    largest: half of fp16's smallest step, 2^-25, with the largest at 2^7 or more.  The rows are many, so that no
     other CTA takes part of one."""
     n = 131072
     c = make_cache([n], 128, 2, 64, dtype, 56, poison=False)
@@ -539,3 +539,27 @@ def test_strides_of_a_dimension_of_one_do_not_matter():
     same = kda.paged_decode(q, kda.KVPages(k.contiguous(), v), table, lens)
     kda.check()
     assert torch.equal(o, same)
+
+
+# ---- queries of unequal channels ----
+
+@pytest.mark.parametrize("amp", [2.0 ** 8, 2.0 ** 20, 2.0 ** 27])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_query_channels_far_larger_than_others(prefill, dtype, amp):
+    """One channel of q is far larger than the others and meets keys of zero: the logits
+    are the other channels' (their error is bounded by the sum of |q k| alone)."""
+    c = make_cache([700], 32, 2, 128, dtype, 78, poison=False)
+    k = c["k"].view(torch.uint8) if dtype == E4M3 else c["k"]
+    k[..., 17] = 0
+    q = rand_q(300 if prefill else 1, 4, 128, 79)
+    q[..., 17] = amp
+    if prefill:
+        o, lse = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, 300]),
+                                   return_lse=True)
+        ref = ref_prefill(q, c, [300], 128 ** -0.5)
+    else:
+        o, lse = kda.paged_decode(q, kv(c), c["table"], c["lens"], return_lse=True)
+        ref = ref_decode(q, c, 128 ** -0.5)
+    kda.check()
+    check_attention(o, lse, ref)

@@ -42,8 +42,8 @@
 // Measured: a call costs about 9 us beside its bytes (5 to start and find its
 // work, 3 to join rows that several CTAs share), which then pass at the copy
 // rate (64 rows of 2048 tokens 49 us, of 4096 89 us: 6.8 TB/s between them).
-// 64 rows of 200 to 8192 tokens, 16 heads over 4, D = 128, bf16: 50 us, 5.6 TB/s,
-// and DRAM reads 283.2 MB, what the rows hold.  Two CTAs on an SM with D = 128,
+// 64 rows of 200 to 8192 tokens, 16 heads over 4, D = 128, bf16: 51 us in a graph, 5.5
+// TB/s, and DRAM reads 283.2 MB, what the rows hold.  Two CTAs on an SM with D = 128,
 // three with D = 64 (the window rows: 46 us against 40 then); more make no
 // difference, and neither do smaller shares handed out as CTAs get done.
 #include "kda_paged.cuh"

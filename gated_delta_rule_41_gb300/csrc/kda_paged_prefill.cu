@@ -15,7 +15,7 @@
 // exponentials 1024 of the special function units.  A pair of tiles takes 2900
 // cycles: a chain of S -> weights (1500) -> P V and the next S (1100) -> on to
 // the softmax again (300) is longer than the tensor core's work.  A prompt of
-// 8192 tokens, 16 heads over 4, D = 128: 204 us, 1350 TFLOP/s, 0.72 of the
+// 8192 tokens, 16 heads over 4, D = 128: 206 us in a graph, 1335 TFLOP/s, 0.72 of the
 // bf16 rate of cuBLAS; the first and the last tile of an item, which are
 // slower, and the items' unequal lengths are the rest.
 //
@@ -34,7 +34,7 @@
 // of it): a long tail behind one strong token would show it if the reference weighed
 // 1.  That leaves 2^9 for larger logits: a prompt of 8192 tokens does not look
 // more often (at 2^9 for the reference it does: 225 us against 209), a window's rows, which
-// start from a few sinks, do (137 us against 132).
+// start from a few sinks, do (138 us against 132).
 //
 // K and V tiles arrive by TMA, one box per page, into rings of slots, and a
 // warpgroup turns what is not ready for the products into it, in place:

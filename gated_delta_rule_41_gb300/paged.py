@@ -236,7 +236,8 @@ def _outputs(q, out, lse, return_lse, stream):
 def paged_decode_workspace(pages: KVPages, S, HQ, max_pages=1) -> Optional[torch.Tensor]:
     """A workspace for ``paged_decode`` calls of S sequences and HQ heads (any
     lengths), zeroed as it must be before its first use.  Calls that overlap on
-    the GPU need one each."""
+    the GPU need one each.  (A call that gets none, or a smaller one, makes a
+    fresh one for itself.)"""
     need = int(_lib().kda_paged_decode_workspace_bytes(pages.dims(S, HQ, max_pages)))
     return torch.zeros(need, dtype=torch.uint8, device=pages.k.device) if need else None
 
@@ -265,7 +266,9 @@ def paged_decode(q, pages: KVPages, block_table, kv_lens, scale=None, window=0, 
 
 
 def paged_prefill_workspace(pages: KVPages, S, T, HQ, max_pages=1) -> Optional[torch.Tensor]:
-    """A workspace for ``paged_prefill`` calls of T query tokens in S sequences."""
+    """A workspace for ``paged_prefill`` calls of T query tokens in S sequences.
+    (What they need does not rise with T throughout; a call that gets none, or a
+    smaller one, makes a fresh one for itself.)"""
     need = int(_lib().kda_paged_prefill_workspace_bytes(pages.dims(S, HQ, max_pages), T))
     return torch.zeros(need, dtype=torch.uint8, device=pages.k.device) if need else None
 

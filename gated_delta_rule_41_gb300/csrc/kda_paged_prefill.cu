@@ -855,9 +855,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 hi = max3(hi, v[c][e], v[c][e + 1]);
                                 lo = min3(lo, v[c][e], v[c][e + 1]);
                             }
+                        // (larger in S: the products may round to the same number)
                         const float s_top = f < 0.f ? lo : hi, top = s_top * f;
-                        if (top > m) {
-                            keep = m == -INFINITY ? 0.f : ex2((s_ref - s_top) * f);
+                        const float rise = (s_top - s_ref) * f;
+                        if (m == -INFINITY ? top > -INFINITY : rise > 0.f) {
+                            keep = m == -INFINITY ? 0.f : ex2(-rise);
                             m = top;
                             s_ref = s_top;
                         }

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import gated_delta_rule_41_gb300 as kda
-from paged_util import E4M3, check_attention, make_cache, ref_decode, ref_prefill
+from paged_util import (E4M3, check_attention, make_cache, ref_decode, ref_prefill,
+                        tokens_of)
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -563,3 +564,33 @@ def test_query_channels_far_larger_than_others(prefill, dtype, amp):
         ref = ref_decode(q, c, 128 ** -0.5)
     kda.check()
     check_attention(o, lse, ref)
+
+
+@pytest.mark.parametrize("scale", [0.74, 0.75, 0.7513, 0.752, 0.76, -0.7513])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_neighbouring_logits_whose_products_round_alike(dtype, scale):
+    """S of later keys is the next float above that of earlier ones, 2^5 at 2^29, so that
+    the logits differ by 30 and more in base 2: later keys alone count where they are
+    seen, though scale S may round to the same number.  Bound as above."""
+    c = make_cache([600], 32, 1, 128, dtype, 80, poison=False)
+    if c["ks"] is not None:
+        c["ks"].fill_(1.0)
+    c["k"].zero_()
+    c["k"][..., 0] = 1.0
+    late = 200
+    raw = c["k"].view(torch.uint8) if dtype == E4M3 else c["k"]
+    one = raw[c["table"][0, 0].item(), 0, 0, 0].item()
+    for j in range(late, 600):
+        raw[c["table"][0, j // 32].item(), j % 32, 0, 1] = one
+    q = torch.zeros(600, 2, 128, dtype=BF16, device="cuda")
+    q[..., 0] = math.copysign(1.9375 * 2.0 ** 28, scale)
+    q[..., 1] = math.copysign(2.0 ** 5, scale)
+    o = kda.paged_prefill(q, kv(c), c["table"], c["lens"], ints([0, 600]), scale=scale)
+    kda.check()
+    assert o.isfinite().all()
+    v = tokens_of(c["v"], c["vs"], c["table"], 0, 600)[:, 0]
+    i = torch.arange(1, 601, dtype=torch.float64)[:, None]
+    n = torch.where(i > late, i - late, i)
+    mean, big = (torch.cat((x[:late].cumsum(0), x[late:].cumsum(0))) / n for x in (v, v.abs()))
+    bound = (2.0 ** -8 * mean.abs() + 2.0 ** -10 * big)[:, None]
+    assert ((o.double().cpu() - mean[:, None]).abs() <= bound).all()

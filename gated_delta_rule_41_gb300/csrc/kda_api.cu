@@ -14,7 +14,7 @@ using namespace kda;
 
 // The kernels' error words, read and cleared together: one launch, one copy and one wait
 // for a check, whatever the number of words.
-constexpr int kErrorWords = 6, kCheckSlots = 64;
+constexpr int kErrorWords = 7, kCheckSlots = 64;
 struct ErrorWords {
     int* p[kErrorWords];
     int code[kErrorWords];   // what a word that is not 0 stands for; 0: itself
@@ -38,8 +38,8 @@ bool error_words(ErrorWords& w) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     if (!have[dev].load(std::memory_order_acquire)) {
         w = {{tc_error_word(), simt_error_word(), paged_error_word(), paged_decode_error_word(),
-              paged_prefill_error_word(), pages_error_word()},
-             {KDA_ERR_TIMEOUT, KDA_ERR_SHAPE, 0, 0, 0, 0}};
+              paged_prefill_error_word(), pages_error_word(), scan_error_word()},
+             {KDA_ERR_TIMEOUT, KDA_ERR_SHAPE, 0, 0, 0, 0, 0}};
         for (int* p : w.p)
             if (!p) return false;
         static std::mutex m;

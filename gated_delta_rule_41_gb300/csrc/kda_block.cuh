@@ -1,0 +1,363 @@
+// Shared pieces of the operators around a mixing layer (gated recurrence, gated norm,
+// residual sum with norm, 8-bit activations).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "kda_paged.cuh"
+
+namespace kda {
+namespace block {
+
+// Neighbours that share a scale, and the largest finite e4m3 value.
+constexpr int kScaleBlock = 32;
+constexpr float kCodeMax = 448.0f;
+constexpr int kMaxWidth = 16384;   // elements of a row that the norms keep in registers
+
+using paged::sm_count;
+
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// E neighbouring elements of type T as they lie in memory: 16-byte accesses for E = 8, one
+// element for E = 1.
+template <typename T, int E>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16, 8> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        r = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        unpack2(r.x, v[0], v[1]);
+        unpack2(r.y, v[2], v[3]);
+        unpack2(r.z, v[4], v[5]);
+        unpack2(r.w, v[6], v[7]);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
+                                                  pack2(v[4], v[5]), pack2(v[6], v[7]));
+    }
+};
+template <>
+struct Chunk<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+template <typename T>
+struct Chunk<T, 1> {
+    T r;
+    __device__ __forceinline__ void load(const T* p) { r = *p; }
+    __device__ __forceinline__ void zero() { r = from_f<T>(0.f); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f<T>(r); }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { *p = from_f<T>(v[0]); }
+};
+
+// ---- 8-bit blocks: 32 neighbours share the smallest 2^e, e >= -126, with max |x| <= 448 2^e ----
+
+// e + 127 from the largest finite magnitude of a block.  448 = 1.75 * 2^8: with top = m * 2^k,
+// 1 <= m < 2, e = k - 8, or k - 7 where m > 1.75; both read from the bits of top (a subnormal top
+// has k < -126 and ends at the lower limit).
+__device__ __forceinline__ uint32_t scale_byte(float top) {
+    const uint32_t b = __float_as_uint(top);
+    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u);
+    return (uint32_t)(max(e, -126) + 127);
+}
+// 2^e and 2^-e of a scale byte (1..247: both are normal numbers)
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float inverse_of(uint32_t byte) {
+    return __uint_as_float((254u - byte) << 23);
+}
+// A magnitude for the block's maximum: 0 for infinities and NaN.
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? a : 0.f;
+}
+// With the largest scale a code of 256 would stand for 2^128: values next to the largest float go
+// to the code below it, 240, which is no further off than 2^-4.
+constexpr uint32_t kTopScale = 247;
+template <int E>
+__device__ __forceinline__ void below_top(float (&v)[E]) {
+    constexpr float most = 240.f * 1.329227995784916e36f;   // 240 * 2^120
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (finite_abs(v[j]) > most) v[j] = copysignf(most, v[j]);
+}
+// Codes of a pair times the scale's inverse (the lower byte is a's).  x + 0 x is x, or NaN for an
+// infinity: that may not pass for a finite value in the backward pass.
+__device__ __forceinline__ uint32_t code2(float a, float b, float inv) {
+    const float2 v = make_float2(fmaf(a, 0.f, a * inv), fmaf(b, 0.f, b * inv));
+    return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ void values2(uint32_t two, float& a, float& b) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    a = f.x;
+    b = f.y;
+}
+
+// E codes as they lie in memory, and the scale of their block (E = 8 or 1).
+template <int E>
+struct Codes;
+template <>
+struct Codes<8> {
+    uint2 r;
+    uint32_t s;
+    __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* scale) {
+        r = __ldcs(reinterpret_cast<const uint2*>(p));
+        s = *scale;
+    }
+    __device__ __forceinline__ void zero() {
+        r = make_uint2(0, 0);
+        s = 127;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        values2(r.x & 0xffffu, v[0], v[1]);
+        values2(r.x >> 16, v[2], v[3]);
+        values2(r.y & 0xffffu, v[4], v[5]);
+        values2(r.y >> 16, v[6], v[7]);
+        const float f = scale_of(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= f;
+    }
+    static __device__ __forceinline__ void store(uint8_t* p, const float (&v)[8], float inv) {
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(code2(v[0], v[1], inv) | code2(v[2], v[3], inv) << 16,
+                       code2(v[4], v[5], inv) | code2(v[6], v[7], inv) << 16);
+    }
+};
+template <>
+struct Codes<1> {
+    uint8_t r;
+    uint32_t s;
+    __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* scale) {
+        r = *p;
+        s = *scale;
+    }
+    __device__ __forceinline__ void zero() {
+        r = 0;
+        s = 127;
+    }
+    __device__ __forceinline__ void get(float (&v)[1]) const {
+        float unused;
+        values2(r, v[0], unused);
+        v[0] *= scale_of(s);
+    }
+    static __device__ __forceinline__ void store(uint8_t* p, const float (&v)[1], float inv) {
+        *p = (uint8_t)code2(v[0], 0.f, inv);
+    }
+};
+
+// A parameter vector, float32 or bf16; ones where there is none.
+struct Param {
+    const void* p;
+    bool bf16;
+    __device__ __forceinline__ float operator[](int i) const {
+        if (!p) return 1.f;
+        return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+                    : static_cast<const float*>(p)[i];
+    }
+};
+
+// Sums over the TPR threads of a row (a power of two), for every thread of it.  Rows of more than
+// a warp go through shared memory: `red` has one entry per warp of the CTA for each of two turns,
+// so that one barrier a turn is enough.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn, int warps) {
+#pragma unroll
+    for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) {
+        v.x += __shfl_xor_sync(~0u, v.x, d);
+        v.y += __shfl_xor_sync(~0u, v.y, d);
+    }
+    if (TPR > 32) {
+        float2* at = red + (turn & 1) * warps;
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) at[warp] = v;
+        __syncthreads();
+        constexpr int W = TPR > 32 ? TPR / 32 : 1;
+        const int first = warp / W * W;
+        v = at[first];
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const float2 o = at[first + i];
+            v.x += o.x;
+            v.y += o.y;
+        }
+    }
+    return v;
+}
+
+// Where a thread's rows lie: threads per row, rows per CTA.
+template <int TPR>
+struct Rows {
+    static constexpr int kThreads = TPR > 256 ? TPR : 256;
+    static constexpr int kRows = kThreads / TPR;
+};
+
+// Picks the widths a kernel is made for: a row's elements stay in registers, E * NC of them in
+// each of TPR threads.  Rows of 16-byte accesses (E = 8) where width, strides and pointers allow,
+// else single elements.  F: template <int E, int TPR, int NC> struct with a static run(args...).
+template <template <int, int, int> class F, typename... A>
+kda_status by_width(bool wide, int D, A&&... args) {
+    if (wide) {
+        if (D <= 32) return F<8, 4, 1>::run(args...);
+        if (D <= 64) return F<8, 8, 1>::run(args...);
+        if (D <= 128) return F<8, 16, 1>::run(args...);
+        if (D <= 256) return F<8, 32, 1>::run(args...);
+        if (D <= 512) return F<8, 32, 2>::run(args...);
+        if (D <= 1024) return F<8, 64, 2>::run(args...);
+        if (D <= 2048) return F<8, 256, 1>::run(args...);
+        if (D <= 4096) return F<8, 256, 2>::run(args...);
+        if (D <= 8192) return F<8, 256, 4>::run(args...);
+        return F<8, 512, 4>::run(args...);
+    }
+    if (D <= 128) return F<1, 32, 4>::run(args...);
+    if (D <= 512) return F<1, 128, 4>::run(args...);
+    if (D <= 2048) return F<1, 256, 8>::run(args...);
+    return F<1, 1024, 16>::run(args...);
+}
+
+inline bool aligned16(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+    return true;
+}
+
+// CTAs of a kernel that walks over its rows: all that an SM holds at once, or fewer.
+template <typename K>
+int resident(K kernel, int threads) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)
+        n = 1;
+    return n;
+}
+inline int grid_of(int per_sm, long long ctas_of_work) {
+    return (int)std::min<long long>((long long)per_sm * sm_count(), ctas_of_work);
+}
+
+// Column sums over rows: each CTA leaves one row of partial sums in the workspace, and
+// sum_parts_launch adds them up in order, so that the same call gives the same bits.
+constexpr int kPartsPerSm = 8;
+inline int parts_bound(long long rows) {
+    return (int)std::min<long long>((long long)kPartsPerSm * sm_count(), rows);
+}
+
+// The sums of a CTA's rows into its row of partial sums: the row groups one after the other,
+// through shared memory.
+template <int E, int TPR, int NC>
+__device__ __forceinline__ void store_part(const float (&v)[NC][E], float* part, int D) {
+    constexpr int G = Rows<TPR>::kRows;
+    __shared__ float sum[G > 1 ? TPR * NC * E : 1];
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    for (int g = 0; g < G; ++g) {
+        if (G > 1) __syncthreads();
+        if (g != group) continue;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int c = (i * TPR + lane) * E + j, k = G > 1 ? (i * E + j) * TPR + lane : 0;
+                float x = v[i][j];
+                if (G > 1 && g > 0) x += sum[k];
+                if (g == G - 1) {
+                    if (c < D) part[c] = x;
+                } else {
+                    sum[k] = x;
+                }
+            }
+    }
+}
+
+}  // namespace block
+
+// Column sums of part [P][D] into out0, and of the [P][D] behind it into out1 (null: left out).
+kda_status sum_parts_launch(const float* part, int P, int D, float* out0, float* out1,
+                            cudaStream_t s);
+
+// ---- launchers (validated arguments only) ----
+struct ScanArgs {
+    int B, T, C;
+    bool tied;
+    long long x_batch, x_token, g_batch, g_token;
+    const void *x, *g;
+    const float* h0;        // [B or nseq][C], may be null
+    const int* cu;          // null: B sequences of T tokens
+    int nseq;
+    void* o;                // may be null (states alone)
+    float *ht, *states;     // may be null
+    // backward
+    const void* dout;
+    const float* dht;
+    void *dx, *dg;
+    float* dh0;
+};
+kda_status scan_fwd_launch(const ScanArgs& a, bool bf16, cudaStream_t s);
+kda_status scan_bwd_launch(const ScanArgs& a, bool bf16, cudaStream_t s);
+kda_status scan_step_launch(int B, int C, bool bf16, bool tied, const void* x, long long x_row,
+                            const void* g, long long g_row, const float* state, float* next,
+                            void* o, cudaStream_t s);
+
+struct GatedArgs {
+    int T, H, D;
+    int act;                        // kda_gate
+    float eps;
+    long long x_stride, z_stride;   // of tokens, in elements
+    const void *x, *z;
+    block::Param w;
+    void* y;
+    uint8_t *xc, *xs, *zc, *zs;     // forward: kept codes and scales, or null; backward: inputs
+    const void* dy;
+    void *dx, *dz;
+    float* dw;                      // may be null
+    float* part;                    // workspace
+};
+kda_status gated_norm_fwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s);
+kda_status gated_norm_bwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s);
+size_t gated_norm_ws_bytes(int T, int H, int D);
+
+struct AddArgs {
+    int T, D;
+    float eps, alpha;
+    long long r_stride, x_stride;
+    const void *r, *x;              // x may be null
+    block::Param av, w;             // av.p null: alpha
+    void *r_out, *y;
+    const void *dy, *dr;            // dr may be null
+    void *dres, *dx;                // dx may be null
+    float *dw, *da;                 // may be null
+    float* part;
+};
+// type: 0 all bf16, 1 all float32, 2 bf16 beside a float32 residual stream
+kda_status add_norm_fwd_launch(const AddArgs& a, int type, cudaStream_t s);
+kda_status add_norm_bwd_launch(const AddArgs& a, int type, cudaStream_t s);
+size_t add_norm_ws_bytes(int T, int D);
+
+kda_status pack8_launch(const void* x, bool bf16, long long rows, int D, long long stride,
+                        uint8_t* codes, uint8_t* scales, cudaStream_t s);
+kda_status unpack8_launch(const uint8_t* codes, const uint8_t* scales, long long rows, int D,
+                          void* x, bool bf16, cudaStream_t s);
+
+}  // namespace kda

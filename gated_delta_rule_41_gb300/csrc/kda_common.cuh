@@ -156,4 +156,7 @@ kda_status pages_copy_launch(const kda_page_pool* pools, int num_pools, int num_
                              const int* src, const int* dst, int n, cudaStream_t s);
 int* pages_error_word();
 
+// Device error word of the gated scan (a kda_status).
+int* scan_error_word();
+
 }  // namespace kda

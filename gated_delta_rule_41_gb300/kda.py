@@ -178,6 +178,14 @@ def chunk_kda_fwd(q, k, v, g, beta, scale=None, initial_state=None, output_final
     return o, ht
 
 
+def _unpacked(do, stream, *inputs):
+    """Tensors as they are; ``Packed8`` ones as tensors of do's type."""
+    if all(isinstance(t, torch.Tensor) for t in inputs):
+        return inputs
+    from .block import unpack8
+    return [t if isinstance(t, torch.Tensor) else unpack8(t, do.dtype, stream=stream) for t in inputs]
+
+
 def chunk_kda_bwd(q, k, v, g, beta, do, dht=None, scale=None, initial_state=None,
                   chunk_size=64, impl="auto", workspace=None, grads=None, stream=None,
                   saved=None, use_qk_l2norm_in_kernel=False):
@@ -185,8 +193,11 @@ def chunk_kda_bwd(q, k, v, g, beta, do, dht=None, scale=None, initial_state=None
     With ``saved`` (from a saving forward on the same inputs) the tensor-core
     kernels start from the saved intermediates instead of recomputing them.
     With ``use_qk_l2norm_in_kernel``, dq and dk are the gradients with respect
-    to the raw (unnormalised) q and k."""
+    to the raw (unnormalised) q and k.  Inputs kept in 8 bits (``Packed8``, from
+    ``pack8``) are given back in do's type first; the gradients are then those at
+    the values that they stand for (without ``saved``, that is)."""
     lib = load_library()
+    q, k, v, g = _unpacked(do, stream, q, k, v, g)
     _check_dev(q, k, v, g, beta, do, dht, initial_state)
     dims = make_dims(q, v, chunk_size, scale, impl, use_qk_l2norm_in_kernel)
     if grads is None:
@@ -258,8 +269,10 @@ def chunk_kda_bwd_varlen(q, k, v, g, beta, do, cu_seqlens, dht=None, scale=None,
     """Backward of chunk_kda_fwd_varlen.  Returns dict dq, dk, dv, dg, dbeta,
     dh0 (dh0 [N,HV,K,V] when ``initial_state`` is given).  With ``saved``
     (from a saving forward on the same inputs and cu_seqlens) the tensor-core
-    kernels start from the saved intermediates."""
+    kernels start from the saved intermediates.  ``Packed8`` inputs as for
+    ``chunk_kda_bwd``."""
     lib = load_library()
+    q, k, v, g = _unpacked(do, stream, q, k, v, g)
     _check_dev(q, k, v, g, beta, do, dht, initial_state)
     nseq = _check_cu(cu_seqlens)
     dims = make_dims(q, v, chunk_size, scale, impl, use_qk_l2norm_in_kernel)

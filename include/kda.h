@@ -1,7 +1,8 @@
 /*
  * kda.h -- C ABI of libkda.so: Kimi Delta Attention (KDA) chunk scan and
  * single-token decode step, and the paged key-value cache of the softmax
- * attention layers beside them, hand-written CUDA for sm_103a (GB300).
+ * attention layers beside them, and what stands around a layer (gated
+ * recurrence, norms, 8-bit activations), hand-written CUDA for sm_103a (GB300).
  *
  * The operation (per batch b and value head hv, state S of K x V floats):
  *
@@ -454,10 +455,153 @@ kda_status kda_pages_compact(const kda_pages_dims* dims, const kda_page_pool* po
 kda_status kda_pages_copy(const kda_page_pool* pools, int num_pools, int num_pages,
                           const int* src, const int* dst, int n, void* stream);
 
+/* ---- Around a mixing layer ------------------------------------------------
+ *
+ * What stands before, behind and beside the KDA scan in a model's layers: a
+ * diagonal gated recurrence, the norm of a layer's output with its gate, the
+ * residual sum with the norm before the next layer, and activations kept in 8
+ * bits for the backward pass.  Forward and backward; a serving step runs the
+ * same norms with few rows, and the recurrence's single-token step.
+ *
+ * Types     Tensors are float32 or bf16 (`dtype`); states, gradients of
+ *           parameters and all sums, norms and states inside the kernels
+ *           float32.  Each result is rounded once.
+ * Layout    Rows are contiguous; where a stride is given (in elements) the
+ *           tokens of that tensor may lie apart, as slices of a wider
+ *           projection do.  The other tensors are dense.  Results may not
+ *           overlap inputs but where that is said.
+ * Alignment Pointers to their element size.  (Rows whose width and strides are
+ *           multiples of 8 elements, at 16-byte aligned pointers, are moved by
+ *           16-byte accesses, others element by element.)
+ * Sizes     Fewer than 2^30 rows (tokens, or tokens times heads), at most 65535
+ *           sequences or batch entries of a scan; rows of a norm at most 16384 wide; else
+ *           KDA_ERR_UNSUPPORTED.  Offsets are 64-bit.
+ * Order     The same call gives the same bits: no sum depends on which CTA is first.
+ *
+ * The gated recurrence, per channel c of C:
+ *
+ *     h_t = exp(g_t) h_{t-1} + u_t x_t,   o_t = h_t
+ *
+ * with u_t = 1, or with `tied` u_t = 1 - exp(g_t) (the state is then a mean of
+ * the inputs).  g is a log-decay as in the KDA scan, one per channel, not
+ * clamped; -inf forgets the state.  The states advance in float32 from token
+ * to token, with a decay near one held as its small distance from one. */
+typedef struct {
+    int B, T, C;          /* x, g, o [B][T][C] */
+    kda_dtype dtype;      /* of x, g, o and their gradients */
+    int tied;
+    long long x_batch, x_token, g_batch, g_token;   /* strides in elements */
+} kda_scan_dims;
+
+/* Tokens between the states that a forward pass keeps for its backward. */
+#define KDA_SCAN_STATE_EVERY 64
+
+/* Forward scan.  cu_seqlens: NULL for B sequences of T tokens each; else B is 1 and
+ * int32 [num_seqs + 1] (device) packs sequences along T, as in the varlen entry
+ * points above: it must rise from 0 to T (kda_check reports KDA_ERR_SHAPE
+ * otherwise; the call then leaves o and states alone and the final states are
+ * the initial ones).
+ *   h0      initial states [B or num_seqs][C] f32, NULL: zeros.
+ *   o       [B][T][C] (dtype), or NULL.
+ *   ht      final states [B or num_seqs][C] f32, or NULL.  Of a sequence without
+ *           tokens: its initial state.
+ *   states  f32 [B][ceil(T / 64)][C], or NULL: the states that enter tokens 0,
+ *           64, 128, ... of T, for the backward pass.  (Where such a token
+ *           begins a packed sequence: its initial state.) */
+kda_status kda_gated_scan_fwd(const kda_scan_dims* dims, const int* cu_seqlens, int num_seqs,
+                              const void* x, const void* g, const float* h0, void* o, float* ht,
+                              float* states, void* stream);
+
+/* Backward of kda_gated_scan_fwd on the same x, g, h0 and cu_seqlens, from the states that it
+ * kept: dout [B][T][C] (dtype), dht [B or num_seqs][C] f32 or NULL; dx, dg [B][T][C] (dtype), dh0
+ * [B or num_seqs][C] f32 or NULL. */
+kda_status kda_gated_scan_bwd(const kda_scan_dims* dims, const int* cu_seqlens, int num_seqs,
+                              const void* x, const void* g, const float* h0, const float* states,
+                              const void* dout, const float* dht, void* dx, void* dg, float* dh0,
+                              void* stream);
+
+/* One token for each of B sequences: x, g [B][C] (rows x_batch, g_batch elements apart; T
+ * and the token strides are ignored), state [B][C] f32 in, new_state out (may be `state`),
+ * o [B][C]. */
+kda_status kda_gated_scan_step(const kda_scan_dims* dims, const void* x, const void* g,
+                               const float* state, float* new_state, void* o, void* stream);
+
+/* The norm of a layer's output with its gate, over the D elements of each of T
+ * tokens' H heads:
+ *
+ *     y = w s(gate) x / sqrt(mean(x^2) + eps),   s(z) = sigmoid(z) or z sigmoid(z)
+ */
+typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
+typedef struct {
+    int T, H, D;
+    kda_dtype dtype, w_dtype;         /* w: float32 or bf16 */
+    kda_gate gate;
+    float eps;                        /* > 0 */
+    long long x_stride, gate_stride;  /* of tokens, in elements */
+} kda_gated_norm_dims;
+
+/* w [D] is shared by the heads (NULL: ones), y [T][H][D].  With the four last pointers the
+ * pass also leaves x and gate in 8 bits for the backward pass, as kda_pack8 does: codes
+ * [T][H][D], scales [T][H][ceil(D / 32)]. */
+kda_status kda_gated_norm_fwd(const kda_gated_norm_dims* dims, const void* x, const void* gate,
+                              const void* w, void* y, void* x_codes, unsigned char* x_scales,
+                              void* gate_codes, unsigned char* gate_scales, void* stream);
+
+/* Backward: dy, dx, dgate [T][H][D], dw [D] f32 (NULL: left out).  With x_scales and
+ * gate_scales, x and gate are dense codes, and the gradients are those at the values
+ * that the codes stand for.  The workspace is for dw. */
+size_t kda_gated_norm_workspace_bytes(const kda_gated_norm_dims* dims);
+kda_status kda_gated_norm_bwd(const kda_gated_norm_dims* dims, const void* x,
+                              const unsigned char* x_scales, const void* gate,
+                              const unsigned char* gate_scales, const void* w, const void* dy,
+                              void* dx, void* dgate, float* dw, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* The residual sum and the norm before the next layer, over the D elements of each of T tokens:
+ *
+ *     r' = r + alpha x,   y = w r' / sqrt(mean(r'^2) + eps)
+ *
+ * alpha is a vector [D] or a number.  The residual stream (r, r' and their gradients) may be
+ * float32 beside bf16 x and y. */
+typedef struct {
+    int T, D;
+    kda_dtype dtype, res_dtype, w_dtype;   /* x, y; r, r'; w and the alpha vector */
+    float eps, alpha;                      /* eps > 0; alpha where there is no vector */
+    long long r_stride, x_stride;          /* of tokens, in elements */
+} kda_add_norm_dims;
+
+/* x NULL: r' is r (the norm alone).  alpha, w [D] or NULL (dims->alpha; ones).  r_out [T][D]:
+ * r', may be r itself where that is dense; NULL only without x.  y is the norm of r' before its rounding. */
+kda_status kda_add_norm_fwd(const kda_add_norm_dims* dims, const void* r, const void* x,
+                            const void* alpha, const void* w, void* r_out, void* y, void* stream);
+
+/* Backward: r is the forward's r' (r_stride apart), dy the gradient of y, dr that of r' from
+ * what else reads it (dense, or NULL); dres [T][D] the gradient of the forward's r, dx = alpha dres (NULL:
+ * left out), dw, dalpha [D] f32 (NULL: left out; dalpha needs the forward's x).  dres may be
+ * dr.  The workspace is for dw and dalpha. */
+size_t kda_add_norm_workspace_bytes(const kda_add_norm_dims* dims);
+kda_status kda_add_norm_bwd(const kda_add_norm_dims* dims, const void* r, const void* x,
+                            const void* alpha, const void* w, const void* dy, const void* dr,
+                            void* dres, void* dx, float* dw, float* dalpha, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Activations in 8 bits: the 32 neighbours of a block along a row share a scale 2^e, the smallest
+ * with e >= -126 and max |x| <= 448 * 2^e over the block's finite elements.  Kept are e4m3
+ * codes of x / 2^e, rounded to nearest even (but down to 240 * 2^120 where that would pass
+ * the largest float32), and e + 127 in a byte.  A value is off by at most 2^-4 of itself, or 2^-10 * 2^e
+ * where that is more; NaN and infinities become NaN.
+ * x [rows][D], rows x_stride elements apart; codes [rows][D], scales [rows][ceil(D / 32)],
+ * dense.  unpack8 gives back code * 2^e (exact in bf16 down to its subnormals); its scales are
+ * bytes that pack8 wrote, 1 to 247. */
+kda_status kda_pack8(const void* x, kda_dtype dtype, long long rows, int D, long long x_stride,
+                     void* codes, unsigned char* scales, void* stream);
+kda_status kda_unpack8(const void* codes, const unsigned char* scales, long long rows, int D,
+                       void* x, kda_dtype dtype, void* stream);
+
 /* Synchronise `stream`, then report (and clear) any error a kernel recorded on
  * the device since the last check: KDA_ERR_TIMEOUT for an expired bounded
  * wait, KDA_ERR_SHAPE for cu_seqlens that break the rules of the varlen
- * entry points or tables that break those of the paged cache, KDA_ERR_PAGES
+ * entry points or the gated scan, or tables that break those of the paged cache, KDA_ERR_PAGES
  * for a page request that was refused, KDA_ERR_CUDA for a runtime error. */
 kda_status kda_check(void* stream);
 

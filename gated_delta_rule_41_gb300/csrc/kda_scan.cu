@@ -23,29 +23,72 @@ using namespace block;
 
 constexpr int kStateEvery = KDA_SCAN_STATE_EVERY;   // tokens between kept states
 
-// The decay exp(g) as keep + d, keep = 1 or 0, held in d alone: d = exp(g) - 1 <= 0 (keep = 1) for
-// g in (-1/4, 0], since a rounded exp(g) close to one would be off by that rounding in each of the
-// thousands of tokens that it acts over; else d = exp(g) > 0 (keep = 0), since h + (exp(g) - 1) h
-// would lose what is small beside h.  exp(g) - 1 is the Taylor series of six terms, its next one
-// under 2^-24 there.  A decay that underflows counts as 2^-126.
-template <typename T>
-__device__ __forceinline__ float decay(float g) {
-    float p = fmaf(g, 1.f / 6.f, 1.f);
-    p = fmaf(g * (1.f / 5.f), p, 1.f);
-    p = fmaf(g * (1.f / 4.f), p, 1.f);
-    p = fmaf(g * (1.f / 3.f), p, 1.f);
-    p = fmaf(g * (1.f / 2.f), p, 1.f);
-    float e = sizeof(T) == 2 ? __expf(g) : expf(g);
-    e = e < 1.17549435e-38f ? 1.17549435e-38f : e;
-    return g > -0.25f && g <= 0.f ? g * p : e;
+// A lane's channels, and packed arithmetic on the two of bf16.
+template <int N>
+struct V {
+    float v[N];
+};
+__device__ __forceinline__ V<1> fma(V<1> a, V<1> b, V<1> c) { return {{fmaf(a.v[0], b.v[0], c.v[0])}}; }
+__device__ __forceinline__ V<1> mul(V<1> a, V<1> b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ V<1> add(V<1> a, V<1> b) { return {{a.v[0] + b.v[0]}}; }
+__device__ __forceinline__ float2 f2(V<2> a) { return make_float2(a.v[0], a.v[1]); }
+__device__ __forceinline__ V<2> v2(float2 a) { return {{a.x, a.y}}; }
+__device__ __forceinline__ V<2> fma(V<2> a, V<2> b, V<2> c) { return v2(__ffma2_rn(f2(a), f2(b), f2(c))); }
+__device__ __forceinline__ V<2> mul(V<2> a, V<2> b) { return v2(__fmul2_rn(f2(a), f2(b))); }
+__device__ __forceinline__ V<2> add(V<2> a, V<2> b) { return v2(__fadd2_rn(f2(a), f2(b))); }
+template <int N>
+__device__ __forceinline__ V<N> all(float x) {
+    V<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = x;
+    return r;
 }
-__device__ __forceinline__ float kept(float d) { return d > 0.f ? 0.f : 1.f; }
-// exp(g) h + u
-__device__ __forceinline__ float advance(float d, float h, float u) {
-    return fmaf(kept(d), h, fmaf(d, h, u));
+
+// The decay exp(g) as keep + d, keep = 1 or 0, held in d alone.  For g in (-1/4, -0] keep is 1 and
+// d = exp(g) - 1 <= -0: a rounded exp(g) close to one would be off by that rounding in each of the
+// thousands of tokens that it acts over.  Else keep is 0 and d = exp(g) > 0: h + (exp(g) - 1) h would
+// lose what is small beside h.  exp(g) - 1 is the Taylor series of six terms, its next one under
+// 2^-24 there; exp(g) has 2^-126 added to it, so that d stays above 0 where it underflows.  (As
+// integers, the bits of the numbers from -0 down to -1/4 are the least of all.)
+template <typename T, int N>
+__device__ __forceinline__ V<N> decay(V<N> g) {
+    V<N> p = fma(g, all<N>(1.f / 720.f), all<N>(1.f / 120.f));
+    p = fma(g, p, all<N>(1.f / 24.f));
+    p = fma(g, p, all<N>(1.f / 6.f));
+    p = fma(g, p, all<N>(1.f / 2.f));
+    p = fma(g, p, all<N>(1.f));
+    p = mul(g, p);
+    V<N> e;
+#pragma unroll
+    for (int j = 0; j < N; ++j) e.v[j] = sizeof(T) == 2 ? __expf(g.v[j]) : expf(g.v[j]);
+    e = add(e, all<N>(1.17549435e-38f));
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        p.v[j] = __float_as_int(g.v[j]) < __float_as_int(-0.25f) ? p.v[j] : e.v[j];
+    return p;
 }
-// 1 - exp(g)
-__device__ __forceinline__ float rest(float d) { return (1.f - kept(d)) - d; }
+// keep, from d's sign
+template <int N>
+__device__ __forceinline__ V<N> kept(V<N> d) {
+    V<N> k;
+#pragma unroll
+    for (int j = 0; j < N; ++j) k.v[j] = __int_as_float(__float_as_int(d.v[j]) >> 31 & 0x3f800000);
+    return k;
+}
+// exp(g) h, and with an input
+template <int N>
+__device__ __forceinline__ V<N> decayed(V<N> d, V<N> k, V<N> h) {
+    return fma(k, h, mul(d, h));
+}
+template <int N>
+__device__ __forceinline__ V<N> advance(V<N> d, V<N> k, V<N> h, V<N> u) {
+    return fma(k, h, fma(d, h, u));
+}
+// (1 - exp(g)) x; 1 - keep is exact
+template <int N>
+__device__ __forceinline__ V<N> remainder(V<N> d, V<N> k, V<N> x) {
+    return mul(fma(d, all<N>(-1.f), fma(k, all<N>(-1.f), all<N>(1.f))), x);
+}
 
 // ---- the scan over long sequences ----
 //
@@ -56,54 +99,89 @@ __device__ __forceinline__ float rest(float d) { return (1.f - kept(d)) - d; }
 // shared memory, and the state that enters a warp's run goes to its tokens by one product each.  So
 // the dependent chain of a tile is 16 + 8 steps instead of 128, and the data passes once.
 //
-// Where slabs are few, a cluster of K CTAs walks along one slab, K tiles at a time: the CTAs'
-// maps are combined through distributed shared memory, with one cluster barrier for K tiles.
+// Where slabs are few, a cluster of K CTAs walks along one slab, K tiles at a time.  Each CTA
+// pushes its tile's map into the others' shared memory (asynchronous stores that complete on the
+// receiver's mbarrier: a cluster barrier would wait for the outputs' stores each time).
 constexpr int kWarps = 8, kRun = 16, kTile = kWarps * kRun, kThreads = kWarps * 32;
 constexpr int kRowBytes = 128, kTileBytes = kTile * kRowBytes;
 constexpr int kMaxCluster = 16;
+constexpr long long kWaitCycles = 4000000000ll;   // about two seconds
 
 template <typename T>
 struct Lane {
     static constexpr int N = 4 / sizeof(T), kSlab = 32 * N;   // channels of a lane, of a slab
-    static __device__ __forceinline__ void get(uint32_t w, float (&v)[N]) {
+    static __device__ __forceinline__ V<N> get(uint32_t w) {
+        V<N> r;
         if constexpr (N == 2)
-            unpack2(w, v[0], v[1]);
+            unpack2(w, r.v[0], r.v[1]);
         else
-            v[0] = __uint_as_float(w);
+            r.v[0] = __uint_as_float(w);
+        return r;
     }
-    // all of the lane's channels, or those below C
-    static __device__ __forceinline__ void put(T* p, const float (&v)[N], int left, bool word) {
+    // the lane's channels (`left` of them are inside C), in one word or each by itself
+    template <bool WORD>
+    static __device__ __forceinline__ void put(T* p, const V<N>& r, int left) {
         if constexpr (N == 2) {
-            if (word) {
-                if (left > 0) *reinterpret_cast<uint32_t*>(p) = pack2(v[0], v[1]);
+            if (WORD) {
+                *reinterpret_cast<uint32_t*>(p) = pack2(r.v[0], r.v[1]);
             } else {
-                if (left > 0) p[0] = __float2bfloat16_rn(v[0]);
-                if (left > 1) p[1] = __float2bfloat16_rn(v[1]);
+                p[0] = __float2bfloat16_rn(r.v[0]);
+                if (left > 1) p[1] = __float2bfloat16_rn(r.v[1]);
             }
         } else {
-            if (left > 0) p[0] = v[0];
+            p[0] = r.v[0];
         }
     }
-    static __device__ __forceinline__ void get32(const float* p, float (&v)[N], int left) {
+    static __device__ __forceinline__ V<N> get32(const float* p, int left) {
+        V<N> r;
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = p && left > j ? p[j] : 0.f;
+        for (int j = 0; j < N; ++j) r.v[j] = p && left > j ? p[j] : 0.f;
+        return r;
     }
-    static __device__ __forceinline__ void put32(float* p, const float (&v)[N], int left) {
+    static __device__ __forceinline__ void put32(float* p, const V<N>& r, int left) {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            if (left > j) p[j] = v[j];
+            if (left > j) p[j] = r.v[j];
     }
 };
 
-// The map of a run of tokens, h -> A h + H; `cut`: it forgets h.
+// The map of a run of tokens, h -> A h + H.  In a packed batch a run in which a sequence begins
+// forgets h: its A is then a NaN of our own, which no arithmetic makes.
+constexpr uint32_t kCut = 0x7fc0c0deu;
 template <int N>
 struct Map {
-    float A[N], H[N];
+    V<N> A, H;
 };
 template <int N>
-__device__ __forceinline__ void apply(const Map<N>& m, bool cut, float (&h)[N]) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) h[j] = cut ? m.H[j] : fmaf(m.A[j], h[j], m.H[j]);
+__device__ __forceinline__ bool is_cut(const Map<N>& m) {
+    return __float_as_uint(m.A.v[0]) == kCut;
+}
+template <bool VL, int N>
+__device__ __forceinline__ V<N> apply(const Map<N>& m, V<N> h) {
+    const V<N> r = fma(m.A, h, m.H);
+    return VL && is_cut(m) ? m.H : r;
+}
+// first, then next
+template <bool VL, int N>
+__device__ __forceinline__ Map<N> compose(const Map<N>& first, const Map<N>& next) {
+    Map<N> r;
+    r.H = apply<VL>(next, first.H);
+    r.A = mul(first.A, next.A);
+    if (VL && (is_cut(first) || is_cut(next))) r.A = all<N>(__uint_as_float(kCut));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ float4 to4(const Map<N>& m) {
+    return make_float4(m.A.v[0], m.A.v[N - 1], m.H.v[0], m.H.v[N - 1]);
+}
+template <int N>
+__device__ __forceinline__ Map<N> from4(const float4& v) {
+    Map<N> m;
+    m.A.v[0] = v.x;
+    m.H.v[0] = v.z;
+    m.A.v[N - 1] = v.y;
+    m.H.v[N - 1] = v.w;
+    return m;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -115,16 +193,29 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
-// A 16-byte read of another CTA's shared memory, at the address of this one's `p`.
-__device__ __forceinline__ float4 read_peer(const void* p, uint32_t rank) {
+__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
     uint32_t at;
-    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(at)
+    return at;
+}
+// 16 bytes into a peer's shared memory; they count on its mbarrier.
+__device__ __forceinline__ void push16(uint32_t to, uint32_t bar, const float4& v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::
+                     "r"(to), "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
+                 "r"(__float_as_uint(v.w)), "r"(bar)
                  : "memory");
-    return v;
+}
+// A wait that gives up, and says so, after kWaitCycles.
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (clock64() - t0 > kWaitCycles) {
+            atomicExch(&g_scan_error, (int)KDA_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
 }
 
 __device__ __forceinline__ void copy16(void* to, const void* from, bool in) {
@@ -132,7 +223,6 @@ __device__ __forceinline__ void copy16(void* to, const void* from, bool in) {
                  "r"(in ? 16 : 0)
                  : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -144,11 +234,14 @@ template <typename T, bool WIDE>
 __device__ __forceinline__ void fill(char* to, const T* p, long long stride, int t0, int T_, int left) {
     constexpr int E = 16 / sizeof(T);
     if (WIDE) {
+        const int row0 = threadIdx.x / 8, c = threadIdx.x % 8 * E;
+        const T* from = p + (t0 + row0) * stride + c;
+        const int rows = c < left ? T_ - t0 - row0 : 0;
 #pragma unroll
         for (int i = 0; i < kTileBytes / 16 / kThreads; ++i) {
-            const int k = i * kThreads + threadIdx.x, row = k / 8, c = k % 8 * E;
-            const bool in = t0 + row < T_ && c < left;
-            copy16(to + k * 16, in ? p + (t0 + row) * stride + c : p, in);
+            const bool in = i * (kThreads / 8) < rows;
+            copy16(to + (i * kThreads + threadIdx.x) * 16, in ? from : p, in);
+            from += kThreads / 8 * stride;
         }
     } else {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -198,55 +291,56 @@ __device__ __forceinline__ void mark(Marks& m, const int* cu, int nseq, int t0, 
     m.last[i] = (uint16_t)last;
 }
 
-template <int N>
 struct __align__(16) Shared {
-    float4 map[kWarps][32];          // the warps' maps (A, H); N = 1 uses half of each
-    float2 back[kWarps][32];         // backward: H of the map that runs the other way
-    float4 mine[2][32];              // this CTA's map, in two turns, read by its cluster
-    float4 peers[kMaxCluster][32];   // the cluster's maps
-    int cut[kWarps], cut_back[kWarps], mine_cut[2][4], peers_cut[kMaxCluster];
+    float4 peers[2][kMaxCluster - 1][32];   // maps of the cluster's other CTAs, in two turns
+    uint64_t arrived[2];                    // ... and that they are here
     Marks marks[2];
 };
 
-template <int N>
-__device__ __forceinline__ float4 to4(const Map<N>& m) {
-    return make_float4(m.A[0], m.A[N - 1], m.H[0], m.H[N - 1]);
-}
-template <int N>
-__device__ __forceinline__ Map<N> from4(const float4& v) {
-    Map<N> m;
-    m.A[0] = v.x;
-    m.H[0] = v.z;
-    m.A[N - 1] = v.y;
-    m.H[N - 1] = v.w;
-    return m;
-}
+// Exchanges of a cluster's maps, one a turn.
+template <bool VL, int N, bool BACK>
+struct Cluster {
+    Shared& sh;
+    const int K, rank;
+    bool lost = false;   // a wait gave up: no more waits, the results are not to be used
 
-// The state that enters this CTA's tile, and behind the cluster's tiles of this turn, from the
-// state `carry` before them; tiles in the order of the ranks (or against it).
-template <int N, bool BACK>
-__device__ __forceinline__ void combine(Shared<N>& sh, int K, int rank, int turn, const Map<N>& own,
-                                        bool own_cut, float (&carry)[N], float (&enter)[N]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (warp == 0) {
-        sh.mine[turn][lane] = to4<N>(own);
-        if (lane == 0) sh.mine_cut[turn][0] = own_cut;
-    }
-    cluster_sync();
-    for (int r = warp; r < K; r += kWarps) {
-        sh.peers[r][lane] = read_peer(&sh.mine[turn][lane], r);
-        if (lane == 0) sh.peers_cut[r] = __float_as_int(read_peer(&sh.mine_cut[turn][0], r).x);
-    }
-    __syncthreads();
-    for (int i = 0; i < K; ++i) {
-        const int r = BACK ? K - 1 - i : i;
-        if (r == rank) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) enter[j] = carry[j];
+    // Before the first turn; also a barrier of the cluster.
+    __device__ __forceinline__ void begin() {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.arrived[i], 1);
+            ptx::fence_mbar_init();
+            for (int i = 0; i < 2; ++i) expect(i);
         }
-        apply<N>(from4<N>(sh.peers[r][lane]), sh.peers_cut[r] != 0, carry);
+        cluster_sync();
     }
-}
+    __device__ __forceinline__ void expect(int i) {
+        ptx::mbar_arrive_expect_tx(&sh.arrived[i], (K - 1) * 32 * (unsigned)sizeof(float4));
+    }
+    // The state that enters this CTA's tile; `carry` goes from before the cluster's tiles of this
+    // turn to behind them.  Tiles in the order of the ranks, or against it.  A buffer is written again two turns
+    // later, by CTAs that have this one's map of the turn between: its reads are over by then.
+    __device__ __forceinline__ V<N> exchange(int turn, const Map<N>& own, V<N>& carry) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = turn & 1;
+        for (int r = warp; r < K; r += kWarps) {
+            if (r == rank) continue;
+            const int slot = rank < r ? rank : rank - 1;
+            push16(peer_address(&sh.peers[i][slot][lane], r), peer_address(&sh.arrived[i], r), to4<N>(own));
+        }
+        if (!lost) lost = !await(&sh.arrived[i], turn >> 1 & 1);
+        if (threadIdx.x == 0) expect(i);
+        V<N> enter = carry;
+        for (int j = 0; j < K; ++j) {
+            const int r = BACK ? K - 1 - j : j;
+            if (r == rank) {
+                enter = carry;
+                carry = apply<VL>(own, carry);
+            } else {
+                carry = apply<VL>(from4<N>(sh.peers[i][r < rank ? r : r - 1][lane]), carry);
+            }
+        }
+        return enter;
+    }
+};
 
 constexpr int kFwdStages = 3, kBwdStages = 2;
 
@@ -255,14 +349,13 @@ template <typename T, bool VL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, int K) {
     constexpr int N = Lane<T>::N;
     extern __shared__ __align__(128) char stages[];
-    Shared<N>& sh = *reinterpret_cast<Shared<N>*>(stages + kFwdStages * 2 * kTileBytes);
+    Shared& sh = *reinterpret_cast<Shared*>(stages + kFwdStages * 2 * kTileBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = K > 1 ? (int)cluster_rank() : 0, slab = blockIdx.x / K, b = blockIdx.y;
     const int c0 = slab * Lane<T>::kSlab, c = c0 + lane * N, left = a.C - c;
     const int tiles = (a.T + kTile - 1) / kTile, turns = (tiles + K - 1) / K;
     const T* x = static_cast<const T*>(a.x) + b * a.x_batch + c0;
     const T* g = static_cast<const T*>(a.g) + b * a.g_batch + c0;
-    T* o = a.o ? static_cast<T*>(a.o) + (long long)b * a.T * a.C + c : nullptr;
     const int every = (a.T + kStateEvery - 1) / kStateEvery;
     float* states = a.states ? a.states + (long long)b * every * a.C + c : nullptr;
     auto h0_of = [&](int s) { return a.h0 ? a.h0 + (long long)s * a.C + c : nullptr; };
@@ -272,11 +365,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         if (bad && threadIdx.x == 0) atomicCAS(&g_scan_error, 0, (int)KDA_ERR_SHAPE);
         // sequences without tokens (all of them, where cu_seqlens is wrong) end as they begin
         for (int s = rank * kWarps + warp; a.ht && s < a.nseq; s += K * kWarps)
-            if (bad || a.cu[s] == a.cu[s + 1]) {
-                float v[N];
-                Lane<T>::get32(h0_of(s), v, left);
-                Lane<T>::put32(a.ht + (long long)s * a.C + c, v, left);
-            }
+            if (bad || a.cu[s] == a.cu[s + 1])
+                Lane<T>::put32(a.ht + (long long)s * a.C + c, Lane<T>::get32(h0_of(s), left), left);
         if (bad) return;   // alike in all CTAs of a cluster
     }
     auto load = [&](int turn) {
@@ -286,12 +376,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             fill<T, WIDE>(to, x, a.x_token, t0, a.T, a.C - c0);
             fill<T, WIDE>(to + kTileBytes, g, a.g_token, t0, a.T, a.C - c0);
         }
-        copies_commit();
+        ptx::cp_async_commit();
     };
     load(0);
     load(1);
-    float carry[N];
-    Lane<T>::get32(VL ? nullptr : h0_of(b), carry, left);
+    Cluster<VL, N, false> cluster{sh, K, rank};
+    if (K > 1) cluster.begin();
+    V<N> carry = Lane<T>::get32(VL ? nullptr : h0_of(b), left);
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = (turn * K + rank) * kTile, tw = t0 + warp * kRun;
@@ -300,9 +391,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         copies_wait<1>();
         __syncthreads();
         load(turn + 2);
-        const uint32_t* xs = reinterpret_cast<const uint32_t*>(
-                                 stages + turn % kFwdStages * 2 * kTileBytes) + warp * kRun * 32 + lane;
+        char* stage = stages + turn % kFwdStages * 2 * kTileBytes;
+        const uint32_t* xs = reinterpret_cast<uint32_t*>(stage) + warp * kRun * 32 + lane;
         const uint32_t* gs = xs + kTileBytes / 4;
+        // the warps' maps go where their rows of g were
+        auto map_of = [&](int w) {
+            return reinterpret_cast<float4*>(stage + kTileBytes + w * kRun * kRowBytes) + lane;
+        };
 
         // tokens of the run that begin and end a sequence
         unsigned firsts = 0, lasts = 0;
@@ -311,86 +406,57 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             lasts = __ballot_sync(~0u, marks.last[warp * kRun + lane % kRun] != kNone) & 0xffffu;
         }
         // from a zero state: each token's local state and product of decays
-        float h[kRun][N], P[kRun][N];
-        float hc[N], pc[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) hc[j] = 0.f, pc[j] = 1.f;
+        V<N> h[kRun], P[kRun];
+        Map<N> m = {all<N>(1.f), all<N>(0.f)};
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            float xv[N], gv[N];
-            Lane<T>::get(xs[i * 32], xv);
-            Lane<T>::get(gs[i * 32], gv);
-            if (VL && (firsts >> i & 1)) Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), hc, left);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float d = decay<T>(gv[j]);
-                hc[j] = advance(d, hc[j], a.tied ? rest(d) * xv[j] : xv[j]);
-                pc[j] = advance(d, pc[j], 0.f);
-                h[i][j] = hc[j];
-                P[i][j] = pc[j];
-            }
+            const V<N> xv = Lane<T>::get(xs[i * 32]);
+            const V<N> d = decay<T>(Lane<T>::get(gs[i * 32])), k = kept(d);
+            if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
+            m.H = advance(d, k, m.H, a.tied ? remainder(d, k, xv) : xv);
+            m.A = decayed(d, k, m.A);
+            h[i] = m.H;
+            P[i] = m.A;
         }
-        Map<N> m;
-#pragma unroll
-        for (int j = 0; j < N; ++j) m.A[j] = pc[j], m.H[j] = hc[j];
-        sh.map[warp][lane] = to4<N>(m);
-        if (VL && lane == 0) sh.cut[warp] = firsts != 0;
+        if (VL && firsts) m.A = all<N>(__uint_as_float(kCut));
+        __syncwarp();
+        *map_of(warp) = to4<N>(m);
         __syncthreads();
 
-        float enter[N];
-        if (K > 1) {
-            // the CTA's map, then the cluster's
-            Map<N> own = from4<N>(sh.map[0][lane]);
-            bool cut = VL && sh.cut[0];
+        // the warps before this one, and all of them
+        Map<N> sum = from4<N>(*map_of(0)), before = {all<N>(1.f), all<N>(0.f)};
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const Map<N> next = from4<N>(sh.map[w][lane]);
-                const bool c1 = VL && sh.cut[w];
-                apply<N>(next, c1, own.H);
-#pragma unroll
-                for (int j = 0; j < N; ++j) own.A[j] *= next.A[j];
-                cut |= c1;
-            }
-            combine<N, false>(sh, K, rank, turn & 1, own, cut, carry, enter);
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) enter[j] = carry[j];
+        for (int w = 1; w < kWarps; ++w) {
+            if (w == warp) before = sum;
+            sum = compose<VL>(sum, from4<N>(*map_of(w)));
         }
-        float into[N];   // the state that enters this warp's run
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) into[j] = enter[j];
-            }
-            apply<N>(from4<N>(sh.map[w][lane]), VL && sh.cut[w], enter);
-        }
-        if (K == 1) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) carry[j] = enter[j];
-        }
+        V<N> into = carry;
+        if (K > 1)
+            into = cluster.exchange(turn, sum, carry);
+        else
+            carry = apply<VL>(sum, carry);
+        into = apply<VL>(before, into);   // the state that enters this warp's run
 
         if (states && tw % kStateEvery == 0 && tw < a.T) {
-            float v[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = into[j];
-            if (VL && (firsts & 1)) Lane<T>::get32(h0_of(marks.first[warp * kRun]), v, left);
+            const V<N> v = VL && (firsts & 1) ? Lane<T>::get32(h0_of(marks.first[warp * kRun]), left) : into;
             Lane<T>::put32(states + (long long)(tw / kStateEvery) * a.C, v, left);
         }
         const int from = VL && firsts ? __ffs(firsts) - 1 : kRun;   // what entered ends there
+        const int rows = a.o && left > 0 ? a.T - tw : 0;
+        T* o = static_cast<T*>(a.o) + ((long long)b * a.T + tw) * a.C + c;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            float v[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = VL && i >= from ? h[i][j] : fmaf(P[i][j], into[j], h[i][j]);
-            if (o && tw + i < a.T) Lane<T>::put(o + (long long)(tw + i) * a.C, v, left, WIDE);
+            V<N> v = fma(P[i], into, h[i]);
+            if (VL && i >= from) v = h[i];
+            if (i < rows) Lane<T>::template put<WIDE>(o, v, left);
+            o += a.C;
             if (VL && (lasts >> i & 1) && a.ht)
                 Lane<T>::put32(a.ht + (long long)marks.last[warp * kRun + i] * a.C + c, v, left);
         }
     }
     if (!VL && a.ht && rank == 0 && warp == 0) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
     copies_wait<0>();
-    if (K > 1) cluster_sync();   // no CTA leaves while another may read its shared memory
+    if (K > 1) cluster_sync();   // no CTA leaves while another may write to its shared memory
 }
 
 // Tiles from the last to the first.  The states inside a tile are formed again from the kept ones
@@ -400,16 +466,14 @@ template <typename T, bool VL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a, int K) {
     constexpr int N = Lane<T>::N;
     extern __shared__ __align__(128) char stages[];
-    Shared<N>& sh = *reinterpret_cast<Shared<N>*>(stages + kBwdStages * 3 * kTileBytes);
+    Shared& sh = *reinterpret_cast<Shared*>(stages + kBwdStages * 3 * kTileBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = K > 1 ? (int)cluster_rank() : 0, slab = blockIdx.x / K, b = blockIdx.y;
     const int c0 = slab * Lane<T>::kSlab, c = c0 + lane * N, left = a.C - c;
     const int tiles = (a.T + kTile - 1) / kTile, turns = (tiles + K - 1) / K;
     const T* x = static_cast<const T*>(a.x) + b * a.x_batch + c0;
     const T* g = static_cast<const T*>(a.g) + b * a.g_batch + c0;
-    const long long row0 = (long long)b * a.T * a.C;
-    const T* dout = static_cast<const T*>(a.dout) + row0 + c0;
-    T *dx = static_cast<T*>(a.dx) + row0 + c, *dg = static_cast<T*>(a.dg) + row0 + c;
+    const T* dout = static_cast<const T*>(a.dout) + (long long)b * a.T * a.C + c0;
     const int every = (a.T + kStateEvery - 1) / kStateEvery;
     const float* states = a.states + (long long)b * every * a.C + c;
     auto h0_of = [&](int s) { return a.h0 ? a.h0 + (long long)s * a.C + c : nullptr; };
@@ -419,11 +483,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         const bool bad = bad_cu(a.cu, a.nseq, a.T);
         if (bad && threadIdx.x == 0) atomicCAS(&g_scan_error, 0, (int)KDA_ERR_SHAPE);
         for (int s = rank * kWarps + warp; a.dh0 && s < a.nseq; s += K * kWarps)
-            if (bad || a.cu[s] == a.cu[s + 1]) {
-                float v[N];
-                Lane<T>::get32(dht_of(s), v, left);
-                Lane<T>::put32(a.dh0 + (long long)s * a.C + c, v, left);
-            }
+            if (bad || a.cu[s] == a.cu[s + 1])
+                Lane<T>::put32(a.dh0 + (long long)s * a.C + c, Lane<T>::get32(dht_of(s), left), left);
         if (bad) return;
     }
     // tile of a turn: the cluster's tiles from behind
@@ -436,138 +497,98 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             fill<T, WIDE>(to + kTileBytes, g, a.g_token, t0, a.T, a.C - c0);
             fill<T, WIDE>(to + 2 * kTileBytes, dout, a.C, t0, a.T, a.C - c0);
         }
-        copies_commit();
+        ptx::cp_async_commit();
     };
     load(0);
-    float carry[N];
-    Lane<T>::get32(VL ? nullptr : dht_of(b), carry, left);
+    Cluster<VL, N, true> cluster{sh, K, rank};
+    if (K > 1) cluster.begin();
+    V<N> carry = Lane<T>::get32(VL ? nullptr : dht_of(b), left);
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = tile_of(turn) * kTile, tw = t0 + warp * kRun;
         Marks& marks = sh.marks[turn & 1];
         if (VL) mark(marks, a.cu, a.nseq, t0, a.T);
         // the kept state of this warp's 64 tokens
-        float into[N];
         const int block = tw / kStateEvery;
-        Lane<T>::get32(block < every ? states + (long long)block * a.C : nullptr, into, left);
+        V<N> into = Lane<T>::get32(block < every ? states + (long long)block * a.C : nullptr, left);
         copies_wait<0>();
         __syncthreads();
         load(turn + 1);
-        const uint32_t* xs = reinterpret_cast<const uint32_t*>(
-                                 stages + turn % kBwdStages * 3 * kTileBytes) + warp * kRun * 32 + lane;
+        char* stage = stages + turn % kBwdStages * 3 * kTileBytes;
+        const uint32_t* xs = reinterpret_cast<uint32_t*>(stage) + warp * kRun * 32 + lane;
         const uint32_t *gs = xs + kTileBytes / 4, *ds = gs + kTileBytes / 4;
+        // the warps' maps go where their rows of g were: that of the states, and that of m
+        auto map_of = [&](int w) {
+            return reinterpret_cast<float4*>(stage + kTileBytes + w * kRun * kRowBytes) + lane;
+        };
         unsigned firsts = 0, lasts = 0;
         if (VL) {
             firsts = __ballot_sync(~0u, marks.first[warp * kRun + lane % kRun] != kNone) & 0xffffu;
             lasts = __ballot_sync(~0u, marks.last[warp * kRun + lane % kRun] != kNone) & 0xffffu;
         }
-        // the run's map, and its map the other way (of m), which has the same product of decays
-        float d[kRun][N];
-        Map<N> m;
-        float back[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) m.A[j] = 1.f, m.H[j] = 0.f, back[j] = 0.f;
+        V<N> d[kRun];
+        Map<N> m = {all<N>(1.f), all<N>(0.f)}, back = m;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            float xv[N], gv[N];
-            Lane<T>::get(xs[i * 32], xv);
-            Lane<T>::get(gs[i * 32], gv);
-            if (VL && (firsts >> i & 1)) Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), m.H, left);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                d[i][j] = decay<T>(gv[j]);
-                m.H[j] = advance(d[i][j], m.H[j], a.tied ? rest(d[i][j]) * xv[j] : xv[j]);
-                m.A[j] = advance(d[i][j], m.A[j], 0.f);
-            }
+            const V<N> xv = Lane<T>::get(xs[i * 32]);
+            d[i] = decay<T>(Lane<T>::get(gs[i * 32]));
+            const V<N> k = kept(d[i]);
+            if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
+            m.H = advance(d[i], k, m.H, a.tied ? remainder(d[i], k, xv) : xv);
+            m.A = decayed(d[i], k, m.A);
         }
+        back.A = m.A;
 #pragma unroll
         for (int i = kRun - 1; i >= 0; --i) {
-            float dv[N];
-            Lane<T>::get(ds[i * 32], dv);
-            if (VL && (lasts >> i & 1)) Lane<T>::get32(dht_of(marks.last[warp * kRun + i]), back, left);
-#pragma unroll
-            for (int j = 0; j < N; ++j) back[j] = advance(d[i][j], dv[j] + back[j], 0.f);
+            if (VL && (lasts >> i & 1)) back.H = Lane<T>::get32(dht_of(marks.last[warp * kRun + i]), left);
+            back.H = decayed(d[i], kept(d[i]), add(Lane<T>::get(ds[i * 32]), back.H));
         }
-        sh.map[warp][lane] = to4<N>(m);
-        sh.back[warp][lane] = make_float2(back[0], back[N - 1]);
-        if (VL && lane == 0) {
-            sh.cut[warp] = firsts != 0;
-            sh.cut_back[warp] = lasts != 0;
-        }
+        if (VL && firsts) m.A = all<N>(__uint_as_float(kCut));
+        if (VL && lasts) back.A = all<N>(__uint_as_float(kCut));
+        __syncwarp();
+        map_of(warp)[0] = to4<N>(m);
+        map_of(warp)[32] = to4<N>(back);
         __syncthreads();
 
-        // the states: from the kept one over the warps before this one
+        // the state that enters this warp's run: from the kept one over the warps before it
         constexpr int kPer = kStateEvery / kRun;
+        for (int w = warp / kPer * kPer; w < warp; ++w) into = apply<VL>(from4<N>(map_of(w)[0]), into);
+        // m behind it: over the warps after it, and all of them
+        Map<N> sum = from4<N>(map_of(kWarps - 1)[32]), behind = {all<N>(1.f), all<N>(0.f)};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (w / kPer == warp / kPer && w < warp) apply<N>(from4<N>(sh.map[w][lane]), VL && sh.cut[w], into);
-        // m: from the end over the warps behind
-        auto back_of = [&](int w) {
-            Map<N> v = from4<N>(sh.map[w][lane]);
-            const float2 e = sh.back[w][lane];
-            v.H[0] = e.x;
-            v.H[N - 1] = N == 2 ? e.y : e.x;
-            return v;
-        };
-        float enter[N], mc[N];
-        if (K > 1) {
-            Map<N> own = back_of(kWarps - 1);
-            bool cut = VL && sh.cut_back[kWarps - 1];
-#pragma unroll
-            for (int w = kWarps - 2; w >= 0; --w) {
-                const Map<N> next = back_of(w);
-                const bool c1 = VL && sh.cut_back[w];
-                apply<N>(next, c1, own.H);
-#pragma unroll
-                for (int j = 0; j < N; ++j) own.A[j] *= next.A[j];
-                cut |= c1;
-            }
-            combine<N, true>(sh, K, rank, turn & 1, own, cut, carry, enter);
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) enter[j] = carry[j];
+        for (int w = kWarps - 2; w >= 0; --w) {
+            if (w == warp) behind = sum;
+            sum = compose<VL>(sum, from4<N>(map_of(w)[32]));
         }
-#pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (w == warp) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) mc[j] = enter[j];
-            }
-            apply<N>(back_of(w), VL && sh.cut_back[w], enter);
-        }
-        if (K == 1) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) carry[j] = enter[j];
-        }
+        V<N> mc = carry;
+        if (K > 1)
+            mc = cluster.exchange(turn, sum, carry);
+        else
+            carry = apply<VL>(sum, carry);
+        mc = apply<VL>(behind, mc);
 
-        float before[kRun][N];
+        V<N> w[kRun];   // h_{t-1}, less x where tied
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            float xv[N];
-            Lane<T>::get(xs[i * 32], xv);
-            if (VL && (firsts >> i & 1)) Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), into, left);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                before[i][j] = a.tied ? into[j] - xv[j] : into[j];
-                into[j] = advance(d[i][j], into[j], a.tied ? rest(d[i][j]) * xv[j] : xv[j]);
-            }
+            const V<N> xv = Lane<T>::get(xs[i * 32]), k = kept(d[i]);
+            if (VL && (firsts >> i & 1)) into = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
+            w[i] = a.tied ? fma(xv, all<N>(-1.f), into) : into;
+            into = advance(d[i], k, into, a.tied ? remainder(d[i], k, xv) : xv);
         }
+        const int rows = left > 0 ? a.T - tw : 0;
+        const long long end = ((long long)b * a.T + tw + kRun - 1) * a.C + c;
+        T *dx = static_cast<T*>(a.dx) + end, *dg = static_cast<T*>(a.dg) + end;
 #pragma unroll
         for (int i = kRun - 1; i >= 0; --i) {
-            float dv[N], dxv[N], dgv[N];
-            Lane<T>::get(ds[i * 32], dv);
-            if (VL && (lasts >> i & 1)) Lane<T>::get32(dht_of(marks.last[warp * kRun + i]), mc, left);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float l = dv[j] + mc[j];
-                mc[j] = advance(d[i][j], l, 0.f);
-                dxv[j] = a.tied ? rest(d[i][j]) * l : l;
-                dgv[j] = mc[j] * before[i][j];
+            if (VL && (lasts >> i & 1)) mc = Lane<T>::get32(dht_of(marks.last[warp * kRun + i]), left);
+            const V<N> l = add(Lane<T>::get(ds[i * 32]), mc), k = kept(d[i]);
+            mc = decayed(d[i], k, l);
+            if (i < rows) {
+                Lane<T>::template put<WIDE>(dx, a.tied ? remainder(d[i], k, l) : l, left);
+                Lane<T>::template put<WIDE>(dg, mul(mc, w[i]), left);
             }
-            if (tw + i < a.T) {
-                Lane<T>::put(dx + (long long)(tw + i) * a.C, dxv, left, WIDE);
-                Lane<T>::put(dg + (long long)(tw + i) * a.C, dgv, left, WIDE);
-            }
+            dx -= a.C;
+            dg -= a.C;
             if (VL && (firsts >> i & 1) && a.dh0)
                 Lane<T>::put32(a.dh0 + (long long)marks.first[warp * kRun + i] * a.C + c, mc, left);
         }
@@ -580,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
 // CTAs of a cluster: as many as keep all slabs' CTAs resident (two per SM), tiles allowing.
 int cluster_of(long long slabs, int T) {
     int K = 1;
-    while (K < kMaxCluster && 2 * K * slabs <= 2 * sm_count() && K * kTile < T) K *= 2;
+    while (K < kMaxCluster && K * slabs <= sm_count() && K * kTile < T) K *= 2;
     return K;
 }
 
@@ -589,7 +610,7 @@ kda_status launch(const ScanArgs& a, cudaStream_t s) {
     auto* k = BWD ? scan_bwd_kernel<T, VL, WIDE> : scan_fwd_kernel<T, VL, WIDE>;
     const int slabs = (a.C + Lane<T>::kSlab - 1) / Lane<T>::kSlab;
     const int K = cluster_of((long long)slabs * a.B, a.T);
-    const size_t smem = (BWD ? kBwdStages * 3 : kFwdStages * 2) * kTileBytes + sizeof(Shared<Lane<T>::N>);
+    const size_t smem = (BWD ? kBwdStages * 3 : kFwdStages * 2) * kTileBytes + sizeof(Shared);
     // once per device; a second time does no harm
     static std::atomic<unsigned long long> ready{0};
     int dev = 0;
@@ -643,8 +664,8 @@ __global__ void __launch_bounds__(256) step_kernel(int B, int C, bool tied, cons
         hr.get(h);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const float d = decay<T>(gv[j]);
-            h[j] = advance(d, h[j], tied ? rest(d) * xv[j] : xv[j]);
+            const V<1> d = decay<T>(V<1>{{gv[j]}}), k = kept(d), v = {{xv[j]}};
+            h[j] = advance(d, k, V<1>{{h[j]}}, tied ? remainder(d, k, v) : v).v[0];
         }
         Chunk<float, E>::store(next + b * C + c, h);
         Chunk<T, E>::store(o + b * C + c, h);

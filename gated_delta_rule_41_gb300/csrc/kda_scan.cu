@@ -48,23 +48,32 @@ __device__ __forceinline__ V<N> all(float x) {
 // d = exp(g) - 1 <= -0: a rounded exp(g) close to one would be off by that rounding in each of the
 // thousands of tokens that it acts over.  Else keep is 0 and d = exp(g) > 0: h + (exp(g) - 1) h would
 // lose what is small beside h.  exp(g) - 1 is the Taylor series of six terms, its next one under
-// 2^-24 there; exp(g) has 2^-126 added to it, so that d stays above 0 where it underflows.  (As
-// integers, the bits of the numbers from -0 down to -1/4 are the least of all.)
-template <typename T, int N>
-__device__ __forceinline__ V<N> decay(V<N> g) {
+// 2^-24 there; exp(g), by the fast power of two (2^-22 of it, and the rounding of its argument), has
+// 2^-126 added to it, so that d stays above 0 where it underflows.  (As integers, the bits of the
+// numbers from -0 down to -1/4 are the least of all.)
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int N>
+__device__ __forceinline__ V<N> decay(V<N> g, V<N>& keep) {
     V<N> p = fma(g, all<N>(1.f / 720.f), all<N>(1.f / 120.f));
     p = fma(g, p, all<N>(1.f / 24.f));
     p = fma(g, p, all<N>(1.f / 6.f));
     p = fma(g, p, all<N>(1.f / 2.f));
     p = fma(g, p, all<N>(1.f));
     p = mul(g, p);
-    V<N> e;
+    V<N> e = mul(g, all<N>(1.44269504f));
 #pragma unroll
-    for (int j = 0; j < N; ++j) e.v[j] = sizeof(T) == 2 ? __expf(g.v[j]) : expf(g.v[j]);
+    for (int j = 0; j < N; ++j) e.v[j] = exp2_fast(e.v[j]);
     e = add(e, all<N>(1.17549435e-38f));
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        p.v[j] = __float_as_int(g.v[j]) < __float_as_int(-0.25f) ? p.v[j] : e.v[j];
+    for (int j = 0; j < N; ++j) {
+        const bool near = __float_as_int(g.v[j]) < __float_as_int(-0.25f);
+        p.v[j] = near ? p.v[j] : e.v[j];
+        keep.v[j] = near ? 1.f : 0.f;
+    }
     return p;
 }
 // keep, from d's sign
@@ -118,6 +127,13 @@ struct Lane {
             r.v[0] = __uint_as_float(w);
         return r;
     }
+    // two values: a token's two channels, or one channel of two tokens
+    static __device__ __forceinline__ V<2> pair(const uint32_t* w) {
+        if constexpr (N == 2)
+            return get(w[0]);
+        else
+            return {{__uint_as_float(w[0]), __uint_as_float(w[32])}};
+    }
     // the lane's channels (`left` of them are inside C), in one word or each by itself
     template <bool WORD>
     static __device__ __forceinline__ void put(T* p, const V<N>& r, int left) {
@@ -144,6 +160,15 @@ struct Lane {
             if (left > j) p[j] = r.v[j];
     }
 };
+
+// token i's channels of such a pair
+template <int N>
+__device__ __forceinline__ V<N> part(const V<2>& p, int i) {
+    V<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = p.v[N == 2 ? j : i];
+    return r;
+}
 
 // The map of a run of tokens, h -> A h + H.  In a packed batch a run in which a sequence begins
 // forgets h: its A is then a NaN of our own, which no arithmetic makes.
@@ -347,7 +372,7 @@ constexpr int kFwdStages = 3, kBwdStages = 2;
 // VL: a packed batch.  WIDE: 16-byte copies and 4-byte stores.
 template <typename T, bool VL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, int K) {
-    constexpr int N = Lane<T>::N;
+    constexpr int N = Lane<T>::N, S = 2 / N;   // tokens of a pair of values
     extern __shared__ __align__(128) char stages[];
     Shared& sh = *reinterpret_cast<Shared*>(stages + kFwdStages * 2 * kTileBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -409,14 +434,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         V<N> h[kRun], P[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)};
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const V<N> xv = Lane<T>::get(xs[i * 32]);
-            const V<N> d = decay<T>(Lane<T>::get(gs[i * 32])), k = kept(d);
-            if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
-            m.H = advance(d, k, m.H, a.tied ? remainder(d, k, xv) : xv);
-            m.A = decayed(d, k, m.A);
-            h[i] = m.H;
-            P[i] = m.A;
+        for (int p = 0; p < kRun; p += S) {
+            V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
+            const V<2> d2 = decay(Lane<T>::pair(gs + p * 32), k2);
+            if (a.tied) u2 = remainder(d2, k2, u2);
+#pragma unroll
+            for (int i = p; i < p + S; ++i) {
+                const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p);
+                if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
+                m.H = advance(d, k, m.H, part<N>(u2, i - p));
+                m.A = decayed(d, k, m.A);
+                h[i] = m.H;
+                P[i] = m.A;
+            }
         }
         if (VL && firsts) m.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
@@ -464,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
 // carry m the other way.
 template <typename T, bool VL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a, int K) {
-    constexpr int N = Lane<T>::N;
+    constexpr int N = Lane<T>::N, S = 2 / N;   // tokens of a pair of values
     extern __shared__ __align__(128) char stages[];
     Shared& sh = *reinterpret_cast<Shared*>(stages + kBwdStages * 3 * kTileBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -529,13 +559,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         V<N> d[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)}, back = m;
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const V<N> xv = Lane<T>::get(xs[i * 32]);
-            d[i] = decay<T>(Lane<T>::get(gs[i * 32]));
-            const V<N> k = kept(d[i]);
-            if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
-            m.H = advance(d[i], k, m.H, a.tied ? remainder(d[i], k, xv) : xv);
-            m.A = decayed(d[i], k, m.A);
+        for (int p = 0; p < kRun; p += S) {
+            V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
+            const V<2> d2 = decay(Lane<T>::pair(gs + p * 32), k2);
+            if (a.tied) u2 = remainder(d2, k2, u2);
+#pragma unroll
+            for (int i = p; i < p + S; ++i) {
+                d[i] = part<N>(d2, i - p);
+                const V<N> k = part<N>(k2, i - p);
+                if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
+                m.H = advance(d[i], k, m.H, part<N>(u2, i - p));
+                m.A = decayed(d[i], k, m.A);
+            }
         }
         back.A = m.A;
 #pragma unroll
@@ -664,7 +699,8 @@ __global__ void __launch_bounds__(256) step_kernel(int B, int C, bool tied, cons
         hr.get(h);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            const V<1> d = decay<T>(V<1>{{gv[j]}}), k = kept(d), v = {{xv[j]}};
+            V<1> k;
+            const V<1> d = decay(V<1>{{gv[j]}}, k), v = {{xv[j]}};
             h[j] = advance(d, k, V<1>{{h[j]}}, tied ? remainder(d, k, v) : v).v[0];
         }
         Chunk<float, E>::store(next + b * C + c, h);

@@ -134,6 +134,13 @@ struct Lane {
         else
             return {{__uint_as_float(w[0]), __uint_as_float(w[32])}};
     }
+    // the same, element by element, zeros past `left`
+    static __device__ __forceinline__ V<N> from(const T* p, int left) {
+        V<N> r;
+#pragma unroll
+        for (int j = 0; j < N; ++j) r.v[j] = j < left ? to_f<T>(p[j]) : 0.f;
+        return r;
+    }
     // the lane's channels (`left` of them are inside C), in one word or each by itself
     template <bool WORD>
     static __device__ __forceinline__ void put(T* p, const V<N>& r, int left) {
@@ -171,7 +178,7 @@ __device__ __forceinline__ V<N> part(const V<2>& p, int i) {
 }
 
 // The map of a run of tokens, h -> A h + H.  In a packed batch a run in which a sequence begins
-// forgets h: its A is then a NaN of our own, which no arithmetic makes.
+// forgets h: its A is then a NaN with bits that no arithmetic makes.
 constexpr uint32_t kCut = 0x7fc0c0deu;
 template <int N>
 struct Map {
@@ -257,16 +264,22 @@ __device__ __forceinline__ void copies_wait() {
 // x, g and do leave states as they are.  WIDE: 16-byte copies in flight; else element by element.
 template <typename T, bool WIDE>
 __device__ __forceinline__ void fill(char* to, const T* p, long long stride, int t0, int T_, int left) {
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = 16 / sizeof(T), kCopies = kTileBytes / 16 / kThreads;
     if (WIDE) {
         const int row0 = threadIdx.x / 8, c = threadIdx.x % 8 * E;
         const T* from = p + (t0 + row0) * stride + c;
-        const int rows = c < left ? T_ - t0 - row0 : 0;
+        to += threadIdx.x * 16;
+        if (t0 + kTile <= T_ && left >= Lane<T>::kSlab) {
 #pragma unroll
-        for (int i = 0; i < kTileBytes / 16 / kThreads; ++i) {
-            const bool in = i * (kThreads / 8) < rows;
-            copy16(to + (i * kThreads + threadIdx.x) * 16, in ? from : p, in);
-            from += kThreads / 8 * stride;
+            for (int i = 0; i < kCopies; ++i, from += kThreads / 8 * stride)
+                ptx::cp_async16(to + i * kThreads * 16, from);
+        } else {
+            const int rows = c < left ? T_ - t0 - row0 : 0;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i, from += kThreads / 8 * stride) {
+                const bool in = i * (kThreads / 8) < rows;
+                copy16(to + i * kThreads * 16, in ? from : p, in);
+            }
         }
     } else {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -291,15 +304,16 @@ __device__ bool bad_cu(const int* cu, int nseq, int T) {
     return __syncthreads_or(bad);
 }
 
-// The sequences (fewer than 65536) that begin and end at the tokens of a tile.
-constexpr unsigned kNone = 0xffff;
+// The tokens of a warp's run that begin and end a sequence, as bits, and these sequences, for token
+// i in lane i.
 struct Marks {
-    uint16_t first[kTile], last[kTile];
+    unsigned firsts = 0, lasts = 0;
+    int first = 0, last = 0;
 };
-__device__ __forceinline__ void mark(Marks& m, const int* cu, int nseq, int t0, int T) {
-    const int i = threadIdx.x, t = t0 + i;
-    if (i >= kTile) return;
-    unsigned first = kNone, last = kNone;
+__device__ __forceinline__ Marks marks_of(const int* cu, int nseq, int tw, int T) {
+    Marks m;
+    const int t = tw + (threadIdx.x & 31) % kRun;
+    bool begins = false, ends = false;
     if (t < T) {
         int lo = 0, hi = nseq;   // cu[lo] <= t < cu[hi]
         while (hi - lo > 1) {
@@ -309,17 +323,18 @@ __device__ __forceinline__ void mark(Marks& m, const int* cu, int nseq, int t0, 
             else
                 hi = mid;
         }
-        if (cu[lo] == t) first = lo;
-        if (cu[lo + 1] == t + 1) last = lo;
+        m.first = m.last = lo;
+        begins = cu[lo] == t;
+        ends = cu[lo + 1] == t + 1;
     }
-    m.first[i] = (uint16_t)first;
-    m.last[i] = (uint16_t)last;
+    m.firsts = __ballot_sync(~0u, begins) & ((1u << kRun) - 1);
+    m.lasts = __ballot_sync(~0u, ends) & ((1u << kRun) - 1);
+    return m;
 }
 
 struct __align__(16) Shared {
-    float4 peers[2][kMaxCluster - 1][32];   // maps of the cluster's other CTAs, in two turns
-    uint64_t arrived[2];                    // ... and that they are here
-    Marks marks[2];
+    float4 peers[2][kMaxCluster][32];   // maps of the cluster's CTAs, in two turns
+    uint64_t arrived[2];                // ... and that they are here
 };
 
 // Exchanges of a cluster's maps, one a turn.
@@ -339,30 +354,24 @@ struct Cluster {
         cluster_sync();
     }
     __device__ __forceinline__ void expect(int i) {
-        ptx::mbar_arrive_expect_tx(&sh.arrived[i], (K - 1) * 32 * (unsigned)sizeof(float4));
+        ptx::mbar_arrive_expect_tx(&sh.arrived[i], K * 32 * (unsigned)sizeof(float4));
     }
     // The state that enters this CTA's tile; `carry` goes from before the cluster's tiles of this
     // turn to behind them.  Tiles in the order of the ranks, or against it.  A buffer is written again two turns
     // later, by CTAs that have this one's map of the turn between: its reads are over by then.
     __device__ __forceinline__ V<N> exchange(int turn, const Map<N>& own, V<N>& carry) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = turn & 1;
-        for (int r = warp; r < K; r += kWarps) {
-            if (r == rank) continue;
-            const int slot = rank < r ? rank : rank - 1;
-            push16(peer_address(&sh.peers[i][slot][lane], r), peer_address(&sh.arrived[i], r), to4<N>(own));
-        }
+        for (int r = warp; r < K; r += kWarps)
+            push16(peer_address(&sh.peers[i][rank][lane], r), peer_address(&sh.arrived[i], r), to4<N>(own));
         if (!lost) lost = !await(&sh.arrived[i], turn >> 1 & 1);
         if (threadIdx.x == 0) expect(i);
-        V<N> enter = carry;
-        for (int j = 0; j < K; ++j) {
-            const int r = BACK ? K - 1 - j : j;
-            if (r == rank) {
-                enter = carry;
-                carry = apply<VL>(own, carry);
-            } else {
-                carry = apply<VL>(from4<N>(sh.peers[i][r < rank ? r : r - 1][lane]), carry);
-            }
-        }
+        const int step = BACK ? -1 : 1;
+        int r = BACK ? K - 1 : 0;
+#pragma unroll 4
+        for (; r != rank; r += step) carry = apply<VL>(from4<N>(sh.peers[i][r][lane]), carry);
+        const V<N> enter = carry;
+#pragma unroll 4
+        for (; r != (BACK ? -1 : K); r += step) carry = apply<VL>(from4<N>(sh.peers[i][r][lane]), carry);
         return enter;
     }
 };
@@ -370,7 +379,7 @@ struct Cluster {
 constexpr int kFwdStages = 3, kBwdStages = 2;
 
 // VL: a packed batch.  WIDE: 16-byte copies and 4-byte stores.
-template <typename T, bool VL, bool WIDE>
+template <typename T, bool TIED, bool VL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, int K) {
     constexpr int N = Lane<T>::N, S = 2 / N;   // tokens of a pair of values
     extern __shared__ __align__(128) char stages[];
@@ -411,8 +420,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = (turn * K + rank) * kTile, tw = t0 + warp * kRun;
-        Marks& marks = sh.marks[turn & 1];
-        if (VL) mark(marks, a.cu, a.nseq, t0, a.T);
+        const Marks marks = VL ? marks_of(a.cu, a.nseq, tw, a.T) : Marks{};
+        // a run with the begin or end of a sequence in it, a rare one, goes token by token
+        const bool marked = VL && (marks.firsts | marks.lasts);
+        auto first_state = [&](int i) {
+            return Lane<T>::get32(h0_of(__shfl_sync(~0u, marks.first, i)), left);
+        };
         copies_wait<1>();
         __syncthreads();
         load(turn + 2);
@@ -424,31 +437,36 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             return reinterpret_cast<float4*>(stage + kTileBytes + w * kRun * kRowBytes) + lane;
         };
 
-        // tokens of the run that begin and end a sequence
-        unsigned firsts = 0, lasts = 0;
-        if (VL) {
-            firsts = __ballot_sync(~0u, marks.first[warp * kRun + lane % kRun] != kNone) & 0xffffu;
-            lasts = __ballot_sync(~0u, marks.last[warp * kRun + lane % kRun] != kNone) & 0xffffu;
-        }
         // from a zero state: each token's local state and product of decays
         V<N> h[kRun], P[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)};
-#pragma unroll
-        for (int p = 0; p < kRun; p += S) {
-            V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
-            const V<2> d2 = decay(Lane<T>::pair(gs + p * 32), k2);
-            if (a.tied) u2 = remainder(d2, k2, u2);
-#pragma unroll
-            for (int i = p; i < p + S; ++i) {
-                const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p);
-                if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
-                m.H = advance(d, k, m.H, part<N>(u2, i - p));
+        if (marked) {
+#pragma unroll 1
+            for (int i = 0; i < kRun; ++i) {
+                V<N> k, u = Lane<T>::get(xs[i * 32]);
+                const V<N> d = decay(Lane<T>::get(gs[i * 32]), k);
+                if (TIED) u = remainder(d, k, u);
+                if (marks.firsts >> i & 1) m.H = first_state(i);
+                m.H = advance(d, k, m.H, u);
                 m.A = decayed(d, k, m.A);
-                h[i] = m.H;
-                P[i] = m.A;
+            }
+            if (marks.firsts) m.A = all<N>(__uint_as_float(kCut));
+        } else {
+#pragma unroll
+            for (int p = 0; p < kRun; p += S) {
+                V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
+                const V<2> d2 = decay(Lane<T>::pair(gs + p * 32), k2);
+                if (TIED) u2 = remainder(d2, k2, u2);
+#pragma unroll
+                for (int i = p; i < p + S; ++i) {
+                    const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p);
+                    m.H = advance(d, k, m.H, part<N>(u2, i - p));
+                    m.A = decayed(d, k, m.A);
+                    h[i] = m.H;
+                    P[i] = m.A;
+                }
             }
         }
-        if (VL && firsts) m.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
         *map_of(warp) = to4<N>(m);
         __syncthreads();
@@ -468,20 +486,34 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         into = apply<VL>(before, into);   // the state that enters this warp's run
 
         if (states && tw % kStateEvery == 0 && tw < a.T) {
-            const V<N> v = VL && (firsts & 1) ? Lane<T>::get32(h0_of(marks.first[warp * kRun]), left) : into;
+            const V<N> v = VL && (marks.firsts & 1) ? first_state(0) : into;
             Lane<T>::put32(states + (long long)(tw / kStateEvery) * a.C, v, left);
         }
-        const int from = VL && firsts ? __ffs(firsts) - 1 : kRun;   // what entered ends there
         const int rows = a.o && left > 0 ? a.T - tw : 0;
         T* o = static_cast<T*>(a.o) + ((long long)b * a.T + tw) * a.C + c;
+        if (marked) {
+            // again, from the state that enters (this run's g is overwritten: from global memory)
+#pragma unroll 1
+            for (int i = 0; i < kRun; ++i, o += a.C) {
+                V<N> k, u = Lane<T>::get(xs[i * 32]);
+                const V<N> d = decay(Lane<T>::from(g + (tw + i) * a.g_token + lane * N, tw + i < a.T ? left : 0), k);
+                if (TIED) u = remainder(d, k, u);
+                if (marks.firsts >> i & 1) into = first_state(i);
+                into = advance(d, k, into, u);
+                if (i < rows) Lane<T>::template put<WIDE>(o, into, left);
+                if (marks.lasts >> i & 1) {
+                    const int s = __shfl_sync(~0u, marks.last, i);
+                    if (a.ht) Lane<T>::put32(a.ht + (long long)s * a.C + c, into, left);
+                }
+            }
+        } else if (rows >= kRun) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            V<N> v = fma(P[i], into, h[i]);
-            if (VL && i >= from) v = h[i];
-            if (i < rows) Lane<T>::template put<WIDE>(o, v, left);
-            o += a.C;
-            if (VL && (lasts >> i & 1) && a.ht)
-                Lane<T>::put32(a.ht + (long long)marks.last[warp * kRun + i] * a.C + c, v, left);
+            for (int i = 0; i < kRun; ++i, o += a.C)
+                Lane<T>::template put<WIDE>(o, fma(P[i], into, h[i]), left);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i, o += a.C)
+                if (i < rows) Lane<T>::template put<WIDE>(o, fma(P[i], into, h[i]), left);
         }
     }
     if (!VL && a.ht && rank == 0 && warp == 0) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
@@ -492,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
 // Tiles from the last to the first.  The states inside a tile are formed again from the kept ones
 // (one each 64 tokens, in 32 bits), so nothing is read of the rounded outputs; the same passes
 // carry m the other way.
-template <typename T, bool VL, bool WIDE>
+template <typename T, bool TIED, bool VL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a, int K) {
     constexpr int N = Lane<T>::N, S = 2 / N;   // tokens of a pair of values
     extern __shared__ __align__(128) char stages[];
@@ -536,8 +568,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = tile_of(turn) * kTile, tw = t0 + warp * kRun;
-        Marks& marks = sh.marks[turn & 1];
-        if (VL) mark(marks, a.cu, a.nseq, t0, a.T);
+        const Marks marks = VL ? marks_of(a.cu, a.nseq, tw, a.T) : Marks{};
+        const bool marked = VL && (marks.firsts | marks.lasts);   // such a run goes token by token
+        auto first_state = [&](int i) {
+            return Lane<T>::get32(h0_of(__shfl_sync(~0u, marks.first, i)), left);
+        };
+        auto last_grad = [&](int i) {
+            return Lane<T>::get32(dht_of(__shfl_sync(~0u, marks.last, i)), left);
+        };
         // the kept state of this warp's 64 tokens
         const int block = tw / kStateEvery;
         V<N> into = Lane<T>::get32(block < every ? states + (long long)block * a.C : nullptr, left);
@@ -551,35 +589,47 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         auto map_of = [&](int w) {
             return reinterpret_cast<float4*>(stage + kTileBytes + w * kRun * kRowBytes) + lane;
         };
-        unsigned firsts = 0, lasts = 0;
-        if (VL) {
-            firsts = __ballot_sync(~0u, marks.first[warp * kRun + lane % kRun] != kNone) & 0xffffu;
-            lasts = __ballot_sync(~0u, marks.last[warp * kRun + lane % kRun] != kNone) & 0xffffu;
-        }
         V<N> d[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)}, back = m;
-#pragma unroll
-        for (int p = 0; p < kRun; p += S) {
-            V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
-            const V<2> d2 = decay(Lane<T>::pair(gs + p * 32), k2);
-            if (a.tied) u2 = remainder(d2, k2, u2);
-#pragma unroll
-            for (int i = p; i < p + S; ++i) {
-                d[i] = part<N>(d2, i - p);
-                const V<N> k = part<N>(k2, i - p);
-                if (VL && (firsts >> i & 1)) m.H = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
-                m.H = advance(d[i], k, m.H, part<N>(u2, i - p));
-                m.A = decayed(d[i], k, m.A);
+        if (marked) {
+#pragma unroll 1
+            for (int i = 0; i < kRun; ++i) {
+                V<N> k, u = Lane<T>::get(xs[i * 32]);
+                const V<N> e = decay(Lane<T>::get(gs[i * 32]), k);
+                if (TIED) u = remainder(e, k, u);
+                if (marks.firsts >> i & 1) m.H = first_state(i);
+                m.H = advance(e, k, m.H, u);
+                m.A = decayed(e, k, m.A);
             }
-        }
-        back.A = m.A;
+            back.A = m.A;
+#pragma unroll 1
+            for (int i = kRun - 1; i >= 0; --i) {
+                V<N> k;
+                const V<N> e = decay(Lane<T>::get(gs[i * 32]), k);
+                if (marks.lasts >> i & 1) back.H = last_grad(i);
+                back.H = decayed(e, k, add(Lane<T>::get(ds[i * 32]), back.H));
+            }
+            if (marks.firsts) m.A = all<N>(__uint_as_float(kCut));
+            if (marks.lasts) back.A = all<N>(__uint_as_float(kCut));
+        } else {
 #pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
-            if (VL && (lasts >> i & 1)) back.H = Lane<T>::get32(dht_of(marks.last[warp * kRun + i]), left);
-            back.H = decayed(d[i], kept(d[i]), add(Lane<T>::get(ds[i * 32]), back.H));
+            for (int p = 0; p < kRun; p += S) {
+                V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
+                const V<2> d2 = decay(Lane<T>::pair(gs + p * 32), k2);
+                if (TIED) u2 = remainder(d2, k2, u2);
+#pragma unroll
+                for (int i = p; i < p + S; ++i) {
+                    d[i] = part<N>(d2, i - p);
+                    const V<N> k = part<N>(k2, i - p);
+                    m.H = advance(d[i], k, m.H, part<N>(u2, i - p));
+                    m.A = decayed(d[i], k, m.A);
+                }
+            }
+            back.A = m.A;
+#pragma unroll
+            for (int i = kRun - 1; i >= 0; --i)
+                back.H = decayed(d[i], kept(d[i]), add(Lane<T>::get(ds[i * 32]), back.H));
         }
-        if (VL && firsts) m.A = all<N>(__uint_as_float(kCut));
-        if (VL && lasts) back.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
         map_of(warp)[0] = to4<N>(m);
         map_of(warp)[32] = to4<N>(back);
@@ -602,30 +652,55 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             carry = apply<VL>(sum, carry);
         mc = apply<VL>(behind, mc);
 
-        V<N> w[kRun];   // h_{t-1}, less x where tied
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const V<N> xv = Lane<T>::get(xs[i * 32]), k = kept(d[i]);
-            if (VL && (firsts >> i & 1)) into = Lane<T>::get32(h0_of(marks.first[warp * kRun + i]), left);
-            w[i] = a.tied ? fma(xv, all<N>(-1.f), into) : into;
-            into = advance(d[i], k, into, a.tied ? remainder(d[i], k, xv) : xv);
-        }
         const int rows = left > 0 ? a.T - tw : 0;
         const long long end = ((long long)b * a.T + tw + kRun - 1) * a.C + c;
         T *dx = static_cast<T*>(a.dx) + end, *dg = static_cast<T*>(a.dg) + end;
-#pragma unroll
-        for (int i = kRun - 1; i >= 0; --i) {
-            if (VL && (lasts >> i & 1)) mc = Lane<T>::get32(dht_of(marks.last[warp * kRun + i]), left);
-            const V<N> l = add(Lane<T>::get(ds[i * 32]), mc), k = kept(d[i]);
-            mc = decayed(d[i], k, l);
-            if (i < rows) {
-                Lane<T>::template put<WIDE>(dx, a.tied ? remainder(d[i], k, l) : l, left);
-                Lane<T>::template put<WIDE>(dg, mul(mc, w[i]), left);
+        auto put = [&](V<N> e, V<N> k, V<N> w, int i) {
+            const V<N> l = add(Lane<T>::get(ds[i * 32]), mc);
+            mc = decayed(e, k, l);
+            Lane<T>::template put<WIDE>(dx, TIED ? remainder(e, k, l) : l, left);
+            Lane<T>::template put<WIDE>(dg, mul(mc, w), left);
+        };
+        if (marked) {
+            auto decay_of = [&](int i, V<N>& k) {
+                return decay(Lane<T>::from(g + (tw + i) * a.g_token + lane * N, tw + i < a.T ? left : 0), k);
+            };
+            V<N> w[kRun];
+#pragma unroll 1
+            for (int i = 0; i < kRun; ++i) {
+                V<N> k, u = Lane<T>::get(xs[i * 32]);
+                const V<N> e = decay_of(i, k);
+                if (marks.firsts >> i & 1) into = first_state(i);
+                w[i] = TIED ? fma(u, all<N>(-1.f), into) : into;
+                into = advance(e, k, into, TIED ? remainder(e, k, u) : u);
             }
-            dx -= a.C;
-            dg -= a.C;
-            if (VL && (firsts >> i & 1) && a.dh0)
-                Lane<T>::put32(a.dh0 + (long long)marks.first[warp * kRun + i] * a.C + c, mc, left);
+#pragma unroll 1
+            for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
+                V<N> k;
+                const V<N> e = decay_of(i, k);
+                if (marks.lasts >> i & 1) mc = last_grad(i);
+                if (i < rows) put(e, k, w[i], i);
+                if (marks.firsts >> i & 1) {
+                    const int s = __shfl_sync(~0u, marks.first, i);
+                    if (a.dh0) Lane<T>::put32(a.dh0 + (long long)s * a.C + c, mc, left);
+                }
+            }
+        } else {
+            V<N> w[kRun];   // h_{t-1}, less x where tied
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const V<N> xv = Lane<T>::get(xs[i * 32]), k = kept(d[i]);
+                w[i] = TIED ? fma(xv, all<N>(-1.f), into) : into;
+                into = advance(d[i], k, into, TIED ? remainder(d[i], k, xv) : xv);
+            }
+            if (rows >= kRun) {
+#pragma unroll
+                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) put(d[i], kept(d[i]), w[i], i);
+            } else {
+#pragma unroll
+                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C)
+                    if (i < rows) put(d[i], kept(d[i]), w[i], i);
+            }
         }
     }
     if (!VL && a.dh0 && rank == 0 && warp == 0) Lane<T>::put32(a.dh0 + (long long)b * a.C + c, carry, left);
@@ -640,9 +715,9 @@ int cluster_of(long long slabs, int T) {
     return K;
 }
 
-template <typename T, bool BWD, bool VL, bool WIDE>
+template <typename T, bool BWD, bool TIED, bool VL, bool WIDE>
 kda_status launch(const ScanArgs& a, cudaStream_t s) {
-    auto* k = BWD ? scan_bwd_kernel<T, VL, WIDE> : scan_fwd_kernel<T, VL, WIDE>;
+    auto* k = BWD ? scan_bwd_kernel<T, TIED, VL, WIDE> : scan_fwd_kernel<T, TIED, VL, WIDE>;
     const int slabs = (a.C + Lane<T>::kSlab - 1) / Lane<T>::kSlab;
     const int K = cluster_of((long long)slabs * a.B, a.T);
     const size_t smem = (BWD ? kBwdStages * 3 : kFwdStages * 2) * kTileBytes + sizeof(Shared);
@@ -670,13 +745,13 @@ kda_status launch(const ScanArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, a, K) == cudaSuccess ? launch_status() : KDA_ERR_CUDA;
 }
 
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool TIED>
 kda_status pick(const ScanArgs& a, cudaStream_t s) {
     constexpr int E = 16 / sizeof(T);
     const bool wide = a.C % E == 0 && a.x_batch % E == 0 && a.x_token % E == 0 && a.g_batch % E == 0 &&
                       a.g_token % E == 0 && aligned16({a.x, a.g, a.o, a.dout, a.dx, a.dg});
-    if (a.cu) return wide ? launch<T, BWD, true, true>(a, s) : launch<T, BWD, true, false>(a, s);
-    return wide ? launch<T, BWD, false, true>(a, s) : launch<T, BWD, false, false>(a, s);
+    if (a.cu) return wide ? launch<T, BWD, TIED, true, true>(a, s) : launch<T, BWD, TIED, true, false>(a, s);
+    return wide ? launch<T, BWD, TIED, false, true>(a, s) : launch<T, BWD, TIED, false, false>(a, s);
 }
 
 // One token per row, the state read and written once.
@@ -725,11 +800,13 @@ kda_status step(int B, int C, bool tied, const void* x, long long x_row, const v
 }  // namespace
 
 kda_status scan_fwd_launch(const ScanArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? pick<__nv_bfloat16, false>(a, s) : pick<float, false>(a, s);
+    if (a.tied) return bf16 ? pick<__nv_bfloat16, false, true>(a, s) : pick<float, false, true>(a, s);
+    return bf16 ? pick<__nv_bfloat16, false, false>(a, s) : pick<float, false, false>(a, s);
 }
 
 kda_status scan_bwd_launch(const ScanArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? pick<__nv_bfloat16, true>(a, s) : pick<float, true>(a, s);
+    if (a.tied) return bf16 ? pick<__nv_bfloat16, true, true>(a, s) : pick<float, true, true>(a, s);
+    return bf16 ? pick<__nv_bfloat16, true, false>(a, s) : pick<float, true, false>(a, s);
 }
 
 kda_status scan_step_launch(int B, int C, bool bf16, bool tied, const void* x, long long x_row,

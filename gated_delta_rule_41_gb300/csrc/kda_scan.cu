@@ -8,6 +8,7 @@
 // A = prod exp(g), H its end state from zero, and maps h to A h + H.  A packed batch is one line
 // of tokens with a map that forgets what came before at every first token.
 #include <atomic>
+#include <mutex>
 
 #include "kda_block.cuh"
 #include "kda_ptx.cuh"
@@ -134,25 +135,18 @@ struct Lane {
         else
             return {{__uint_as_float(w[0]), __uint_as_float(w[32])}};
     }
-    // the same, element by element, zeros past `left`
-    static __device__ __forceinline__ V<N> from(const T* p, int left) {
-        V<N> r;
-#pragma unroll
-        for (int j = 0; j < N; ++j) r.v[j] = j < left ? to_f<T>(p[j]) : 0.f;
-        return r;
-    }
     // the lane's channels (`left` of them are inside C), in one word or each by itself
     template <bool WORD>
     static __device__ __forceinline__ void put(T* p, const V<N>& r, int left) {
         if constexpr (N == 2) {
             if (WORD) {
-                *reinterpret_cast<uint32_t*>(p) = pack2(r.v[0], r.v[1]);
+                if (left > 0) *reinterpret_cast<uint32_t*>(p) = pack2(r.v[0], r.v[1]);
             } else {
-                p[0] = __float2bfloat16_rn(r.v[0]);
+                if (left > 0) p[0] = __float2bfloat16_rn(r.v[0]);
                 if (left > 1) p[1] = __float2bfloat16_rn(r.v[1]);
             }
         } else {
-            p[0] = r.v[0];
+            if (left > 0) p[0] = r.v[0];
         }
     }
     static __device__ __forceinline__ V<N> get32(const float* p, int left) {
@@ -250,6 +244,9 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity) {
     return true;
 }
 
+__device__ __forceinline__ void prefetch(const void* p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void copy16(void* to, const void* from, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(to)), "l"(from),
                  "r"(in ? 16 : 0)
@@ -309,6 +306,12 @@ __device__ bool bad_cu(const int* cu, int nseq, int T) {
 struct Marks {
     unsigned firsts = 0, lasts = 0;
     int first = 0, last = 0;
+    // where there is at most one of each: their places, -1 for none; else the run goes token by token
+    __device__ __forceinline__ int f() const { return __ffs(firsts) - 1; }
+    __device__ __forceinline__ int l() const { return __ffs(lasts) - 1; }
+    __device__ __forceinline__ bool several() const {
+        return (firsts & (firsts - 1)) != 0 || (lasts & (lasts - 1)) != 0;
+    }
 };
 __device__ __forceinline__ Marks marks_of(const int* cu, int nseq, int tw, int T) {
     Marks m;
@@ -417,15 +420,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     Cluster<VL, N, false> cluster{sh, K, rank};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : h0_of(b), left);
+    V<N> again[VL ? kRun : 1];   // decays of a run that goes token by token
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = (turn * K + rank) * kTile, tw = t0 + warp * kRun;
         const Marks marks = VL ? marks_of(a.cu, a.nseq, tw, a.T) : Marks{};
-        // a run with the begin or end of a sequence in it, a rare one, goes token by token
-        const bool marked = VL && (marks.firsts | marks.lasts);
+        const bool several = VL && marks.several();
+        const int f = VL ? marks.f() : -1, l = VL ? marks.l() : -1;
         auto first_state = [&](int i) {
             return Lane<T>::get32(h0_of(__shfl_sync(~0u, marks.first, i)), left);
         };
+        auto last_state = [&](int i, V<N> v) {
+            const int s = __shfl_sync(~0u, marks.last, i);
+            if (a.ht) Lane<T>::put32(a.ht + (long long)s * a.C + c, v, left);
+        };
+        if (VL && a.h0 && marks.firsts) {   // (shuffles need the whole warp, lanes past C too)
+            const int s = __shfl_sync(~0u, marks.first, f);
+            if (left > 0) prefetch(h0_of(s));
+        }
         copies_wait<1>();
         __syncthreads();
         load(turn + 2);
@@ -440,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         // from a zero state: each token's local state and product of decays
         V<N> h[kRun], P[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)};
-        if (marked) {
+        if (several) {
 #pragma unroll 1
             for (int i = 0; i < kRun; ++i) {
                 V<N> k, u = Lane<T>::get(xs[i * 32]);
@@ -449,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 if (marks.firsts >> i & 1) m.H = first_state(i);
                 m.H = advance(d, k, m.H, u);
                 m.A = decayed(d, k, m.A);
+                again[i] = d;
             }
-            if (marks.firsts) m.A = all<N>(__uint_as_float(kCut));
         } else {
 #pragma unroll
             for (int p = 0; p < kRun; p += S) {
@@ -460,6 +472,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
 #pragma unroll
                 for (int i = p; i < p + S; ++i) {
                     const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p);
+                    if (VL && i == f) {   // what enters the run ends here
+                        m.H = first_state(i);
+                        m.A = all<N>(0.f);
+                    }
                     m.H = advance(d, k, m.H, part<N>(u2, i - p));
                     m.A = decayed(d, k, m.A);
                     h[i] = m.H;
@@ -467,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 }
             }
         }
+        if (VL && marks.firsts) m.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
         *map_of(warp) = to4<N>(m);
         __syncthreads();
@@ -489,31 +506,34 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             const V<N> v = VL && (marks.firsts & 1) ? first_state(0) : into;
             Lane<T>::put32(states + (long long)(tw / kStateEvery) * a.C, v, left);
         }
-        const int rows = a.o && left > 0 ? a.T - tw : 0;
+        const int rows = a.o ? a.T - tw : 0;   // alike in all lanes: what follows shuffles
         T* o = static_cast<T*>(a.o) + ((long long)b * a.T + tw) * a.C + c;
-        if (marked) {
-            // again, from the state that enters (this run's g is overwritten: from global memory)
+        if (several) {
+            // again, from the state that enters
 #pragma unroll 1
             for (int i = 0; i < kRun; ++i, o += a.C) {
-                V<N> k, u = Lane<T>::get(xs[i * 32]);
-                const V<N> d = decay(Lane<T>::from(g + (tw + i) * a.g_token + lane * N, tw + i < a.T ? left : 0), k);
-                if (TIED) u = remainder(d, k, u);
+                const V<N> d = again[i], k = kept(d), xv = Lane<T>::get(xs[i * 32]);
                 if (marks.firsts >> i & 1) into = first_state(i);
-                into = advance(d, k, into, u);
+                into = advance(d, k, into, TIED ? remainder(d, k, xv) : xv);
                 if (i < rows) Lane<T>::template put<WIDE>(o, into, left);
-                if (marks.lasts >> i & 1) {
-                    const int s = __shfl_sync(~0u, marks.last, i);
-                    if (a.ht) Lane<T>::put32(a.ht + (long long)s * a.C + c, into, left);
-                }
+                if (marks.lasts >> i & 1) last_state(i, into);
             }
         } else if (rows >= kRun) {
 #pragma unroll
-            for (int i = 0; i < kRun; ++i, o += a.C)
-                Lane<T>::template put<WIDE>(o, fma(P[i], into, h[i]), left);
+            for (int i = 0; i < kRun; ++i, o += a.C) {
+                if (VL && i == f) into = all<N>(0.f);
+                const V<N> v = fma(P[i], into, h[i]);
+                Lane<T>::template put<WIDE>(o, v, left);
+                if (VL && i == l) last_state(i, v);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < kRun; ++i, o += a.C)
-                if (i < rows) Lane<T>::template put<WIDE>(o, fma(P[i], into, h[i]), left);
+            for (int i = 0; i < kRun; ++i, o += a.C) {
+                if (VL && i == f) into = all<N>(0.f);
+                const V<N> v = fma(P[i], into, h[i]);
+                if (i < rows) Lane<T>::template put<WIDE>(o, v, left);
+                if (VL && i == l) last_state(i, v);
+            }
         }
     }
     if (!VL && a.ht && rank == 0 && warp == 0) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
@@ -565,17 +585,31 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
     Cluster<VL, N, true> cluster{sh, K, rank};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : dht_of(b), left);
+    V<N> again[VL ? kRun : 1];   // decays of a run that goes token by token
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = tile_of(turn) * kTile, tw = t0 + warp * kRun;
         const Marks marks = VL ? marks_of(a.cu, a.nseq, tw, a.T) : Marks{};
-        const bool marked = VL && (marks.firsts | marks.lasts);   // such a run goes token by token
+        const bool several = VL && marks.several();
+        const int f = VL ? marks.f() : -1, l = VL ? marks.l() : -1;
         auto first_state = [&](int i) {
             return Lane<T>::get32(h0_of(__shfl_sync(~0u, marks.first, i)), left);
         };
         auto last_grad = [&](int i) {
             return Lane<T>::get32(dht_of(__shfl_sync(~0u, marks.last, i)), left);
         };
+        auto first_grad = [&](int i, V<N> v) {
+            const int s = __shfl_sync(~0u, marks.first, i);
+            if (a.dh0) Lane<T>::put32(a.dh0 + (long long)s * a.C + c, v, left);
+        };
+        if (VL && a.h0 && marks.firsts) {   // (shuffles need the whole warp, lanes past C too)
+            const int s = __shfl_sync(~0u, marks.first, f);
+            if (left > 0) prefetch(h0_of(s));
+        }
+        if (VL && a.dht && marks.lasts) {
+            const int s = __shfl_sync(~0u, marks.last, l);
+            if (left > 0) prefetch(dht_of(s));
+        }
         // the kept state of this warp's 64 tokens
         const int block = tw / kStateEvery;
         V<N> into = Lane<T>::get32(block < every ? states + (long long)block * a.C : nullptr, left);
@@ -591,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         };
         V<N> d[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)}, back = m;
-        if (marked) {
+        if (several) {
 #pragma unroll 1
             for (int i = 0; i < kRun; ++i) {
                 V<N> k, u = Lane<T>::get(xs[i * 32]);
@@ -600,17 +634,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
                 if (marks.firsts >> i & 1) m.H = first_state(i);
                 m.H = advance(e, k, m.H, u);
                 m.A = decayed(e, k, m.A);
+                again[i] = e;
             }
             back.A = m.A;
 #pragma unroll 1
             for (int i = kRun - 1; i >= 0; --i) {
-                V<N> k;
-                const V<N> e = decay(Lane<T>::get(gs[i * 32]), k);
                 if (marks.lasts >> i & 1) back.H = last_grad(i);
-                back.H = decayed(e, k, add(Lane<T>::get(ds[i * 32]), back.H));
+                back.H = decayed(again[i], kept(again[i]), add(Lane<T>::get(ds[i * 32]), back.H));
             }
-            if (marks.firsts) m.A = all<N>(__uint_as_float(kCut));
-            if (marks.lasts) back.A = all<N>(__uint_as_float(kCut));
         } else {
 #pragma unroll
             for (int p = 0; p < kRun; p += S) {
@@ -621,15 +652,20 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
                 for (int i = p; i < p + S; ++i) {
                     d[i] = part<N>(d2, i - p);
                     const V<N> k = part<N>(k2, i - p);
+                    if (VL && i == f) m.H = first_state(i);
                     m.H = advance(d[i], k, m.H, part<N>(u2, i - p));
                     m.A = decayed(d[i], k, m.A);
                 }
             }
             back.A = m.A;
 #pragma unroll
-            for (int i = kRun - 1; i >= 0; --i)
+            for (int i = kRun - 1; i >= 0; --i) {
+                if (VL && i == l) back.H = last_grad(i);
                 back.H = decayed(d[i], kept(d[i]), add(Lane<T>::get(ds[i * 32]), back.H));
+            }
         }
+        if (VL && marks.firsts) m.A = all<N>(__uint_as_float(kCut));
+        if (VL && marks.lasts) back.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
         map_of(warp)[0] = to4<N>(m);
         map_of(warp)[32] = to4<N>(back);
@@ -652,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             carry = apply<VL>(sum, carry);
         mc = apply<VL>(behind, mc);
 
-        const int rows = left > 0 ? a.T - tw : 0;
+        const int rows = a.T - tw;   // alike in all lanes: what follows shuffles
         const long long end = ((long long)b * a.T + tw + kRun - 1) * a.C + c;
         T *dx = static_cast<T*>(a.dx) + end, *dg = static_cast<T*>(a.dg) + end;
         auto put = [&](V<N> e, V<N> k, V<N> w, int i) {
@@ -661,45 +697,44 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             Lane<T>::template put<WIDE>(dx, TIED ? remainder(e, k, l) : l, left);
             Lane<T>::template put<WIDE>(dg, mul(mc, w), left);
         };
-        if (marked) {
-            auto decay_of = [&](int i, V<N>& k) {
-                return decay(Lane<T>::from(g + (tw + i) * a.g_token + lane * N, tw + i < a.T ? left : 0), k);
-            };
+        if (several) {
             V<N> w[kRun];
 #pragma unroll 1
             for (int i = 0; i < kRun; ++i) {
-                V<N> k, u = Lane<T>::get(xs[i * 32]);
-                const V<N> e = decay_of(i, k);
+                const V<N> e = again[i], k = kept(e), xv = Lane<T>::get(xs[i * 32]);
                 if (marks.firsts >> i & 1) into = first_state(i);
-                w[i] = TIED ? fma(u, all<N>(-1.f), into) : into;
-                into = advance(e, k, into, TIED ? remainder(e, k, u) : u);
+                w[i] = TIED ? fma(xv, all<N>(-1.f), into) : into;
+                into = advance(e, k, into, TIED ? remainder(e, k, xv) : xv);
             }
 #pragma unroll 1
             for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
-                V<N> k;
-                const V<N> e = decay_of(i, k);
                 if (marks.lasts >> i & 1) mc = last_grad(i);
-                if (i < rows) put(e, k, w[i], i);
-                if (marks.firsts >> i & 1) {
-                    const int s = __shfl_sync(~0u, marks.first, i);
-                    if (a.dh0) Lane<T>::put32(a.dh0 + (long long)s * a.C + c, mc, left);
-                }
+                if (i < rows) put(again[i], kept(again[i]), w[i], i);
+                if (marks.firsts >> i & 1) first_grad(i, mc);
             }
         } else {
             V<N> w[kRun];   // h_{t-1}, less x where tied
 #pragma unroll
             for (int i = 0; i < kRun; ++i) {
                 const V<N> xv = Lane<T>::get(xs[i * 32]), k = kept(d[i]);
+                if (VL && i == f) into = first_state(i);
                 w[i] = TIED ? fma(xv, all<N>(-1.f), into) : into;
                 into = advance(d[i], k, into, TIED ? remainder(d[i], k, xv) : xv);
             }
             if (rows >= kRun) {
 #pragma unroll
-                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) put(d[i], kept(d[i]), w[i], i);
+                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
+                    if (VL && i == l) mc = last_grad(i);
+                    put(d[i], kept(d[i]), w[i], i);
+                    if (VL && i == f) first_grad(i, mc);
+                }
             } else {
 #pragma unroll
-                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C)
+                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
+                    if (VL && i == l) mc = last_grad(i);
                     if (i < rows) put(d[i], kept(d[i]), w[i], i);
+                    if (VL && i == f) first_grad(i, mc);
+                }
             }
         }
     }
@@ -708,10 +743,45 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
     if (K > 1) cluster_sync();
 }
 
-// CTAs of a cluster: as many as keep all slabs' CTAs resident (two per SM), tiles allowing.
-int cluster_of(long long slabs, int T) {
-    int K = 1;
-    while (K < kMaxCluster && K * slabs <= sm_count() && K * kTile < T) K *= 2;
+// What a kernel needs once per device: its attributes, and how many clusters of each size the
+// device holds at once (sizes of nine to sixteen fit badly into its parts: 14 clusters of 16 CTAs,
+// where 36 of 8 fit).
+struct Setup {
+    std::atomic<bool> ready{false};
+    std::mutex lock;
+    int clusters[kMaxCluster + 1];
+};
+template <typename K>
+bool prepare(Setup& s, K kernel, size_t smem) {
+    if (s.ready.load(std::memory_order_acquire)) return true;
+    std::lock_guard<std::mutex> hold(s.lock);
+    if (s.ready.load(std::memory_order_relaxed)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    for (int k = 1; k <= kMaxCluster; ++k) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {(unsigned)k, 1, 1};
+        cfg.gridDim = dim3(k);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&s.clusters[k], kernel, &cfg) != cudaSuccess) {
+            s.clusters[k] = 0;
+            cudaGetLastError();
+        }
+    }
+    s.ready.store(true, std::memory_order_release);
+    return true;
+}
+// CTAs of a cluster: as many as still let all slabs run at once, and find tiles.
+int cluster_of(const Setup& s, long long slabs, int T) {
+    const int tiles = (T + kTile - 1) / kTile;
+    int K = tiles < kMaxCluster ? tiles : kMaxCluster;
+    while (K > 1 && s.clusters[K] < slabs) --K;
     return K;
 }
 
@@ -719,18 +789,12 @@ template <typename T, bool BWD, bool TIED, bool VL, bool WIDE>
 kda_status launch(const ScanArgs& a, cudaStream_t s) {
     auto* k = BWD ? scan_bwd_kernel<T, TIED, VL, WIDE> : scan_fwd_kernel<T, TIED, VL, WIDE>;
     const int slabs = (a.C + Lane<T>::kSlab - 1) / Lane<T>::kSlab;
-    const int K = cluster_of((long long)slabs * a.B, a.T);
     const size_t smem = (BWD ? kBwdStages * 3 : kFwdStages * 2) * kTileBytes + sizeof(Shared);
-    // once per device; a second time does no harm
-    static std::atomic<unsigned long long> ready{0};
+    static Setup setups[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
-    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return KDA_ERR_CUDA;
-        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || !prepare(setups[dev], k, smem))
+        return KDA_ERR_CUDA;
+    const int K = cluster_of(setups[dev], (long long)slabs * a.B, a.T);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(slabs * K, a.B);
     cfg.blockDim = dim3(kThreads);

@@ -85,6 +85,14 @@ __device__ __forceinline__ V<N> kept(V<N> d) {
     for (int j = 0; j < N; ++j) k.v[j] = __int_as_float(__float_as_int(d.v[j]) >> 31 & 0x3f800000);
     return k;
 }
+// The same, formed again and not taken from an earlier pass: held since then it would need
+// registers that are not there.
+template <int N>
+__device__ __forceinline__ V<N> kept_again(V<N> d) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm volatile("" : "+f"(d.v[j]));
+    return kept(d);
+}
 // exp(g) h, and with an input
 template <int N>
 __device__ __forceinline__ V<N> decayed(V<N> d, V<N> k, V<N> h) {
@@ -94,10 +102,20 @@ template <int N>
 __device__ __forceinline__ V<N> advance(V<N> d, V<N> k, V<N> h, V<N> u) {
     return fma(k, h, fma(d, h, u));
 }
+template <int N>
+__device__ __forceinline__ V<N> less(V<N> a, V<N> b) {
+    V<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = a.v[j] - b.v[j];
+    return r;
+}
 // (1 - exp(g)) x; 1 - keep is exact
 template <int N>
 __device__ __forceinline__ V<N> remainder(V<N> d, V<N> k, V<N> x) {
-    return mul(fma(d, all<N>(-1.f), fma(k, all<N>(-1.f), all<N>(1.f))), x);
+    V<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = (1.f - k.v[j]) - d.v[j];
+    return mul(r, x);
 }
 
 // ---- the scan over long sequences ----
@@ -302,10 +320,39 @@ __device__ bool bad_cu(const int* cu, int nseq, int T) {
 }
 
 // The tokens of a warp's run that begin and end a sequence, as bits, and these sequences, for token
-// i in lane i.
+// i in lane i.  A run inside the sequence that was last looked up needs no look-up.
 struct Marks {
     unsigned firsts = 0, lasts = 0;
     int first = 0, last = 0;
+    int begin = 0, end = 0;   // of that sequence
+
+    template <bool BACK>
+    __device__ __forceinline__ void look_up(const int* cu, int nseq, int tw, int T) {
+        firsts = lasts = 0;
+        if (tw > begin && tw + kRun < end) return;
+        const int t = tw + (threadIdx.x & 31) % kRun;
+        bool begins = false, ends = false;
+        int from = 0, to = 0;
+        if (t < T) {
+            int lo = 0, hi = nseq;   // cu[lo] <= t < cu[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (cu[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            first = last = lo;
+            from = cu[lo];
+            to = cu[lo + 1];
+            begins = from == t;
+            ends = to == t + 1;
+        }
+        firsts = __ballot_sync(~0u, begins) & ((1u << kRun) - 1);
+        lasts = __ballot_sync(~0u, ends) & ((1u << kRun) - 1);
+        begin = __shfl_sync(~0u, from, BACK ? 0 : kRun - 1);
+        end = __shfl_sync(~0u, to, BACK ? 0 : kRun - 1);
+    }
     // where there is at most one of each: their places, -1 for none; else the run goes token by token
     __device__ __forceinline__ int f() const { return __ffs(firsts) - 1; }
     __device__ __forceinline__ int l() const { return __ffs(lasts) - 1; }
@@ -313,34 +360,13 @@ struct Marks {
         return (firsts & (firsts - 1)) != 0 || (lasts & (lasts - 1)) != 0;
     }
 };
-__device__ __forceinline__ Marks marks_of(const int* cu, int nseq, int tw, int T) {
-    Marks m;
-    const int t = tw + (threadIdx.x & 31) % kRun;
-    bool begins = false, ends = false;
-    if (t < T) {
-        int lo = 0, hi = nseq;   // cu[lo] <= t < cu[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (cu[mid] <= t)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        m.first = m.last = lo;
-        begins = cu[lo] == t;
-        ends = cu[lo + 1] == t + 1;
-    }
-    m.firsts = __ballot_sync(~0u, begins) & ((1u << kRun) - 1);
-    m.lasts = __ballot_sync(~0u, ends) & ((1u << kRun) - 1);
-    return m;
-}
 
 struct __align__(16) Shared {
     float4 peers[2][kMaxCluster][32];   // maps of the cluster's CTAs, in two turns
     uint64_t arrived[2];                // ... and that they are here
 };
 
-// Exchanges of a cluster's maps, one a turn.
+// Exchanges of a cluster's maps, one a turn, by one warp of each CTA.
 template <bool VL, int N, bool BACK>
 struct Cluster {
     Shared& sh;
@@ -363,11 +389,13 @@ struct Cluster {
     // turn to behind them.  Tiles in the order of the ranks, or against it.  A buffer is written again two turns
     // later, by CTAs that have this one's map of the turn between: its reads are over by then.
     __device__ __forceinline__ V<N> exchange(int turn, const Map<N>& own, V<N>& carry) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = turn & 1;
-        for (int r = warp; r < K; r += kWarps)
+        const int lane = threadIdx.x & 31, i = turn & 1;
+#pragma unroll 4
+        for (int r = 0; r < K; ++r)
             push16(peer_address(&sh.peers[i][rank][lane], r), peer_address(&sh.arrived[i], r), to4<N>(own));
         if (!lost) lost = !await(&sh.arrived[i], turn >> 1 & 1);
-        if (threadIdx.x == 0) expect(i);
+        __syncwarp();
+        if (lane == 0) expect(i);
         const int step = BACK ? -1 : 1;
         int r = BACK ? K - 1 : 0;
 #pragma unroll 4
@@ -377,7 +405,40 @@ struct Cluster {
         for (; r != (BACK ? -1 : K); r += step) carry = apply<VL>(from4<N>(sh.peers[i][r][lane]), carry);
         return enter;
     }
+
+    // What enters each warp's run, from the warps' maps: map_of(w)[0], in the order of the warps or
+    // against it, left at into_of(w).
+    template <typename M, typename I>
+    __device__ __forceinline__ void enter_runs(int turn, V<N>& carry, M map_of, I into_of) {
+        Map<N> m[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m[w] = from4<N>(*map_of(BACK ? kWarps - 1 - w : w));
+        V<N> into = carry;
+        if (K > 1) {
+            Map<N> sum = m[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) sum = compose<VL>(sum, m[w]);
+            into = exchange(turn, sum, carry);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            *into_of(BACK ? kWarps - 1 - w : w) = make_float2(into.v[0], into.v[N - 1]);
+            into = apply<VL>(m[w], into);
+        }
+        if (K == 1) carry = into;
+    }
 };
+template <int N>
+__device__ __forceinline__ V<N> from2(const float2& v) {
+    V<N> r;
+    r.v[0] = v.x;
+    r.v[N - 1] = N == 2 ? v.y : v.x;
+    return r;
+}
+
+// Keeps the compiler from moving the loads of an unrolled pass to its beginning, where they would
+// take registers that are not there.
+__device__ __forceinline__ void hold_loads() { asm volatile("" ::: "memory"); }
 
 constexpr int kFwdStages = 3, kBwdStages = 2;
 
@@ -417,14 +478,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     };
     load(0);
     load(1);
+    // one warp combines the maps; not the same one in CTAs that share an SM
+    const int lead = blockIdx.x % kWarps;
     Cluster<VL, N, false> cluster{sh, K, rank};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : h0_of(b), left);
     V<N> again[VL ? kRun : 1];   // decays of a run that goes token by token
+    Marks marks;
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = (turn * K + rank) * kTile, tw = t0 + warp * kRun;
-        const Marks marks = VL ? marks_of(a.cu, a.nseq, tw, a.T) : Marks{};
+        if (VL) marks.look_up<false>(a.cu, a.nseq, tw, a.T);
         const bool several = VL && marks.several();
         const int f = VL ? marks.f() : -1, l = VL ? marks.l() : -1;
         auto first_state = [&](int i) {
@@ -444,10 +508,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         char* stage = stages + turn % kFwdStages * 2 * kTileBytes;
         const uint32_t* xs = reinterpret_cast<uint32_t*>(stage) + warp * kRun * 32 + lane;
         const uint32_t* gs = xs + kTileBytes / 4;
-        // the warps' maps go where their rows of g were
+        // the warps' maps go where their rows of g were, and what enters their runs behind them
         auto map_of = [&](int w) {
             return reinterpret_cast<float4*>(stage + kTileBytes + w * kRun * kRowBytes) + lane;
         };
+        auto into_of = [&](int w) { return reinterpret_cast<float2*>(map_of(w) - lane + 32) + lane; };
 
         // from a zero state: each token's local state and product of decays
         V<N> h[kRun], P[kRun];
@@ -488,19 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         *map_of(warp) = to4<N>(m);
         __syncthreads();
 
-        // the warps before this one, and all of them
-        Map<N> sum = from4<N>(*map_of(0)), before = {all<N>(1.f), all<N>(0.f)};
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            if (w == warp) before = sum;
-            sum = compose<VL>(sum, from4<N>(*map_of(w)));
-        }
-        V<N> into = carry;
-        if (K > 1)
-            into = cluster.exchange(turn, sum, carry);
-        else
-            carry = apply<VL>(sum, carry);
-        into = apply<VL>(before, into);   // the state that enters this warp's run
+        if (warp == lead) cluster.enter_runs(turn, carry, map_of, into_of);
+        __syncthreads();
+        V<N> into = from2<N>(*into_of(warp));
 
         if (states && tw % kStateEvery == 0 && tw < a.T) {
             const V<N> v = VL && (marks.firsts & 1) ? first_state(0) : into;
@@ -536,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             }
         }
     }
-    if (!VL && a.ht && rank == 0 && warp == 0) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
+    if (!VL && a.ht && rank == 0 && warp == lead) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
     copies_wait<0>();
     if (K > 1) cluster_sync();   // no CTA leaves while another may write to its shared memory
 }
@@ -582,14 +637,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         ptx::cp_async_commit();
     };
     load(0);
+    // one warp combines the maps of m, one those of the states
+    constexpr int kPer = kStateEvery / kRun;
+    const int lead = blockIdx.x % kWarps, second = (lead + 2) % kWarps;
     Cluster<VL, N, true> cluster{sh, K, rank};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : dht_of(b), left);
     V<N> again[VL ? kRun : 1];   // decays of a run that goes token by token
+    Marks marks;
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = tile_of(turn) * kTile, tw = t0 + warp * kRun;
-        const Marks marks = VL ? marks_of(a.cu, a.nseq, tw, a.T) : Marks{};
+        if (VL) marks.look_up<true>(a.cu, a.nseq, tw, a.T);
         const bool several = VL && marks.several();
         const int f = VL ? marks.f() : -1, l = VL ? marks.l() : -1;
         auto first_state = [&](int i) {
@@ -610,19 +669,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             const int s = __shfl_sync(~0u, marks.last, l);
             if (left > 0) prefetch(dht_of(s));
         }
-        // the kept state of this warp's 64 tokens
-        const int block = tw / kStateEvery;
-        V<N> into = Lane<T>::get32(block < every ? states + (long long)block * a.C : nullptr, left);
+        V<N> into, kept_state[kWarps / kPer];
+        if (warp == second) {
+#pragma unroll
+            for (int i = 0; i < kWarps / kPer; ++i) {
+                const int block = t0 / kStateEvery + i;
+                kept_state[i] = Lane<T>::get32(block < every ? states + (long long)block * a.C : nullptr, left);
+            }
+        }
         copies_wait<0>();
         __syncthreads();
         load(turn + 1);
         char* stage = stages + turn % kBwdStages * 3 * kTileBytes;
         const uint32_t* xs = reinterpret_cast<uint32_t*>(stage) + warp * kRun * 32 + lane;
         const uint32_t *gs = xs + kTileBytes / 4, *ds = gs + kTileBytes / 4;
-        // the warps' maps go where their rows of g were: that of the states, and that of m
-        auto map_of = [&](int w) {
+        // the warps' maps go where their rows of g were: that of m and that of the states, and behind
+        // them what enters their runs
+        auto back_of = [&](int w) {
             return reinterpret_cast<float4*>(stage + kTileBytes + w * kRun * kRowBytes) + lane;
         };
+        auto map_of = [&](int w) { return back_of(w) + 32; };
+        auto m_of = [&](int w) { return reinterpret_cast<float2*>(back_of(w) - lane + 64) + lane; };
+        auto into_of = [&](int w) { return m_of(w) + 32; };
         V<N> d[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)}, back = m;
         if (several) {
@@ -667,26 +735,23 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         if (VL && marks.firsts) m.A = all<N>(__uint_as_float(kCut));
         if (VL && marks.lasts) back.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
-        map_of(warp)[0] = to4<N>(m);
-        map_of(warp)[32] = to4<N>(back);
+        *map_of(warp) = to4<N>(m);
+        *back_of(warp) = to4<N>(back);
         __syncthreads();
 
-        // the state that enters this warp's run: from the kept one over the warps before it
-        constexpr int kPer = kStateEvery / kRun;
-        for (int w = warp / kPer * kPer; w < warp; ++w) into = apply<VL>(from4<N>(map_of(w)[0]), into);
-        // m behind it: over the warps after it, and all of them
-        Map<N> sum = from4<N>(map_of(kWarps - 1)[32]), behind = {all<N>(1.f), all<N>(0.f)};
+        if (warp == lead) cluster.enter_runs(turn, carry, back_of, m_of);
+        if (warp == second) {
+            // the states that enter the runs, from those kept each kPer runs
 #pragma unroll
-        for (int w = kWarps - 2; w >= 0; --w) {
-            if (w == warp) behind = sum;
-            sum = compose<VL>(sum, from4<N>(map_of(w)[32]));
+            for (int w = 0; w < kWarps; ++w) {
+                if (w % kPer == 0) into = kept_state[w / kPer];
+                *into_of(w) = make_float2(into.v[0], into.v[N - 1]);
+                into = apply<VL>(from4<N>(*map_of(w)), into);
+            }
         }
-        V<N> mc = carry;
-        if (K > 1)
-            mc = cluster.exchange(turn, sum, carry);
-        else
-            carry = apply<VL>(sum, carry);
-        mc = apply<VL>(behind, mc);
+        __syncthreads();
+        into = from2<N>(*into_of(warp));
+        V<N> mc = from2<N>(*m_of(warp));
 
         const int rows = a.T - tw;   // alike in all lanes: what follows shuffles
         const long long end = ((long long)b * a.T + tw + kRun - 1) * a.C + c;
@@ -703,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             for (int i = 0; i < kRun; ++i) {
                 const V<N> e = again[i], k = kept(e), xv = Lane<T>::get(xs[i * 32]);
                 if (marks.firsts >> i & 1) into = first_state(i);
-                w[i] = TIED ? fma(xv, all<N>(-1.f), into) : into;
+                w[i] = TIED ? less(into, xv) : into;
                 into = advance(e, k, into, TIED ? remainder(e, k, xv) : xv);
             }
 #pragma unroll 1
@@ -713,32 +778,59 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
                 if (marks.firsts >> i & 1) first_grad(i, mc);
             }
         } else {
-            V<N> w[kRun];   // h_{t-1}, less x where tied
+            // h_{t-1}, less x where tied.  Tied with two channels to a lane these do not fit into the
+            // registers (spilled, at 10 % of L1 hits, they took 237 us for 160): they go where this
+            // run's x and g were.
+            constexpr bool kStash = TIED && N == 2;
+            V<N> w[kStash ? 1 : kRun];
+            uint32_t *stash = const_cast<uint32_t*>(xs), *stash2 = const_cast<uint32_t*>(gs);
+            auto keep_w = [&](int i, const V<N>& v) {
+                if constexpr (kStash) {
+                    stash[i * 32] = __float_as_uint(v.v[0]);
+                    stash2[i * 32] = __float_as_uint(v.v[N - 1]);
+                } else {
+                    w[i] = v;
+                }
+            };
+            auto w_of = [&](int i) {
+                if constexpr (kStash) {
+                    V<N> v;
+                    v.v[0] = __uint_as_float(stash[i * 32]);
+                    v.v[N - 1] = __uint_as_float(stash2[i * 32]);
+                    return v;
+                } else {
+                    return w[i];
+                }
+            };
+            if (kStash) __syncwarp();   // what entered the run, among g's rows, has been read
 #pragma unroll
             for (int i = 0; i < kRun; ++i) {
-                const V<N> xv = Lane<T>::get(xs[i * 32]), k = kept(d[i]);
+                if (i % 4 == 0) hold_loads();
+                const V<N> xv = Lane<T>::get(xs[i * 32]), k = TIED ? kept_again(d[i]) : kept(d[i]);
                 if (VL && i == f) into = first_state(i);
-                w[i] = TIED ? fma(xv, all<N>(-1.f), into) : into;
+                keep_w(i, TIED ? less(into, xv) : into);
                 into = advance(d[i], k, into, TIED ? remainder(d[i], k, xv) : xv);
             }
             if (rows >= kRun) {
 #pragma unroll
                 for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
+                    if (i % 4 == 3) hold_loads();
                     if (VL && i == l) mc = last_grad(i);
-                    put(d[i], kept(d[i]), w[i], i);
+                    put(d[i], TIED ? kept_again(d[i]) : kept(d[i]), w_of(i), i);
                     if (VL && i == f) first_grad(i, mc);
                 }
             } else {
 #pragma unroll
                 for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
+                    if (i % 4 == 3) hold_loads();
                     if (VL && i == l) mc = last_grad(i);
-                    if (i < rows) put(d[i], kept(d[i]), w[i], i);
+                    if (i < rows) put(d[i], TIED ? kept_again(d[i]) : kept(d[i]), w_of(i), i);
                     if (VL && i == f) first_grad(i, mc);
                 }
             }
         }
     }
-    if (!VL && a.dh0 && rank == 0 && warp == 0) Lane<T>::put32(a.dh0 + (long long)b * a.C + c, carry, left);
+    if (!VL && a.dh0 && rank == 0 && warp == lead) Lane<T>::put32(a.dh0 + (long long)b * a.C + c, carry, left);
     copies_wait<0>();
     if (K > 1) cluster_sync();
 }

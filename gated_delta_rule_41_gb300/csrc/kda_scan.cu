@@ -9,6 +9,7 @@
 // of tokens with a map that forgets what came before at every first token.
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "kda_block.cuh"
 #include "kda_ptx.cuh"
@@ -353,12 +354,7 @@ struct Marks {
         begin = __shfl_sync(~0u, from, BACK ? 0 : kRun - 1);
         end = __shfl_sync(~0u, to, BACK ? 0 : kRun - 1);
     }
-    // where there is at most one of each: their places, -1 for none; else the run goes token by token
-    __device__ __forceinline__ int f() const { return __ffs(firsts) - 1; }
-    __device__ __forceinline__ int l() const { return __ffs(lasts) - 1; }
-    __device__ __forceinline__ bool several() const {
-        return (firsts & (firsts - 1)) != 0 || (lasts & (lasts - 1)) != 0;
-    }
+    __device__ __forceinline__ bool any() const { return (firsts | lasts) != 0; }
 };
 
 struct __align__(16) Shared {
@@ -483,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     Cluster<VL, N, false> cluster{sh, K, rank};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : h0_of(b), left);
-    V<N> again[VL ? kRun : 1];   // decays of a run that goes token by token
     Marks marks;
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = (turn * K + rank) * kTile, tw = t0 + warp * kRun;
         if (VL) marks.look_up<false>(a.cu, a.nseq, tw, a.T);
-        const bool several = VL && marks.several();
-        const int f = VL ? marks.f() : -1, l = VL ? marks.l() : -1;
+        // runs with a border in them take code of their own: its tests at each token would keep the
+        // tokens of the others apart, too
+        const bool marked = VL && marks.any();
         auto first_state = [&](int i) {
             return Lane<T>::get32(h0_of(__shfl_sync(~0u, marks.first, i)), left);
         };
@@ -499,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             if (a.ht) Lane<T>::put32(a.ht + (long long)s * a.C + c, v, left);
         };
         if (VL && a.h0 && marks.firsts) {   // (shuffles need the whole warp, lanes past C too)
-            const int s = __shfl_sync(~0u, marks.first, f);
+            const int s = __shfl_sync(~0u, marks.first, __ffs(marks.firsts) - 1);
             if (left > 0) prefetch(h0_of(s));
         }
         copies_wait<1>();
@@ -517,18 +513,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         // from a zero state: each token's local state and product of decays
         V<N> h[kRun], P[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)};
-        if (several) {
-#pragma unroll 1
-            for (int i = 0; i < kRun; ++i) {
-                V<N> k, u = Lane<T>::get(xs[i * 32]);
-                const V<N> d = decay(Lane<T>::get(gs[i * 32]), k);
-                if (TIED) u = remainder(d, k, u);
-                if (marks.firsts >> i & 1) m.H = first_state(i);
-                m.H = advance(d, k, m.H, u);
-                m.A = decayed(d, k, m.A);
-                again[i] = d;
-            }
-        } else {
+        auto scan = [&](auto with_marks) {
+            constexpr bool M = decltype(with_marks)::value;
 #pragma unroll
             for (int p = 0; p < kRun; p += S) {
                 V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
@@ -537,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
 #pragma unroll
                 for (int i = p; i < p + S; ++i) {
                     const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p);
-                    if (VL && i == f) {   // what enters the run ends here
+                    if (M && (marks.firsts >> i & 1)) {   // what enters the run ends here
                         m.H = first_state(i);
                         m.A = all<N>(0.f);
                     }
@@ -547,7 +533,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                     P[i] = m.A;
                 }
             }
-        }
+        };
+        if (marked)
+            scan(std::true_type{});
+        else
+            scan(std::false_type{});
         if (VL && marks.firsts) m.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
         *map_of(warp) = to4<N>(m);
@@ -563,33 +553,22 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         }
         const int rows = a.o ? a.T - tw : 0;   // alike in all lanes: what follows shuffles
         T* o = static_cast<T*>(a.o) + ((long long)b * a.T + tw) * a.C + c;
-        if (several) {
-            // again, from the state that enters
-#pragma unroll 1
-            for (int i = 0; i < kRun; ++i, o += a.C) {
-                const V<N> d = again[i], k = kept(d), xv = Lane<T>::get(xs[i * 32]);
-                if (marks.firsts >> i & 1) into = first_state(i);
-                into = advance(d, k, into, TIED ? remainder(d, k, xv) : xv);
-                if (i < rows) Lane<T>::template put<WIDE>(o, into, left);
-                if (marks.lasts >> i & 1) last_state(i, into);
-            }
-        } else if (rows >= kRun) {
+        auto write = [&](auto with_marks, auto whole) {
+            constexpr bool M = decltype(with_marks)::value, W = decltype(whole)::value;
 #pragma unroll
             for (int i = 0; i < kRun; ++i, o += a.C) {
-                if (VL && i == f) into = all<N>(0.f);
+                if (M && (marks.firsts >> i & 1)) into = all<N>(0.f);
                 const V<N> v = fma(P[i], into, h[i]);
-                Lane<T>::template put<WIDE>(o, v, left);
-                if (VL && i == l) last_state(i, v);
+                if (W || i < rows) Lane<T>::template put<WIDE>(o, v, left);
+                if (M && (marks.lasts >> i & 1)) last_state(i, v);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kRun; ++i, o += a.C) {
-                if (VL && i == f) into = all<N>(0.f);
-                const V<N> v = fma(P[i], into, h[i]);
-                if (i < rows) Lane<T>::template put<WIDE>(o, v, left);
-                if (VL && i == l) last_state(i, v);
-            }
-        }
+        };
+        if (marked)
+            write(std::true_type{}, std::false_type{});
+        else if (rows >= kRun)
+            write(std::false_type{}, std::true_type{});
+        else
+            write(std::false_type{}, std::false_type{});
     }
     if (!VL && a.ht && rank == 0 && warp == lead) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
     copies_wait<0>();
@@ -643,14 +622,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
     Cluster<VL, N, true> cluster{sh, K, rank};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : dht_of(b), left);
-    V<N> again[VL ? kRun : 1];   // decays of a run that goes token by token
     Marks marks;
 
     for (int turn = 0; turn < turns; ++turn) {
         const int t0 = tile_of(turn) * kTile, tw = t0 + warp * kRun;
         if (VL) marks.look_up<true>(a.cu, a.nseq, tw, a.T);
-        const bool several = VL && marks.several();
-        const int f = VL ? marks.f() : -1, l = VL ? marks.l() : -1;
+        // runs with a border in them take code of their own: its tests at each token would keep the
+        // tokens of the others apart, too
+        const bool marked = VL && marks.any();
         auto first_state = [&](int i) {
             return Lane<T>::get32(h0_of(__shfl_sync(~0u, marks.first, i)), left);
         };
@@ -662,11 +641,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             if (a.dh0) Lane<T>::put32(a.dh0 + (long long)s * a.C + c, v, left);
         };
         if (VL && a.h0 && marks.firsts) {   // (shuffles need the whole warp, lanes past C too)
-            const int s = __shfl_sync(~0u, marks.first, f);
+            const int s = __shfl_sync(~0u, marks.first, __ffs(marks.firsts) - 1);
             if (left > 0) prefetch(h0_of(s));
         }
         if (VL && a.dht && marks.lasts) {
-            const int s = __shfl_sync(~0u, marks.last, l);
+            const int s = __shfl_sync(~0u, marks.last, 31 - __clz(marks.lasts));
             if (left > 0) prefetch(dht_of(s));
         }
         V<N> into, kept_state[kWarps / kPer];
@@ -693,24 +672,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         auto into_of = [&](int w) { return m_of(w) + 32; };
         V<N> d[kRun];
         Map<N> m = {all<N>(1.f), all<N>(0.f)}, back = m;
-        if (several) {
-#pragma unroll 1
-            for (int i = 0; i < kRun; ++i) {
-                V<N> k, u = Lane<T>::get(xs[i * 32]);
-                const V<N> e = decay(Lane<T>::get(gs[i * 32]), k);
-                if (TIED) u = remainder(e, k, u);
-                if (marks.firsts >> i & 1) m.H = first_state(i);
-                m.H = advance(e, k, m.H, u);
-                m.A = decayed(e, k, m.A);
-                again[i] = e;
-            }
-            back.A = m.A;
-#pragma unroll 1
-            for (int i = kRun - 1; i >= 0; --i) {
-                if (marks.lasts >> i & 1) back.H = last_grad(i);
-                back.H = decayed(again[i], kept(again[i]), add(Lane<T>::get(ds[i * 32]), back.H));
-            }
-        } else {
+        auto scan = [&](auto with_marks) {
+            constexpr bool M = decltype(with_marks)::value;
 #pragma unroll
             for (int p = 0; p < kRun; p += S) {
                 V<2> k2, u2 = Lane<T>::pair(xs + p * 32);
@@ -720,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
                 for (int i = p; i < p + S; ++i) {
                     d[i] = part<N>(d2, i - p);
                     const V<N> k = part<N>(k2, i - p);
-                    if (VL && i == f) m.H = first_state(i);
+                    if (M && (marks.firsts >> i & 1)) m.H = first_state(i);
                     m.H = advance(d[i], k, m.H, part<N>(u2, i - p));
                     m.A = decayed(d[i], k, m.A);
                 }
@@ -728,10 +691,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
             back.A = m.A;
 #pragma unroll
             for (int i = kRun - 1; i >= 0; --i) {
-                if (VL && i == l) back.H = last_grad(i);
+                if (M && (marks.lasts >> i & 1)) back.H = last_grad(i);
                 back.H = decayed(d[i], kept(d[i]), add(Lane<T>::get(ds[i * 32]), back.H));
             }
-        }
+        };
+        if (marked)
+            scan(std::true_type{});
+        else
+            scan(std::false_type{});
         if (VL && marks.firsts) m.A = all<N>(__uint_as_float(kCut));
         if (VL && marks.lasts) back.A = all<N>(__uint_as_float(kCut));
         __syncwarp();
@@ -756,79 +723,60 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         const int rows = a.T - tw;   // alike in all lanes: what follows shuffles
         const long long end = ((long long)b * a.T + tw + kRun - 1) * a.C + c;
         T *dx = static_cast<T*>(a.dx) + end, *dg = static_cast<T*>(a.dg) + end;
-        auto put = [&](V<N> e, V<N> k, V<N> w, int i) {
-            const V<N> l = add(Lane<T>::get(ds[i * 32]), mc);
-            mc = decayed(e, k, l);
-            Lane<T>::template put<WIDE>(dx, TIED ? remainder(e, k, l) : l, left);
-            Lane<T>::template put<WIDE>(dg, mul(mc, w), left);
+        // h_{t-1}, less x where tied.  Tied with two channels to a lane these do not fit into the
+        // registers (spilled, at 10 % of L1 hits, they took 237 us for 163): they go where this
+        // run's x and g were.
+        constexpr bool kStash = TIED && N == 2;
+        V<N> w[kStash ? 1 : kRun];
+        uint32_t *stash = const_cast<uint32_t*>(xs), *stash2 = const_cast<uint32_t*>(gs);
+        auto keep_w = [&](int i, const V<N>& v) {
+            if constexpr (kStash) {
+                stash[i * 32] = __float_as_uint(v.v[0]);
+                stash2[i * 32] = __float_as_uint(v.v[N - 1]);
+            } else {
+                w[i] = v;
+            }
         };
-        if (several) {
-            V<N> w[kRun];
-#pragma unroll 1
-            for (int i = 0; i < kRun; ++i) {
-                const V<N> e = again[i], k = kept(e), xv = Lane<T>::get(xs[i * 32]);
-                if (marks.firsts >> i & 1) into = first_state(i);
-                w[i] = TIED ? less(into, xv) : into;
-                into = advance(e, k, into, TIED ? remainder(e, k, xv) : xv);
+        auto w_of = [&](int i) {
+            if constexpr (kStash) {
+                V<N> v;
+                v.v[0] = __uint_as_float(stash[i * 32]);
+                v.v[N - 1] = __uint_as_float(stash2[i * 32]);
+                return v;
+            } else {
+                return w[i];
             }
-#pragma unroll 1
-            for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
-                if (marks.lasts >> i & 1) mc = last_grad(i);
-                if (i < rows) put(again[i], kept(again[i]), w[i], i);
-                if (marks.firsts >> i & 1) first_grad(i, mc);
-            }
-        } else {
-            // h_{t-1}, less x where tied.  Tied with two channels to a lane these do not fit into the
-            // registers (spilled, at 10 % of L1 hits, they took 237 us for 160): they go where this
-            // run's x and g were.
-            constexpr bool kStash = TIED && N == 2;
-            V<N> w[kStash ? 1 : kRun];
-            uint32_t *stash = const_cast<uint32_t*>(xs), *stash2 = const_cast<uint32_t*>(gs);
-            auto keep_w = [&](int i, const V<N>& v) {
-                if constexpr (kStash) {
-                    stash[i * 32] = __float_as_uint(v.v[0]);
-                    stash2[i * 32] = __float_as_uint(v.v[N - 1]);
-                } else {
-                    w[i] = v;
-                }
-            };
-            auto w_of = [&](int i) {
-                if constexpr (kStash) {
-                    V<N> v;
-                    v.v[0] = __uint_as_float(stash[i * 32]);
-                    v.v[N - 1] = __uint_as_float(stash2[i * 32]);
-                    return v;
-                } else {
-                    return w[i];
-                }
-            };
-            if (kStash) __syncwarp();   // what entered the run, among g's rows, has been read
+        };
+        if (kStash) __syncwarp();   // what entered the run, among g's rows, has been read
+        auto write = [&](auto with_marks, auto whole) {
+            constexpr bool M = decltype(with_marks)::value, W = decltype(whole)::value;
 #pragma unroll
             for (int i = 0; i < kRun; ++i) {
                 if (i % 4 == 0) hold_loads();
                 const V<N> xv = Lane<T>::get(xs[i * 32]), k = TIED ? kept_again(d[i]) : kept(d[i]);
-                if (VL && i == f) into = first_state(i);
+                if (M && (marks.firsts >> i & 1)) into = first_state(i);
                 keep_w(i, TIED ? less(into, xv) : into);
                 into = advance(d[i], k, into, TIED ? remainder(d[i], k, xv) : xv);
             }
-            if (rows >= kRun) {
 #pragma unroll
-                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
-                    if (i % 4 == 3) hold_loads();
-                    if (VL && i == l) mc = last_grad(i);
-                    put(d[i], TIED ? kept_again(d[i]) : kept(d[i]), w_of(i), i);
-                    if (VL && i == f) first_grad(i, mc);
+            for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
+                if (i % 4 == 3) hold_loads();
+                if (M && (marks.lasts >> i & 1)) mc = last_grad(i);
+                const V<N> k = TIED ? kept_again(d[i]) : kept(d[i]), l = add(Lane<T>::get(ds[i * 32]), mc);
+                mc = decayed(d[i], k, l);
+                if (W || i < rows) {
+                    Lane<T>::template put<WIDE>(dx, TIED ? remainder(d[i], k, l) : l, left);
+                    Lane<T>::template put<WIDE>(dg, mul(mc, w_of(i)), left);
                 }
-            } else {
-#pragma unroll
-                for (int i = kRun - 1; i >= 0; --i, dx -= a.C, dg -= a.C) {
-                    if (i % 4 == 3) hold_loads();
-                    if (VL && i == l) mc = last_grad(i);
-                    if (i < rows) put(d[i], TIED ? kept_again(d[i]) : kept(d[i]), w_of(i), i);
-                    if (VL && i == f) first_grad(i, mc);
-                }
+                if (M && (marks.firsts >> i & 1)) first_grad(i, mc);
             }
-        }
+        };
+        if (marked)
+            write(std::true_type{}, std::false_type{});
+        else if (rows >= kRun)
+            write(std::false_type{}, std::true_type{});
+        else
+            write(std::false_type{}, std::false_type{});
     }
     if (!VL && a.dh0 && rank == 0 && warp == lead) Lane<T>::put32(a.dh0 + (long long)b * a.C + c, carry, left);
     copies_wait<0>();

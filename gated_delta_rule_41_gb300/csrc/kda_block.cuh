@@ -171,14 +171,33 @@ struct Codes<1> {
     }
 };
 
-// A parameter vector, float32 or bf16; ones where there is none.
+// A parameter vector, float32 or bf16; ones where there is none.  Read again for each row: it
+// stays in L1, and registers are better spent on rows in flight.
 struct Param {
     const void* p;
     bool bf16;
-    __device__ __forceinline__ float operator[](int i) const {
-        if (!p) return 1.f;
-        return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-                    : static_cast<const float*>(p)[i];
+    template <int E>
+    __device__ __forceinline__ void get(int c, float (&v)[E]) const {
+        if (!p) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = 1.f;
+        } else if (E == 8) {
+            if (bf16) {
+                const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c));
+                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int j = 0; j < E; j += 2) unpack2(w[j / 2 % 4], v[j], v[(j + 1) % E]);
+            } else {
+                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+                const float4 x = __ldg(q), y = __ldg(q + 1);
+                const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = f[j % 8];
+            }
+        } else {
+            v[0] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c])
+                        : __ldg(static_cast<const float*>(p) + c);
+        }
     }
 };
 
@@ -219,8 +238,11 @@ struct Rows {
 
 // Picks the widths a kernel is made for: a row's elements stay in registers, E * NC of them in
 // each of TPR threads.  Rows of 16-byte accesses (E = 8) where width, strides and pointers allow,
-// else single elements.  F: template <int E, int TPR, int NC> struct with a static run(args...).
-template <template <int, int, int> class F, typename... A>
+// else single elements.  A forward pass keeps a row in one warp as long as it can, with many loads
+// in flight and no barrier; a backward pass, with up to four inputs and two sums per column, has
+// registers for fewer elements.  F: template <int E, int TPR, int NC> struct with a static
+// run(args...).
+template <template <int, int, int> class F, bool BWD, typename... A>
 kda_status by_width(bool wide, int D, A&&... args) {
     if (wide) {
         if (D <= 32) return F<8, 4, 1>::run(args...);
@@ -228,11 +250,19 @@ kda_status by_width(bool wide, int D, A&&... args) {
         if (D <= 128) return F<8, 16, 1>::run(args...);
         if (D <= 256) return F<8, 32, 1>::run(args...);
         if (D <= 512) return F<8, 32, 2>::run(args...);
-        if (D <= 1024) return F<8, 64, 2>::run(args...);
-        if (D <= 2048) return F<8, 256, 1>::run(args...);
-        if (D <= 4096) return F<8, 256, 2>::run(args...);
-        if (D <= 8192) return F<8, 256, 4>::run(args...);
-        return F<8, 512, 4>::run(args...);
+        if constexpr (BWD) {
+            if (D <= 1024) return F<8, 64, 2>::run(args...);
+            if (D <= 2048) return F<8, 256, 1>::run(args...);
+            if (D <= 4096) return F<8, 256, 2>::run(args...);
+            if (D <= 8192) return F<8, 256, 4>::run(args...);
+            return F<8, 512, 4>::run(args...);
+        } else {
+            if (D <= 1024) return F<8, 32, 4>::run(args...);
+            if (D <= 2048) return F<8, 32, 8>::run(args...);
+            if (D <= 4096) return F<8, 64, 8>::run(args...);
+            if (D <= 8192) return F<8, 128, 8>::run(args...);
+            return F<8, 256, 8>::run(args...);
+        }
     }
     if (D <= 128) return F<1, 32, 4>::run(args...);
     if (D <= 512) return F<1, 128, 4>::run(args...);

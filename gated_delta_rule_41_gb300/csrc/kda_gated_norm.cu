@@ -79,100 +79,23 @@ __device__ __forceinline__ void keep(float (&v)[E], bool in, uint8_t* code, uint
     if (at % kScaleBlock == 0) scale[at / kScaleBlock] = (uint8_t)b;
 }
 
-template <typename T, int E, int TPR, int NC, bool KEEP>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const GatedArgs a) {
-    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
-    __shared__ float2 red[TPR > 32 ? 2 * W : 1];
-    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const int rows = a.T * a.H, step = gridDim.x * RPC, nblk = (a.D + kScaleBlock - 1) / kScaleBlock;
-    const float inv_d = 1.f / a.D;
-    float w[NC][E];
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int c = (i * TPR + lane) * E + j;
-            w[i][j] = c < a.D ? a.w[c] : 0.f;
-        }
-    Place at(blockIdx.x * RPC + group, step, a.H);
-    int turn = 0;
-    for (int row0 = blockIdx.x * RPC; row0 < rows; row0 += step, at.next(), ++turn) {
-        const int row = row0 + group;
-        const T* x = static_cast<const T*>(a.x) + at.t * a.x_stride + (long long)at.h * a.D;
-        const T* z = static_cast<const T*>(a.z) + at.t * a.z_stride + (long long)at.h * a.D;
-        Chunk<T, E> xr[NC], zr[NC];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = (i * TPR + lane) * E;
-            xr[i].zero();
-            zr[i].zero();
-            if (row < rows && c < a.D) {
-                xr[i].load(x + c);
-                zr[i].load(z + c);
-            }
-        }
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            float v[E];
-            xr[i].get(v);
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum.x = fmaf(v[j], v[j], sum.x);
-        }
-        sum = row_sum<TPR>(sum, red, turn, W);
-        const float r = rsqrtf(fmaf(sum.x, inv_d, a.eps));
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = (i * TPR + lane) * E;
-            const bool in = row < rows && c < a.D;
-            float v[E], g[E], y[E];
-            xr[i].get(v);
-            zr[i].get(g);
-#pragma unroll
-            for (int j = 0; j < E; ++j) y[j] = v[j] * r * w[i][j] * gate<T>(g[j], a.act);
-            if (in) Chunk<T, E>::store(static_cast<T*>(a.y) + (long long)row * a.D + c, y);
-            if (KEEP) {
-                const long long e = (long long)row * a.D, b = (long long)row * nblk;
-                keep<E>(v, in, a.xc + e, a.xs + b, c);
-                keep<E>(g, in, a.zc + e, a.zs + b, c);
-            }
-        }
-    }
-}
+// A thread's part of a row as it lies in memory: x, the gate, and backward dy.  Q8: x and the gate
+// are codes with scales.
+template <typename T, int E, int NC, bool BWD, bool Q8>
+struct Row {
+    Chunk<T, E> x[Q8 ? 1 : NC], z[Q8 ? 1 : NC], y[BWD ? NC : 1];
+    Codes<E> xq[Q8 ? NC : 1], zq[Q8 ? NC : 1];
 
-// Q8: x and z are codes with scales.
-template <typename T, int E, int TPR, int NC, bool Q8>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const GatedArgs a) {
-    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
-    __shared__ float2 red[TPR > 32 ? 2 * W : 1];
-    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const int rows = a.T * a.H, step = gridDim.x * RPC, nblk = (a.D + kScaleBlock - 1) / kScaleBlock;
-    const float inv_d = 1.f / a.D;
-    float w[NC][E], dw[NC][E];
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int c = (i * TPR + lane) * E + j;
-            w[i][j] = c < a.D ? a.w[c] : 0.f;
-            dw[i][j] = 0.f;
-        }
-    Place at(blockIdx.x * RPC + group, step, a.H);
-    int turn = 0;
-    for (int row0 = blockIdx.x * RPC; row0 < rows; row0 += step, at.next(), ++turn) {
-        const int row = row0 + group;
-        const long long e = (long long)row * a.D, b = (long long)row * nblk;
-        const T* x = static_cast<const T*>(a.x) + at.t * a.x_stride + (long long)at.h * a.D;
-        const T* z = static_cast<const T*>(a.z) + at.t * a.z_stride + (long long)at.h * a.D;
-        Chunk<T, E> xr[Q8 ? 1 : NC], zr[Q8 ? 1 : NC], yr[NC];
-        Codes<E> xq[Q8 ? NC : 1], zq[Q8 ? NC : 1];
+    template <int TPR>
+    __device__ __forceinline__ void load(const GatedArgs& a, const Place& at, int row, int rows, int lane) {
+        const long long e = (long long)row * a.D, b = (long long)row * ((a.D + kScaleBlock - 1) / kScaleBlock);
+        const T* xp = static_cast<const T*>(a.x) + at.t * a.x_stride + (long long)at.h * a.D;
+        const T* zp = static_cast<const T*>(a.z) + at.t * a.z_stride + (long long)at.h * a.D;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i * TPR + lane) * E;
             const bool in = row < rows && c < a.D;
-            yr[i].zero();
-            if (in) yr[i].load(static_cast<const T*>(a.dy) + e + c);
-            if (Q8) {
+            if constexpr (Q8) {
                 xq[i].zero();
                 zq[i].zero();
                 if (in) {
@@ -180,27 +103,114 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const Ga
                     zq[i].load(a.zc + e + c, a.zs + b + c / kScaleBlock);
                 }
             } else {
-                xr[i].zero();
-                zr[i].zero();
+                x[i].zero();
+                z[i].zero();
                 if (in) {
-                    xr[i].load(x + c);
-                    zr[i].load(z + c);
+                    x[i].load(xp + c);
+                    z[i].load(zp + c);
                 }
             }
+            if constexpr (BWD) {
+                y[i].zero();
+                if (in) y[i].load(static_cast<const T*>(a.dy) + e + c);
+            }
         }
-        float2 sum = make_float2(0.f, 0.f);   // of x^2 and of dn x
-        float s[NC][E], ds[NC][E];
+    }
+    __device__ __forceinline__ void get_x(int i, float (&v)[E]) const {
+        if constexpr (Q8)
+            xq[i].get(v);
+        else
+            x[i].get(v);
+    }
+    __device__ __forceinline__ void get_z(int i, float (&v)[E]) const {
+        if constexpr (Q8)
+            zq[i].get(v);
+        else
+            z[i].get(v);
+    }
+};
+
+template <typename T, int E, int TPR, int NC, bool KEEP>
+__global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const GatedArgs a) {
+    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
+    constexpr bool kAhead = NC <= 2;   // the next row on its way while this one is worked on
+    __shared__ float2 red[TPR > 32 ? 2 * W : 1];
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int rows = a.T * a.H, step = gridDim.x * RPC, nblk = (a.D + kScaleBlock - 1) / kScaleBlock;
+    const float inv_d = 1.f / a.D;
+    Place at(blockIdx.x * RPC + group, step, a.H);
+    int turn = 0;
+    Row<T, E, NC, false, false> r, ahead;
+    r.template load<TPR>(a, at, blockIdx.x * RPC + group, rows, lane);
+    for (int row0 = blockIdx.x * RPC; row0 < rows; row0 += step, ++turn) {
+        const int row = row0 + group;
+        at.next();
+        if constexpr (kAhead) ahead.template load<TPR>(a, at, row + step, rows, lane);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            float v[E], g[E], y[E];
-            if (Q8) {
-                xq[i].get(v);
-                zq[i].get(g);
-            } else {
-                xr[i].get(v);
-                zr[i].get(g);
+            float v[E];
+            r.get_x(i, v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) sum.x = fmaf(v[j], v[j], sum.x);
+        }
+        sum = row_sum<TPR>(sum, red, turn, W);
+        const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = (i * TPR + lane) * E;
+            const bool in = row < rows && c < a.D;
+            float v[E], g[E], w[E], y[E];
+            r.get_x(i, v);
+            r.get_z(i, g);
+            if (in) {
+                a.w.get(c, w);
+#pragma unroll
+                for (int j = 0; j < E; ++j) y[j] = v[j] * inv * w[j] * gate<T>(g[j], a.act);
+                Chunk<T, E>::store(static_cast<T*>(a.y) + (long long)row * a.D + c, y);
             }
-            yr[i].get(y);
+            if (KEEP) {
+                const long long e = (long long)row * a.D, b = (long long)row * nblk;
+                keep<E>(v, in, a.xc + e, a.xs + b, c);
+                keep<E>(g, in, a.zc + e, a.zs + b, c);
+            }
+        }
+        if constexpr (kAhead)
+            r = ahead;
+        else
+            r.template load<TPR>(a, at, row + step, rows, lane);
+    }
+}
+
+template <typename T, int E, int TPR, int NC, bool Q8>
+__global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const GatedArgs a) {
+    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
+    constexpr bool kAhead = NC <= 2;
+    __shared__ float2 red[TPR > 32 ? 2 * W : 1];
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int rows = a.T * a.H, step = gridDim.x * RPC;
+    const float inv_d = 1.f / a.D;
+    float dw[NC][E] = {};
+    Place at(blockIdx.x * RPC + group, step, a.H);
+    int turn = 0;
+    Row<T, E, NC, true, Q8> r, ahead;
+    r.template load<TPR>(a, at, blockIdx.x * RPC + group, rows, lane);
+    for (int row0 = blockIdx.x * RPC; row0 < rows; row0 += step, ++turn) {
+        const int row = row0 + group;
+        at.next();
+        if constexpr (kAhead) ahead.template load<TPR>(a, at, row + step, rows, lane);
+        float2 sum = make_float2(0.f, 0.f);   // of x^2 and of dn x
+        float s[NC][E], ds[NC][E], w[NC][E];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = (i * TPR + lane) * E;
+            float v[E], g[E], y[E];
+            r.get_x(i, v);
+            r.get_z(i, g);
+            r.y[i].get(y);
+#pragma unroll
+            for (int j = 0; j < E; ++j) w[i][j] = 0.f;
+            if (c < a.D) a.w.get(c, w[i]);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 gate_grad<T>(g[j], a.act, s[i][j], ds[i][j]);
@@ -209,29 +219,31 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const Ga
             }
         }
         sum = row_sum<TPR>(sum, red, turn, W);
-        const float r = rsqrtf(fmaf(sum.x, inv_d, a.eps));
-        const float m = r * r * sum.y * inv_d;
+        const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
+        const float m = inv * inv * sum.y * inv_d;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i * TPR + lane) * E;
             float v[E], y[E], dx[E], dz[E];
-            if (Q8)
-                xq[i].get(v);
-            else
-                xr[i].get(v);
-            yr[i].get(y);
+            r.get_x(i, v);
+            r.y[i].get(y);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float yn = y[j] * v[j] * r;              // dy n
-                dx[j] = r * fmaf(-m, v[j], y[j] * w[i][j] * s[i][j]);
+                const float yn = y[j] * v[j] * inv;              // dy n
+                dx[j] = inv * fmaf(-m, v[j], y[j] * w[i][j] * s[i][j]);
                 dz[j] = yn * w[i][j] * ds[i][j];
                 dw[i][j] = fmaf(yn, s[i][j], dw[i][j]);
             }
             if (row < rows && c < a.D) {
-                Chunk<T, E>::store(static_cast<T*>(a.dx) + e + c, dx);
-                Chunk<T, E>::store(static_cast<T*>(a.dz) + e + c, dz);
+                const long long e = (long long)row * a.D + c;
+                Chunk<T, E>::store(static_cast<T*>(a.dx) + e, dx);
+                Chunk<T, E>::store(static_cast<T*>(a.dz) + e, dz);
             }
         }
+        if constexpr (kAhead)
+            r = ahead;
+        else
+            r.template load<TPR>(a, at, row + step, rows, lane);
     }
     if (a.dw) store_part<E, TPR, NC>(dw, a.part + (long long)blockIdx.x * a.D, a.D);
 }
@@ -279,7 +291,7 @@ struct Bwd {
 // 16-byte accesses need widths, strides and pointers that allow them.
 bool wide(const GatedArgs& a, bool packed) {
     const int E = 8;
-    if (a.D % E || !aligned16({a.x, a.z, a.y, a.dy, a.dx, a.dz, a.xc, a.zc})) return false;
+    if (a.D % E || !aligned16({a.x, a.z, a.y, a.dy, a.dx, a.dz, a.xc, a.zc, a.w.p})) return false;
     return packed || (a.x_stride % E == 0 && a.z_stride % E == 0);
 }
 
@@ -290,11 +302,11 @@ size_t gated_norm_ws_bytes(int T, int H, int D) {
 }
 
 kda_status gated_norm_fwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s) {
-    return by_width<Fwd>(wide(a, false), a.D, a, bf16, s);
+    return by_width<Fwd, false>(wide(a, false), a.D, a, bf16, s);
 }
 
 kda_status gated_norm_bwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s) {
-    return by_width<Bwd>(wide(a, a.xs != nullptr), a.D, a, bf16, s);
+    return by_width<Bwd, true>(wide(a, a.xs != nullptr), a.D, a, bf16, s);
 }
 
 }  // namespace kda

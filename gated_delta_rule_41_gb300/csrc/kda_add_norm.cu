@@ -7,6 +7,7 @@
 // One pass over the data, a row in the registers of its threads, as in the gated norm.  The
 // forward pass norms r' as summed, before it is rounded to the residual stream's type.
 #include "kda_block.cuh"
+#include "kda_ptx.cuh"
 #include "kda_timing.cuh"
 
 namespace kda {
@@ -21,28 +22,114 @@ template <typename R, typename T, int E, int NC, bool BWD>
 struct Row {
     Chunk<R, E> r[NC], u[BWD ? NC : 1];
     Chunk<T, E> x[NC], y[BWD ? NC : 1];
+};
 
-    template <int TPR>
-    __device__ __forceinline__ void load(const AddArgs& a, int row, int lane) {
-        const R* rp = static_cast<const R*>(a.r) + row * a.r_stride;
-        const T* xp = static_cast<const T*>(a.x) + row * a.x_stride;
+// Rows on their way while one is worked on.  Wide rows go through shared memory, each thread by
+// asynchronous copies into slots of its own (no barrier, no registers): with the next row in
+// registers alone, the backward pass of 20011 x 2048 had too few bytes in flight (148 us).
+// Others are loaded where they are used.
+template <typename R, typename T, int E, int TPR, int NC, bool BWD>
+struct Feed {
+    static constexpr int kThreads = Rows<TPR>::kThreads;
+    static constexpr int kR = sizeof(Chunk<R, E>) / 16, kT = sizeof(Chunk<T, E>) / 16;
+    static constexpr int kUnits = NC * (kR + kT) * (BWD ? 2 : 1);      // of 16 bytes, of a thread and row
+    static constexpr int kStage = kUnits * 16 * kThreads;
+    // slots: four as long as two CTAs then fit an SM, or as many as fit; the widest rows have none
+    static constexpr int kSlots = E != 8                     ? 1
+                                  : kStage * 4 <= 100 * 1024 ? 4
+                                  : kStage * 3 <= 100 * 1024 ? 3
+                                  : kStage * 2 <= 200 * 1024 ? 2
+                                                             : 1;
+    static constexpr bool kRing = kSlots > 1;
+    // rows begun before they are used: a slot is filled again one turn after it was read
+    static constexpr int kAhead = kSlots - 1;
+    static constexpr size_t kBytes = kRing ? (size_t)kStage * kSlots : 0;
+
+    const AddArgs& a;
+    const int lane;
+    char* const mine;
+    int put = 0, get = 0;
+
+    __device__ __forceinline__ Feed(const AddArgs& args, char* smem)
+        : a(args), lane(threadIdx.x % TPR), mine(smem + threadIdx.x * 16) {}
+
+    // F(source row, 16-byte units of a chunk, slot) for what a row has
+    template <typename F>
+    __device__ __forceinline__ void each(int row, F f) {
         const bool with_x = BWD ? a.da != nullptr : a.x != nullptr;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i * TPR + lane) * E;
-            const bool in = row < a.T && c < a.D;
+            if (row >= a.T || c >= a.D) continue;
             const long long e = (long long)row * a.D + c;
-            r[i].zero();
-            x[i].zero();
-            if (in) r[i].load(rp + c);
-            if (in && with_x) x[i].load(xp + c);
+            int at = i * (kR + kT) * (BWD ? 2 : 1);
+            f(static_cast<const R*>(a.r) + row * a.r_stride + c, kR, at);
+            at += kR;
+            if (with_x) f(static_cast<const T*>(a.x) + row * a.x_stride + c, kT, at);
+            at += kT;
             if constexpr (BWD) {
-                u[i].zero();
-                y[i].zero();
-                if (in) y[i].load(static_cast<const T*>(a.dy) + e);
-                if (in && a.dr) u[i].load(static_cast<const R*>(a.dr) + e);
+                f(static_cast<const T*>(a.dy) + e, kT, at);
+                at += kT;
+                if (a.dr) f(static_cast<const R*>(a.dr) + e, kR, at);
             }
         }
+    }
+    __device__ __forceinline__ void start(int row) {
+        if constexpr (kRing) {
+            char* to = mine + put * kStage;
+            each(row, [&](const void* from, int units, int at) {
+                for (int k = 0; k < units; ++k)
+                    ptx::cp_async16(to + (at + k) * 16 * kThreads, static_cast<const char*>(from) + k * 16);
+            });
+            ptx::cp_async_commit();
+            put = put + 1 == kSlots ? 0 : put + 1;
+        }
+    }
+    template <typename C>
+    __device__ __forceinline__ void take(C& c, int at) {
+        const char* from = mine + get * kStage + at * 16 * kThreads;
+        uint4* r = reinterpret_cast<uint4*>(&c);
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(C) / 16); ++k)
+            r[k] = *reinterpret_cast<const uint4*>(from + k * 16 * kThreads);
+    }
+    // The row whose copies were begun first, zeros where it has nothing.
+    __device__ __forceinline__ void finish(int row, Row<R, T, E, NC, BWD>& o) {
+        const bool with_x = BWD ? a.da != nullptr : a.x != nullptr;
+        if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = (i * TPR + lane) * E;
+            const bool in = row < a.T && c < a.D;
+            o.r[i].zero();
+            o.x[i].zero();
+            if constexpr (BWD) {
+                o.y[i].zero();
+                o.u[i].zero();
+            }
+            if (!in) continue;
+            if constexpr (kRing) {
+                int at = i * (kR + kT) * (BWD ? 2 : 1);
+                take(o.r[i], at);
+                at += kR;
+                if (with_x) take(o.x[i], at);
+                at += kT;
+                if constexpr (BWD) {
+                    take(o.y[i], at);
+                    at += kT;
+                    if (a.dr) take(o.u[i], at);
+                }
+            } else {
+                const long long e = (long long)row * a.D + c;
+                o.r[i].load(static_cast<const R*>(a.r) + row * a.r_stride + c);
+                if (with_x) o.x[i].load(static_cast<const T*>(a.x) + row * a.x_stride + c);
+                if constexpr (BWD) {
+                    o.y[i].load(static_cast<const T*>(a.dy) + e);
+                    if (a.dr) o.u[i].load(static_cast<const R*>(a.dr) + e);
+                }
+            }
+        }
+        get = get + 1 == kSlots ? 0 : get + 1;
     }
 };
 
@@ -56,17 +143,19 @@ __device__ __forceinline__ void alphas(const AddArgs& a, int c, float (&v)[E]) {
 
 template <typename R, typename T, int E, int TPR, int NC>
 __global__ void __launch_bounds__(Rows<TPR>::kThreads) add_fwd_kernel(const AddArgs a) {
+    using F = Feed<R, T, E, TPR, NC, false>;
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
-    constexpr bool kAhead = NC <= 2;   // the next row on its way while this one is worked on
+    extern __shared__ __align__(16) char slots[];
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR, step = gridDim.x * RPC;
     const float inv_d = 1.f / a.D;
-    int turn = 0;
-    Row<R, T, E, NC, false> cur, ahead;
-    cur.template load<TPR>(a, blockIdx.x * RPC + group, lane);
-    for (int row0 = blockIdx.x * RPC; row0 < a.T; row0 += step, ++turn) {
-        const int row = row0 + group;
-        if constexpr (kAhead) ahead.template load<TPR>(a, row + step, lane);
+    int row = blockIdx.x * RPC + group, turn = 0;
+    F feed(a, slots);
+#pragma unroll
+    for (int k = 0; k < F::kAhead; ++k) feed.start(row + k * step);
+    for (; row - group < a.T; row += step, ++turn) {
+        Row<R, T, E, NC, false> cur;
+        feed.finish(row, cur);
         float v[NC][E];
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -76,14 +165,13 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) add_fwd_kernel(const AddA
                 float f[E], al[E];
                 cur.x[i].get(f);
                 alphas(a, (i * TPR + lane) * E, al);
-#pragma unroll
-                for (int j = 0; j < E; ++j) v[i][j] = fmaf(al[j], f[j], v[i][j]);
+                vfma(v[i], al, f, v[i]);
             }
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum.x = fmaf(v[i][j], v[i][j], sum.x);
+            vdot(sum, v[i], v[i]);
         }
-        if constexpr (!kAhead) cur.template load<TPR>(a, row + step, lane);
-        sum = row_sum<TPR>(sum, red, turn, W);
+        feed.start(row + F::kAhead * step);
+        sum.x += sum.y;
+        sum = row_sum<TPR, false>(sum, red, turn, W);
         const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -93,46 +181,44 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) add_fwd_kernel(const AddA
             if (a.r_out) Chunk<R, E>::store(static_cast<R*>(a.r_out) + e, v[i]);
             float w[E];
             a.w.get(c, w);
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[i][j] *= inv * w[j];
+            vmul(w, w, inv);
+            vmul(v[i], v[i], w);
             Chunk<T, E>::store(static_cast<T*>(a.y) + e, v[i]);
         }
-        if constexpr (kAhead) cur = ahead;
     }
 }
 
 template <typename R, typename T, int E, int TPR, int NC>
 __global__ void __launch_bounds__(Rows<TPR>::kThreads) add_bwd_kernel(const AddArgs a) {
+    using F = Feed<R, T, E, TPR, NC, true>;
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
-    constexpr bool kAhead = NC <= 2;
+    extern __shared__ __align__(16) char slots[];
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR, step = gridDim.x * RPC;
     const float inv_d = 1.f / a.D;
     float dw[NC][E] = {}, da[NC][E] = {};
-    int turn = 0;
-    Row<R, T, E, NC, true> cur, ahead;
-    cur.template load<TPR>(a, blockIdx.x * RPC + group, lane);
-    for (int row0 = blockIdx.x * RPC; row0 < a.T; row0 += step, ++turn) {
-        const int row = row0 + group;
-        if constexpr (kAhead) ahead.template load<TPR>(a, row + step, lane);
-        float2 sum = make_float2(0.f, 0.f);   // of r^2 and of dn r
-        float w[NC][E];
+    int row = blockIdx.x * RPC + group, turn = 0;
+    F feed(a, slots);
+#pragma unroll
+    for (int k = 0; k < F::kAhead; ++k) feed.start(row + k * step);
+    for (; row - group < a.T; row += step, ++turn) {
+        Row<R, T, E, NC, true> cur;
+        feed.finish(row, cur);
+        float2 s2 = make_float2(0.f, 0.f), sn = s2;   // sums of r^2 and of dn r
+        float dn[NC][E];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i * TPR + lane) * E;
-            float v[E], y[E];
+            float v[E], y[E], w[E] = {};
             cur.r[i].get(v);
             cur.y[i].get(y);
-#pragma unroll
-            for (int j = 0; j < E; ++j) w[i][j] = 0.f;
-            if (c < a.D) a.w.get(c, w[i]);
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                sum.x = fmaf(v[j], v[j], sum.x);
-                sum.y = fmaf(y[j] * w[i][j], v[j], sum.y);
-            }
+            if (c < a.D) a.w.get(c, w);
+            vmul(dn[i], y, w);
+            vdot(s2, v, v);
+            vdot(sn, dn[i], v);
         }
-        sum = row_sum<TPR>(sum, red, turn, W);
+        feed.start(row + F::kAhead * step);
+        const float2 sum = row_sum<TPR, true>(make_float2(s2.x + s2.y, sn.x + sn.y), red, turn, W);
         const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
         const float m = inv * inv * sum.y * inv_d;
 #pragma unroll
@@ -140,26 +226,23 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) add_bwd_kernel(const AddA
             const int c = (i * TPR + lane) * E;
             if (row >= a.T || c >= a.D) continue;
             const long long e = (long long)row * a.D + c;
-            float v[E], y[E], u[E], f[E], d[E], dx[E];
+            float v[E], y[E], f[E], d[E];
             cur.r[i].get(v);
             cur.y[i].get(y);
-            cur.u[i].get(u);
+            cur.u[i].get(d);
             cur.x[i].get(f);
-            alphas(a, c, dx);
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                d[j] = fmaf(inv, fmaf(-m, v[j], y[j] * w[i][j]), u[j]);
-                dw[i][j] = fmaf(y[j], v[j] * inv, dw[i][j]);
-                da[i][j] = fmaf(d[j], f[j], da[i][j]);
-                dx[j] *= d[j];
-            }
+            vfma(dn[i], v, -m, dn[i]);
+            vfma(d, dn[i], inv, d);                  // dr
             Chunk<R, E>::store(static_cast<R*>(a.dres) + e, d);
-            if (a.dx) Chunk<T, E>::store(static_cast<T*>(a.dx) + e, dx);
+            vmul(v, v, inv);
+            vfma(dw[i], y, v, dw[i]);
+            vfma(da[i], d, f, da[i]);
+            if (a.dx) {
+                alphas(a, c, f);
+                vmul(f, f, d);
+                Chunk<T, E>::store(static_cast<T*>(a.dx) + e, f);
+            }
         }
-        if constexpr (kAhead)
-            cur = ahead;
-        else
-            cur.template load<TPR>(a, row + step, lane);
     }
     const long long P = gridDim.x;
     if (a.dw) store_part<E, TPR, NC>(dw, a.part + blockIdx.x * (long long)a.D, a.D);
@@ -172,10 +255,11 @@ struct Fwd {
     static kda_status go(const AddArgs& a, cudaStream_t s) {
         constexpr int N = Rows<TPR>::kThreads, RPC = Rows<TPR>::kRows;
         auto* k = add_fwd_kernel<R, T, E, TPR, NC>;
-        static const int per_sm = resident(k, N);
+        constexpr size_t smem = Feed<R, T, E, TPR, NC, false>::kBytes;
+        static const int per_sm = resident(k, N, smem);
         const int grid = grid_of(per_sm, (a.T + RPC - 1) / RPC);
         TimedLaunch tl("add_norm_fwd", s);
-        k<<<grid, N, 0, s>>>(a);
+        k<<<grid, N, smem, s>>>(a);
         return launch_status();
     }
     static kda_status run(const AddArgs& a, int type, cudaStream_t s) {
@@ -190,11 +274,12 @@ struct Bwd {
     static kda_status go(const AddArgs& a, cudaStream_t s) {
         constexpr int N = Rows<TPR>::kThreads, RPC = Rows<TPR>::kRows;
         auto* k = add_bwd_kernel<R, T, E, TPR, NC>;
-        static const int per_sm = resident(k, N);
+        constexpr size_t smem = Feed<R, T, E, TPR, NC, true>::kBytes;
+        static const int per_sm = resident(k, N, smem);
         const int grid = std::min(grid_of(per_sm, (a.T + RPC - 1) / RPC), kPartsPerSm * sm_count());
         {
             TimedLaunch tl("add_norm_bwd", s);
-            k<<<grid, N, 0, s>>>(a);
+            k<<<grid, N, smem, s>>>(a);
         }
         const kda_status st = launch_status();
         if (st != KDA_OK || (!a.dw && !a.da)) return st;
@@ -218,11 +303,11 @@ size_t add_norm_ws_bytes(int T, int D) {
 }
 
 kda_status add_norm_fwd_launch(const AddArgs& a, int type, cudaStream_t s) {
-    return by_width<Fwd, false>(wide(a), a.D, a, type, s);
+    return by_width<Fwd>(wide(a), a.D, a, type, s);
 }
 
 kda_status add_norm_bwd_launch(const AddArgs& a, int type, cudaStream_t s) {
-    return by_width<Bwd, true>(wide(a), a.D, a, type, s);
+    return by_width<Bwd>(wide(a), a.D, a, type, s);
 }
 
 }  // namespace kda

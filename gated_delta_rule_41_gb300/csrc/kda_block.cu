@@ -49,14 +49,15 @@ __global__ void __launch_bounds__(256) pack_wide_kernel(const T* __restrict__ x,
             r[0].load(x + row * stride + at * 16);
             r[1].load(x + row * stride + at * 16 + 8);
         }
-        float v[2][8], top = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            r[j].get(v[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(v[j][e]));
-        }
+        float v[2][8];
+        r[0].get(v[0]);
+        r[1].get(v[1]);
+        float top = largest(v[1], largest(v[0]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        if (top > kMaxFloat) {   // in both threads of the block
+            top = largest_finite(v[1], largest_finite(v[0]));
+            top = fmaxf(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
+        }
         if (!in) continue;
         const uint32_t b = scale_byte(top);
         const float inv = inverse_of(b);
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ x, long
         const long long row = i / per;
         const int c = (int)(i - row * per) * kScaleBlock + lane;
         float v[1] = {c < D ? to_f<T>(x[row * stride + c]) : 0.f};
-        float top = finite_abs(v[0]);
+        float top = largest_finite(v);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
         const uint32_t b = scale_byte(top);

@@ -28,6 +28,59 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Elementwise arithmetic on a chunk, two at a time where there are two.
+template <int E>
+__device__ __forceinline__ void vmul(float (&o)[E], const float (&a)[E], const float (&b)[E]) {
+    if constexpr (E == 1) {
+        o[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            const float2 r = __fmul2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]));
+            o[j] = r.x, o[j + 1] = r.y;
+        }
+    }
+}
+template <int E>
+__device__ __forceinline__ void vfma(float (&o)[E], const float (&a)[E], const float (&b)[E],
+                                     const float (&c)[E]) {
+    if constexpr (E == 1) {
+        o[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            const float2 r = __ffma2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]),
+                                        make_float2(c[j], c[j + 1]));
+            o[j] = r.x, o[j + 1] = r.y;
+        }
+    }
+}
+template <int E>
+__device__ __forceinline__ void vmul(float (&o)[E], const float (&a)[E], float b) {
+    float v[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = b;
+    vmul(o, a, v);
+}
+template <int E>
+__device__ __forceinline__ void vfma(float (&o)[E], const float (&a)[E], float b, const float (&c)[E]) {
+    float v[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = b;
+    vfma(o, a, v, c);
+}
+// A running sum of products, kept in two parts.
+template <int E>
+__device__ __forceinline__ void vdot(float2& sum, const float (&a)[E], const float (&b)[E]) {
+    if constexpr (E == 1) {
+        sum.x = fmaf(a[0], b[0], sum.x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 2)
+            sum = __ffma2_rn(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), sum);
+    }
+}
+
 // E neighbouring elements of type T as they lie in memory: 16-byte accesses for E = 8, one
 // element for E = 1.
 template <typename T, int E>
@@ -91,10 +144,26 @@ __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_floa
 __device__ __forceinline__ float inverse_of(uint32_t byte) {
     return __uint_as_float((254u - byte) << 23);
 }
-// A magnitude for the block's maximum: 0 for infinities and NaN.
-__device__ __forceinline__ float finite_abs(float v) {
-    const float a = fabsf(v);
-    return a <= 3.402823466e38f ? a : 0.f;
+// The largest magnitude of a chunk: infinite where there is an infinity; NaN do not count.
+template <int E>
+__device__ __forceinline__ float largest(const float (&v)[E], float top = 0.f) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) top = fmaxf(top, fabsf(v[j]));
+    return top;
+}
+// With an infinity in the block: the chunk's largest finite magnitude, its infinities made NaN.  (As
+// codes they may not pass for finite values in the backward pass; NaN become NaN by themselves.)
+constexpr float kMaxFloat = 3.402823466e38f;
+template <int E>
+__device__ __forceinline__ float largest_finite(float (&v)[E], float top = 0.f) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        if (fabsf(v[j]) <= kMaxFloat)
+            top = fmaxf(top, fabsf(v[j]));
+        else
+            v[j] = __uint_as_float(0x7fffffffu);
+    }
+    return top;
 }
 // With the largest scale a code of 256 would stand for 2^128: values next to the largest float go
 // to the code below it, 240, which is no further off than 2^-4.
@@ -104,13 +173,12 @@ __device__ __forceinline__ void below_top(float (&v)[E]) {
     constexpr float most = 240.f * 1.329227995784916e36f;   // 240 * 2^120
 #pragma unroll
     for (int j = 0; j < E; ++j)
-        if (finite_abs(v[j]) > most) v[j] = copysignf(most, v[j]);
+        if (fabsf(v[j]) > most) v[j] = copysignf(most, v[j]);
 }
-// Codes of a pair times the scale's inverse (the lower byte is a's).  x + 0 x is x, or NaN for an
-// infinity: that may not pass for a finite value in the backward pass.
+// Codes of a pair times the scale's inverse (the lower byte is a's).
 __device__ __forceinline__ uint32_t code2(float a, float b, float inv) {
-    const float2 v = make_float2(fmaf(a, 0.f, a * inv), fmaf(b, 0.f, b * inv));
-    return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    return __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(a, b), make_float2(inv, inv)), __NV_SATFINITE,
+                                    __NV_E4M3);
 }
 __device__ __forceinline__ void values2(uint32_t two, float& a, float& b) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
@@ -139,9 +207,7 @@ struct Codes<8> {
         values2(r.x >> 16, v[2], v[3]);
         values2(r.y & 0xffffu, v[4], v[5]);
         values2(r.y >> 16, v[6], v[7]);
-        const float f = scale_of(s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f;
+        vmul(v, v, scale_of(s));
     }
     static __device__ __forceinline__ void store(uint8_t* p, const float (&v)[8], float inv) {
         *reinterpret_cast<uint2*>(p) =
@@ -204,12 +270,12 @@ struct Param {
 // Sums over the TPR threads of a row (a power of two), for every thread of it.  Rows of more than
 // a warp go through shared memory: `red` has one entry per warp of the CTA for each of two turns,
 // so that one barrier a turn is enough.
-template <int TPR>
+template <int TPR, bool BOTH>
 __device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn, int warps) {
 #pragma unroll
     for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) {
         v.x += __shfl_xor_sync(~0u, v.x, d);
-        v.y += __shfl_xor_sync(~0u, v.y, d);
+        if (BOTH) v.y += __shfl_xor_sync(~0u, v.y, d);
     }
     if (TPR > 32) {
         float2* at = red + (turn & 1) * warps;
@@ -238,11 +304,8 @@ struct Rows {
 
 // Picks the widths a kernel is made for: a row's elements stay in registers, E * NC of them in
 // each of TPR threads.  Rows of 16-byte accesses (E = 8) where width, strides and pointers allow,
-// else single elements.  A forward pass keeps a row in one warp as long as it can, with many loads
-// in flight and no barrier; a backward pass, with up to four inputs and two sums per column, has
-// registers for fewer elements.  F: template <int E, int TPR, int NC> struct with a static
-// run(args...).
-template <template <int, int, int> class F, bool BWD, typename... A>
+// else single elements.  F: template <int E, int TPR, int NC> struct with a static run(args...).
+template <template <int, int, int> class F, typename... A>
 kda_status by_width(bool wide, int D, A&&... args) {
     if (wide) {
         if (D <= 32) return F<8, 4, 1>::run(args...);
@@ -250,19 +313,11 @@ kda_status by_width(bool wide, int D, A&&... args) {
         if (D <= 128) return F<8, 16, 1>::run(args...);
         if (D <= 256) return F<8, 32, 1>::run(args...);
         if (D <= 512) return F<8, 32, 2>::run(args...);
-        if constexpr (BWD) {
-            if (D <= 1024) return F<8, 64, 2>::run(args...);
-            if (D <= 2048) return F<8, 256, 1>::run(args...);
-            if (D <= 4096) return F<8, 256, 2>::run(args...);
-            if (D <= 8192) return F<8, 256, 4>::run(args...);
-            return F<8, 512, 4>::run(args...);
-        } else {
-            if (D <= 1024) return F<8, 32, 4>::run(args...);
-            if (D <= 2048) return F<8, 32, 8>::run(args...);
-            if (D <= 4096) return F<8, 64, 8>::run(args...);
-            if (D <= 8192) return F<8, 128, 8>::run(args...);
-            return F<8, 256, 8>::run(args...);
-        }
+        if (D <= 1024) return F<8, 64, 2>::run(args...);
+        if (D <= 2048) return F<8, 256, 1>::run(args...);
+        if (D <= 4096) return F<8, 256, 2>::run(args...);
+        if (D <= 8192) return F<8, 256, 4>::run(args...);
+        return F<8, 512, 4>::run(args...);
     }
     if (D <= 128) return F<1, 32, 4>::run(args...);
     if (D <= 512) return F<1, 128, 4>::run(args...);
@@ -278,9 +333,12 @@ inline bool aligned16(std::initializer_list<const void*> ps) {
 
 // CTAs of a kernel that walks over its rows: all that an SM holds at once, or fewer.
 template <typename K>
-int resident(K kernel, int threads) {
+int resident(K kernel, int threads, size_t smem) {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1)
+    // (without the attribute 48 KB, static shared memory included)
+    if ((smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  (int)smem) != cudaSuccess) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1)
         n = 1;
     return n;
 }

@@ -15,25 +15,34 @@ namespace {
 
 using namespace block;
 
-// sigmoid(z) and sigmoid(-z) = 1 - sigmoid(z), each from e = exp(-|z|) without a difference, so that
-// both keep their digits far from zero.  float32 tensors take the exact exponential and division.
+// 1 / (1 + e) of e = exp(-z) (0 where e is infinite) and e itself.  float32 tensors take the exact
+// exponential and division, bf16 ones the fast power of two and reciprocal (2^-22 of it, and the
+// rounding of the argument).
 template <typename T>
-__device__ __forceinline__ void sigmoids(float z, float& s, float& other) {
-    const float e = sizeof(T) == 2 ? __expf(-fabsf(z)) : expf(-fabsf(z));
-    const float p = sizeof(T) == 2 ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e), q = e * p;
-    s = z < 0.f ? q : p;
-    other = z < 0.f ? p : q;
+__device__ __forceinline__ float logistic(float z, float& e) {
+    if (sizeof(T) == 2) {
+        float s;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+        return s;
+    }
+    e = expf(-z);
+    return 1.f / (1.f + e);
 }
-// s(z), and with it s'(z)
 template <typename T>
 __device__ __forceinline__ float gate(float z, int act) {
-    float s, other;
-    sigmoids<T>(z, s, other);
+    float e;
+    const float s = logistic<T>(z, e);
     return act == KDA_GATE_SILU ? z * s : s;
 }
+// s(z) and s'(z).  sigmoid(z) and sigmoid(-z) = 1 - sigmoid(z) come from exp(-|z|) without a
+// difference, so that both keep their digits far from zero.
 template <typename T>
 __device__ __forceinline__ void gate_grad(float z, int act, float& s, float& ds) {
-    sigmoids<T>(z, s, ds);
+    float e;
+    const float p = logistic<T>(fabsf(z), e), q = e * p;
+    s = z < 0.f ? q : p;
+    ds = z < 0.f ? p : q;
     if (act == KDA_GATE_SILU) {
         ds = s * fmaf(z, ds, 1.f);
         s *= z;
@@ -63,15 +72,18 @@ struct Place {
 
 // The codes and the scale of a chunk; the chunks of a block lie in neighbouring lanes.
 template <int E>
-__device__ __forceinline__ void keep(float (&v)[E], bool in, uint8_t* code, uint8_t* scale,
-                                     int at) {
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) top = fmaxf(top, finite_abs(v[j]));
+__device__ __forceinline__ void keep(float (&v)[E], bool in, uint8_t* code, uint8_t* scale, int at) {
+    float top = largest(v);
     if (!in) top = 0.f;
 #pragma unroll
     for (int d = kScaleBlock / E / 2; d > 0; d >>= 1)
         top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (__any_sync(~0u, top > kMaxFloat)) {
+        top = in ? largest_finite(v) : 0.f;
+#pragma unroll
+        for (int d = kScaleBlock / E / 2; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    }
     if (!in) return;
     const uint32_t b = scale_byte(top);
     if (b == kTopScale) below_top(v);
@@ -130,120 +142,132 @@ struct Row {
     }
 };
 
+// Rows on their way while one is worked on, in registers: 32 to 48 bytes a thread and row are too
+// few in flight with one (gated_fwd of 32768 x 16 x 128 with copies in 8 bits: 109 us, with three
+// 96 us).
+template <int NC>
+constexpr int kDepth = NC == 1 ? 3 : NC == 2 ? 2 : 1;
+
 template <typename T, int E, int TPR, int NC, bool KEEP>
 __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const GatedArgs a) {
-    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
-    constexpr bool kAhead = NC <= 2;   // the next row on its way while this one is worked on
+    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int rows = a.T * a.H, step = gridDim.x * RPC, nblk = (a.D + kScaleBlock - 1) / kScaleBlock;
     const float inv_d = 1.f / a.D;
-    Place at(blockIdx.x * RPC + group, step, a.H);
-    int turn = 0;
-    Row<T, E, NC, false, false> r, ahead;
-    r.template load<TPR>(a, at, blockIdx.x * RPC + group, rows, lane);
-    for (int row0 = blockIdx.x * RPC; row0 < rows; row0 += step, ++turn) {
-        const int row = row0 + group;
-        at.next();
-        if constexpr (kAhead) ahead.template load<TPR>(a, at, row + step, rows, lane);
-        float2 sum = make_float2(0.f, 0.f);
+    int row = blockIdx.x * RPC + group, turn = 0;
+    Place at(row, step, a.H);   // of the next row to load
+    Row<T, E, NC, false, false> ring[D];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            float v[E];
-            r.get_x(i, v);
+    for (int k = 0; k < D; ++k, at.next()) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
+    float w[NC <= 2 ? NC : 1][E];
+    if constexpr (NC <= 2) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) sum.x = fmaf(v[j], v[j], sum.x);
-        }
-        sum = row_sum<TPR>(sum, red, turn, W);
-        const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
+        for (int i = 0; i < NC; ++i)
+            if ((i * TPR + lane) * E < a.D) a.w.get((i * TPR + lane) * E, w[i]);
+    }
+    while (row - group < rows) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = (i * TPR + lane) * E;
-            const bool in = row < rows && c < a.D;
-            float v[E], g[E], w[E], y[E];
-            r.get_x(i, v);
-            r.get_z(i, g);
-            if (in) {
-                a.w.get(c, w);
+        for (int k = 0; k < D; ++k, row += step, ++turn) {
+            if (row - group >= rows) break;   // alike in the whole CTA
+            float v[NC][E], g[NC][E];
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < E; ++j) y[j] = v[j] * inv * w[j] * gate<T>(g[j], a.act);
-                Chunk<T, E>::store(static_cast<T*>(a.y) + (long long)row * a.D + c, y);
+            for (int i = 0; i < NC; ++i) {
+                ring[k].get_x(i, v[i]);
+                ring[k].get_z(i, g[i]);
+                vdot(sum, v[i], v[i]);
             }
-            if (KEEP) {
-                const long long e = (long long)row * a.D, b = (long long)row * nblk;
-                keep<E>(v, in, a.xc + e, a.xs + b, c);
-                keep<E>(g, in, a.zc + e, a.zs + b, c);
+            ring[k].template load<TPR>(a, at, row + D * step, rows, lane);
+            at.next();
+            sum.x += sum.y;
+            sum = row_sum<TPR, false>(sum, red, turn, W);
+            const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = (i * TPR + lane) * E;
+                const bool in = row < rows && c < a.D;
+                if (in) {
+                    float f[E], y[E];
+                    if constexpr (NC <= 2) {
+                        vmul(y, v[i], w[i]);
+                    } else {
+                        a.w.get(c, f);
+                        vmul(y, v[i], f);
+                    }
+#pragma unroll
+                    for (int j = 0; j < E; ++j) f[j] = gate<T>(g[i][j], a.act);
+                    vmul(y, y, f);
+                    vmul(y, y, inv);
+                    Chunk<T, E>::store(static_cast<T*>(a.y) + (long long)row * a.D + c, y);
+                }
+                if (KEEP) {
+                    const long long e = (long long)row * a.D, b = (long long)row * nblk;
+                    keep<E>(v[i], in, a.xc + e, a.xs + b, c);
+                    keep<E>(g[i], in, a.zc + e, a.zs + b, c);
+                }
             }
         }
-        if constexpr (kAhead)
-            r = ahead;
-        else
-            r.template load<TPR>(a, at, row + step, rows, lane);
     }
 }
 
 template <typename T, int E, int TPR, int NC, bool Q8>
 __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const GatedArgs a) {
-    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
-    constexpr bool kAhead = NC <= 2;
+    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int rows = a.T * a.H, step = gridDim.x * RPC;
     const float inv_d = 1.f / a.D;
     float dw[NC][E] = {};
-    Place at(blockIdx.x * RPC + group, step, a.H);
-    int turn = 0;
-    Row<T, E, NC, true, Q8> r, ahead;
-    r.template load<TPR>(a, at, blockIdx.x * RPC + group, rows, lane);
-    for (int row0 = blockIdx.x * RPC; row0 < rows; row0 += step, ++turn) {
-        const int row = row0 + group;
-        at.next();
-        if constexpr (kAhead) ahead.template load<TPR>(a, at, row + step, rows, lane);
-        float2 sum = make_float2(0.f, 0.f);   // of x^2 and of dn x
-        float s[NC][E], ds[NC][E], w[NC][E];
+    int row = blockIdx.x * RPC + group, turn = 0;
+    Place at(row, step, a.H);
+    Row<T, E, NC, true, Q8> ring[D];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = (i * TPR + lane) * E;
-            float v[E], g[E], y[E];
-            r.get_x(i, v);
-            r.get_z(i, g);
-            r.y[i].get(y);
+    for (int k = 0; k < D; ++k, at.next()) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
+    while (row - group < rows) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) w[i][j] = 0.f;
-            if (c < a.D) a.w.get(c, w[i]);
+        for (int k = 0; k < D; ++k, row += step, ++turn) {
+            if (row - group >= rows) break;   // alike in the whole CTA
+            float2 s2 = make_float2(0.f, 0.f), sn = s2;   // sums of x^2 and of dn x
+            float v[NC][E], y[NC][E], s[NC][E], wds[NC][E], dn[NC][E];
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                gate_grad<T>(g[j], a.act, s[i][j], ds[i][j]);
-                sum.x = fmaf(v[j], v[j], sum.x);
-                sum.y = fmaf(y[j] * w[i][j] * s[i][j], v[j], sum.y);
+            for (int i = 0; i < NC; ++i) {
+                const int c = (i * TPR + lane) * E;
+                float g[E], w[E] = {}, ds[E];
+                ring[k].get_x(i, v[i]);
+                ring[k].get_z(i, g);
+                ring[k].y[i].get(y[i]);
+                if (c < a.D) a.w.get(c, w);
+#pragma unroll
+                for (int j = 0; j < E; ++j) gate_grad<T>(g[j], a.act, s[i][j], ds[j]);
+                vmul(wds[i], w, ds);
+                vmul(dn[i], y[i], w);
+                vmul(dn[i], dn[i], s[i]);
+                vdot(s2, v[i], v[i]);
+                vdot(sn, dn[i], v[i]);
+            }
+            ring[k].template load<TPR>(a, at, row + D * step, rows, lane);
+            at.next();
+            const float2 sum = row_sum<TPR, true>(make_float2(s2.x + s2.y, sn.x + sn.y), red, turn, W);
+            const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
+            const float m = inv * inv * sum.y * inv_d;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = (i * TPR + lane) * E;
+                float yn[E];
+                vfma(dn[i], v[i], -m, dn[i]);
+                vmul(dn[i], dn[i], inv);                 // dx
+                vmul(yn, v[i], inv);
+                vmul(yn, y[i], yn);                      // dy n
+                vfma(dw[i], yn, s[i], dw[i]);
+                vmul(yn, yn, wds[i]);                    // dz
+                if (row < rows && c < a.D) {
+                    const long long e = (long long)row * a.D + c;
+                    Chunk<T, E>::store(static_cast<T*>(a.dx) + e, dn[i]);
+                    Chunk<T, E>::store(static_cast<T*>(a.dz) + e, yn);
+                }
             }
         }
-        sum = row_sum<TPR>(sum, red, turn, W);
-        const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
-        const float m = inv * inv * sum.y * inv_d;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = (i * TPR + lane) * E;
-            float v[E], y[E], dx[E], dz[E];
-            r.get_x(i, v);
-            r.y[i].get(y);
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const float yn = y[j] * v[j] * inv;              // dy n
-                dx[j] = inv * fmaf(-m, v[j], y[j] * w[i][j] * s[i][j]);
-                dz[j] = yn * w[i][j] * ds[i][j];
-                dw[i][j] = fmaf(yn, s[i][j], dw[i][j]);
-            }
-            if (row < rows && c < a.D) {
-                const long long e = (long long)row * a.D + c;
-                Chunk<T, E>::store(static_cast<T*>(a.dx) + e, dx);
-                Chunk<T, E>::store(static_cast<T*>(a.dz) + e, dz);
-            }
-        }
-        if constexpr (kAhead)
-            r = ahead;
-        else
-            r.template load<TPR>(a, at, row + step, rows, lane);
     }
     if (a.dw) store_part<E, TPR, NC>(dw, a.part + (long long)blockIdx.x * a.D, a.D);
 }
@@ -254,7 +278,7 @@ struct Fwd {
     static kda_status go(const GatedArgs& a, cudaStream_t s) {
         constexpr int N = Rows<TPR>::kThreads, R = Rows<TPR>::kRows;
         auto* k = gated_fwd_kernel<T, E, TPR, NC, KEEP>;
-        static const int per_sm = resident(k, N);
+        static const int per_sm = resident(k, N, 0);
         const int grid = grid_of(per_sm, (a.T * a.H + R - 1) / R);
         TimedLaunch tl("gated_norm_fwd", s);
         k<<<grid, N, 0, s>>>(a);
@@ -272,7 +296,7 @@ struct Bwd {
     static kda_status go(const GatedArgs& a, cudaStream_t s) {
         constexpr int N = Rows<TPR>::kThreads, R = Rows<TPR>::kRows;
         auto* k = gated_bwd_kernel<T, E, TPR, NC, Q8>;
-        static const int per_sm = resident(k, N);
+        static const int per_sm = resident(k, N, 0);
         const int grid = std::min(grid_of(per_sm, (a.T * a.H + R - 1) / R), kPartsPerSm * sm_count());
         {
             TimedLaunch tl("gated_norm_bwd", s);
@@ -302,11 +326,11 @@ size_t gated_norm_ws_bytes(int T, int H, int D) {
 }
 
 kda_status gated_norm_fwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s) {
-    return by_width<Fwd, false>(wide(a, false), a.D, a, bf16, s);
+    return by_width<Fwd>(wide(a, false), a.D, a, bf16, s);
 }
 
 kda_status gated_norm_bwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s) {
-    return by_width<Bwd, true>(wide(a, a.xs != nullptr), a.D, a, bf16, s);
+    return by_width<Bwd>(wide(a, a.xs != nullptr), a.D, a, bf16, s);
 }
 
 }  // namespace kda

@@ -31,11 +31,11 @@ struct Row {
 template <typename R, typename T, int E, int TPR, int NC, bool BWD>
 struct Feed {
     static constexpr int kThreads = Rows<TPR>::kThreads;
-    static constexpr int kR = sizeof(Chunk<R, E>) / 16, kT = sizeof(Chunk<T, E>) / 16;
-    static constexpr int kUnits = NC * (kR + kT) * (BWD ? 2 : 1);      // of 16 bytes, of a thread and row
-    static constexpr int kStage = kUnits * 16 * kThreads;
+    // bytes of a thread's chunk of each type, and of its part of a row
+    static constexpr int kR = sizeof(Chunk<R, E>), kT = sizeof(Chunk<T, E>);
+    static constexpr int kStage = NC * (kR + kT) * (BWD ? 2 : 1) * kThreads;
     // slots: four as long as two CTAs then fit an SM, or as many as fit; the widest rows have none
-    static constexpr int kSlots = E != 8                     ? 1
+    static constexpr int kSlots = E == 1                     ? 1
                                   : kStage * 4 <= 100 * 1024 ? 4
                                   : kStage * 3 <= 100 * 1024 ? 3
                                   : kStage * 2 <= 200 * 1024 ? 2
@@ -47,13 +47,28 @@ struct Feed {
 
     const AddArgs& a;
     const int lane;
-    char* const mine;
+    char* const slots;
     int put = 0, get = 0;
 
     __device__ __forceinline__ Feed(const AddArgs& args, char* smem)
-        : a(args), lane(threadIdx.x % TPR), mine(smem + threadIdx.x * 16) {}
+        : a(args), lane(threadIdx.x % TPR), slots(smem) {}
 
-    // F(source row, 16-byte units of a chunk, slot) for what a row has
+    // A copy of N bytes, 16 or 8, and where a thread's chunk lies that has `before` bytes a thread
+    // in front of it.
+    template <int N>
+    static __device__ __forceinline__ void copy(char* to, const void* from) {
+        if constexpr (N == 16)
+            ptx::cp_async16(to, from);
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(to)), "l"(from)
+                         : "memory");
+    }
+    template <int N>
+    static __device__ __forceinline__ char* slot(char* stage, int before) {
+        return stage + before * kThreads + threadIdx.x * N;
+    }
+
+    // f(source, type of its chunk, bytes in front) for what a row has
     template <typename F>
     __device__ __forceinline__ void each(int row, F f) {
         const bool with_x = BWD ? a.da != nullptr : a.x != nullptr;
@@ -63,23 +78,22 @@ struct Feed {
             if (row >= a.T || c >= a.D) continue;
             const long long e = (long long)row * a.D + c;
             int at = i * (kR + kT) * (BWD ? 2 : 1);
-            f(static_cast<const R*>(a.r) + row * a.r_stride + c, kR, at);
+            f(static_cast<const R*>(a.r) + row * a.r_stride + c, Chunk<R, E>{}, at);
             at += kR;
-            if (with_x) f(static_cast<const T*>(a.x) + row * a.x_stride + c, kT, at);
+            if (with_x) f(static_cast<const T*>(a.x) + row * a.x_stride + c, Chunk<T, E>{}, at);
             at += kT;
             if constexpr (BWD) {
-                f(static_cast<const T*>(a.dy) + e, kT, at);
+                f(static_cast<const T*>(a.dy) + e, Chunk<T, E>{}, at);
                 at += kT;
-                if (a.dr) f(static_cast<const R*>(a.dr) + e, kR, at);
+                if (a.dr) f(static_cast<const R*>(a.dr) + e, Chunk<R, E>{}, at);
             }
         }
     }
     __device__ __forceinline__ void start(int row) {
         if constexpr (kRing) {
-            char* to = mine + put * kStage;
-            each(row, [&](const void* from, int units, int at) {
-                for (int k = 0; k < units; ++k)
-                    ptx::cp_async16(to + (at + k) * 16 * kThreads, static_cast<const char*>(from) + k * 16);
+            char* to = slots + put * kStage;
+            each(row, [&](const void* from, auto chunk, int at) {
+                copy<sizeof(chunk)>(slot<sizeof(chunk)>(to, at), from);
             });
             ptx::cp_async_commit();
             put = put + 1 == kSlots ? 0 : put + 1;
@@ -87,11 +101,7 @@ struct Feed {
     }
     template <typename C>
     __device__ __forceinline__ void take(C& c, int at) {
-        const char* from = mine + get * kStage + at * 16 * kThreads;
-        uint4* r = reinterpret_cast<uint4*>(&c);
-#pragma unroll
-        for (int k = 0; k < (int)(sizeof(C) / 16); ++k)
-            r[k] = *reinterpret_cast<const uint4*>(from + k * 16 * kThreads);
+        c = *reinterpret_cast<const C*>(slot<sizeof(C)>(slots + get * kStage, at));
     }
     // The row whose copies were begun first, zeros where it has nothing.
     __device__ __forceinline__ void finish(int row, Row<R, T, E, NC, BWD>& o) {
@@ -142,7 +152,7 @@ __device__ __forceinline__ void alphas(const AddArgs& a, int c, float (&v)[E]) {
 }
 
 template <typename R, typename T, int E, int TPR, int NC>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads) add_fwd_kernel(const AddArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) add_fwd_kernel(const AddArgs a) {
     using F = Feed<R, T, E, TPR, NC, false>;
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
     extern __shared__ __align__(16) char slots[];
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) add_fwd_kernel(const AddA
 }
 
 template <typename R, typename T, int E, int TPR, int NC>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads) add_bwd_kernel(const AddArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) add_bwd_kernel(const AddArgs a) {
     using F = Feed<R, T, E, TPR, NC, true>;
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
     extern __shared__ __align__(16) char slots[];
@@ -263,8 +273,11 @@ struct Fwd {
         return launch_status();
     }
     static kda_status run(const AddArgs& a, int type, cudaStream_t s) {
-        if (type == 0) return go<__nv_bfloat16, __nv_bfloat16>(a, s);
-        return type == 1 ? go<float, float>(a, s) : go<float, __nv_bfloat16>(a, s);
+        if constexpr (E != 8) {
+            if (type == 1) return go<float, float>(a, s);
+            if (type == 2) return go<float, __nv_bfloat16>(a, s);
+        }
+        return go<__nv_bfloat16, __nv_bfloat16>(a, s);
     }
 };
 
@@ -286,14 +299,26 @@ struct Bwd {
         return sum_parts_launch(a.part, grid, a.D, a.dw, a.da, s);
     }
     static kda_status run(const AddArgs& a, int type, cudaStream_t s) {
-        if (type == 0) return go<__nv_bfloat16, __nv_bfloat16>(a, s);
-        return type == 1 ? go<float, float>(a, s) : go<float, __nv_bfloat16>(a, s);
+        if constexpr (E != 8) {
+            if (type == 1) return go<float, float>(a, s);
+            if (type == 2) return go<float, __nv_bfloat16>(a, s);
+        }
+        return go<__nv_bfloat16, __nv_bfloat16>(a, s);
     }
 };
 
-bool wide(const AddArgs& a) {
-    return a.D % 8 == 0 && a.r_stride % 8 == 0 && a.x_stride % 8 == 0 &&
-           aligned16({a.r, a.x, a.r_out, a.y, a.dy, a.dr, a.dres, a.dx, a.av.p, a.w.p});
+// Elements of an access: 8 where all is bf16, else 4, where widths, strides and pointers allow them.
+int chunk_of(const AddArgs& a, int type) {
+    if (!aligned16({a.r, a.x, a.r_out, a.y, a.dy, a.dr, a.dres, a.dx, a.av.p, a.w.p})) return 1;
+    for (int E = type == 0 ? 8 : 4; E >= 4; E /= 2)
+        if (a.D % E == 0 && a.r_stride % E == 0 && a.x_stride % E == 0) return E;
+    return 1;
+}
+template <template <int, int, int> class F>
+kda_status launch(const AddArgs& a, int type, cudaStream_t s) {
+    const int E = chunk_of(a, type);
+    if (E == 8) return by_width<F, 8>(a.D, a, type, s);
+    return E == 4 ? by_width<F, 4>(a.D, a, type, s) : by_width<F, 1>(a.D, a, type, s);
 }
 
 }  // namespace
@@ -303,11 +328,11 @@ size_t add_norm_ws_bytes(int T, int D) {
 }
 
 kda_status add_norm_fwd_launch(const AddArgs& a, int type, cudaStream_t s) {
-    return by_width<Fwd>(wide(a), a.D, a, type, s);
+    return launch<Fwd>(a, type, s);
 }
 
 kda_status add_norm_bwd_launch(const AddArgs& a, int type, cudaStream_t s) {
-    return by_width<Bwd>(wide(a), a.D, a, type, s);
+    return launch<Bwd>(a, type, s);
 }
 
 }  // namespace kda

@@ -32,67 +32,143 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int 
 
 // ---- 8 bits ----
 
-// Two threads per block of 32, 16 elements each: rows of D % 32 == 0 elements, 16-byte accesses.
-// A pass bounded by HBM.
+// 16 neighbouring elements.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[2][8]) {
+    Chunk<__nv_bfloat16, 8> r[2];
+    r[0].load(p);
+    r[1].load(p + 8);
+    r[0].get(v[0]);
+    r[1].get(v[1]);
+}
+__device__ __forceinline__ void load16(const float* p, float (&v)[2][8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 r = __ldcs(reinterpret_cast<const float4*>(p) + j);
+        float* o = v[j / 2] + j % 2 * 4;
+        o[0] = r.x, o[1] = r.y, o[2] = r.z, o[3] = r.w;
+    }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[2][8]) {
+    Chunk<__nv_bfloat16, 8>::store(p, v[0]);
+    Chunk<__nv_bfloat16, 8>::store(p + 8, v[1]);
+}
+__device__ __forceinline__ void store16(float* p, const float (&v)[2][8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float* o = v[j / 2] + j % 2 * 4;
+        reinterpret_cast<float4*>(p)[j] = make_float4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// Two threads per block of 32, 16 elements each, and two such items of a thread on their way: rows
+// of D % 32 == 0 elements, 16-byte accesses.  A pass bounded by HBM.
 template <typename T>
 __global__ void __launch_bounds__(256) pack_wide_kernel(const T* __restrict__ x, long long rows, int D,
                                                         long long stride, uint8_t* codes,
                                                         uint8_t* scales) {
-    const long long per = D / 16, n = rows * per;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i - threadIdx.x < n; i += gridDim.x * 256ll) {
-        const bool in = i < n;
-        const long long row = rows == 1 ? 0 : i / per, at = i - row * per;
-        Chunk<T, 8> r[2];
-        r[0].zero();
-        r[1].zero();
-        if (in) {
-            r[0].load(x + row * stride + at * 16);
-            r[1].load(x + row * stride + at * 16 + 8);
-        }
-        float v[2][8];
-        r[0].get(v[0]);
-        r[1].get(v[1]);
-        float top = largest(v[1], largest(v[0]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        if (top > kMaxFloat) {   // in both threads of the block
-            top = largest_finite(v[1], largest_finite(v[0]));
-            top = fmaxf(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
-        }
-        if (!in) continue;
-        const uint32_t b = scale_byte(top);
-        const float inv = inverse_of(b);
-        if (b == kTopScale) {
-            below_top(v[0]);
-            below_top(v[1]);
-        }
-        uint32_t w[4];
+    constexpr int U = 2;
+    const long long per = D / 16, n = rows * per, step = gridDim.x * 256ll;
+    for (long long i0 = blockIdx.x * 256ll + threadIdx.x; i0 - threadIdx.x < n; i0 += U * step) {
+        float v[U][2][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = code2(v[j / 2][j % 2 * 4], v[j / 2][j % 2 * 4 + 1], inv) |
-                   code2(v[j / 2][j % 2 * 4 + 2], v[j / 2][j % 2 * 4 + 3], inv) << 16;
-        reinterpret_cast<uint4*>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        if ((i & 1) == 0) scales[i / 2] = (uint8_t)b;
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * step, row = rows == 1 || i >= n ? 0 : i / per;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][0][e] = v[u][1][e] = 0.f;
+            if (i < n) load16(x + row * stride + (i - row * per) * 16, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * step;
+            float(&w)[2][8] = v[u];
+            float top = largest(w[1], largest(w[0]));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            if (top > kMaxFloat) {   // in both threads of the block
+                top = largest_finite(w[1], largest_finite(w[0]));
+                top = fmaxf(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
+            }
+            if (i >= n) continue;
+            const uint32_t b = scale_byte(top);
+            const float inv = inverse_of(b);
+            if (b == kTopScale) {
+                below_top(w[0]);
+                below_top(w[1]);
+            }
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                c[j] = code2(w[j / 2][j % 2 * 4], w[j / 2][j % 2 * 4 + 1], inv) |
+                       code2(w[j / 2][j % 2 * 4 + 2], w[j / 2][j % 2 * 4 + 3], inv) << 16;
+            reinterpret_cast<uint4*>(codes)[i] = make_uint4(c[0], c[1], c[2], c[3]);
+            if ((i & 1) == 0) scales[i / 2] = (uint8_t)b;
+        }
     }
 }
 
-// A warp per block, a lane per element: any width, stride and alignment.
+// A warp per block, a lane per element, four blocks on their way: any width, stride and alignment.
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ x, long long rows, int D,
                                                    long long stride, uint8_t* codes,
                                                    uint8_t* scales) {
+    constexpr int U = 4;
     const int lane = threadIdx.x & 31, per = (D + kScaleBlock - 1) / kScaleBlock;
     const long long n = rows * per;
-    for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < n; i += gridDim.x * 8ll) {
-        const long long row = i / per;
-        const int c = (int)(i - row * per) * kScaleBlock + lane;
-        float v[1] = {c < D ? to_f<T>(x[row * stride + c]) : 0.f};
-        float top = largest_finite(v);
+    for (long long i0 = (blockIdx.x * 8ll + (threadIdx.x >> 5)) * U; i0 < n; i0 += gridDim.x * 8ll * U) {
+        long long row = n <= 0x7fffffff ? (unsigned)i0 / (unsigned)per : i0 / per;
+        int block = (int)(i0 - row * per);
+        float v[U][1];
+        long long at[U];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        const uint32_t b = scale_byte(top);
-        if (b == kTopScale) below_top(v);
-        if (c < D) Codes<1>::store(codes + row * D + c, v, inverse_of(b));
-        if (lane == 0) scales[i] = (uint8_t)b;
+        for (int u = 0; u < U; ++u) {
+            const int c = block * kScaleBlock + lane;
+            const bool in = i0 + u < n && c < D;
+            at[u] = in ? row * D + c : -1;
+            v[u][0] = in ? to_f<T>(x[row * stride + c]) : 0.f;
+            if (++block == per) block = 0, ++row;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float top = largest_finite(v[u]);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            const uint32_t b = scale_byte(top);
+            if (b == kTopScale) below_top(v[u]);
+            if (at[u] >= 0) Codes<1>::store(codes + at[u], v[u], inverse_of(b));
+            if (lane == 0 && i0 + u < n) scales[i0 + u] = (uint8_t)b;
+        }
+    }
+}
+
+// 16 elements of a block per thread: D % 32 == 0.
+template <typename T>
+__global__ void __launch_bounds__(256) unpack_wide_kernel(const uint8_t* __restrict__ codes,
+                                                          const uint8_t* __restrict__ scales, long long n,
+                                                          T* x) {
+    constexpr int U = 2;
+    const long long step = gridDim.x * 256ll;
+    for (long long i0 = blockIdx.x * 256ll + threadIdx.x; i0 < n; i0 += U * step) {
+        uint4 r[U];
+        uint32_t s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * step;
+            if (i >= n) continue;
+            r[u] = __ldcs(reinterpret_cast<const uint4*>(codes) + i);
+            s[u] = scales[i / 2];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * step;
+            if (i >= n) continue;
+            Codes<8> c;
+            float v[2][8];
+            c.s = s[u];
+            c.r = make_uint2(r[u].x, r[u].y);
+            c.get(v[0]);
+            c.r = make_uint2(r[u].z, r[u].w);
+            c.get(v[1]);
+            store16(x + i * 16, v);
+        }
     }
 }
 
@@ -104,7 +180,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
     const long long n = rows * D;
     const int per = (D + kScaleBlock - 1) / kScaleBlock;
     for (long long i = (blockIdx.x * 256ll + threadIdx.x) * E; i < n; i += gridDim.x * 256ll * E) {
-        const long long row = i / D;
+        const long long row = n <= 0x7fffffff ? (unsigned)i / (unsigned)D : i / D;
         int c = (int)(i - row * D);
         const uint8_t* s = scales + row * per;
         if (E > 1 && i + E > n) {
@@ -119,11 +195,10 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
         }
         Codes<E> r;
         r.load(codes + i, s + c / kScaleBlock);
-        const uint32_t first = r.s;
+        uint32_t b = r.s;
         r.s = 127;
         float v[E];
         r.get(v);
-        uint32_t b = first;
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             v[k] *= scale_of(b);
@@ -150,10 +225,10 @@ kda_status pack(const void* x, long long rows, int D, long long stride, uint8_t*
     const T* p = static_cast<const T*>(x);
     TimedLaunch tl("pack8", s);
     if (D % kScaleBlock == 0 && stride % 8 == 0 && aligned16({x, codes}))
-        pack_wide_kernel<T><<<grid_all((rows * (D / 16) + 255) / 256), 256, 0, s>>>(p, rows, D, stride,
+        pack_wide_kernel<T><<<grid_all((rows * (D / 16) + 511) / 512), 256, 0, s>>>(p, rows, D, stride,
                                                                                   codes, scales);
     else
-        pack_kernel<T><<<grid_all((rows * ((D + 31) / 32) + 7) / 8), 256, 0, s>>>(p, rows, D, stride,
+        pack_kernel<T><<<grid_all((rows * ((D + 31) / 32) + 31) / 32), 256, 0, s>>>(p, rows, D, stride,
                                                                                 codes, scales);
     return launch_status();
 }
@@ -164,8 +239,10 @@ kda_status unpack(const uint8_t* codes, const uint8_t* scales, long long rows, i
     T* p = static_cast<T*>(x);
     const long long n = rows * D;
     TimedLaunch tl("unpack8", s);
-    if (aligned16({codes, x}))
-        unpack_kernel<T, 8><<<grid_all((n + 2047) / 2048), 256, 0, s>>>(codes, scales, rows, D, p);
+    if (D % kScaleBlock == 0 && aligned16({codes, x}))
+        unpack_wide_kernel<T><<<grid_all((n / 16 + 511) / 512), 256, 0, s>>>(codes, scales, n / 16, p);
+    else if (aligned16({codes, x}))
+        unpack_kernel<T, 4><<<grid_all((n + 1023) / 1024), 256, 0, s>>>(codes, scales, rows, D, p);
     else
         unpack_kernel<T, 1><<<grid_all((n + 255) / 256), 256, 0, s>>>(codes, scales, rows, D, p);
     return launch_status();

@@ -81,8 +81,9 @@ __device__ __forceinline__ void vdot(float2& sum, const float (&a)[E], const flo
     }
 }
 
-// E neighbouring elements of type T as they lie in memory: 16-byte accesses for E = 8, one
-// element for E = 1.
+// E neighbouring elements of type T as they lie in memory: E = 8 for bf16, 4 for float32 and what
+// is beside it (16-byte accesses; neighbouring lanes then read whole sectors), 1 for rows that
+// allow no more.
 template <typename T, int E>
 struct Chunk;
 template <>
@@ -104,20 +105,30 @@ struct Chunk<__nv_bfloat16, 8> {
     }
 };
 template <>
-struct Chunk<float, 8> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+struct Chunk<__nv_bfloat16, 4> {
+    uint2 r;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        r = __ldcs(reinterpret_cast<const uint2*>(p));
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        unpack2(r.x, v[0], v[1]);
+        unpack2(r.y, v[2], v[3]);
     }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[4]) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    }
+};
+template <>
+struct Chunk<float, 4> {
+    float4 r;
+    __device__ __forceinline__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     }
 };
 template <typename T>
@@ -187,7 +198,7 @@ __device__ __forceinline__ void values2(uint32_t two, float& a, float& b) {
     b = f.y;
 }
 
-// E codes as they lie in memory, and the scale of their block (E = 8 or 1).
+// E codes as they lie in memory, and the scale of their block.
 template <int E>
 struct Codes;
 template <>
@@ -213,6 +224,26 @@ struct Codes<8> {
         *reinterpret_cast<uint2*>(p) =
             make_uint2(code2(v[0], v[1], inv) | code2(v[2], v[3], inv) << 16,
                        code2(v[4], v[5], inv) | code2(v[6], v[7], inv) << 16);
+    }
+};
+template <>
+struct Codes<4> {
+    uint32_t r, s;
+    __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* scale) {
+        r = __ldcs(reinterpret_cast<const uint32_t*>(p));
+        s = *scale;
+    }
+    __device__ __forceinline__ void zero() {
+        r = 0;
+        s = 127;
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        values2(r & 0xffffu, v[0], v[1]);
+        values2(r >> 16, v[2], v[3]);
+        vmul(v, v, scale_of(s));
+    }
+    static __device__ __forceinline__ void store(uint8_t* p, const float (&v)[4], float inv) {
+        *reinterpret_cast<uint32_t*>(p) = code2(v[0], v[1], inv) | code2(v[2], v[3], inv) << 16;
     }
 };
 template <>
@@ -247,22 +278,24 @@ struct Param {
         if (!p) {
 #pragma unroll
             for (int j = 0; j < E; ++j) v[j] = 1.f;
-        } else if (E == 8) {
-            if (bf16) {
-                const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c));
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int j = 0; j < E; j += 2) unpack2(w[j / 2 % 4], v[j], v[(j + 1) % E]);
-            } else {
-                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
-                const float4 x = __ldg(q), y = __ldg(q + 1);
-                const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = f[j % 8];
-            }
-        } else {
+        } else if constexpr (E == 1) {
             v[0] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c])
                         : __ldg(static_cast<const float*>(p) + c);
+        } else if (bf16) {
+            const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
+#pragma unroll
+            for (int j = 0; j < E; j += 4) {
+                const uint2 r = __ldg(q + j / 4);
+                unpack2(r.x, v[j], v[j + 1]);
+                unpack2(r.y, v[j + 2], v[j + 3]);
+            }
+        } else {
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+#pragma unroll
+            for (int j = 0; j < E; j += 4) {
+                const float4 r = __ldg(q + j / 4);
+                v[j] = r.x, v[j + 1] = r.y, v[j + 2] = r.z, v[j + 3] = r.w;
+            }
         }
     }
 };
@@ -303,26 +336,31 @@ struct Rows {
 };
 
 // Picks the widths a kernel is made for: a row's elements stay in registers, E * NC of them in
-// each of TPR threads.  Rows of 16-byte accesses (E = 8) where width, strides and pointers allow,
-// else single elements.  F: template <int E, int TPR, int NC> struct with a static run(args...).
-template <template <int, int, int> class F, typename... A>
-kda_status by_width(bool wide, int D, A&&... args) {
-    if (wide) {
-        if (D <= 32) return F<8, 4, 1>::run(args...);
-        if (D <= 64) return F<8, 8, 1>::run(args...);
-        if (D <= 128) return F<8, 16, 1>::run(args...);
-        if (D <= 256) return F<8, 32, 1>::run(args...);
-        if (D <= 512) return F<8, 32, 2>::run(args...);
-        if (D <= 1024) return F<8, 64, 2>::run(args...);
-        if (D <= 2048) return F<8, 256, 1>::run(args...);
-        if (D <= 4096) return F<8, 256, 2>::run(args...);
-        if (D <= 8192) return F<8, 256, 4>::run(args...);
-        return F<8, 512, 4>::run(args...);
+// each of TPR threads.  F: template <int E, int TPR, int NC> struct with a static run(args...).
+// E: as chunk_of gives it.
+template <template <int, int, int> class F, int E, typename... A>
+kda_status by_width(int D, A&&... args) {
+    if constexpr (E == 1) {
+        if (D <= 128) return F<1, 32, 4>::run(args...);
+        if (D <= 512) return F<1, 128, 4>::run(args...);
+        if (D <= 2048) return F<1, 256, 8>::run(args...);
+        return F<1, 1024, 16>::run(args...);
+    } else {
+        // (never fewer threads than a block of 32 elements takes)
+        if constexpr (4 * E >= kScaleBlock)
+            if (D <= 4 * E) return F<E, 4, 1>::run(args...);
+        if (D <= 8 * E) return F<E, 8, 1>::run(args...);
+        if (D <= 16 * E) return F<E, 16, 1>::run(args...);
+        if (D <= 32 * E) return F<E, 32, 1>::run(args...);
+        if (D <= 64 * E) return F<E, 32, 2>::run(args...);
+        if (D <= 128 * E) return F<E, 64, 2>::run(args...);
+        if (D <= 256 * E) return F<E, 256, 1>::run(args...);
+        if (D <= 512 * E) return F<E, 256, 2>::run(args...);
+        if (D <= 1024 * E) return F<E, 256, 4>::run(args...);
+        if constexpr (2048 * E < kMaxWidth)
+            if (D > 2048 * E) return F<E, 1024, 4>::run(args...);
+        return F<E, 512, 4>::run(args...);
     }
-    if (D <= 128) return F<1, 32, 4>::run(args...);
-    if (D <= 512) return F<1, 128, 4>::run(args...);
-    if (D <= 2048) return F<1, 256, 8>::run(args...);
-    return F<1, 1024, 16>::run(args...);
 }
 
 inline bool aligned16(std::initializer_list<const void*> ps) {

@@ -51,21 +51,37 @@ __device__ __forceinline__ void gate_grad(float z, int act, float& s, float& ds)
     }
 }
 
-// (token, head) of a thread's rows, stepped without a division.
+// Where a row begins in x, the gate and the dense tensors, stepped from one of a thread's rows to
+// the next without a division or a product.
 struct Place {
-    int t, h, dt, dh, H;
-    __device__ __forceinline__ Place(int row, int step, int heads) : H(heads) {
-        t = row / H;
+    long long x, z, e, b;     // elements; scale bytes
+    long long dx, dz, de, db, wx, wz;
+    int h, dh, H;
+    __device__ __forceinline__ Place(const GatedArgs& a, int row, int step) : H(a.H) {
+        const int nblk = (a.D + kScaleBlock - 1) / kScaleBlock, t = row / H, dt = step / H;
         h = row - t * H;
-        dt = step / H;
         dh = step - dt * H;
+        x = t * a.x_stride + (long long)h * a.D;
+        z = t * a.z_stride + (long long)h * a.D;
+        dx = dt * a.x_stride + (long long)dh * a.D;
+        dz = dt * a.z_stride + (long long)dh * a.D;
+        wx = a.x_stride - (long long)H * a.D;   // where the heads of a token end
+        wz = a.z_stride - (long long)H * a.D;
+        e = (long long)row * a.D;
+        de = (long long)step * a.D;
+        b = (long long)row * nblk;
+        db = (long long)step * nblk;
     }
     __device__ __forceinline__ void next() {
-        t += dt;
+        x += dx;
+        z += dz;
+        e += de;
+        b += db;
         h += dh;
         if (h >= H) {
             h -= H;
-            ++t;
+            x += wx;
+            z += wz;
         }
     }
 };
@@ -100,9 +116,6 @@ struct Row {
 
     template <int TPR>
     __device__ __forceinline__ void load(const GatedArgs& a, const Place& at, int row, int rows, int lane) {
-        const long long e = (long long)row * a.D, b = (long long)row * ((a.D + kScaleBlock - 1) / kScaleBlock);
-        const T* xp = static_cast<const T*>(a.x) + at.t * a.x_stride + (long long)at.h * a.D;
-        const T* zp = static_cast<const T*>(a.z) + at.t * a.z_stride + (long long)at.h * a.D;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i * TPR + lane) * E;
@@ -111,20 +124,20 @@ struct Row {
                 xq[i].zero();
                 zq[i].zero();
                 if (in) {
-                    xq[i].load(a.xc + e + c, a.xs + b + c / kScaleBlock);
-                    zq[i].load(a.zc + e + c, a.zs + b + c / kScaleBlock);
+                    xq[i].load(a.xc + at.e + c, a.xs + at.b + c / kScaleBlock);
+                    zq[i].load(a.zc + at.e + c, a.zs + at.b + c / kScaleBlock);
                 }
             } else {
                 x[i].zero();
                 z[i].zero();
                 if (in) {
-                    x[i].load(xp + c);
-                    z[i].load(zp + c);
+                    x[i].load(static_cast<const T*>(a.x) + at.x + c);
+                    z[i].load(static_cast<const T*>(a.z) + at.z + c);
                 }
             }
             if constexpr (BWD) {
                 y[i].zero();
-                if (in) y[i].load(static_cast<const T*>(a.dy) + e + c);
+                if (in) y[i].load(static_cast<const T*>(a.dy) + at.e + c);
             }
         }
     }
@@ -145,18 +158,19 @@ struct Row {
 // Rows on their way while one is worked on, in registers: 32 to 48 bytes a thread and row are too
 // few in flight with one (gated_fwd of 32768 x 16 x 128 with copies in 8 bits: 109 us, with three
 // 96 us).
-template <int NC>
-constexpr int kDepth = NC == 1 ? 3 : NC == 2 ? 2 : 1;
+template <int NC, bool BWD>
+constexpr int kDepth = NC == 1 ? (BWD ? 2 : 3) : NC == 2 && !BWD ? 2 : 1;
 
 template <typename T, int E, int TPR, int NC, bool KEEP>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const GatedArgs a) {
-    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC>;
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_fwd_kernel(const GatedArgs a) {
+    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC, false>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const int rows = a.T * a.H, step = gridDim.x * RPC, nblk = (a.D + kScaleBlock - 1) / kScaleBlock;
+    const int rows = a.T * a.H, step = gridDim.x * RPC;
     const float inv_d = 1.f / a.D;
     int row = blockIdx.x * RPC + group, turn = 0;
-    Place at(row, step, a.H);   // of the next row to load
+    Place at(a, row, step);   // of the next row to load
+    long long e = at.e, b = at.b;
     Row<T, E, NC, false, false> ring[D];
 #pragma unroll
     for (int k = 0; k < D; ++k, at.next()) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
@@ -168,7 +182,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const Ga
     }
     while (row - group < rows) {
 #pragma unroll
-        for (int k = 0; k < D; ++k, row += step, ++turn) {
+        for (int k = 0; k < D; ++k, row += step, e += at.de, b += at.db, ++turn) {
             if (row - group >= rows) break;   // alike in the whole CTA
             float v[NC][E], g[NC][E];
             float2 sum = make_float2(0.f, 0.f);
@@ -199,10 +213,9 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const Ga
                     for (int j = 0; j < E; ++j) f[j] = gate<T>(g[i][j], a.act);
                     vmul(y, y, f);
                     vmul(y, y, inv);
-                    Chunk<T, E>::store(static_cast<T*>(a.y) + (long long)row * a.D + c, y);
+                    Chunk<T, E>::store(static_cast<T*>(a.y) + e + c, y);
                 }
                 if (KEEP) {
-                    const long long e = (long long)row * a.D, b = (long long)row * nblk;
                     keep<E>(v[i], in, a.xc + e, a.xs + b, c);
                     keep<E>(g[i], in, a.zc + e, a.zs + b, c);
                 }
@@ -212,32 +225,36 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_fwd_kernel(const Ga
 }
 
 template <typename T, int E, int TPR, int NC, bool Q8>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const GatedArgs a) {
-    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC>;
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_bwd_kernel(const GatedArgs a) {
+    constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC, true>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int rows = a.T * a.H, step = gridDim.x * RPC;
     const float inv_d = 1.f / a.D;
-    float dw[NC][E] = {};
+    float dw[NC][E] = {}, w1[E] = {};
+    if (NC == 1 && lane * E < a.D) a.w.get(lane * E, w1);
     int row = blockIdx.x * RPC + group, turn = 0;
-    Place at(row, step, a.H);
+    Place at(a, row, step);
+    long long e = at.e;
     Row<T, E, NC, true, Q8> ring[D];
 #pragma unroll
     for (int k = 0; k < D; ++k, at.next()) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
     while (row - group < rows) {
 #pragma unroll
-        for (int k = 0; k < D; ++k, row += step, ++turn) {
+        for (int k = 0; k < D; ++k, row += step, e += at.de, ++turn) {
             if (row - group >= rows) break;   // alike in the whole CTA
             float2 s2 = make_float2(0.f, 0.f), sn = s2;   // sums of x^2 and of dn x
             float v[NC][E], y[NC][E], s[NC][E], wds[NC][E], dn[NC][E];
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = (i * TPR + lane) * E;
-                float g[E], w[E] = {}, ds[E];
+                float g[E], w[E], ds[E];
                 ring[k].get_x(i, v[i]);
                 ring[k].get_z(i, g);
                 ring[k].y[i].get(y[i]);
-                if (c < a.D) a.w.get(c, w);
+#pragma unroll
+                for (int j = 0; j < E; ++j) w[j] = NC == 1 ? w1[j] : 0.f;
+                if (NC > 1 && c < a.D) a.w.get(c, w);
 #pragma unroll
                 for (int j = 0; j < E; ++j) gate_grad<T>(g[j], a.act, s[i][j], ds[j]);
                 vmul(wds[i], w, ds);
@@ -262,9 +279,8 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads) gated_bwd_kernel(const Ga
                 vfma(dw[i], yn, s[i], dw[i]);
                 vmul(yn, yn, wds[i]);                    // dz
                 if (row < rows && c < a.D) {
-                    const long long e = (long long)row * a.D + c;
-                    Chunk<T, E>::store(static_cast<T*>(a.dx) + e, dn[i]);
-                    Chunk<T, E>::store(static_cast<T*>(a.dz) + e, yn);
+                    Chunk<T, E>::store(static_cast<T*>(a.dx) + e + c, dn[i]);
+                    Chunk<T, E>::store(static_cast<T*>(a.dz) + e + c, yn);
                 }
             }
         }
@@ -285,8 +301,9 @@ struct Fwd {
         return launch_status();
     }
     static kda_status run(const GatedArgs& a, bool bf16, cudaStream_t s) {
-        if (a.xc) return bf16 ? go<__nv_bfloat16, true>(a, s) : go<float, true>(a, s);
-        return bf16 ? go<__nv_bfloat16, false>(a, s) : go<float, false>(a, s);
+        if constexpr (E != 8)
+            if (!bf16) return a.xc ? go<float, true>(a, s) : go<float, false>(a, s);
+        return a.xc ? go<__nv_bfloat16, true>(a, s) : go<__nv_bfloat16, false>(a, s);
     }
 };
 
@@ -307,16 +324,24 @@ struct Bwd {
         return sum_parts_launch(a.part, grid, a.D, a.dw, nullptr, s);
     }
     static kda_status run(const GatedArgs& a, bool bf16, cudaStream_t s) {
-        if (a.xs) return bf16 ? go<__nv_bfloat16, true>(a, s) : go<float, true>(a, s);
-        return bf16 ? go<__nv_bfloat16, false>(a, s) : go<float, false>(a, s);
+        if constexpr (E != 8)
+            if (!bf16) return a.xs ? go<float, true>(a, s) : go<float, false>(a, s);
+        return a.xs ? go<__nv_bfloat16, true>(a, s) : go<__nv_bfloat16, false>(a, s);
     }
 };
 
-// 16-byte accesses need widths, strides and pointers that allow them.
-bool wide(const GatedArgs& a, bool packed) {
-    const int E = 8;
-    if (a.D % E || !aligned16({a.x, a.z, a.y, a.dy, a.dx, a.dz, a.xc, a.zc, a.w.p})) return false;
-    return packed || (a.x_stride % E == 0 && a.z_stride % E == 0);
+// Elements of an access: 8 of bf16 or 4 where widths, strides and pointers allow them.
+int chunk_of(const GatedArgs& a, bool bf16, bool packed) {
+    if (!aligned16({a.x, a.z, a.y, a.dy, a.dx, a.dz, a.xc, a.zc, a.w.p})) return 1;
+    for (int E = bf16 ? 8 : 4; E >= 4; E /= 2)
+        if (a.D % E == 0 && (packed || (a.x_stride % E == 0 && a.z_stride % E == 0))) return E;
+    return 1;
+}
+template <template <int, int, int> class F>
+kda_status launch(const GatedArgs& a, bool bf16, bool packed, cudaStream_t s) {
+    const int E = chunk_of(a, bf16, packed);
+    if (E == 8) return by_width<F, 8>(a.D, a, bf16, s);
+    return E == 4 ? by_width<F, 4>(a.D, a, bf16, s) : by_width<F, 1>(a.D, a, bf16, s);
 }
 
 }  // namespace
@@ -326,11 +351,11 @@ size_t gated_norm_ws_bytes(int T, int H, int D) {
 }
 
 kda_status gated_norm_fwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s) {
-    return by_width<Fwd>(wide(a, false), a.D, a, bf16, s);
+    return launch<Fwd>(a, bf16, false, s);
 }
 
 kda_status gated_norm_bwd_launch(const GatedArgs& a, bool bf16, cudaStream_t s) {
-    return by_width<Bwd>(wide(a, a.xs != nullptr), a.D, a, bf16, s);
+    return launch<Bwd>(a, bf16, a.xs != nullptr, s);
 }
 
 }  // namespace kda

@@ -891,11 +891,11 @@ template <typename T>
 kda_status step(int B, int C, bool tied, const void* x, long long x_row, const void* g,
                 long long g_row, const float* state, float* next, void* o, cudaStream_t s) {
     TimedLaunch tl("gated_scan_step", s);
-    const bool wide = C % 8 == 0 && x_row % 8 == 0 && g_row % 8 == 0 &&
+    const bool wide = C % 4 == 0 && x_row % 4 == 0 && g_row % 4 == 0 &&
                       aligned16({x, g, state, next, o});
-    const long long n = (long long)B * (wide ? C / 8 : C);
+    const long long n = (long long)B * (wide ? C / 4 : C);
     const int grid = (int)std::min<long long>((n + 255) / 256, 8ll * sm_count());
-    auto* k = wide ? step_kernel<T, 8> : step_kernel<T, 1>;
+    auto* k = wide ? step_kernel<T, 4> : step_kernel<T, 1>;
     k<<<grid, 256, 0, s>>>(B, C, tied, static_cast<const T*>(x), x_row, static_cast<const T*>(g), g_row,
                            state, next, static_cast<T*>(o));
     return launch_status();

@@ -152,7 +152,7 @@ __device__ __forceinline__ void alphas(const AddArgs& a, int c, float (&v)[E]) {
 }
 
 template <typename R, typename T, int E, int TPR, int NC>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) add_fwd_kernel(const AddArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) add_fwd_kernel(const AddArgs a) {
     using F = Feed<R, T, E, TPR, NC, false>;
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
     extern __shared__ __align__(16) char slots[];
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) add_fwd_kernel(const A
 }
 
 template <typename R, typename T, int E, int TPR, int NC>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) add_bwd_kernel(const AddArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) add_bwd_kernel(const AddArgs a) {
     using F = Feed<R, T, E, TPR, NC, true>;
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32;
     extern __shared__ __align__(16) char slots[];

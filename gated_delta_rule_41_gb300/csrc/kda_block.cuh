@@ -333,6 +333,8 @@ template <int TPR>
 struct Rows {
     static constexpr int kThreads = TPR > 256 ? TPR : 256;
     static constexpr int kRows = kThreads / TPR;
+    // CTAs that an SM has to hold: left to the compiler, but for the widest (it would spill for two)
+    static constexpr int kMin = kThreads > 256 ? 1 : 0;
 };
 
 // Picks the widths a kernel is made for: a row's elements stay in registers, E * NC of them in

@@ -51,40 +51,26 @@ __device__ __forceinline__ void gate_grad(float z, int act, float& s, float& ds)
     }
 }
 
-// Where a row begins in x, the gate and the dense tensors, stepped from one of a thread's rows to
-// the next without a division or a product.
+// (token, head) of a thread's rows, stepped without a division.
 struct Place {
-    long long x, z, e, b;     // elements; scale bytes
-    long long dx, dz, de, db, wx, wz;
-    int h, dh, H;
-    __device__ __forceinline__ Place(const GatedArgs& a, int row, int step) : H(a.H) {
-        const int nblk = (a.D + kScaleBlock - 1) / kScaleBlock, t = row / H, dt = step / H;
-        h = row - t * H;
-        dh = step - dt * H;
-        x = t * a.x_stride + (long long)h * a.D;
-        z = t * a.z_stride + (long long)h * a.D;
-        dx = dt * a.x_stride + (long long)dh * a.D;
-        dz = dt * a.z_stride + (long long)dh * a.D;
-        wx = a.x_stride - (long long)H * a.D;   // where the heads of a token end
-        wz = a.z_stride - (long long)H * a.D;
-        e = (long long)row * a.D;
-        de = (long long)step * a.D;
-        b = (long long)row * nblk;
-        db = (long long)step * nblk;
+    int t, h, dt, dh;
+    __device__ __forceinline__ Place(const GatedArgs& a, int row, int step) {
+        t = row / a.H;
+        h = row - t * a.H;
+        dt = step / a.H;
+        dh = step - dt * a.H;
     }
-    __device__ __forceinline__ void next() {
-        x += dx;
-        z += dz;
-        e += de;
-        b += db;
+    __device__ __forceinline__ void next(const GatedArgs& a) {
+        t += dt;
         h += dh;
-        if (h >= H) {
-            h -= H;
-            x += wx;
-            z += wz;
+        if (h >= a.H) {
+            h -= a.H;
+            ++t;
         }
     }
 };
+
+__host__ __device__ __forceinline__ int blocks_of(int D) { return (D + kScaleBlock - 1) / kScaleBlock; }
 
 // The codes and the scale of a chunk; the chunks of a block lie in neighbouring lanes.
 template <int E>
@@ -116,6 +102,7 @@ struct Row {
 
     template <int TPR>
     __device__ __forceinline__ void load(const GatedArgs& a, const Place& at, int row, int rows, int lane) {
+        const long long e = (long long)row * a.D;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = (i * TPR + lane) * E;
@@ -124,20 +111,22 @@ struct Row {
                 xq[i].zero();
                 zq[i].zero();
                 if (in) {
-                    xq[i].load(a.xc + at.e + c, a.xs + at.b + c / kScaleBlock);
-                    zq[i].load(a.zc + at.e + c, a.zs + at.b + c / kScaleBlock);
+                    const long long b = (long long)row * blocks_of(a.D) + c / kScaleBlock;
+                    xq[i].load(a.xc + e + c, a.xs + b);
+                    zq[i].load(a.zc + e + c, a.zs + b);
                 }
             } else {
                 x[i].zero();
                 z[i].zero();
                 if (in) {
-                    x[i].load(static_cast<const T*>(a.x) + at.x + c);
-                    z[i].load(static_cast<const T*>(a.z) + at.z + c);
+                    const long long h = (long long)at.h * a.D + c;
+                    x[i].load(static_cast<const T*>(a.x) + at.t * a.x_stride + h);
+                    z[i].load(static_cast<const T*>(a.z) + at.t * a.z_stride + h);
                 }
             }
             if constexpr (BWD) {
                 y[i].zero();
-                if (in) y[i].load(static_cast<const T*>(a.dy) + at.e + c);
+                if (in) y[i].load(static_cast<const T*>(a.dy) + e + c);
             }
         }
     }
@@ -162,7 +151,7 @@ template <int NC, bool BWD>
 constexpr int kDepth = NC == 1 ? (BWD ? 2 : 3) : NC == 2 && !BWD ? 2 : 1;
 
 template <typename T, int E, int TPR, int NC, bool KEEP>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_fwd_kernel(const GatedArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) gated_fwd_kernel(const GatedArgs a) {
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC, false>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
@@ -170,10 +159,9 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_fwd_kernel(const
     const float inv_d = 1.f / a.D;
     int row = blockIdx.x * RPC + group, turn = 0;
     Place at(a, row, step);   // of the next row to load
-    long long e = at.e, b = at.b;
     Row<T, E, NC, false, false> ring[D];
 #pragma unroll
-    for (int k = 0; k < D; ++k, at.next()) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
+    for (int k = 0; k < D; ++k, at.next(a)) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
     float w[NC <= 2 ? NC : 1][E];
     if constexpr (NC <= 2) {
 #pragma unroll
@@ -182,7 +170,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_fwd_kernel(const
     }
     while (row - group < rows) {
 #pragma unroll
-        for (int k = 0; k < D; ++k, row += step, e += at.de, b += at.db, ++turn) {
+        for (int k = 0; k < D; ++k, row += step, ++turn) {
             if (row - group >= rows) break;   // alike in the whole CTA
             float v[NC][E], g[NC][E];
             float2 sum = make_float2(0.f, 0.f);
@@ -193,10 +181,11 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_fwd_kernel(const
                 vdot(sum, v[i], v[i]);
             }
             ring[k].template load<TPR>(a, at, row + D * step, rows, lane);
-            at.next();
+            at.next(a);
             sum.x += sum.y;
             sum = row_sum<TPR, false>(sum, red, turn, W);
             const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
+            const long long e = (long long)row * a.D, b = (long long)row * blocks_of(a.D);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = (i * TPR + lane) * E;
@@ -225,7 +214,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_fwd_kernel(const
 }
 
 template <typename T, int E, int TPR, int NC, bool Q8>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_bwd_kernel(const GatedArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) gated_bwd_kernel(const GatedArgs a) {
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC, true>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
@@ -235,13 +224,12 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_bwd_kernel(const
     if (NC == 1 && lane * E < a.D) a.w.get(lane * E, w1);
     int row = blockIdx.x * RPC + group, turn = 0;
     Place at(a, row, step);
-    long long e = at.e;
     Row<T, E, NC, true, Q8> ring[D];
 #pragma unroll
-    for (int k = 0; k < D; ++k, at.next()) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
+    for (int k = 0; k < D; ++k, at.next(a)) ring[k].template load<TPR>(a, at, row + k * step, rows, lane);
     while (row - group < rows) {
 #pragma unroll
-        for (int k = 0; k < D; ++k, row += step, e += at.de, ++turn) {
+        for (int k = 0; k < D; ++k, row += step, ++turn) {
             if (row - group >= rows) break;   // alike in the whole CTA
             float2 s2 = make_float2(0.f, 0.f), sn = s2;   // sums of x^2 and of dn x
             float v[NC][E], y[NC][E], s[NC][E], wds[NC][E], dn[NC][E];
@@ -264,10 +252,11 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, 1) gated_bwd_kernel(const
                 vdot(sn, dn[i], v[i]);
             }
             ring[k].template load<TPR>(a, at, row + D * step, rows, lane);
-            at.next();
+            at.next(a);
             const float2 sum = row_sum<TPR, true>(make_float2(s2.x + s2.y, sn.x + sn.y), red, turn, W);
             const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
             const float m = inv * inv * sum.y * inv_d;
+            const long long e = (long long)row * a.D;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = (i * TPR + lane) * E;

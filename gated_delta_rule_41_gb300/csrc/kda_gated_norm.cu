@@ -145,10 +145,11 @@ struct Row {
 };
 
 // Rows on their way while one is worked on, in registers: 32 to 48 bytes a thread and row are too
-// few in flight with one (gated_fwd of 32768 x 16 x 128 with copies in 8 bits: 109 us, with three
-// 96 us).
+// few in flight with one.  (32768 x 16 x 128 bf16: forward with 8-bit copies 109 us with one and 91
+// with three; backward from them 114 us with one at three CTAs per SM, 116 with two and 107 with three at
+// two.)
 template <int NC, bool BWD>
-constexpr int kDepth = NC == 1 ? (BWD ? 2 : 3) : NC == 2 && !BWD ? 2 : 1;
+constexpr int kDepth = NC == 1 ? 3 : NC == 2 && !BWD ? 2 : 1;
 
 template <typename T, int E, int TPR, int NC, bool KEEP>
 __global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) gated_fwd_kernel(const GatedArgs a) {
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) gated_fw
 }
 
 template <typename T, int E, int TPR, int NC, bool Q8>
-__global__ void __launch_bounds__(Rows<TPR>::kThreads, Rows<TPR>::kMin) gated_bwd_kernel(const GatedArgs a) {
+__global__ void __launch_bounds__(Rows<TPR>::kThreads, NC == 1 && TPR <= 256 ? 2 : Rows<TPR>::kMin) gated_bwd_kernel(const GatedArgs a) {
     constexpr int RPC = Rows<TPR>::kRows, W = Rows<TPR>::kThreads / 32, D = kDepth<NC, true>;
     __shared__ float2 red[TPR > 32 ? 2 * W : 1];
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;

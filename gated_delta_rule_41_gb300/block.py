@@ -97,10 +97,25 @@ def _here(*tensors):
     """The kernels run on the current device: so must their tensors be."""
     dev = torch.cuda.current_device() if _get_device is None else _get_device()
     for t in tensors:
-        if isinstance(t, Packed8):
-            t = t.codes
-        if isinstance(t, torch.Tensor) and t.get_device() != dev:
+        if t is not None and t.get_device() != dev:
             raise KdaError(1, "tensors must be CUDA tensors on the current device")
+
+
+# What was found right and made for calls of these sizes, strides and types: a small call's time
+# is the host's.
+_plans = {}
+
+
+def _plan(key, make):
+    if len(_plans) >= 1024:
+        _plans.clear()
+    got = _plans[key] = make()
+    return got
+
+
+def _like(w):
+    """What a plan knows of an optional tensor."""
+    return None if w is None else (w.shape, w.stride(), w.dtype)
 
 
 def _dense(name, t, shape, dtype=None):
@@ -185,7 +200,7 @@ def pack8(x, out: Optional[Packed8] = None, stream=None) -> Packed8:
     neighbours share the smallest 2^e with max |x| <= 448 * 2^e, so a value is
     off by 2^-4 of itself at most (or 2^-10 of 2^e).  Infinities and NaN become
     NaN."""
-    _here(x, out)
+    _here(x, None if out is None else out.codes)
     lib, t = _lib(), _code("x", x)
     if not x.is_cuda or x.dim() < 1 or x.shape[-1] < 1:
         raise KdaError(1, "x must be a CUDA tensor [..., D]")
@@ -202,12 +217,14 @@ def pack8(x, out: Optional[Packed8] = None, stream=None) -> Packed8:
 def unpack8(p: Packed8, dtype=torch.bfloat16, out=None, stream=None):
     """The values that ``p`` stands for, in bf16 (which holds them exactly) or
     fp32."""
-    _here(p, out)
-    lib = _lib()
-    D = p.shape[-1]
-    out = _out(out, p.shape, dtype, p.codes, stream)
-    _raise(lib.kda_unpack8(p.codes.data_ptr(), p.scales.data_ptr(), p.codes.numel() // max(D, 1), D,
-                           out.data_ptr(), _code("out", out), _raw_stream(stream)), "kda_unpack8")
+    _here(p.codes, out)
+    codes = p.codes
+    out = _out(out, codes.shape, dtype, codes, stream)
+    D = codes.shape[-1]
+    st = _lib().kda_unpack8(codes.data_ptr(), p.scales.data_ptr(), codes.numel() // max(D, 1), D,
+                            out.data_ptr(), _code("out", out), _raw_stream(stream))
+    if st:
+        _raise(st, "kda_unpack8")
     return out
 
 
@@ -294,22 +311,27 @@ def gated_scan_step(x, g, state, tied=False, new_state=None, out=None, stream=No
     in place (or left, where ``new_state`` takes the new one).  Returns o
     [B, C]."""
     _here(x, g, state, new_state, out)
-    lib = _lib()
+    key = ("step", x.shape, x.stride(), x.dtype, g.shape, g.stride(), g.dtype, tied)
+    d = _plans.get(key) or _plan(key, lambda: _step_dims(x, g, tied))
+    h = _dense("state", state, x.shape, torch.float32)
+    to = h if new_state is None else _dense("new_state", new_state, x.shape, torch.float32)
+    out = _out(out, x.shape, x.dtype, x, stream)
+    st = _lib().kda_gated_scan_step(d, x.data_ptr(), g.data_ptr(), h, to, out.data_ptr(),
+                                    _raw_stream(stream))
+    if st:
+        _raise(st, "kda_gated_scan_step")
+    return out
+
+
+def _step_dims(x, g, tied):
     if x.dim() != 2 or g.shape != x.shape or g.dtype != x.dtype:
         raise KdaError(1, "x and g must be tensors [B, C] of one type")
     for n, t in (("x", x), ("g", g)):
-        if not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1):
-            raise KdaError(1, f"{n} must be a CUDA tensor with contiguous channels")
+        if t.stride(1) != 1 and t.shape[1] > 1:
+            raise KdaError(1, f"{n} must have contiguous channels")
     B, C = x.shape
-    d = KdaScanDims(B, 1, C, _code("x", x), int(bool(tied)), x.stride(0), C, g.stride(0), C)
-    h = _dense("state", state, x.shape, torch.float32)
-    if h is None:
-        raise KdaError(1, "state must be a float32 CUDA tensor [B, C]")
-    to = h if new_state is None else _dense("new_state", new_state, x.shape, torch.float32)
-    out = _out(out, x.shape, x.dtype, x, stream)
-    _raise(lib.kda_gated_scan_step(d, x.data_ptr(), g.data_ptr(), h, to, out.data_ptr(),
-                                   _raw_stream(stream)), "kda_gated_scan_step")
-    return out
+    return ctypes.pointer(KdaScanDims(B, 1, C, _code("x", x), int(bool(tied)), x.stride(0), C,
+                                      g.stride(0), C))
 
 
 # ---- the norms ----
@@ -344,17 +366,24 @@ def gated_norm_fwd(x, gate, weight=None, eps=1e-5, act="sigmoid", keep8=False, o
     ``keep8`` (y, x, gate) with the inputs as ``Packed8`` for
     ``gated_norm_bwd``."""
     _here(x, gate, weight, out)
-    lib = _lib()
-    if x.dim() != 3 or gate.dtype != x.dtype:
-        raise KdaError(1, "x and gate must be tensors [T, H, D] of one type")
-    d = _gated_dims(x, gate, weight, _code("x", x), eps, act)
-    w = _vector("weight", weight, x.shape[2])
+    key = ("gated", x.shape, x.stride(), x.dtype, gate.shape, gate.stride(), gate.dtype, _like(weight),
+           eps, act)
+    d = _plans.get(key) or _plan(key, lambda: _gated_fwd_dims(x, gate, weight, eps, act))
     y = _out(out, x.shape, x.dtype, x, stream)
     kept = [Packed8.empty(x.shape, x.device, stream) for _ in range(2)] if keep8 else []
-    ptrs = [t.data_ptr() for p in kept for t in (p.codes, p.scales)] or [None] * 4
-    _raise(lib.kda_gated_norm_fwd(d, x.data_ptr(), gate.data_ptr(), w, y.data_ptr(), *ptrs,
-                                  _raw_stream(stream)), "kda_gated_norm_fwd")
+    ptrs = [t.data_ptr() for p in kept for t in (p.codes, p.scales)] or (None,) * 4
+    st = _lib().kda_gated_norm_fwd(d, x.data_ptr(), gate.data_ptr(), _at(weight), y.data_ptr(), *ptrs,
+                                   _raw_stream(stream))
+    if st:
+        _raise(st, "kda_gated_norm_fwd")
     return (y, *kept) if keep8 else y
+
+
+def _gated_fwd_dims(x, gate, weight, eps, act):
+    if x.dim() != 3 or gate.dtype != x.dtype:
+        raise KdaError(1, "x and gate must be tensors [T, H, D] of one type")
+    _vector("weight", weight, x.shape[2])
+    return ctypes.pointer(_gated_dims(x, gate, weight, _code("x", x), eps, act))
 
 
 def _workspace(need, workspace, like, stream):
@@ -367,13 +396,14 @@ def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None,
     """Backward of ``gated_norm_fwd``: dict dx, dgate (dy's type), dw (float32).
     x and gate as given to the forward pass, or both as the ``Packed8`` that it
     kept; then the gradients are those at the values that these stand for."""
-    _here(x, gate, weight, dy, workspace)
-    lib = _lib()
-    if len(x.shape) != 3 or gate.shape != x.shape:
-        raise KdaError(1, "x and gate must be [T, H, D]")
     packed = isinstance(x, Packed8)
     if packed != isinstance(gate, Packed8):
         raise KdaError(1, "x and gate must both be Packed8, or neither")
+    src = (x.codes, x.scales, gate.codes, gate.scales) if packed else (x, None, gate, None)
+    _here(*src, weight, dy, workspace)
+    lib = _lib()
+    if len(x.shape) != 3 or gate.shape != x.shape:
+        raise KdaError(1, "x and gate must be [T, H, D]")
     if not packed and (x.dtype != dy.dtype or gate.dtype != dy.dtype):
         raise KdaError(1, "x, gate and dy must have one type")
     d = _gated_dims(x, gate, weight, _code("dy", dy), eps, act)
@@ -387,7 +417,6 @@ def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None,
           _dense("dw", grads.get("dw"), (D,), torch.float32))
     need = int(lib.kda_gated_norm_workspace_bytes(d)) if to[2] is not None else 0
     ws = _workspace(need, workspace, dy, stream)
-    src = (x.codes, x.scales, gate.codes, gate.scales) if packed else (x, None, gate, None)
     _raise(lib.kda_gated_norm_bwd(d, *(_at(t) for t in src), w, up, *to, ws.data_ptr(), need,
                                   _raw_stream(stream)), "kda_gated_norm_bwd")
     return grads
@@ -424,16 +453,21 @@ def add_norm_fwd(residual, x, weight=None, alpha=None, eps=1e-5, out=None, out_r
     alone).  The residual stream may be fp32 beside bf16 x.  Returns (r, y);
     ``out_residual`` may be ``residual`` itself.  (y is of x's type, without x
     of ``out``'s or the residual's.)"""
-    _here(residual, x, weight, alpha, out, out_residual)
-    lib = _lib()
+    _here(residual, x, weight, alpha if isinstance(alpha, torch.Tensor) else None, out, out_residual)
     like = x if x is not None else out if out is not None else residual
-    d, w, av = _add_dims(residual, x, weight, alpha, _code("x", like), eps)
+    vec = isinstance(alpha, torch.Tensor)
+    key = ("add", residual.shape, residual.stride(), residual.dtype, _like(x), _like(weight),
+           _like(alpha) if vec else alpha, like.dtype, eps)
+    d = _plans.get(key) or _plan(key, lambda: ctypes.pointer(
+        _add_dims(residual, x, weight, alpha, _code("x", like), eps)[0]))
     y = _out(out, residual.shape, like.dtype, residual, stream)
     r = out_residual
     if x is not None or r is not None:
         r = _out(r, residual.shape, residual.dtype, residual, stream, "out_residual")
-    _raise(lib.kda_add_norm_fwd(d, residual.data_ptr(), _at(x), av, w, _at(r), y.data_ptr(),
-                                _raw_stream(stream)), "kda_add_norm_fwd")
+    st = _lib().kda_add_norm_fwd(d, residual.data_ptr(), _at(x), alpha.data_ptr() if vec else None,
+                                 _at(weight), _at(r), y.data_ptr(), _raw_stream(stream))
+    if st:
+        _raise(st, "kda_add_norm_fwd")
     return (residual if r is None else r), y
 
 
@@ -444,7 +478,7 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     Returns dict dres (of the residual that went in), dx = alpha dres, dw and
     dalpha (float32; dalpha for a vector alpha, which needs the forward's x).
     Without alpha, and in one type, dx is the tensor dres itself."""
-    _here(residual, weight, dy, dres, x, alpha, workspace)
+    _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace)
     lib = _lib()
     d, w, av = _add_dims(residual, x, weight, alpha, _code("dy", dy), eps)
     T, D = residual.shape

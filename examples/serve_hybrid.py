@@ -4,8 +4,9 @@ samples forked from one prompt, ended sequences released and the cache
 compacted.
 
 Every sequence-mixing step runs in the library: the chunk scan and the decode
-step of the KDA layers, the paged key-value cache of the others.  The
-projections around them are plain matrix products.
+step of the KDA layers with the norm and gate of their outputs, the paged
+key-value cache of the others, and the residual sums with the norms between
+layers.  The projections around them are plain matrix products.
 
     python examples/serve_hybrid.py [--layers 8] [--steps 32] [--cache e4m3]
 """
@@ -51,7 +52,8 @@ class Hybrid:
             n = heads * head
             if i % 4 != 3:
                 self.layers.append(dict(kind="kda", qkv=w(width, 3 * n), g=w(width, n),
-                                        beta=w(width, heads), out=w(n, width),
+                                        beta=w(width, heads), out=w(n, width), z=w(width, n),
+                                        norm=torch.ones(head, device="cuda"),
                                         state=torch.zeros(rows, heads, head, head, device="cuda")))
             else:
                 t = BF16 if cache == "bf16" else torch.float8_e4m3fn
@@ -72,9 +74,19 @@ class Hybrid:
         first = next(l for l in self.layers if l["kind"] == "attn")["kv"]
         self.ws = kda.paged_decode_workspace(first, rows, heads)
 
-    def _norm(self, x):
-        x = x.float()
-        return (x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)).to(BF16)
+    def _gated(self, l, o, y):
+        """The norm of a KDA layer's output with its gate, per head."""
+        z = (y @ l["z"]).view(-1, self.H, self.D)
+        return kda.gated_norm_fwd(o.reshape(z.shape), z, l["norm"], eps=1e-6)
+
+    def _run(self, x, mix):
+        """The layers on token embeddings: each mixes the norm of the residual stream and adds
+        to it; ``mix(layer, y)`` gives a layer's heads.  Returns the norm of the stream behind the last."""
+        x, y = kda.add_norm_fwd(x, None, eps=1e-6)
+        for l in self.layers:
+            o = mix(l, y)
+            x, y = kda.add_norm_fwd(x, o.reshape(x.shape[0], -1) @ l["out"], eps=1e-6, out_residual=x)
+        return y
 
     def _kda_inputs(self, l, x):
         n, H, D = x.shape[0], self.H, self.D
@@ -96,20 +108,20 @@ class Hybrid:
         ids = torch.tensor([t for i in order for t in tokens[i]], device="cuda")
         cu = ints(cu)
         self.book.extend(ints(add), self.table, self.lens, self.refs, granted=self.granted)
-        x = self.emb[ids]
-        for l in self.layers:
-            y = self._norm(x)
-            if l["kind"] == "kda":
-                q, k, v, g, beta = (t[None] for t in self._kda_inputs(l, y))
-                o, ht = kda.chunk_kda_fwd_varlen(q, k, v, g, beta, cu, output_final_state=True,
-                                                 use_qk_l2norm_in_kernel=True)
-                rows = torch.tensor(slots, device="cuda")
-                l["state"][rows] = ht[rows]
-            else:
-                o = self._attend(l, y, cu)
-            x = x + o.reshape(len(ids), -1) @ l["out"]
+
+        def mix(l, y):
+            if l["kind"] == "attn":
+                return self._attend(l, y, cu)
+            q, k, v, g, beta = (t[None] for t in self._kda_inputs(l, y))
+            o, ht = kda.chunk_kda_fwd_varlen(q, k, v, g, beta, cu, output_final_state=True,
+                                             use_qk_l2norm_in_kernel=True)
+            rows = torch.tensor(slots, device="cuda")
+            l["state"][rows] = ht[rows]
+            return self._gated(l, o[0], y)
+
+        y = self._run(self.emb[ids], mix)
         last = torch.tensor([sum(add[:s]) + add[s] - 1 for s in slots], device="cuda")
-        return self._norm(x[last]).float() @ self.emb.float().T
+        return y[last].float() @ self.emb.float().T
 
     def _attend(self, l, y, cu=None):
         H, HKV, D = self.H, self.HKV, self.D
@@ -123,16 +135,14 @@ class Hybrid:
     def step(self, ids):
         """One token for each row (idle rows go along); logits [rows, vocab]."""
         self.book.extend(1, self.table, self.lens, self.refs, granted=self.granted)
-        x = self.emb[ids]
-        for l in self.layers:
-            y = self._norm(x)
-            if l["kind"] == "kda":
-                o = kda.recurrent_step(*self._kda_inputs(l, y), l["state"],
-                                       use_qk_l2norm_in_kernel=True)
-            else:
-                o = self._attend(l, y)
-            x = x + o.reshape(self.rows, -1) @ l["out"]
-        return self._norm(x).float() @ self.emb.float().T
+
+        def mix(l, y):
+            if l["kind"] == "attn":
+                return self._attend(l, y)
+            o = kda.recurrent_step(*self._kda_inputs(l, y), l["state"], use_qk_l2norm_in_kernel=True)
+            return self._gated(l, o, y)
+
+        return self._run(self.emb[ids], mix).float() @ self.emb.float().T
 
     def fork(self, parents, children):
         p, c = ints(parents), ints(children)

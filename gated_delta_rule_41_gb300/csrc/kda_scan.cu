@@ -817,11 +817,21 @@ bool prepare(Setup& s, K kernel, size_t smem) {
     s.ready.store(true, std::memory_order_release);
     return true;
 }
-// CTAs of a cluster: as many as still let all slabs run at once, and find tiles.
+// CTAs of a cluster: a turn takes about as long whatever their number (2.2 us forward), so the
+// size with the fewest turns one after the other, over all the rounds that the slabs need.  (Five batch
+// entries of 8192 x 2048, 160 slabs: 64 turns of single CTAs, 39 of clusters of five.)
 int cluster_of(const Setup& s, long long slabs, int T) {
     const int tiles = (T + kTile - 1) / kTile;
-    int K = tiles < kMaxCluster ? tiles : kMaxCluster;
-    while (K > 1 && s.clusters[K] < slabs) --K;
+    long long best = -1;
+    int K = 1;
+    for (int k = 1; k <= kMaxCluster && k <= tiles; ++k) {
+        if (s.clusters[k] < 1) continue;
+        const long long turns = (slabs + s.clusters[k] - 1) / s.clusters[k] * ((tiles + k - 1) / k);
+        if (best < 0 || turns < best) {
+            best = turns;
+            K = k;
+        }
+    }
     return K;
 }
 

@@ -522,13 +522,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 if (TIED) u2 = remainder(d2, k2, u2);
 #pragma unroll
                 for (int i = p; i < p + S; ++i) {
-                    const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p);
-                    if (M && (marks.firsts >> i & 1)) {   // what enters the run ends here
+                    const V<N> d = part<N>(d2, i - p), k = part<N>(k2, i - p), u = part<N>(u2, i - p);
+                    if (M) {
+                        P[i] = d;   // (the tests below would keep these, too, in order)
+                        h[i] = u;
+                    } else {
+                        m.H = advance(d, k, m.H, u);
+                        m.A = decayed(d, k, m.A);
+                        h[i] = m.H;
+                        P[i] = m.A;
+                    }
+                }
+            }
+            if constexpr (M) {
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    if (marks.firsts >> i & 1) {   // what enters the run ends here
                         m.H = first_state(i);
                         m.A = all<N>(0.f);
                     }
-                    m.H = advance(d, k, m.H, part<N>(u2, i - p));
-                    m.A = decayed(d, k, m.A);
+                    const V<N> k = kept(P[i]);
+                    m.H = advance(P[i], k, m.H, h[i]);
+                    m.A = decayed(P[i], k, m.A);
                     h[i] = m.H;
                     P[i] = m.A;
                 }
@@ -683,8 +698,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
                 for (int i = p; i < p + S; ++i) {
                     d[i] = part<N>(d2, i - p);
                     const V<N> k = part<N>(k2, i - p);
-                    if (M && (marks.firsts >> i & 1)) m.H = first_state(i);
+                    if (M) continue;   // (the tests below would keep the decays, too, in order)
                     m.H = advance(d[i], k, m.H, part<N>(u2, i - p));
+                    m.A = decayed(d[i], k, m.A);
+                }
+            }
+            if constexpr (M) {
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    const V<N> k = kept(d[i]), xv = Lane<T>::get(xs[i * 32]);
+                    if (marks.firsts >> i & 1) m.H = first_state(i);
+                    m.H = advance(d[i], k, m.H, TIED ? remainder(d[i], k, xv) : xv);
                     m.A = decayed(d[i], k, m.A);
                 }
             }

@@ -231,14 +231,19 @@ def unpack8(p: Packed8, dtype=torch.bfloat16, out=None, stream=None):
 # ---- the gated recurrence ----
 
 def _scan(x, g, tied):
+    key = ("scan", x.shape, x.stride(), x.dtype, g.shape, g.stride(), g.dtype, tied)
+    return _plans.get(key) or _plan(key, lambda: _scan_dims(x, g, tied))
+
+
+def _scan_dims(x, g, tied):
     if x.dim() != 3 or g.shape != x.shape or g.dtype != x.dtype:
         raise KdaError(1, "x and g must be tensors [B, T, C] of one type")
     for n, t in (("x", x), ("g", g)):
-        if not t.is_cuda or (t.stride(2) != 1 and t.shape[2] > 1):
-            raise KdaError(1, f"{n} must be a CUDA tensor with contiguous channels")
+        if t.stride(2) != 1 and t.shape[2] > 1:
+            raise KdaError(1, f"{n} must have contiguous channels")
     B, T, C = x.shape
-    return KdaScanDims(B, T, C, _code("x", x), int(bool(tied)), x.stride(0), x.stride(1),
-                       g.stride(0), g.stride(1))
+    return ctypes.pointer(KdaScanDims(B, T, C, _code("x", x), int(bool(tied)), x.stride(0), x.stride(1),
+                                      g.stride(0), g.stride(1)))
 
 
 def _scan_seqs(x, cu_seqlens):
@@ -262,7 +267,7 @@ def gated_scan_fwd(x, g, initial_state=None, output_final_state=False, tied=Fals
     lib, d = _lib(), _scan(x, g, tied)
     cu, n, rows = _scan_seqs(x, cu_seqlens)
     B, T, C = x.shape
-    h0 = _dense("initial_state", initial_state, (rows, C), torch.float32)
+    h0 = None if initial_state is None else _dense("initial_state", initial_state, (rows, C), torch.float32)
     out = _out(out, x.shape, x.dtype, x, stream)
     if output_final_state:
         final_state = _out(final_state, (rows, C), torch.float32, x, stream, "final_state")
@@ -271,9 +276,10 @@ def gated_scan_fwd(x, g, initial_state=None, output_final_state=False, tied=Fals
     saved = None
     if save_for_backward:
         saved = _fresh(stream, (B, -(-T // STATE_EVERY), C), torch.float32, x.device)
-    _raise(lib.kda_gated_scan_fwd(d, cu, n, x.data_ptr(), g.data_ptr(), h0, out.data_ptr(),
-                                  _at(final_state), _at(saved), _raw_stream(stream)),
-           "kda_gated_scan_fwd")
+    st = lib.kda_gated_scan_fwd(d, cu, n, x.data_ptr(), g.data_ptr(), h0, out.data_ptr(),
+                                _at(final_state), _at(saved), _raw_stream(stream))
+    if st:
+        _raise(st, "kda_gated_scan_fwd")
     return (out, final_state, saved) if save_for_backward else (out, final_state)
 
 
@@ -402,24 +408,32 @@ def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None,
     src = (x.codes, x.scales, gate.codes, gate.scales) if packed else (x, None, gate, None)
     _here(*src, weight, dy, workspace)
     lib = _lib()
-    if len(x.shape) != 3 or gate.shape != x.shape:
-        raise KdaError(1, "x and gate must be [T, H, D]")
-    if not packed and (x.dtype != dy.dtype or gate.dtype != dy.dtype):
-        raise KdaError(1, "x, gate and dy must have one type")
-    d = _gated_dims(x, gate, weight, _code("dy", dy), eps, act)
+    key = ("gated_bwd", packed, src[0].shape, src[0].stride(), src[0].dtype, src[2].shape, src[2].stride(),
+           src[2].dtype, _like(weight), dy.dtype, eps, act)
+    d, need = _plans.get(key) or _plan(key, lambda: _gated_bwd_dims(x, gate, weight, dy, eps, act, packed))
     D = x.shape[2]
-    w, up = _vector("weight", weight, D), _dense("dy", dy, x.shape)
+    w, up = _at(weight), _dense("dy", dy, x.shape)
     if grads is None:
         grads = dict(dx=_fresh(stream, x.shape, dy.dtype, dy.device),
                      dgate=_fresh(stream, x.shape, dy.dtype, dy.device),
                      dw=None if weight is None else _fresh(stream, (D,), torch.float32, dy.device))
     to = (_dense("dx", grads["dx"], x.shape, dy.dtype), _dense("dgate", grads["dgate"], x.shape, dy.dtype),
           _dense("dw", grads.get("dw"), (D,), torch.float32))
-    need = int(lib.kda_gated_norm_workspace_bytes(d)) if to[2] is not None else 0
+    need = need if to[2] is not None else 0
     ws = _workspace(need, workspace, dy, stream)
     _raise(lib.kda_gated_norm_bwd(d, *(_at(t) for t in src), w, up, *to, ws.data_ptr(), need,
                                   _raw_stream(stream)), "kda_gated_norm_bwd")
     return grads
+
+
+def _gated_bwd_dims(x, gate, weight, dy, eps, act, packed):
+    if len(x.shape) != 3 or gate.shape != x.shape:
+        raise KdaError(1, "x and gate must be [T, H, D]")
+    if not packed and (x.dtype != dy.dtype or gate.dtype != dy.dtype):
+        raise KdaError(1, "x, gate and dy must have one type")
+    _vector("weight", weight, x.shape[2])
+    d = ctypes.pointer(_gated_dims(x, gate, weight, _code("dy", dy), eps, act))
+    return d, int(_lib().kda_gated_norm_workspace_bytes(d))
 
 
 def _tokens2(name, t, T, D):
@@ -471,6 +485,16 @@ def add_norm_fwd(residual, x, weight=None, alpha=None, eps=1e-5, out=None, out_r
     return (residual if r is None else r), y
 
 
+def _add_bwd_dims(residual, weight, dy, x, alpha, eps):
+    d, _, av = _add_dims(residual, x, weight, alpha, _code("dy", dy), eps)
+    if av is not None and x is None:
+        raise KdaError(1, "a vector alpha needs x")
+    if x is not None and x.dtype != dy.dtype:
+        raise KdaError(1, "x and dy must have one type")
+    d = ctypes.pointer(d)
+    return d, int(_lib().kda_add_norm_workspace_bytes(d))
+
+
 def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, workspace=None,
                  grads=None, stream=None):
     """Backward of ``add_norm_fwd``.  ``residual`` is the r that it returned,
@@ -480,12 +504,12 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     Without alpha, and in one type, dx is the tensor dres itself."""
     _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace)
     lib = _lib()
-    d, w, av = _add_dims(residual, x, weight, alpha, _code("dy", dy), eps)
-    T, D = residual.shape
-    if av is not None and x is None:
-        raise KdaError(1, "a vector alpha needs x")
-    if x is not None and x.dtype != dy.dtype:
-        raise KdaError(1, "x and dy must have one type")
+    vec = isinstance(alpha, torch.Tensor)
+    key = ("add_bwd", residual.shape, residual.stride(), residual.dtype, _like(x), _like(weight),
+           _like(alpha) if vec else alpha, dy.dtype, eps)
+    d, need = _plans.get(key) or _plan(key, lambda: _add_bwd_dims(residual, weight, dy, x, alpha, eps))
+    D = residual.shape[1]
+    w, av = _at(weight), alpha.data_ptr() if vec else None
     at = _dense("dy", dy, residual.shape), _dense("dres", dres, residual.shape, residual.dtype)
     if grads is None:
         one = alpha is None and dy.dtype == residual.dtype
@@ -501,7 +525,7 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
           _dense("dalpha", grads.get("dalpha"), (D,), torch.float32))
     if to[3] is not None and x is None:
         raise KdaError(1, "dalpha needs x")
-    need = int(lib.kda_add_norm_workspace_bytes(d)) if to[2] is not None or to[3] is not None else 0
+    need = need if to[2] is not None or to[3] is not None else 0
     ws = _workspace(need, workspace, dy, stream)
     _raise(lib.kda_add_norm_bwd(d, residual.data_ptr(), _at(x), av, w, *at, *to, ws.data_ptr(), need,
                                 _raw_stream(stream)), "kda_add_norm_bwd")

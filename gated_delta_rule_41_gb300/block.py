@@ -200,7 +200,7 @@ def pack8(x, out: Optional[Packed8] = None, stream=None) -> Packed8:
     neighbours share the smallest 2^e with max |x| <= 448 * 2^e, so a value is
     off by 2^-4 of itself at most (or 2^-10 of 2^e).  Infinities and NaN become
     NaN."""
-    _here(x, None if out is None else out.codes)
+    _here(x, *(() if out is None else (out.codes, out.scales)))
     lib, t = _lib(), _code("x", x)
     if not x.is_cuda or x.dim() < 1 or x.shape[-1] < 1:
         raise KdaError(1, "x must be a CUDA tensor [..., D]")
@@ -217,7 +217,7 @@ def pack8(x, out: Optional[Packed8] = None, stream=None) -> Packed8:
 def unpack8(p: Packed8, dtype=torch.bfloat16, out=None, stream=None):
     """The values that ``p`` stands for, in bf16 (which holds them exactly) or
     fp32."""
-    _here(p.codes, out)
+    _here(p.codes, p.scales, out)
     codes = p.codes
     out = _out(out, codes.shape, dtype, codes, stream)
     D = codes.shape[-1]
@@ -231,7 +231,7 @@ def unpack8(p: Packed8, dtype=torch.bfloat16, out=None, stream=None):
 # ---- the gated recurrence ----
 
 def _scan(x, g, tied):
-    key = ("scan", x.shape, x.stride(), x.dtype, g.shape, g.stride(), g.dtype, tied)
+    key = ("scan", x.shape, x.stride(), x.dtype, g.shape, g.stride(), g.dtype, bool(tied))
     return _plans.get(key) or _plan(key, lambda: _scan_dims(x, g, tied))
 
 
@@ -258,7 +258,7 @@ def gated_scan_fwd(x, g, initial_state=None, output_final_state=False, tied=Fals
                    save_for_backward=False, out=None, final_state=None, stream=None):
     """The gated linear recurrence h_t = exp(g_t) h_{t-1} + u_t x_t per channel,
     o_t = h_t, with u_t = 1, or 1 - exp(g_t) if ``tied``.  x, g [B, T, C] (bf16
-    or fp32; slices of a wider projection will do), g a log-decay.  Returns (o,
+    or fp32; slices of a wider projection will do), g a log-decay (<= 0).  Returns (o,
     final_state or None), plus the kept states when ``save_for_backward`` is
     set (pass them to ``gated_scan_bwd``).  ``initial_state`` and the final
     state are float32 [B, C]; with ``cu_seqlens`` (int32 [N + 1], B = 1) the
@@ -317,7 +317,7 @@ def gated_scan_step(x, g, state, tied=False, new_state=None, out=None, stream=No
     in place (or left, where ``new_state`` takes the new one).  Returns o
     [B, C]."""
     _here(x, g, state, new_state, out)
-    key = ("step", x.shape, x.stride(), x.dtype, g.shape, g.stride(), g.dtype, tied)
+    key = ("step", x.shape, x.stride(), x.dtype, g.shape, g.stride(), g.dtype, bool(tied))
     d = _plans.get(key) or _plan(key, lambda: _step_dims(x, g, tied))
     h = _dense("state", state, x.shape, torch.float32)
     to = h if new_state is None else _dense("new_state", new_state, x.shape, torch.float32)
@@ -400,6 +400,7 @@ def _workspace(need, workspace, like, stream):
 
 def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None, grads=None, stream=None):
     """Backward of ``gated_norm_fwd``: dict dx, dgate (dy's type), dw (float32).
+    (``workspace``, for dw: calls that may overlap need one each; without, a call makes its own.)
     x and gate as given to the forward pass, or both as the ``Packed8`` that it
     kept; then the gradients are those at the values that these stand for."""
     packed = isinstance(x, Packed8)
@@ -501,7 +502,8 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     ``dy`` the gradient of y, ``dres`` that of r from what else reads it.
     Returns dict dres (of the residual that went in), dx = alpha dres, dw and
     dalpha (float32; dalpha for a vector alpha, which needs the forward's x).
-    Without alpha, and in one type, dx is the tensor dres itself."""
+    Without alpha, and in one type, dx is the tensor dres itself.  (``workspace`` as for
+    ``gated_norm_bwd``.)"""
     _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace)
     lib = _lib()
     vec = isinstance(alpha, torch.Tensor)

@@ -484,8 +484,11 @@ kda_status kda_pages_copy(const kda_page_pool* pools, int num_pools, int num_pag
  *
  * with u_t = 1, or with `tied` u_t = 1 - exp(g_t) (the state is then a mean of
  * the inputs).  g is a log-decay as in the KDA scan, one per channel, not
- * clamped; -inf forgets the state.  The states advance in float32 from token
- * to token, with a decay near one held as its small distance from one. */
+ * clamped; -inf forgets a (finite) state, and a decay below 2^-126 counts as 2^-126.  Values
+ * above 0 are not supported (products of growth over runs of tokens may overflow where no
+ * state does).  The states advance in float32 from token to token, with a decay near
+ * one held as its small distance from one; the tokens of a tile are combined as maps h -> A h + H.
+ * An infinity or NaN stays in its channel and its sequence. */
 typedef struct {
     int B, T, C;          /* x, g, o [B][T][C] */
     kda_dtype dtype;      /* of x, g, o and their gradients */
@@ -500,7 +503,7 @@ typedef struct {
  * int32 [num_seqs + 1] (device) packs sequences along T, as in the varlen entry
  * points above: it must rise from 0 to T (kda_check reports KDA_ERR_SHAPE
  * otherwise; the call then leaves o and states alone and the final states are
- * the initial ones).
+ * the initial ones; with T == 0 it is not looked at).
  *   h0      initial states [B or num_seqs][C] f32, NULL: zeros.
  *   o       [B][T][C] (dtype), or NULL.
  *   ht      final states [B or num_seqs][C] f32, or NULL.  Of a sequence without
@@ -549,7 +552,7 @@ kda_status kda_gated_norm_fwd(const kda_gated_norm_dims* dims, const void* x, co
 
 /* Backward: dy, dx, dgate [T][H][D], dw [D] f32 (NULL: left out).  With x_scales and
  * gate_scales, x and gate are dense codes, and the gradients are those at the values
- * that the codes stand for.  The workspace is for dw. */
+ * that the codes stand for.  The workspace is for dw; calls that may overlap need one each. */
 size_t kda_gated_norm_workspace_bytes(const kda_gated_norm_dims* dims);
 kda_status kda_gated_norm_bwd(const kda_gated_norm_dims* dims, const void* x,
                               const unsigned char* x_scales, const void* gate,
@@ -578,7 +581,7 @@ kda_status kda_add_norm_fwd(const kda_add_norm_dims* dims, const void* r, const 
 /* Backward: r is the forward's r' (r_stride apart), dy the gradient of y, dr that of r' from
  * what else reads it (dense, or NULL); dres [T][D] the gradient of the forward's r, dx = alpha dres (NULL:
  * left out), dw, dalpha [D] f32 (NULL: left out; dalpha needs the forward's x).  dres may be
- * dr.  The workspace is for dw and dalpha. */
+ * dr.  The workspace is for dw and dalpha; calls that may overlap need one each. */
 size_t kda_add_norm_workspace_bytes(const kda_add_norm_dims* dims);
 kda_status kda_add_norm_bwd(const kda_add_norm_dims* dims, const void* r, const void* x,
                             const void* alpha, const void* w, const void* dy, const void* dr,

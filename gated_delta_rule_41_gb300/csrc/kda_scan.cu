@@ -824,36 +824,46 @@ struct Setup {
     std::atomic<bool> ready{false};
     std::mutex lock;
     int clusters[kMaxCluster + 1];
+    int alone[kMaxCluster + 1];   // with one CTA to an SM
 };
 template <typename K>
 bool prepare(Setup& s, K kernel, size_t smem) {
     if (s.ready.load(std::memory_order_acquire)) return true;
     std::lock_guard<std::mutex> hold(s.lock);
     if (s.ready.load(std::memory_order_relaxed)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+    constexpr size_t kAloneBytes = 120 * 1024;   // two of these do not fit an SM
+    static_assert(kAloneBytes >= (kBwdStages * 3) * kTileBytes + sizeof(Shared), "");
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAloneBytes) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return false;
-    for (int k = 1; k <= kMaxCluster; ++k) {
+    auto count = [&](int k, size_t bytes) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim = {(unsigned)k, 1, 1};
         cfg.gridDim = dim3(k);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = bytes;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&s.clusters[k], kernel, &cfg) != cudaSuccess) {
-            s.clusters[k] = 0;
-            cudaGetLastError();
-        }
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+        cudaGetLastError();
+        return 0;
+    };
+    for (int k = 1; k <= kMaxCluster; ++k) {
+        s.clusters[k] = count(k, smem);
+        s.alone[k] = count(k, kAloneBytes);   // (asked about, never launched)
     }
     s.ready.store(true, std::memory_order_release);
     return true;
 }
-// CTAs of a cluster: a turn takes about as long whatever their number (2.2 us forward), so the
-// size with the fewest turns one after the other, over all the rounds that the slabs need.  (Five batch
-// entries of 8192 x 2048, 160 slabs: 64 turns of single CTAs, 39 of clusters of five.)
+// CTAs of a cluster: the size with the least time for its turns one after the other, over all the
+// rounds that the slabs need.  A turn takes about 1.75 times as long where CTAs share an SM (forward
+// 1.3 us alone and 2.2 to 2.6 shared, backward 2.3 and 4.1), which they do not where the device has
+// room for all of them one to an SM.  (Times by size, the chosen last: 16 slabs of 65536 float32 tokens 124 us
+// with 6, 139 with 7, 90 with 13; 8 slabs of bf16 104 us with 16, 91 with 12; 160 slabs of 8192 tokens 138 us with
+// 1, 110 with 5.)
 int cluster_of(const Setup& s, long long slabs, int T) {
     const int tiles = (T + kTile - 1) / kTile;
     long long best = -1;
@@ -861,8 +871,9 @@ int cluster_of(const Setup& s, long long slabs, int T) {
     for (int k = 1; k <= kMaxCluster && k <= tiles; ++k) {
         if (s.clusters[k] < 1) continue;
         const long long turns = (slabs + s.clusters[k] - 1) / s.clusters[k] * ((tiles + k - 1) / k);
-        if (best < 0 || turns < best) {
-            best = turns;
+        const long long cost = turns * (slabs <= s.alone[k] ? 4 : 7);
+        if (best < 0 || cost < best) {
+            best = cost;
             K = k;
         }
     }

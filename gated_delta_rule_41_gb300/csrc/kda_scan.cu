@@ -133,9 +133,9 @@ __device__ __forceinline__ V<N> remainder(V<N> d, V<N> k, V<N> x) {
 // receiver's mbarrier: a cluster barrier would wait for the outputs' stores each time).
 //
 // What bounds it: 3 elements a step forward and 5 backward are the floor, but a turn of tiles takes
-// 2.2 us forward and 4.1 backward whether 208 or 304 CTAs run: issue (28 and 43 instructions an element,
-// 58 % of the issue slots) and the chain scan, barrier, combine, barrier.  With 304 CTAs busy that is
-// near HBM, with fewer it is not.  One GB300, in a graph:
+// 1.3 us forward and 2.3 backward with one CTA to an SM, 2.2 to 2.6 and 4.1 with two: the chain scan,
+// barrier, combine, barrier, and 21, 36 and (tied) 46 instructions an element at half of the
+// issue slots.  With 256 CTAs busy that is near HBM, with fewer it is not.  One GB300, in a graph:
 //   4 x 8192 x 2048 bf16      forward 81 us, 4.95 TB/s (0.74); backward 127 us, 5.3 TB/s (0.79), tied 160 us
 //   1 x 65536 x 512 float32   forward, tied 87 us, 4.6 TB/s (0.69; 16 slabs, clusters of 13)
 //   1 x 65536 x 1024 float32  forward, tied 132 us, 6.1 TB/s (0.91; 32 slabs, clusters of 8)

@@ -471,8 +471,8 @@ kda_status kda_pages_copy(const kda_page_pool* pools, int num_pools, int num_pag
  *           projection do.  The other tensors are dense.  Results may not
  *           overlap inputs but where that is said.
  * Alignment Pointers to their element size.  (Rows whose width and strides are
- *           multiples of 8 elements, at 16-byte aligned pointers, are moved by
- *           16-byte accesses, others element by element.)
+ *           multiples of 8 elements, or of 4, at 16-byte aligned pointers, are moved by
+ *           wide accesses, others element by element: three times as slow and more.)
  * Sizes     Fewer than 2^30 rows (tokens, or tokens times heads), at most 65535
  *           sequences or batch entries of a scan; rows of a norm at most 16384 wide; else
  *           KDA_ERR_UNSUPPORTED.  Offsets are 64-bit.

@@ -89,6 +89,13 @@ def _code(name, t):
         raise KdaError(3, f"{name}: {t.dtype} (bf16 or fp32 only)") from None
 
 
+def _sizes(shape):
+    """The C entries take 32-bit sizes."""
+    if any(n >= 1 << 31 for n in shape):
+        raise KdaError(3, f"sizes {tuple(shape)} (below 2^31 each)")
+    return shape
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -176,14 +183,15 @@ class Packed8:
 def _rows(name, x):
     """x as rows of one stride: (rows, width, stride).  A strided tensor's
     contiguous last dimensions count as one where blocks do not cross them."""
-    D = x.shape[-1]
+    D = _sizes(x.shape[-1:])[0]
     n = x.numel() // D if D else 0
     if x.is_contiguous():
         return n, D, D
     if x.stride(-1) == 1 or D == 1:
         dims = [(s, st) for s, st in zip(x.shape[:-1], x.stride()[:-1]) if s > 1]
         width = D
-        while D % SCALE_BLOCK == 0 and dims and dims[-1][1] == width:
+        while D % SCALE_BLOCK == 0 and dims and dims[-1][1] == width \
+                and width * dims[-1][0] < 1 << 31:
             width *= dims.pop()[0]
         run = dims[-1][1] if dims else width
         for s, st in reversed(dims):
@@ -219,8 +227,10 @@ def unpack8(p: Packed8, dtype=torch.bfloat16, out=None, stream=None):
     fp32."""
     _here(p.codes, p.scales, out)
     codes = p.codes
-    out = _out(out, codes.shape, dtype, codes, stream)
     D = codes.shape[-1]
+    if D >= 1 << 31:
+        _sizes(codes.shape[-1:])
+    out = _out(out, codes.shape, dtype, codes, stream)
     st = _lib().kda_unpack8(codes.data_ptr(), p.scales.data_ptr(), codes.numel() // max(D, 1), D,
                             out.data_ptr(), _code("out", out), _raw_stream(stream))
     if st:
@@ -241,7 +251,7 @@ def _scan_dims(x, g, tied):
     for n, t in (("x", x), ("g", g)):
         if t.stride(2) != 1 and t.shape[2] > 1:
             raise KdaError(1, f"{n} must have contiguous channels")
-    B, T, C = x.shape
+    B, T, C = _sizes(x.shape)
     return ctypes.pointer(KdaScanDims(B, T, C, _code("x", x), int(bool(tied)), x.stride(0), x.stride(1),
                                       g.stride(0), g.stride(1)))
 
@@ -335,7 +345,7 @@ def _step_dims(x, g, tied):
     for n, t in (("x", x), ("g", g)):
         if t.stride(1) != 1 and t.shape[1] > 1:
             raise KdaError(1, f"{n} must have contiguous channels")
-    B, C = x.shape
+    B, C = _sizes(x.shape)
     return ctypes.pointer(KdaScanDims(B, 1, C, _code("x", x), int(bool(tied)), x.stride(0), C,
                                       g.stride(0), C))
 
@@ -356,7 +366,7 @@ def _heads(name, t, shape):
 def _gated_dims(x, gate, weight, dtype, eps, act):
     if act not in GATES:
         raise KdaError(1, f"gate {act!r} (sigmoid or silu)")
-    T, H, D = x.shape
+    T, H, D = _sizes(x.shape)
     packed = isinstance(x, Packed8)
     return KdaGatedNormDims(
         T, H, D, dtype, KDA_BF16 if weight is not None and weight.dtype == torch.bfloat16 else KDA_F32,
@@ -447,7 +457,7 @@ def _tokens2(name, t, T, D):
 def _add_dims(residual, x, weight, alpha, dtype, eps):
     if residual.dim() != 2:
         raise KdaError(1, "residual must be a tensor [T, D]")
-    T, D = residual.shape
+    T, D = _sizes(residual.shape)
     vec = isinstance(alpha, torch.Tensor)
     w = _vector("weight", weight, D)
     av = _vector("alpha", alpha, D) if vec else None

@@ -153,6 +153,22 @@ def test_pack(lib):
     assert unpack(rows=-1) == 2 and unpack(rows=1 << 40) == 3 and unpack(rows=0, x=None) == 0
 
 
+def test_sizes_past_32_bits():
+    """Refused before they are cut to the C entries' ints; rows that would be longer are not joined."""
+    huge = (1 << 31) + 64
+    x = torch.empty(1).expand(1, huge, 1)
+    for make in (lambda: block._scan_dims(x, x, False), lambda: block._step_dims(x[0], x[0], False),
+                 lambda: block._gated_dims(x.transpose(0, 1), x.transpose(0, 1), None, 0, 1e-5, "silu"),
+                 lambda: block._add_dims(x[0], None, None, None, 0, 1e-5), lambda: block._rows("x", x[0, :, 0])):
+        with pytest.raises(block.KdaError) as e:
+            make()
+        assert e.value.status == 3
+    y = torch.empty(4, 1 << 22, 1024, device="meta")[:, :1 << 21]      # 2^31 elements of 2^32 a row
+    assert block._rows("x", y[:, :1 << 20]) == (4, 1 << 30, 1 << 32)
+    with pytest.raises(block.KdaError):
+        block._rows("x", y)
+
+
 def test_reference_codes():
     """The trial of exponents and the grid of codes against torch's own 8-bit type."""
     x = torch.randn(50, 64, generator=torch.Generator().manual_seed(1)) * 100

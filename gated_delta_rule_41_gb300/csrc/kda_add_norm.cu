@@ -268,7 +268,9 @@ struct Fwd {
         constexpr int N = Rows<TPR>::kThreads, RPC = Rows<TPR>::kRows;
         auto* k = add_fwd_kernel<R, T, E, TPR, NC>;
         constexpr size_t smem = Feed<R, T, E, TPR, NC, false>::kBytes;
-        static const int per_sm = resident(k, N, smem);
+        static Resident resident;
+        int per_sm = 0;
+        if (resident.get(k, N, smem, per_sm) != KDA_OK) return KDA_ERR_CUDA;
         const int grid = grid_of(per_sm, (a.T + RPC - 1) / RPC);
         TimedLaunch tl("add_norm_fwd", s);
         k<<<grid, N, smem, s>>>(a);
@@ -290,7 +292,9 @@ struct Bwd {
         constexpr int N = Rows<TPR>::kThreads, RPC = Rows<TPR>::kRows;
         auto* k = add_bwd_kernel<R, T, E, TPR, NC>;
         constexpr size_t smem = Feed<R, T, E, TPR, NC, true>::kBytes;
-        static const int per_sm = resident(k, N, smem);
+        static Resident resident;
+        int per_sm = 0;
+        if (resident.get(k, N, smem, per_sm) != KDA_OK) return KDA_ERR_CUDA;
         const int grid = std::min(grid_of(per_sm, (a.T + RPC - 1) / RPC), kPartsPerSm * sm_count());
         {
             TimedLaunch tl("add_norm_bwd", s);

@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "kda_paged.cuh"
@@ -373,17 +374,28 @@ inline bool aligned16(std::initializer_list<const void*> ps) {
     return true;
 }
 
-// CTAs of a kernel that walks over its rows: all that an SM holds at once, or fewer.
-template <typename K>
-int resident(K kernel, int threads, size_t smem) {
-    int n = 0;
-    // (without the attribute 48 KB, static shared memory included)
-    if ((smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  (int)smem) != cudaSuccess) ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1)
-        n = 1;
-    return n;
-}
+// CTAs of a kernel that walks over its rows: all that an SM holds at once, or fewer.  Shared memory
+// is allowed and the CTAs are counted for one device at a time, so both are kept per device.
+struct Resident {
+    std::atomic<int> n[64] = {};   // 0: not known yet
+    template <typename K>
+    kda_status get(K kernel, int threads, size_t smem, int& per_sm) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_CUDA;
+        per_sm = n[dev].load(std::memory_order_acquire);
+        if (per_sm) return KDA_OK;
+        // (without the attribute 48 KB, static shared memory included)
+        if ((smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      (int)smem) != cudaSuccess) ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess ||
+            per_sm < 1) {
+            cudaGetLastError();   // said here, not by the next call
+            return KDA_ERR_CUDA;
+        }
+        n[dev].store(per_sm, std::memory_order_release);
+        return KDA_OK;
+    }
+};
 inline int grid_of(int per_sm, long long ctas_of_work) {
     return (int)std::min<long long>((long long)per_sm * sm_count(), ctas_of_work);
 }

@@ -287,7 +287,9 @@ struct Fwd {
     static kda_status go(const GatedArgs& a, cudaStream_t s) {
         constexpr int N = Rows<TPR>::kThreads, R = Rows<TPR>::kRows;
         auto* k = gated_fwd_kernel<T, E, TPR, NC, KEEP>;
-        static const int per_sm = resident(k, N, 0);
+        static Resident resident;
+        int per_sm = 0;
+        if (resident.get(k, N, 0, per_sm) != KDA_OK) return KDA_ERR_CUDA;
         const int grid = grid_of(per_sm, (a.T * a.H + R - 1) / R);
         TimedLaunch tl("gated_norm_fwd", s);
         k<<<grid, N, 0, s>>>(a);
@@ -306,7 +308,9 @@ struct Bwd {
     static kda_status go(const GatedArgs& a, cudaStream_t s) {
         constexpr int N = Rows<TPR>::kThreads, R = Rows<TPR>::kRows;
         auto* k = gated_bwd_kernel<T, E, TPR, NC, Q8>;
-        static const int per_sm = resident(k, N, 0);
+        static Resident resident;
+        int per_sm = 0;
+        if (resident.get(k, N, 0, per_sm) != KDA_OK) return KDA_ERR_CUDA;
         const int grid = std::min(grid_of(per_sm, (a.T * a.H + R - 1) / R), kPartsPerSm * sm_count());
         {
             TimedLaunch tl("gated_norm_bwd", s);

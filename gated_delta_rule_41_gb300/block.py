@@ -101,15 +101,16 @@ def _at(t):
 
 
 def _here(*tensors):
-    """The kernels run on the current device: so must their tensors be."""
+    """The kernels run on the current device, which is returned: so must their tensors be."""
     dev = torch.cuda.current_device() if _get_device is None else _get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise KdaError(1, "tensors must be CUDA tensors on the current device")
+    return dev
 
 
-# What was found right and made for calls of these sizes, strides and types: a small call's time
-# is the host's.
+# What was found right and made for calls of these sizes, strides and types (and, where a workspace's
+# size is a part of it, on this device: it goes by the SMs): a small call's time is the host's.
 _plans = {}
 
 
@@ -417,9 +418,9 @@ def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None,
     if packed != isinstance(gate, Packed8):
         raise KdaError(1, "x and gate must both be Packed8, or neither")
     src = (x.codes, x.scales, gate.codes, gate.scales) if packed else (x, None, gate, None)
-    _here(*src, weight, dy, workspace)
+    dev = _here(*src, weight, dy, workspace)
     lib = _lib()
-    key = ("gated_bwd", packed, src[0].shape, src[0].stride(), src[0].dtype, src[2].shape, src[2].stride(),
+    key = ("gated_bwd", dev, packed, src[0].shape, src[0].stride(), src[0].dtype, src[2].shape, src[2].stride(),
            src[2].dtype, _like(weight), dy.dtype, eps, act)
     d, need = _plans.get(key) or _plan(key, lambda: _gated_bwd_dims(x, gate, weight, dy, eps, act, packed))
     D = x.shape[2]
@@ -514,10 +515,10 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     dalpha (float32; dalpha for a vector alpha, which needs the forward's x).
     Without alpha, and in one type, dx is the tensor dres itself.  (``workspace`` as for
     ``gated_norm_bwd``.)"""
-    _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace)
+    dev = _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace)
     lib = _lib()
     vec = isinstance(alpha, torch.Tensor)
-    key = ("add_bwd", residual.shape, residual.stride(), residual.dtype, _like(x), _like(weight),
+    key = ("add_bwd", dev, residual.shape, residual.stride(), residual.dtype, _like(x), _like(weight),
            _like(alpha) if vec else alpha, dy.dtype, eps)
     d, need = _plans.get(key) or _plan(key, lambda: _add_bwd_dims(residual, weight, dy, x, alpha, eps))
     D = residual.shape[1]

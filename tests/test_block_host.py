@@ -1,0 +1,81 @@
+"""The Python calls of the operators around a mixing layer without a GPU: what they check and hand to
+the library, with tensors that say which device they are on and a library that only listens."""
+import pytest
+import torch
+
+from gated_delta_rule_41_gb300 import block
+from gated_delta_rule_41_gb300.block import KdaError
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+class On(torch.Tensor):
+    """A tensor in the host's memory that passes for one on CUDA device ``dev``."""
+    dev = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.dev
+
+
+def on(dev, *shape, dtype=BF16):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(On)
+    t.dev = dev
+    return t
+
+
+class Listening:
+    """Every entry succeeds; the calls' arguments by name.  Workspaces grow with the device's number."""
+
+    def __init__(self, host):
+        self.host, self.calls = host, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_workspace_bytes"):
+                return 1000 * (1 + self.host["dev"])
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """Current device and library."""
+    h = dict(dev=0)
+    h["lib"] = Listening(h)
+    monkeypatch.setattr(block, "_get_device", lambda: h["dev"])
+    monkeypatch.setattr(block, "_raw_stream", lambda stream: 0)
+    monkeypatch.setattr(block, "_lib", lambda: h["lib"])
+
+    def fresh(stream, shape, dtype, device):
+        return on(h["dev"], shape, dtype=dtype)
+
+    monkeypatch.setattr(block, "_fresh", fresh)
+    monkeypatch.setattr(block, "_plans", {})
+    return h
+
+
+def gated_bwd(dev, **kw):
+    t = lambda: on(dev, 6, 2, 64)  # noqa: E731
+    return block.gated_norm_bwd(t(), t(), on(dev, 64, dtype=F32), t(), **kw)
+
+
+def add_bwd(dev, **kw):
+    t = lambda: on(dev, 6, 64)  # noqa: E731
+    return block.add_norm_bwd(t(), on(dev, 64, dtype=F32), t(), t(), **kw)
+
+
+def scan_bwd(dev, **kw):
+    t = lambda: on(dev, 2, 70, 64)  # noqa: E731
+    return block.gated_scan_bwd(t(), t(), t(), on(dev, 2, 2, 64, dtype=F32), **kw)
+
+
+@pytest.mark.parametrize("call", [gated_bwd, add_bwd])
+def test_workspaces_are_as_large_as_the_device_asks(host, call):
+    """The same call on devices of unequal size, in turn."""
+    for dev in (0, 1, 0):
+        host["dev"] = dev
+        call(dev)
+        _, args = host["lib"].calls[-1]
+        assert args[-2] == 1000 * (1 + dev)

@@ -109,6 +109,11 @@ def _here(*tensors):
     return dev
 
 
+def _given(grads):
+    """The tensors that a caller gives for a backward pass's results."""
+    return () if grads is None else grads.values()
+
+
 # What was found right and made for calls of these sizes, strides and types (and, where a workspace's
 # size is a part of it, on this device: it goes by the SMs): a small call's time is the host's.
 _plans = {}
@@ -299,7 +304,7 @@ def gated_scan_bwd(x, g, do, saved=None, dht=None, initial_state=None, tied=Fals
     """Backward of ``gated_scan_fwd``.  Returns dict dx, dg, dh0 (dh0 with
     ``initial_state``).  ``saved`` are the states kept by the forward pass on
     the same inputs; without them they are computed again."""
-    _here(x, g, do, saved, dht, initial_state, cu_seqlens)
+    _here(x, g, do, saved, dht, initial_state, cu_seqlens, *_given(grads))
     lib, d = _lib(), _scan(x, g, tied)
     cu, n, rows = _scan_seqs(x, cu_seqlens)
     B, T, C = x.shape
@@ -418,7 +423,7 @@ def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None,
     if packed != isinstance(gate, Packed8):
         raise KdaError(1, "x and gate must both be Packed8, or neither")
     src = (x.codes, x.scales, gate.codes, gate.scales) if packed else (x, None, gate, None)
-    dev = _here(*src, weight, dy, workspace)
+    dev = _here(*src, weight, dy, workspace, *_given(grads))
     lib = _lib()
     key = ("gated_bwd", dev, packed, src[0].shape, src[0].stride(), src[0].dtype, src[2].shape, src[2].stride(),
            src[2].dtype, _like(weight), dy.dtype, eps, act)
@@ -515,7 +520,8 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     dalpha (float32; dalpha for a vector alpha, which needs the forward's x).
     Without alpha, and in one type, dx is the tensor dres itself.  (``workspace`` as for
     ``gated_norm_bwd``.)"""
-    dev = _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace)
+    dev = _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace,
+                *_given(grads))
     lib = _lib()
     vec = isinstance(alpha, torch.Tensor)
     key = ("add_bwd", dev, residual.shape, residual.stride(), residual.dtype, _like(x), _like(weight),

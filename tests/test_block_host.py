@@ -79,3 +79,27 @@ def test_workspaces_are_as_large_as_the_device_asks(host, call):
         call(dev)
         _, args = host["lib"].calls[-1]
         assert args[-2] == 1000 * (1 + dev)
+
+
+def grads_of(call, dev):
+    """Tensors for a call's results, on this device."""
+    if call is scan_bwd:
+        return dict(dx=on(dev, 2, 70, 64), dg=on(dev, 2, 70, 64), dh0=on(dev, 2, 64, dtype=F32))
+    if call is gated_bwd:
+        return dict(dx=on(dev, 6, 2, 64), dgate=on(dev, 6, 2, 64), dw=on(dev, 64, dtype=F32))
+    return dict(dres=on(dev, 6, 64), dx=on(dev, 6, 64), dw=on(dev, 64, dtype=F32),
+                dalpha=on(dev, 64, dtype=F32))
+
+
+@pytest.mark.parametrize("call", [scan_bwd, gated_bwd, add_bwd])
+def test_grads_on_another_device_are_refused(host, call):
+    """As all other tensors are; nothing is launched."""
+    kw = dict(x=on(0, 6, 64), alpha=on(0, 64, dtype=F32)) if call is add_bwd else {}
+    for name in grads_of(call, 0):
+        grads = grads_of(call, 0)
+        grads[name].dev = 1
+        with pytest.raises(KdaError) as e:
+            call(0, grads=grads, **kw)
+        assert e.value.status == 1 and not host["lib"].calls
+    call(0, grads=grads_of(call, 0), **kw)
+    assert host["lib"].calls

@@ -409,6 +409,8 @@ def _gated_fwd_dims(x, gate, weight, eps, act):
 
 
 def _workspace(need, workspace, like, stream):
+    if workspace is not None and not workspace.is_contiguous():
+        raise KdaError(1, "workspace must be a contiguous CUDA tensor")
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         return workspace
     return _fresh(stream, max(need, 1), torch.uint8, like.device)

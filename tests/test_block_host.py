@@ -103,3 +103,24 @@ def test_grads_on_another_device_are_refused(host, call):
         assert e.value.status == 1 and not host["lib"].calls
     call(0, grads=grads_of(call, 0), **kw)
     assert host["lib"].calls
+
+
+@pytest.mark.parametrize("call", [gated_bwd, add_bwd])
+def test_a_workspace_holds_what_it_says(host, call):
+    """One whose elements share memory, or lie apart, is refused: the kernels write as many bytes as its
+    elements have from its first one on."""
+    one = on(0, 1, dtype=torch.uint8)
+    wide = one.expand(1 << 20)
+    wide.dev = 0
+    apart = on(0, 1 << 12, dtype=torch.uint8)[::2]
+    apart.dev = 0
+    for ws in (wide, apart):
+        assert isinstance(ws, On) and not ws.is_contiguous()
+        with pytest.raises(KdaError) as e:
+            call(0, workspace=ws)
+        assert e.value.status == 1 and not host["lib"].calls
+    ws = on(0, 4096, dtype=torch.uint8)
+    call(0, workspace=ws)
+    assert host["lib"].calls[-1][1][-3] == ws.data_ptr()
+    call(0, workspace=on(0, 10, dtype=torch.uint8))            # too small: the call makes its own
+    assert len(host["lib"].calls) == 2

@@ -520,7 +520,7 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     ``dy`` the gradient of y, ``dres`` that of r from what else reads it.
     Returns dict dres (of the residual that went in), dx = alpha dres, dw and
     dalpha (float32; dalpha for a vector alpha, which needs the forward's x).
-    Without alpha, and in one type, dx is the tensor dres itself.  (``workspace`` as for
+    Without alpha, and in one type, dx is the tensor dres itself, as it may be in ``grads``.  (``workspace`` as for
     ``gated_norm_bwd``.)"""
     dev = _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace,
                 *_given(grads))
@@ -539,9 +539,11 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
                      dw=None if weight is None else _fresh(stream, (D,), torch.float32, dy.device),
                      dalpha=None if av is None else _fresh(stream, (D,), torch.float32, dy.device))
     else:
-        one = False
+        one = residual.numel() > 0 and _at(grads.get("dx")) == _at(grads["dres"])
+        if one and alpha is not None and (vec or alpha != 1):
+            raise KdaError(1, "dx and dres are one tensor")
     to = (_dense("dres", grads["dres"], residual.shape, residual.dtype),
-          _dense("dx", grads.get("dx"), residual.shape, dy.dtype),
+          _dense("dx", grads.get("dx"), residual.shape, dy.dtype) if not one else None,
           _dense("dw", grads.get("dw"), (D,), torch.float32),
           _dense("dalpha", grads.get("dalpha"), (D,), torch.float32))
     if to[3] is not None and x is None:

@@ -124,3 +124,24 @@ def test_a_workspace_holds_what_it_says(host, call):
     assert host["lib"].calls[-1][1][-3] == ws.data_ptr()
     call(0, workspace=on(0, 10, dtype=torch.uint8))            # too small: the call makes its own
     assert len(host["lib"].calls) == 2
+
+
+def test_gradients_that_are_one_tensor(host):
+    """Without alpha dx may be the tensor dres, as in what a call returns; with another factor these are
+    two results, and one tensor for both is refused."""
+    call = lambda **kw: add_bwd(0, **kw)  # noqa: E731
+    got = call()
+    assert got["dx"] is got["dres"]
+    again = call(grads=got)
+    assert again is got and got["dx"] is got["dres"]
+    name, args = host["lib"].calls[-1]
+    assert name == "kda_add_norm_bwd" and args[7] == got["dres"].data_ptr() and args[8] is None
+    empty = torch.zeros(0, 64, dtype=BF16).as_subclass(On)
+    w = on(0, 64, dtype=F32)
+    block.add_norm_bwd(empty, w, empty, alpha=0.5, grads=dict(dres=empty, dx=torch.empty_like(empty), dw=w))
+    before = len(host["lib"].calls)
+    for kw in (dict(alpha=0.5), dict(alpha=on(0, 64, dtype=F32), x=on(0, 6, 64))):
+        with pytest.raises(KdaError) as e:
+            call(grads=got, **kw)
+        assert e.value.status == 1
+    assert len(host["lib"].calls) == before

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ x, long
                                                    long long stride, uint8_t* codes,
                                                    uint8_t* scales) {
     constexpr int U = 4;
-    const int lane = threadIdx.x & 31, per = (D + kScaleBlock - 1) / kScaleBlock;
+    const int lane = threadIdx.x & 31, per = blocks_of(D);
     const long long n = rows * per;
     for (long long i0 = (blockIdx.x * 8ll + (threadIdx.x >> 5)) * U; i0 < n; i0 += gridDim.x * 8ll * U) {
         long long row = n <= 0x7fffffff ? (unsigned)i0 / (unsigned)per : i0 / per;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
                                                      const uint8_t* __restrict__ scales, long long rows,
                                                      int D, T* x) {
     const long long n = rows * D;
-    const int per = (D + kScaleBlock - 1) / kScaleBlock;
+    const int per = blocks_of(D);
     for (long long i = (blockIdx.x * 256ll + threadIdx.x) * E; i < n; i += gridDim.x * 256ll * E) {
         const long long row = n <= 0x7fffffff ? (unsigned)i / (unsigned)D : i / D;
         int c = (int)(i - row * D);
@@ -188,7 +188,7 @@ kda_status pack(const void* x, long long rows, int D, long long stride, uint8_t*
         pack_wide_kernel<T><<<(unsigned)((rows * (D / 16) + 255) / 256), 256, 0, s>>>(p, rows, D, stride,
                                                                                     codes, scales);
     else
-        pack_kernel<T><<<grid_all((rows * ((D + 31) / 32) + 31) / 32), 256, 0, s>>>(p, rows, D, stride,
+        pack_kernel<T><<<grid_all((rows * blocks_of(D) + 31) / 32), 256, 0, s>>>(p, rows, D, stride,
                                                                                 codes, scales);
     return launch_status();
 }

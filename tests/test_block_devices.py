@@ -98,3 +98,17 @@ def test_a_failed_attribute_is_reported_and_not_kept(lib):
     lib.fake_fail_attributes(1)
     assert call() == 6 and not launched(lib)
     assert call() == 0 and max(x.smem for x in launched(lib)) > 48 * 1024
+
+
+@pytest.mark.parametrize("D", [(1 << 31) - 31, (1 << 31) - 1, (1 << 31) - 32, 1])
+def test_rows_of_almost_2_31(lib, D):
+    """Blocks of a row are counted without an overflow of 32 bits."""
+    for t in (1, 0):
+        for at in (FAKE, FAKE + 4):           # at 4 bytes past a 16-byte boundary: element by element
+            lib.fake_reset()
+            assert lib.kda_pack8(at, t, 1, D, D, FAKE, FAKE, None) == 0
+            assert lib.kda_unpack8(FAKE, FAKE, 1, D, at, t, None) == 0
+            assert len(launched(lib)) == 2
+            if D > 1 and D % 32:
+                # as many CTAs as walk over rows of this size
+                assert [x.grid[0] for x in launched(lib)] == [8 * 152] * 2

@@ -374,3 +374,24 @@ def test_a_layer(cu):
                             ("dw", gg["dw"], rg["dw"]), ("dx", gs["dx"], rs["dx"]), ("dg", gs["dg"], rs["dg"])):
         err = (d64(got).view(want.shape) - want).norm() / want.norm()
         assert err < 2.0 ** -14, (name, float(err))
+
+
+@pytest.mark.parametrize("less", [31, 1])
+def test_pack_of_the_longest_rows(less):
+    """A row of 2^31 - 31 and of 2^31 - 1 elements: its last blocks, and some in between."""
+    D = (1 << 31) - less
+    x = torch.zeros(1, D, dtype=BF16, device="cuda")
+    places = [0, 1 << 20, (1 << 30) - 32, (1 << 31) - 4096 - 64, (D - 1) // 32 * 32 - 64]
+    parts = [slice(p, min(p + 160, D)) for p in places]
+    for i, s in enumerate(parts):
+        x[0, s] = rnd(i, x[0, s].shape[0], dtype=BF16)
+    p = kda.pack8(x)
+    for s in parts:
+        codes, scales = ref_pack(x[:, s])
+        assert torch.equal(p.codes[:, s].cpu().double(), codes)
+        assert torch.equal(p.scales[:, s.start // 32:-(-s.stop // 32)].cpu(), scales)
+    back = kda.unpack8(p)
+    for s in parts:
+        b = slice(s.start // 32, -(-s.stop // 32))
+        assert torch.equal(d64(back[:, s]), ref_unpack(p.codes[:, s], p.scales[:, b]))
+    assert int(torch.count_nonzero(back.view(torch.int16))) <= 160 * len(parts)

@@ -395,3 +395,66 @@ def test_pack_of_the_longest_rows(less):
         b = slice(s.start // 32, -(-s.stop // 32))
         assert torch.equal(d64(back[:, s]), ref_unpack(p.codes[:, s], p.scales[:, b]))
     assert int(torch.count_nonzero(back.view(torch.int16))) <= 160 * len(parts)
+
+
+# Rows by which a CTA's groups of threads come to their ring's slots again: each shape has more than twice
+# as many turns as the ring has slots (four, three or two; two or three CTAs of an SM, seven for the
+# smallest rings), and a last turn that some groups do not have.
+RINGS = [(BF16, BF16, 9583, 2048), (BF16, BF16, 16421, 1024), (BF16, BF16, 4111, 4096), (BF16, BF16, 2135, 8192),
+         (BF16, BF16, 767, 16384), (F32, F32, 9583, 1024), (F32, F32, 2135, 4096), (F32, BF16, 9583, 1024),
+         (F32, BF16, 1527, 8192), (BF16, BF16, 25003, 77)]
+
+
+@pytest.mark.parametrize("R,t,T,D", RINGS)
+def test_add_many_turns(R, t, T, D):
+    r, x, dy, dr = rnd(9, T, D, dtype=R), rnd(1, T, D, dtype=t), rnd(2, T, D, dtype=t), rnd(3, T, D, dtype=R)
+    run_add(r, sliced(x), 1 + 0.2 * rnd(5, D), 0.5 + 0.2 * rnd(6, D), dy, dr)
+
+
+GATED_RINGS = [(BF16, 10303, 5, 128), (BF16, 643, 5, 2048), (BF16, 1851, 5, 1024), (F32, 4801, 5, 128),
+               (F32, 1851, 5, 512), (BF16, 2003, 5, 77)]
+
+
+@pytest.mark.parametrize("dtype,T,H,D", GATED_RINGS)
+def test_gated_many_turns(dtype, T, H, D):
+    """Five heads: a step over rows carries from the head into the token."""
+    x, z, dy = (rnd(i, T, H, D, dtype=dtype) for i in range(3))
+    check_gated(sliced(x), sliced(z), 1 + 0.2 * rnd(5, D), "silu", dy)
+
+
+def counted(name, got, one, rows):
+    """Sums of ``rows`` equal terms, none left out and none taken twice.  A sum passes at most 22 rows of a
+    thread, 32 groups of a CTA, 38 partial rows of a warp and 5 steps among the warps, each rounded once, as
+    is the one term: 98 * 2^-24 of it, under a third of one of 51,515 terms."""
+    want = d64(one) * rows
+    assert ((d64(got) - want).abs() <= 98 * 2.0 ** -24 * want.abs()).all(), name
+
+
+@pytest.mark.parametrize("R,t,T,D", RINGS)
+def test_add_counts_every_row(R, t, T, D):
+    def rows(n, *a, **k):
+        return rnd(*a, 1, D, **k).expand(n, D).contiguous()
+
+    w, al = 1 + 0.2 * rnd(5, D), 0.5 + 0.2 * rnd(6, D)
+    got, one = (kda.add_norm_bwd(rows(n, 1, dtype=R), w, rows(n, 2, dtype=t), rows(n, 3, dtype=R),
+                                 x=rows(n, 4, dtype=t), alpha=al) for n in (T, 1))
+    for n in ("dw", "dalpha"):
+        counted(n, got[n], one[n], T)
+    for n in ("dres", "dx"):
+        assert torch.equal(got[n], one[n].expand(T, D)), n
+
+
+@pytest.mark.parametrize("dtype,T,H,D", GATED_RINGS)
+def test_gated_counts_every_row(dtype, T, H, D):
+    def rows(n, seed):
+        return rnd(seed, 1, 1, D, dtype=dtype).expand(n, H, D).contiguous()
+
+    w = 1 + 0.2 * rnd(5, D)
+    for packed in (False, True):
+        got, one = (kda.gated_norm_bwd(*((kda.pack8(t) if packed else t) for t in (rows(n, 1), rows(n, 2))), w,
+                                       rows(n, 3)) for n in (T, 1))
+        alone = kda.gated_norm_bwd(*((kda.pack8(t) if packed else t) for t in (rows(1, 1)[:, :1], rows(1, 2)[:, :1])),
+                                   w, rows(1, 3)[:, :1].contiguous())
+        counted("dw", got["dw"], alone["dw"], T * H)
+        for n in ("dx", "dgate"):
+            assert torch.equal(got[n], one[n].expand(T, H, D)), n

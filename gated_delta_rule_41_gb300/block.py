@@ -229,8 +229,8 @@ def pack8(x, out: Optional[Packed8] = None, stream=None) -> Packed8:
 
 
 def unpack8(p: Packed8, dtype=torch.bfloat16, out=None, stream=None):
-    """The values that ``p`` stands for, in bf16 (which holds them exactly) or
-    fp32."""
+    """The values that ``p`` stands for, in fp32 (exact) or bf16 (exact down to its
+    smallest steps, 2^-133: codes at the least scale reach 2^-135)."""
     _here(p.codes, p.scales, out)
     codes = p.codes
     D = codes.shape[-1]

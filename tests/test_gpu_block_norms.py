@@ -458,3 +458,18 @@ def test_gated_counts_every_row(dtype, T, H, D):
         counted("dw", got["dw"], alone["dw"], T * H)
         for n in ("dx", "dgate"):
             assert torch.equal(got[n], one[n].expand(T, H, D)), n
+
+
+def test_unpack_to_bf16_rounds_what_it_cannot_hold():
+    """Codes of blocks at the least scale reach 2^-135: exact in float32, in bf16 rounded to its smallest
+    steps of 2^-133, halves to even."""
+    x = torch.arange(-64, 64).float().view(4, 32) * 2.0 ** -135
+    x[1, 0] = 2.0 ** -120
+    for D in (32, 31):
+        p = kda.pack8(x[:, :D].contiguous().cuda())
+        assert (p.scales == 1).all()
+        want = ref_unpack(p.codes, p.scales)
+        assert torch.equal(d64(kda.unpack8(p, F32)), want)
+        got = kda.unpack8(p, BF16)
+        assert torch.equal(d64(got), (want * 2.0 ** 133).round() * 2.0 ** -133)
+        assert not torch.equal(d64(got), want)

@@ -18,24 +18,45 @@ namespace {
 
 using namespace block;
 
-// 1 / (1 + e) of e = exp(-z) (0 where e is infinite) and e itself.  float32 tensors take the exact
-// exponential and division, bf16 ones the fast power of two and reciprocal (2^-22 of it, and the
-// rounding of the argument).
+// Powers of two and reciprocals of bf16 tensors are the fast ones (2^-22 of the result, and the rounding
+// of the argument), float32 ones take the exact exponential and division.  The fast ones give 0 below
+// 2^-126, where both types have subnormal numbers (and z, or a large x, may lift what is below them), so
+// they are kept away from there: exponentials as the square of their root's, sums with both terms times
+// 2^-20.  A sigmoid is then right down to 2^-146, and 0 below.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504f, kBits = 20.f, kDown = 1.f / (1 << 20);
+
+// exp(-|z|) = e and 1 / (1 + e)
 template <typename T>
 __device__ __forceinline__ float logistic(float z, float& e) {
     if (sizeof(T) == 2) {
-        float s;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-        return s;
+        e = exp2_fast(fabsf(z) * (-kLog2e / 2));
+        e *= e;
+        return rcp_fast(1.f + e);
     }
-    e = expf(-z);
+    e = expf(-fabsf(z));
     return 1.f / (1.f + e);
 }
 template <typename T>
 __device__ __forceinline__ float gate(float z, int act) {
-    float e;
-    const float s = logistic<T>(z, e);
+    float s;
+    if (sizeof(T) == 2) {
+        // 1 / (1 + exp(-z)), the sum times 2^-20
+        s = rcp_fast(kDown + exp2_fast(fmaf(z, -kLog2e, -kBits))) * kDown;
+    } else {
+        float e;
+        s = logistic<T>(z, e);
+        if (z < 0.f) s *= e;
+    }
     return act == KDA_GATE_SILU ? z * s : s;
 }
 // s(z) and s'(z).  sigmoid(z) and sigmoid(-z) = 1 - sigmoid(z) come from exp(-|z|) without a
@@ -43,7 +64,7 @@ __device__ __forceinline__ float gate(float z, int act) {
 template <typename T>
 __device__ __forceinline__ void gate_grad(float z, int act, float& s, float& ds) {
     float e;
-    const float p = logistic<T>(fabsf(z), e), q = e * p;
+    const float p = logistic<T>(z, e), q = e * p;
     s = z < 0.f ? q : p;
     ds = z < 0.f ? p : q;
     if (act == KDA_GATE_SILU) {

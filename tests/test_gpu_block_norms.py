@@ -473,3 +473,26 @@ def test_unpack_to_bf16_rounds_what_it_cannot_hold():
         got = kda.unpack8(p, BF16)
         assert torch.equal(d64(got), (want * 2.0 ** 133).round() * 2.0 ** -133)
         assert not torch.equal(d64(got), want)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 33), (F32, 64)])
+def test_gates_far_out(dtype, D, act):
+    """Gates past |z| = 87, whose sigmoid or its derivative is among the subnormal numbers (of float32 down
+    to z = -104, of bf16 to -93), and on to where nothing is left.  A rounding there is off by half of
+    2^-149; a result passes a handful of products of such numbers with others that are under 100 here."""
+    z = torch.linspace(-112, 112, 113 * D).view(113, 1, D).to(dtype).cuda()
+    x, dy = rnd(1, 113, 1, D, dtype=dtype), rnd(2, 113, 1, D, dtype=dtype)
+    w = 1 + 0.2 * rnd(5, D)
+    tiny = 8 * 100 * 2.0 ** -150
+    y, x8, z8 = kda.gated_norm_fwd(x, z, w, act=act, keep8=True)
+    ref = ref_gated(x, z, w, EPS, act, dy)
+    check("y", y, ref["y"], ref["y~"] + tiny)
+    if dtype == F32:
+        assert (y[9:20] != 0).all()               # z from -94 to -72: none is lost
+    got = kda.gated_norm_bwd(x, z, w, dy, act=act)
+    of8 = kda.gated_norm_bwd(x8, z8, w, dy, act=act)
+    ref8 = ref_gated(kda.unpack8(x8, F32), kda.unpack8(z8, F32), w, EPS, act, dy)
+    for n in ("dx", "dgate"):
+        check(n, got[n], ref[n], ref[n + "~"] + tiny)
+        check(n + " of 8 bits", of8[n], ref8[n], ref8[n + "~"] + tiny)

@@ -72,7 +72,8 @@ def _lib():
                 ("kda_add_norm_workspace_bytes", S, [A]),
                 ("kda_add_norm_bwd", I, [A] + [P] * 11 + [S, P]),
                 ("kda_pack8", I, [P, I, L, I, L, P, P, P]),
-                ("kda_unpack8", I, [P, P, L, I, P, I, P])):
+                ("kda_unpack8", I, [P, P, L, I, P, I, P]),
+                ("kda_selftest_exchange", I, [I, I, I, I, L, L, P, P])):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, res
         _bound = lib

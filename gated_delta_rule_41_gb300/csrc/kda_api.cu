@@ -401,6 +401,18 @@ kda_status kda_selftest_wait_timeout(long long limit_cycles, void* stream) {
     return tc_selftest_timeout(limit_cycles, static_cast<cudaStream_t>(stream));
 }
 
+kda_status kda_selftest_exchange(int ctas, int turns, int slow_cta, int slow_turn,
+                                 long long stall_cycles, long long limit_cycles, float* sums,
+                                 void* stream) {
+    const long long most = 4000000000LL;
+    if (limit_cycles < 0 || limit_cycles > most || stall_cycles < 0 || stall_cycles > most || !sums)
+        return KDA_ERR_INVALID_ARG;
+    if (ctas < 1 || ctas > 16 || turns < 0 || turns > 250) return KDA_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(sums) & 3) return KDA_ERR_ALIGNMENT;
+    return scan_selftest_exchange(ctas, turns, slow_cta, slow_turn, stall_cycles, limit_cycles, sums,
+                                  static_cast<cudaStream_t>(stream));
+}
+
 const char* kda_status_str(kda_status s) {
     switch (s) {
         case KDA_OK: return "ok";

@@ -158,5 +158,8 @@ int* pages_error_word();
 
 // Device error word of the gated scan (a kda_status).
 int* scan_error_word();
+// Diagnostic: the exchange among the CTAs of its clusters, and what follows a wait that gave up.
+kda_status scan_selftest_exchange(int ctas, int turns, int slow_cta, int slow_turn, long long stall,
+                                  long long limit, float* sums, cudaStream_t s);
 
 }  // namespace kda

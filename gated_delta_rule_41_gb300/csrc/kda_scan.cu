@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "kda_block.cuh"
+#include "kda_exchange.cuh"
 #include "kda_ptx.cuh"
 #include "kda_timing.cuh"
 
@@ -260,12 +261,12 @@ __device__ __forceinline__ void push16(uint32_t to, uint32_t bar, const float4& 
                  "r"(__float_as_uint(v.w)), "r"(bar)
                  : "memory");
 }
-// A wait that gives up, and says so, after kWaitCycles.
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity) {
+// A wait that gives up, and says so, after `limit` cycles.
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, long long limit) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > limit) {
             atomicExch(&g_scan_error, (int)KDA_ERR_TIMEOUT);
             return false;
         }
@@ -370,38 +371,77 @@ struct Marks {
 struct __align__(16) Shared {
     float4 peers[2][kMaxCluster][32];   // maps of the cluster's CTAs, in two turns
     uint64_t arrived[2];                // ... and that they are here
+    int lost[32];                       // the turns in which lanes' waits gave up
 };
 
-// Exchanges of a cluster's maps, one a turn, by one warp of each CTA.
-template <bool VL, int N, bool BACK>
-struct Cluster {
+// Exchanges of a cluster's maps, one a turn, by one warp of each CTA, as kda_exchange.cuh tells them.
+struct Exchange {
     Shared& sh;
-    const int K, rank;
-    bool lost = false;   // a wait gave up: no more waits, the results are not to be used
+    const int K, rank, turns;
+    long long limit = kWaitCycles;
+    static constexpr unsigned kMapBytes = 32 * sizeof(float4);
 
     // Before the first turn; also a barrier of the cluster.
-    __device__ __forceinline__ void begin() {
+    __device__ __forceinline__ void begin(bool clear) {
+        if (clear && threadIdx.x < 32) sh.lost[threadIdx.x] = -1;
         if (threadIdx.x == 0) {
             for (int i = 0; i < 2; ++i) ptx::mbar_init(&sh.arrived[i], 1);
             ptx::fence_mbar_init();
-            for (int i = 0; i < 2; ++i) expect(i);
+            for (int i = 0; i < 2; ++i) ptx::mbar_arrive_expect_tx(&sh.arrived[i], K * kMapBytes);
         }
         cluster_sync();
     }
-    __device__ __forceinline__ void expect(int i) {
-        ptx::mbar_arrive_expect_tx(&sh.arrived[i], K * 32 * (unsigned)sizeof(float4));
+    // The lane's wait of a turn; what it says is kept.
+    __device__ __forceinline__ bool wait_of(int turn) {
+        if (await(&sh.arrived[turn & 1], turn >> 1 & 1, limit)) return true;
+        sh.lost[threadIdx.x & 31] = turn;
+        return false;
     }
+    __device__ __forceinline__ int lost_turn(int lane) const {
+        return *static_cast<volatile const int*>(&sh.lost[lane]);
+    }
+
+    static __device__ __noinline__ void drain(Shared& sh, int K, int turns, long long limit) {
+        Exchange e{sh, K, 0, turns, limit};
+        exchange_drain(e, turns, sh.lost[0]);
+    }
+    __device__ __forceinline__ bool wait(int turn) {
+        return await(&sh.arrived[turn & 1], turn >> 1 & 1, limit);
+    }
+    __device__ __forceinline__ void expect(int turn, int n) {
+        ptx::mbar_expect_tx(&sh.arrived[turn & 1], n * K * kMapBytes);
+    }
+    __device__ __forceinline__ void arrive(int turn) { ptx::mbar_arrive(&sh.arrived[turn & 1]); }
+};
+
+template <bool VL, int N, bool BACK>
+struct Cluster : Exchange {
+    // Whether this lane's wait gave up is held in a register, backward in shared memory alone.  (There the
+    // register makes 176 us of 156 in a packed pass; forward the reads make 88 of 82.)
+    static constexpr bool kLostInMemory = BACK;
+    bool lost = false;
+
+    __device__ __forceinline__ void begin() { Exchange::begin(kLostInMemory); }
+    // After the last turn; also a barrier of the cluster.  A CTA may end then: nothing comes to its shared
+    // memory any more.
+    __device__ __forceinline__ void end() {
+        cluster_sync();
+        const bool gone = kLostInMemory ? threadIdx.x == 0 && lost_turn(0) >= 0 : lost && (threadIdx.x & 31) == 0;
+        if (gone) drain(sh, K, turns, limit);
+    }
+
     // The state that enters this CTA's tile; `carry` goes from before the cluster's tiles of this
-    // turn to behind them.  Tiles in the order of the ranks, or against it.  A buffer is written again two turns
-    // later, by CTAs that have this one's map of the turn between: its reads are over by then.
+    // turn to behind them.  Tiles in the order of the ranks, or against it.
     __device__ __forceinline__ V<N> exchange(int turn, const Map<N>& own, V<N>& carry) {
         const int lane = threadIdx.x & 31, i = turn & 1;
 #pragma unroll 4
         for (int r = 0; r < K; ++r)
             push16(peer_address(&sh.peers[i][rank][lane], r), peer_address(&sh.arrived[i], r), to4<N>(own));
-        if (!lost) lost = !await(&sh.arrived[i], turn >> 1 & 1);
+        bool gone = kLostInMemory ? lost_turn(lane) >= 0 : lost;
+        if (!gone && !wait_of(turn)) gone = true;
+        lost = gone;
         __syncwarp();
-        if (lane == 0) expect(i);
+        if (lane == 0 && !gone) ptx::mbar_arrive_expect_tx(&sh.arrived[i], K * kMapBytes);
         const int step = BACK ? -1 : 1;
         int r = BACK ? K - 1 : 0;
 #pragma unroll 4
@@ -486,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     load(1);
     // one warp combines the maps; not the same one in CTAs that share an SM
     const int lead = blockIdx.x % kWarps;
-    Cluster<VL, N, false> cluster{sh, K, rank};
+    Cluster<VL, N, false> cluster{{sh, K, rank, turns}};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : h0_of(b), left);
     Marks marks;
@@ -597,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     }
     if (!VL && a.ht && rank == 0 && warp == lead) Lane<T>::put32(a.ht + (long long)b * a.C + c, carry, left);
     copies_wait<0>();
-    if (K > 1) cluster_sync();   // no CTA leaves while another may write to its shared memory
+    if (K > 1) cluster.end();
 }
 
 // Tiles from the last to the first.  The states inside a tile are formed again from the kept ones
@@ -644,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
     // one warp combines the maps of m, one those of the states
     constexpr int kPer = kStateEvery / kRun;
     const int lead = blockIdx.x % kWarps, second = (lead + 2) % kWarps;
-    Cluster<VL, N, true> cluster{sh, K, rank};
+    Cluster<VL, N, true> cluster{{sh, K, rank, turns}};
     if (K > 1) cluster.begin();
     V<N> carry = Lane<T>::get32(VL ? nullptr : dht_of(b), left);
     Marks marks;
@@ -814,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
     }
     if (!VL && a.dh0 && rank == 0 && warp == lead) Lane<T>::put32(a.dh0 + (long long)b * a.C + c, carry, left);
     copies_wait<0>();
-    if (K > 1) cluster_sync();
+    if (K > 1) cluster.end();
 }
 
 // What a kernel needs once per device: its attributes, and how many clusters of each size the
@@ -913,6 +953,25 @@ kda_status pick(const ScanArgs& a, cudaStream_t s) {
     return wide ? launch<T, BWD, TIED, false, true>(a, s) : launch<T, BWD, TIED, false, false>(a, s);
 }
 
+// Diagnostic: the exchange by itself, one warp to a CTA, maps h -> h + (turn + 1) (rank + 1).  CTA
+// slow_cta waits `stall` cycles before slow_turn.
+__global__ void __launch_bounds__(32) exchange_kernel(int K, int turns, int slow_cta, int slow_turn,
+                                                      long long stall, long long limit, float* sums) {
+    __shared__ Shared sh;
+    const int rank = (int)cluster_rank();
+    Cluster<false, 1, false> cluster{{sh, K, rank, turns, limit}};
+    cluster.begin();
+    V<1> carry = all<1>(0.f);
+    for (int turn = 0; turn < turns; ++turn) {
+        if (rank == slow_cta && turn == slow_turn)
+            for (const long long t0 = clock64(); clock64() - t0 < stall;) {}
+        __syncwarp();
+        cluster.exchange(turn, {all<1>(1.f), all<1>((float)((turn + 1) * (rank + 1)))}, carry);
+    }
+    cluster.end();
+    if (threadIdx.x == 0) sums[rank] = cluster.lost ? -1.f : carry.v[0];
+}
+
 // One token per row, the state read and written once: 256 x 2048 bf16 2.4 us, a launch's time.
 template <typename T, int E>
 __global__ void __launch_bounds__(256) step_kernel(int B, int C, bool tied, const T* x, long long x_row,
@@ -973,6 +1032,24 @@ kda_status scan_step_launch(int B, int C, bool bf16, bool tied, const void* x, l
                             void* o, cudaStream_t s) {
     return bf16 ? step<__nv_bfloat16>(B, C, tied, x, x_row, g, g_row, state, next, o, s)
                 : step<float>(B, C, tied, x, x_row, g, g_row, state, next, o, s);
+}
+
+kda_status scan_selftest_exchange(int K, int turns, int slow_cta, int slow_turn, long long stall,
+                                  long long limit, float* sums, cudaStream_t s) {
+    if (cudaFuncSetAttribute(exchange_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(K);
+    cfg.blockDim = dim3(32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)K, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, exchange_kernel, K, turns, slow_cta, slow_turn, stall, limit, sums) == cudaSuccess
+               ? launch_status()
+               : KDA_ERR_CUDA;
 }
 
 int* scan_error_word() {

@@ -640,6 +640,17 @@ kda_status kda_selftest_mma(const void* A, const void* B, float* D, int N, int f
  * and clears it. */
 kda_status kda_selftest_wait_timeout(long long limit_cycles, void* stream);
 
+/* Diagnostics: the exchange among the CTAs (1 to 16) of a cluster of the gated
+ * scan, `turns` (at most 250) times, and what follows a wait that gave up.  sums
+ * [ctas] (device f32) receives in each entry the sum over turns t and CTAs r of
+ * (t + 1) (r + 1).  slow_cta (-1: none) stalls for stall_cycles before slow_turn;
+ * waits of the others that give up after limit_cycles (both 0 .. 4e9) make their
+ * entries -1, those of the rest are then not to be used either, and the next
+ * kda_check returns KDA_ERR_TIMEOUT. */
+kda_status kda_selftest_exchange(int ctas, int turns, int slow_cta, int slow_turn,
+                                 long long stall_cycles, long long limit_cycles, float* sums,
+                                 void* stream);
+
 /* Static description of a status code. */
 const char* kda_status_str(kda_status status);
 

@@ -1,5 +1,8 @@
 """The C ABI of the operators around a mixing layer without a GPU: bad arguments are refused before
 any launch, and empty calls succeed without one.  And the 64-bit references against each other."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -178,3 +181,34 @@ def test_reference_codes():
     top = codes.unflatten(-1, (-1, 32)).abs().amax(-1)
     assert (top <= 448).all() and (top >= 224).all()
     assert ((ref_unpack(codes, scales) - x.double()).abs() <= x.double().abs() * 2.0 ** -4 + 2.0 ** -10 * s).all()
+
+
+def test_exchange_arguments(lib):
+    def call(ctas=4, turns=5, stall=0, limit=1000, sums=FAKE):
+        return lib.kda_selftest_exchange(ctas, turns, -1, 0, stall, limit, sums, None)
+
+    assert call(limit=-1) == 1 and call(limit=1 << 40) == 1 and call(sums=None) == 1
+    assert call(stall=-1) == 1 and call(stall=1 << 40) == 1
+    assert call(ctas=0) == 2 and call(ctas=17) == 2 and call(turns=-1) == 2 and call(turns=251) == 2
+    assert call(sums=ODD) == 4
+
+
+@pytest.fixture(scope="module")
+def model(tmp_path_factory):
+    here, out = os.path.dirname(os.path.abspath(__file__)), str(tmp_path_factory.mktemp("model") / "model")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-pthread", "-I", kbuild.CSRC,
+                    os.path.join(here, "exchange_model.cpp"), "-o", out], check=True)
+    return out
+
+
+@pytest.mark.parametrize("ctas,turns,seeds,rounds", [(1, 5, 20, 1 << 30), (13, 20, 3, 1 << 30), (2, 9, 60, 300),
+                                                     (4, 12, 40, 200), (4, 12, 40, 3000), (16, 9, 12, 300),
+                                                     (16, 200, 2, 300)])
+def test_exchange_of_a_cluster(model, ctas, turns, seeds, rounds):
+    """Nothing comes to a CTA that has ended, no barrier gets an arrival too many, and without a lost CTA no
+    turn reads another's maps, whichever waits give up (and with waits that do not, none is lost)."""
+    r = subprocess.run([model, str(ctas), str(turns), str(seeds), str(rounds)], capture_output=True, text=True,
+                       timeout=120)
+    assert r.returncode == 0, r.stdout
+    lost = int(r.stdout.split()[-1])
+    assert lost == 0 if rounds == 1 << 30 else lost > 0

@@ -300,3 +300,41 @@ def test_refusals():
     refused(1, kda.gated_scan_bwd, x, g, do, saved=h0)
     refused(1, kda.gated_scan_step, x[:, 0], g[:, 0], h0[:1])
     kda.check()
+
+
+def exchange(ctas, turns, slow_cta=-1, slow_turn=0, stall=0, limit=2_000_000_000):
+    """What each CTA sums up over the turns."""
+    from gated_delta_rule_41_gb300 import block
+    sums = torch.zeros(ctas, device="cuda")
+    assert block._lib().kda_selftest_exchange(ctas, turns, slow_cta, slow_turn, stall, limit, sums.data_ptr(),
+                                              torch.cuda.current_stream().cuda_stream) == 0
+    return sums.tolist()
+
+
+def summed(ctas, turns):
+    return [float(turns * (turns + 1) // 2 * (ctas * (ctas + 1) // 2))] * ctas
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 5, 8, 13, 16])
+def test_exchange_of_a_cluster(ctas):
+    for turns in (1, 2, 7, 100):
+        assert exchange(ctas, turns) == summed(ctas, turns)
+        assert exchange(ctas, turns, ctas // 2, turns // 2, 1_000_000) == summed(ctas, turns)
+    kda.check()
+
+
+@pytest.mark.parametrize("ctas", [2, 5, 13])
+@pytest.mark.parametrize("turns,slow_turn", [(1, 0), (2, 0), (9, 0), (9, 3), (9, 7), (9, 8), (200, 100)])
+def test_a_wait_that_gives_up(ctas, turns, slow_turn):
+    """A CTA stalls for 5 ms in one turn and the others' waits run out after 0.1 ms: that is reported, all CTAs
+    end, and what runs next is right."""
+    kda.check()
+    got = exchange(ctas, turns, ctas // 2, slow_turn, 10_000_000, 200_000)
+    assert [v for r, v in enumerate(got) if r != ctas // 2] == [-1.0] * (ctas - 1)
+    with pytest.raises(kda.KdaError) as e:
+        kda.check()
+    assert e.value.status == 7
+    kda.check()
+    assert exchange(ctas, 3) == summed(ctas, 3)
+    x, g, do, h0, dht = make(1, 3000, 40, BF16, 7, 1)
+    run(x, g, do, h0, dht)

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(Rows<TPR>::kThreads, NC == 1 && TPR <= 256 ? 2
             at.next(a);
             const float2 sum = row_sum<TPR, true>(make_float2(s2.x + s2.y, sn.x + sn.y), red, turn, W);
             const float inv = rsqrtf(fmaf(sum.x, inv_d, a.eps));
-            const float m = inv * inv * sum.y * inv_d;
+            const float m = inv * (inv * (sum.y * inv_d));   // (inv * inv may overflow)
             const long long e = (long long)row * a.D;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {

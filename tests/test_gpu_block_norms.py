@@ -496,3 +496,18 @@ def test_gates_far_out(dtype, D, act):
     for n in ("dx", "dgate"):
         check(n, got[n], ref[n], ref[n + "~"] + tiny)
         check(n + " of 8 bits", of8[n], ref8[n], ref8[n + "~"] + tiny)
+
+
+@pytest.mark.parametrize("eps", [1e-5, 1e-30, 1e-40])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_zeros(dtype, eps):
+    """A row of zeros has the gradients that its epsilon makes, of whatever size that is."""
+    r, dy, dr, z = (rnd(i, 3, 64, dtype=dtype) for i in range(4))
+    r[1], w = 0.0, 1 + 0.2 * rnd(5, 64)
+    got, ref = kda.add_norm_bwd(r, w, dy, dr, eps=eps), ref_add_bwd(r, w, dy, dr, None, None, eps)
+    for n in ("dres", "dw"):
+        check(n, got[n], ref[n], ref[n + "~"])
+    x, z, up = (t.view(3, 1, 64) for t in (r, z, dy))
+    got, ref = kda.gated_norm_bwd(x, z, w, up, eps=eps), ref_gated(x, z, w, eps, "sigmoid", up)
+    for n in ("dx", "dgate", "dw"):
+        check(n, got[n], ref[n], ref[n + "~"])

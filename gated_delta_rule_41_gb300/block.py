@@ -279,7 +279,8 @@ def gated_scan_fwd(x, g, initial_state=None, output_final_state=False, tied=Fals
     final_state or None), plus the kept states when ``save_for_backward`` is
     set (pass them to ``gated_scan_bwd``).  ``initial_state`` and the final
     state are float32 [B, C]; with ``cu_seqlens`` (int32 [N + 1], B = 1) the
-    sequences are packed along T and they are [N, C]."""
+    sequences are packed along T and they are [N, C].  An infinite state may be a
+    NaN from the next token on, in its channel and sequence."""
     _here(x, g, initial_state, cu_seqlens, out, final_state)
     lib, d = _lib(), _scan(x, g, tied)
     cu, n, rows = _scan_seqs(x, cu_seqlens)

@@ -488,7 +488,8 @@ kda_status kda_pages_copy(const kda_page_pool* pools, int num_pools, int num_pag
  * above 0 are not supported (products of growth over runs of tokens may overflow where no
  * state does).  The states advance in float32 from token to token, with a decay near
  * one held as its small distance from one; the tokens of a tile are combined as maps h -> A h + H.
- * An infinity or NaN stays in its channel and its sequence. */
+ * An infinity or NaN stays in its channel and its sequence; an infinite state (which the definition
+ * would keep so) may be a NaN from the next token on. */
 typedef struct {
     int B, T, C;          /* x, g, o [B][T][C] */
     kda_dtype dtype;      /* of x, g, o and their gradients */

@@ -338,3 +338,32 @@ def test_a_wait_that_gives_up(ctas, turns, slow_turn):
     assert exchange(ctas, 3) == summed(ctas, 3)
     x, g, do, h0, dht = make(1, 3000, 40, BF16, 7, 1)
     run(x, g, do, h0, dht)
+
+
+@pytest.mark.parametrize("cu", [None, [0, 90, 200, 400]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_infinities(dtype, cu):
+    """A state that meets an infinity is not finite from there to its sequence's end, as an infinity or a NaN,
+    and nothing else is touched; the same for what comes back from an infinite gradient."""
+    T, C = 400, 72
+    x, g, do, h0, dht = make(1, T, C, dtype, 2, 1 if cu is None else len(cu) - 1)
+    x[0, 100, 5], x[0, 127, 6], do[0, 150, 7], h0[0, 8] = float("inf"), -float("inf"), float("inf"), float("inf")
+    dev = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, ht, saved = kda.gated_scan_fwd(x, g, h0, True, cu_seqlens=dev, save_for_backward=True)
+    gr = kda.gated_scan_bwd(x, g, do, saved, dht=dht, initial_state=h0, cu_seqlens=dev)
+    kda.check()
+    first, last = (0, T) if cu is None else (90, 200)
+    want = torch.zeros(T, C, dtype=torch.bool)
+    want[100:last, 5] = want[127:last, 6] = True
+    want[:T if cu is None else 90, 8] = True
+    assert torch.equal(~torch.isfinite(o[0]).cpu(), want)
+    assert torch.isinf(o[0, 100, 5]) and torch.isinf(o[0, 127, 6])
+    want = torch.zeros(T, C, dtype=torch.bool)
+    want[first:151, 7] = True
+    assert torch.equal(~torch.isfinite(gr["dx"][0]).cpu(), want)
+    dg = ~torch.isfinite(gr["dg"][0]).cpu()
+    assert not dg[:, [c for c in range(C) if c not in (5, 6, 7, 8)]].any()
+    h = torch.zeros(1, C, device="cuda")
+    h[0, 3] = float("inf")
+    step = kda.gated_scan_step(x[:, 0], g[:, 0], h)
+    assert (~torch.isfinite(step)).nonzero().tolist() == [[0, 3]] == (~torch.isfinite(h)).nonzero().tolist()

@@ -874,8 +874,10 @@ bool prepare(Setup& s, K kernel, size_t smem) {
     constexpr size_t kAloneBytes = 120 * 1024;   // two of these do not fit an SM
     static_assert(kAloneBytes >= (kBwdStages * 3) * kTileBytes + sizeof(Shared), "");
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAloneBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();   // said here, not by the next call
         return false;
+    }
     auto count = [&](int k, size_t bytes) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute at[1];
@@ -941,7 +943,8 @@ kda_status launch(const ScanArgs& a, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     TimedLaunch tl(BWD ? "gated_scan_bwd" : "gated_scan_fwd", s);
-    return cudaLaunchKernelEx(&cfg, k, a, K) == cudaSuccess ? launch_status() : KDA_ERR_CUDA;
+    cudaLaunchKernelEx(&cfg, k, a, K);
+    return launch_status();
 }
 
 template <typename T, bool BWD, bool TIED>
@@ -1047,9 +1050,8 @@ kda_status scan_selftest_exchange(int K, int turns, int slow_cta, int slow_turn,
     at[0].val.clusterDim = {(unsigned)K, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, exchange_kernel, K, turns, slow_cta, slow_turn, stall, limit, sums) == cudaSuccess
-               ? launch_status()
-               : KDA_ERR_CUDA;
+    cudaLaunchKernelEx(&cfg, exchange_kernel, K, turns, slow_cta, slow_turn, stall, limit, sums);
+    return launch_status();
 }
 
 int* scan_error_word() {

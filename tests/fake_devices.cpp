@@ -17,7 +17,7 @@ struct Launch {
 };
 constexpr int kSms[2] = {152, 80};
 std::mutex lock;
-int device = 0, fail_attributes = 0;
+int device = 0, fail_attributes = 0, fail_launches = 0;
 cudaError_t last = cudaSuccess;
 std::map<const void*, int> allowed[2];   // dynamic shared memory of a kernel, where set
 std::vector<Launch> launches;
@@ -29,6 +29,10 @@ thread_local struct {
 
 cudaError_t launch(const void* kernel, dim3 grid, dim3 block, size_t smem) {
     std::lock_guard<std::mutex> hold(lock);
+    if (fail_launches > 0) {
+        --fail_launches;
+        return last = cudaErrorInvalidValue;
+    }
     const auto it = allowed[device].find(kernel);
     const size_t most = it == allowed[device].end() ? 48 * 1024 : it->second;
     if (smem > most || !grid.x || !grid.y || !grid.z || grid.x > 0x7fffffffu || grid.y > 65535)
@@ -46,10 +50,11 @@ void fake_reset() {
     std::lock_guard<std::mutex> hold(lock);
     launches.clear();
     last = cudaSuccess;
-    fail_attributes = 0;
+    fail_attributes = fail_launches = 0;
 }
 void fake_use(int d) { device = d; }
 void fake_fail_attributes(int n) { fail_attributes = n; }
+void fake_fail_launches(int n) { fail_launches = n; }
 int fake_sms(int d) { return kSms[d]; }
 int fake_launches(Launch* out, int most) {
     const int n = (int)launches.size();

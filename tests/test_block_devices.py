@@ -112,3 +112,17 @@ def test_rows_of_almost_2_31(lib, D):
             if D > 1 and D % 32:
                 # as many CTAs as walk over rows of this size
                 assert [x.grid[0] for x in launched(lib)] == [8 * 152] * 2
+
+
+def test_a_failure_of_the_scan_is_not_the_next_calls_error(lib):
+    """An attribute or a launch that fails is said by the call that meets it, and by no other."""
+    d = KdaScanDims(1, 300, 24, 1, 1, 300 * 24, 24, 300 * 24, 24)       # tied: asked for by no other test
+    for call in (lambda: lib.kda_gated_scan_fwd(d, None, 0, FAKE, FAKE, None, FAKE, None, None, None),
+                 lambda: lib.kda_gated_scan_bwd(d, None, 0, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, FAKE, None,
+                                                None)):
+        for fail in (lib.fake_fail_attributes, lib.fake_fail_launches):
+            lib.fake_reset()
+            fail(1)
+            assert call() == 6 and not launched(lib)
+            assert lib.kda_unpack8(FAKE, FAKE, 4, 64, FAKE, 1, None) == 0
+        assert call() == 0 and len(launched(lib)) == 2

@@ -83,11 +83,11 @@ __global__ void __launch_bounds__(256) pack_wide_kernel(const T* __restrict__ x,
 
 // A warp per block, a lane per element, four blocks on their way: any width, stride and alignment.
 template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ x, long long rows, int D,
+__global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ x, long long rows, int D, int per,
                                                    long long stride, uint8_t* codes,
                                                    uint8_t* scales) {
     constexpr int U = 4;
-    const int lane = threadIdx.x & 31, per = blocks_of(D);
+    const int lane = threadIdx.x & 31;
     const long long n = rows * per;
     for (long long i0 = (blockIdx.x * 8ll + (threadIdx.x >> 5)) * U; i0 < n; i0 += gridDim.x * 8ll * U) {
         long long row = n <= 0x7fffffff ? (unsigned)i0 / (unsigned)per : i0 / per;
@@ -134,9 +134,8 @@ __global__ void __launch_bounds__(256) unpack_wide_kernel(const uint8_t* __restr
 template <typename T, int E>
 __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ scales, long long rows,
-                                                     int D, T* x) {
+                                                     int D, int per, T* x) {
     const long long n = rows * D;
-    const int per = blocks_of(D);
     for (long long i = (blockIdx.x * 256ll + threadIdx.x) * E; i < n; i += gridDim.x * 256ll * E) {
         const long long row = n <= 0x7fffffff ? (unsigned)i / (unsigned)D : i / D;
         int c = (int)(i - row * D);
@@ -175,6 +174,9 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
     }
 }
 
+// Blocks of a row of D elements, of any D that an int holds.  (The kernels get it as an argument.)
+int blocks_of(int D) { return (D - 1) / kScaleBlock + 1; }
+
 // CTAs that walk over what there is.  (The wide kernels' grids cover it: at most 2^40 elements, in
 // CTAs of 1024 or more.)
 int grid_all(long long ctas) { return (int)std::min<long long>(ctas, 8ll * sm_count()); }
@@ -188,8 +190,8 @@ kda_status pack(const void* x, long long rows, int D, long long stride, uint8_t*
         pack_wide_kernel<T><<<(unsigned)((rows * (D / 16) + 255) / 256), 256, 0, s>>>(p, rows, D, stride,
                                                                                     codes, scales);
     else
-        pack_kernel<T><<<grid_all((rows * blocks_of(D) + 31) / 32), 256, 0, s>>>(p, rows, D, stride,
-                                                                                codes, scales);
+        pack_kernel<T><<<grid_all((rows * blocks_of(D) + 31) / 32), 256, 0, s>>>(
+            p, rows, D, blocks_of(D), stride, codes, scales);
     return launch_status();
 }
 
@@ -202,9 +204,9 @@ kda_status unpack(const uint8_t* codes, const uint8_t* scales, long long rows, i
     if (D % kScaleBlock == 0 && aligned16({codes, x}))
         unpack_wide_kernel<T><<<(unsigned)((n * sizeof(T) / 16 + 255) / 256), 256, 0, s>>>(codes, scales, n, p);
     else if (aligned16({codes, x}))
-        unpack_kernel<T, 4><<<grid_all((n + 1023) / 1024), 256, 0, s>>>(codes, scales, rows, D, p);
+        unpack_kernel<T, 4><<<grid_all((n + 1023) / 1024), 256, 0, s>>>(codes, scales, rows, D, blocks_of(D), p);
     else
-        unpack_kernel<T, 1><<<grid_all((n + 255) / 256), 256, 0, s>>>(codes, scales, rows, D, p);
+        unpack_kernel<T, 1><<<grid_all((n + 255) / 256), 256, 0, s>>>(codes, scales, rows, D, blocks_of(D), p);
     return launch_status();
 }
 

@@ -16,9 +16,6 @@ namespace block {
 constexpr int kScaleBlock = 32;    // neighbours that share a scale
 constexpr int kMaxWidth = 16384;   // elements of a row that the norms keep in registers
 
-// Blocks of a row of D > 0 elements, of any D that an int holds.
-__host__ __device__ __forceinline__ int blocks_of(int D) { return (D - 1) / kScaleBlock + 1; }
-
 using paged::sm_count;
 
 __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {

@@ -94,6 +94,8 @@ struct Place {
     }
 };
 
+__host__ __device__ __forceinline__ int blocks_of(int D) { return (D + kScaleBlock - 1) / kScaleBlock; }
+
 // The codes and the scale of a chunk; the chunks of a block lie in neighbouring lanes.
 template <int E>
 __device__ __forceinline__ void keep(float (&v)[E], bool in, uint8_t* code, uint8_t* scale, int at) {

@@ -391,7 +391,7 @@ struct Exchange {
         }
         cluster_sync();
     }
-    // The lane's wait of a turn; what it says is kept.
+    // A lane's wait of a turn; that it gave up is kept.
     __device__ __forceinline__ bool wait_of(int turn) {
         if (await(&sh.arrived[turn & 1], turn >> 1 & 1, limit)) return true;
         sh.lost[threadIdx.x & 31] = turn;
@@ -401,10 +401,7 @@ struct Exchange {
         return *static_cast<volatile const int*>(&sh.lost[lane]);
     }
 
-    static __device__ __noinline__ void drain(Shared& sh, int K, int turns, long long limit) {
-        Exchange e{sh, K, 0, turns, limit};
-        exchange_drain(e, turns, sh.lost[0]);
-    }
+    // What exchange_drain asks for.
     __device__ __forceinline__ bool wait(int turn) {
         return await(&sh.arrived[turn & 1], turn >> 1 & 1, limit);
     }
@@ -427,7 +424,7 @@ struct Cluster : Exchange {
     __device__ __forceinline__ void end() {
         cluster_sync();
         const bool gone = kLostInMemory ? threadIdx.x == 0 && lost_turn(0) >= 0 : lost && (threadIdx.x & 31) == 0;
-        if (gone) drain(sh, K, turns, limit);
+        if (gone) exchange_drain(*static_cast<Exchange*>(this), turns, sh.lost[0]);
     }
 
     // The state that enters this CTA's tile; `carry` goes from before the cluster's tiles of this

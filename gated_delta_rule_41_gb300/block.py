@@ -110,9 +110,9 @@ def _here(*tensors):
     return dev
 
 
-def _given(grads):
+def _given(grads, *names):
     """The tensors that a caller gives for a backward pass's results."""
-    return () if grads is None else grads.values()
+    return () if grads is None else [grads.get(n) for n in names]
 
 
 # What was found right and made for calls of these sizes, strides and types (and, where a workspace's
@@ -306,7 +306,7 @@ def gated_scan_bwd(x, g, do, saved=None, dht=None, initial_state=None, tied=Fals
     """Backward of ``gated_scan_fwd``.  Returns dict dx, dg, dh0 (dh0 with
     ``initial_state``).  ``saved`` are the states kept by the forward pass on
     the same inputs; without them they are computed again."""
-    _here(x, g, do, saved, dht, initial_state, cu_seqlens, *_given(grads))
+    _here(x, g, do, saved, dht, initial_state, cu_seqlens, *_given(grads, "dx", "dg", "dh0"))
     lib, d = _lib(), _scan(x, g, tied)
     cu, n, rows = _scan_seqs(x, cu_seqlens)
     B, T, C = x.shape
@@ -411,7 +411,7 @@ def _gated_fwd_dims(x, gate, weight, eps, act):
 
 
 def _workspace(need, workspace, like, stream):
-    if workspace is not None and not workspace.is_contiguous():
+    if need and workspace is not None and not workspace.is_contiguous():
         raise KdaError(1, "workspace must be a contiguous CUDA tensor")
     if workspace is not None and workspace.numel() * workspace.element_size() >= need:
         return workspace
@@ -427,7 +427,7 @@ def gated_norm_bwd(x, gate, weight, dy, eps=1e-5, act="sigmoid", workspace=None,
     if packed != isinstance(gate, Packed8):
         raise KdaError(1, "x and gate must both be Packed8, or neither")
     src = (x.codes, x.scales, gate.codes, gate.scales) if packed else (x, None, gate, None)
-    dev = _here(*src, weight, dy, workspace, *_given(grads))
+    dev = _here(*src, weight, dy, workspace, *_given(grads, "dx", "dgate", "dw"))
     lib = _lib()
     key = ("gated_bwd", dev, packed, src[0].shape, src[0].stride(), src[0].dtype, src[2].shape, src[2].stride(),
            src[2].dtype, _like(weight), dy.dtype, eps, act)
@@ -525,7 +525,7 @@ def add_norm_bwd(residual, weight, dy, dres=None, x=None, alpha=None, eps=1e-5, 
     Without alpha, and in one type, dx is the tensor dres itself, as it may be in ``grads``.  (``workspace`` as for
     ``gated_norm_bwd``.)"""
     dev = _here(residual, weight, dy, dres, x, alpha if isinstance(alpha, torch.Tensor) else None, workspace,
-                *_given(grads))
+                *_given(grads, "dres", "dx", "dw", "dalpha"))
     lib = _lib()
     vec = isinstance(alpha, torch.Tensor)
     key = ("add_bwd", dev, residual.shape, residual.stride(), residual.dtype, _like(x), _like(weight),

@@ -101,7 +101,7 @@ def test_grads_on_another_device_are_refused(host, call):
         with pytest.raises(KdaError) as e:
             call(0, grads=grads, **kw)
         assert e.value.status == 1 and not host["lib"].calls
-    call(0, grads=grads_of(call, 0), **kw)
+    call(0, grads=dict(grads_of(call, 0), other=on(1, 3)), **kw)      # (what is not asked for is not looked at)
     assert host["lib"].calls
 
 
@@ -124,6 +124,9 @@ def test_a_workspace_holds_what_it_says(host, call):
     assert host["lib"].calls[-1][1][-3] == ws.data_ptr()
     call(0, workspace=on(0, 10, dtype=torch.uint8))            # too small: the call makes its own
     assert len(host["lib"].calls) == 2
+    none = dict(dx=on(0, 6, 2, 64), dgate=on(0, 6, 2, 64)) if call is gated_bwd else dict(dres=on(0, 6, 64))
+    call(0, workspace=apart, grads=none)                       # not used
+    assert len(host["lib"].calls) == 3
 
 
 def test_gradients_that_are_one_tensor(host):

@@ -7,8 +7,8 @@
 // One pass over the data, bounded by HBM: a row stays in the registers of its threads between the sums
 // over it and the results; 16 threads for 128 elements, so that two rows fill a warp and the sums
 // take four shuffles.  32768 x 16 x 128 bf16 on one GB300: forward with 8-bit copies of both inputs
-// 88 us, 6.1 TB/s (0.92 of the copy rate), without 65 us; backward from these copies 103 us, 5.2 TB/s
-// (0.78; 57 % of the issue slots), from bf16 118 us.  With r = 1 / sqrt(mean(x^2) + eps) both sums of the backward pass, those of
+// 88 us, 6.1 TB/s (0.92 of the copy rate), without 64 us; backward from these copies 104 us, 5.2 TB/s
+// (0.78; 57 % of the issue slots), from bf16 114 us.  With r = 1 / sqrt(mean(x^2) + eps) both sums of the backward pass, those of
 // x^2 and of dn x, are formed at once: dx = r (dn - x r^2 mean(dn x)).
 #include "kda_block.cuh"
 #include "kda_timing.cuh"

@@ -137,10 +137,13 @@ __device__ __forceinline__ V<N> remainder(V<N> d, V<N> k, V<N> x) {
 // 1.3 us forward and 2.3 backward with one CTA to an SM, 2.2 to 2.6 and 4.1 with two: the chain scan,
 // barrier, combine, barrier, and 21, 36 and (tied) 46 instructions an element at half of the
 // issue slots.  With 256 CTAs busy that is near HBM, with fewer it is not.  One GB300, in a graph:
-//   4 x 8192 x 2048 bf16      forward 81 us, 4.95 TB/s (0.74); backward 127 us, 5.3 TB/s (0.79), tied 160 us
+//   4 x 8192 x 2048 bf16      forward 82 us, 4.95 TB/s (0.74); backward 129 us, 5.2 TB/s (0.78), tied 152 us
 //   1 x 65536 x 512 float32   forward, tied 87 us, 4.6 TB/s (0.69; 16 slabs, clusters of 13)
+//   1 x 65536 x 512 bf16      forward 82 us, 2.5 TB/s (0.37; 8 slabs, clusters of 12); backward 123 us
 //   1 x 65536 x 1024 float32  forward, tied 132 us, 6.1 TB/s (0.91; 32 slabs, clusters of 8)
-//   32768 x 1000 bf16 in 16 packed sequences, tied, backward 156 us, 2.1 TB/s (0.31)
+//   32768 x 1000 bf16 in 16 packed sequences, tied, forward 98 us (0.30), backward 156 us, 2.1 TB/s (0.32)
+// (The hot loops are at 128 registers, and a condition more or less around the exchange moves these times by
+// 2 to 10 %: the compiler then spills, or orders the loops in another way.)
 // A thread per channel, token by token: 4.7 ms and 7.4 ms for the first, 48 ms for the second.
 constexpr int kWarps = 8, kRun = 16, kTile = kWarps * kRun, kThreads = kWarps * 32;
 constexpr int kRowBytes = 128, kTileBytes = kTile * kRowBytes;
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a,
         T *dx = static_cast<T*>(a.dx) + end, *dg = static_cast<T*>(a.dg) + end;
         // h_{t-1}, less x where tied.  Tied with two channels to a lane these do not fit into the
         // registers (spilled, at 10 % of L1 hits, they took 237 us for 163): they go where this
-        // run's x and g were.
+        // run's x and g were.  (8 bytes of other values are still spilled.)
         constexpr bool kStash = TIED && N == 2;
         V<N> w[kStash ? 1 : kRun];
         uint32_t *stash = const_cast<uint32_t*>(xs), *stash2 = const_cast<uint32_t*>(gs);
@@ -901,8 +904,9 @@ bool prepare(Setup& s, K kernel, size_t smem) {
 // rounds that the slabs need.  A turn takes about 1.75 times as long where CTAs share an SM (forward
 // 1.3 us alone and 2.2 to 2.6 shared, backward 2.3 and 4.1), which they do not where the device has
 // room for all of them one to an SM.  (Times by size, the chosen last: 16 slabs of 65536 float32 tokens 124 us
-// with 6, 139 with 7, 90 with 13; 8 slabs of bf16 104 us with 16, 91 with 12; 160 slabs of 8192 tokens 138 us with
-// 1, 110 with 5.)
+// with 6, 139 with 7, 90 with 13; 8 slabs of bf16 104 us with 16, 82 with 12; 160 slabs of 8192 tokens 138 us with
+// 1, 110 with 5.  One factor for both directions: 4 x 8192 x 2048 bf16 forward takes 79 us with 1 and 82 with 2,
+// backward 144 and 129.)
 int cluster_of(const Setup& s, long long slabs, int T) {
     const int tiles = (T + kTile - 1) / kTile;
     long long best = -1;

@@ -33,6 +33,7 @@ struct World {
     std::vector<bool> ended;
     std::vector<Message> flying;
     long long wrong = 0, mixed = 0, lost = 0;
+    bool gave_up = false;                      // a wait, of any CTA
 
     void fault(const char* what) {
         if (wrong++ < 5) std::printf("%s\n", what);
@@ -121,9 +122,21 @@ void cta(World& w, int rank, unsigned seed) {
     const int stall = gen() % 3 ? -1 : (int)(gen() % w.turns);
     int lost = -1;
     for (int t = 0; t < w.turns; ++t) {
-        if (t == stall) std::this_thread::sleep_for(std::chrono::milliseconds(gen() % 4));
+        if (t == stall) {
+            std::this_thread::sleep_for(std::chrono::milliseconds(gen() % 4));
+            // (on a busy machine the others' waits may take longer than that)
+            for (int i = 0; i < 10000 && w.wait_rounds < 1 << 30 && w.K > 1; ++i) {
+                std::this_thread::sleep_for(std::chrono::microseconds(100));
+                std::lock_guard<std::mutex> hold(w.lock);
+                if (w.gave_up) break;
+            }
+        }
         port.send(t);
-        if (lost < 0 && !port.wait(t)) lost = t;
+        if (lost < 0 && !port.wait(t)) {
+            lost = t;
+            std::lock_guard<std::mutex> hold(w.lock);
+            w.gave_up = true;
+        }
         if (lost >= 0) continue;
         port.arm(t + 2);
         if (gen() % 4 == 0) std::this_thread::yield();

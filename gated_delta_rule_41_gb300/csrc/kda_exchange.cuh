@@ -9,7 +9,7 @@
 // turn by each, and its end can wait for all of them: nothing may be on its way to a CTA that has ended.
 // Messages of a lost CTA that come too early are taken for others of their barrier; the results are not to
 // be used.  A barrier counts fewer than 2^20 bytes: with 512 a message, that holds for any order of messages
-// where K times the turns are at most kExchangeMessages (2^19 tokens of a scan); beyond, as long as no CTA is
+// where K times the turns are at most 4064 (2^19 tokens of a scan); beyond, as long as no CTA is
 // that far ahead of another.
 //
 // (Without a GPU the tests run this on threads.)
@@ -22,8 +22,6 @@
 #endif
 
 namespace kda {
-
-constexpr int kExchangeMessages = 4064;
 
 // The end of a CTA that was lost in turn `lost`, once all CTAs have sent their messages of all turns (a
 // barrier of the cluster says so).  It has expected those of turns up to lost + 1.  The others are now

@@ -9,8 +9,8 @@
 // turn by each, and its end can wait for all of them: nothing may be on its way to a CTA that has ended.
 // Messages of a lost CTA that come too early are taken for others of their barrier; the results are not to
 // be used.  A barrier counts fewer than 2^20 bytes: with 512 a message, that holds for any order of messages
-// where K times the turns are at most 4064 (2^19 tokens of a scan); beyond, as long as no CTA is
-// that far ahead of another.
+// where K times the turns are at most 4064 (2^19 tokens of a scan).  Where more than a barrier counts may be
+// on its way to a lost CTA, that lets its waits' limit pass instead.
 //
 // (Without a GPU the tests run this on threads.)
 #pragma once
@@ -32,8 +32,14 @@ namespace kda {
 //   wait(turn)            for the end of this turn's phase; false if it gives up again
 //   expect(turn, n)       n more messages of each CTA on this turn's barrier, whatever its phase
 //   arrive(turn)          the arrival that a phase of this turn's barrier needs, and none before
+//   pause()               for as long as a wait's limit
 template <typename Port>
-KDA_EXCHANGE_FN void exchange_drain(Port& port, int turns, int lost) {
+KDA_EXCHANGE_FN void exchange_drain(Port& port, int K, int turns, int lost) {
+    constexpr int kMost = (1 << 20) / 512 - 16;   // messages, beside those of a turn
+    if ((long long)(turns - 1 - lost) / 2 * K > kMost) {
+        port.pause();
+        return;
+    }
     for (int turn = lost; turn <= lost + 1 && turn < turns; ++turn) {
         port.expect(turn, (turns - 1 - turn) / 2);
         if (!port.wait(turn)) continue;

@@ -412,6 +412,9 @@ struct Exchange {
         ptx::mbar_expect_tx(&sh.arrived[turn & 1], n * K * kMapBytes);
     }
     __device__ __forceinline__ void arrive(int turn) { ptx::mbar_arrive(&sh.arrived[turn & 1]); }
+    __device__ __forceinline__ void pause() {
+        for (const long long t0 = clock64(); clock64() - t0 < limit;) {}
+    }
 };
 
 template <bool VL, int N, bool BACK>
@@ -427,7 +430,7 @@ struct Cluster : Exchange {
     __device__ __forceinline__ void end() {
         cluster_sync();
         const bool gone = kLostInMemory ? threadIdx.x == 0 && lost_turn(0) >= 0 : lost && (threadIdx.x & 31) == 0;
-        if (gone) exchange_drain(*static_cast<Exchange*>(this), turns, sh.lost[0]);
+        if (gone) exchange_drain(*static_cast<Exchange*>(this), K, turns, sh.lost[0]);
     }
 
     // The state that enters this CTA's tile; `carry` goes from before the cluster's tiles of this

@@ -96,6 +96,7 @@ struct Port {
         b.pending = 0;
         w.complete(b);
     }
+    void pause() { w.fault("too few turns for a pause"); }
     void expect(int turn, int n) {
         std::lock_guard<std::mutex> hold(w.lock);
         Barrier& b = w.bars[rank * 2 + turn % 2];
@@ -145,7 +146,7 @@ void cta(World& w, int rank, unsigned seed) {
     }
     w.sync();
     port.last_wait = true;
-    if (lost >= 0) kda::exchange_drain(port, w.turns, lost);
+    if (lost >= 0) kda::exchange_drain(port, w.K, w.turns, lost);
     std::lock_guard<std::mutex> hold(w.lock);
     w.ended[rank] = true;
     w.lost += lost >= 0;
